@@ -18,8 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdt.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA = 0, -1, -2, -3
-ERR_NONFINITE, ERR_TIMEOUT, ERR_BAD_TEMPERATURE = -4, -5, -6
-F32, BF16 = 0, 1
+ERR_NONFINITE, ERR_TIMEOUT, ERR_BAD_TEMPERATURE, ERR_BAD_PAGE = -4, -5, -6, -7
+F32, BF16, F16, E4M3 = 0, 1, 2, 3
 NUM_PHASE_EVENTS = 4
 OPT_TEST_BARRIER_TIMEOUT = 2  # dt_options.flags: failure-detection test hook
 OPT_MARGINAL = 8             # dt_options.flags: marginal (path-independent) scores
@@ -32,7 +32,9 @@ EXPORTS = ("dt_abi_version", "dt_status_string", "dt_prepared_bytes", "dt_prepar
            "dt_build_trees_host", "dt_select_topm_noalloc", "dt_kernel_launches",
            "dt_chain_prepared_bytes", "dt_prepare_chain", "dt_chain_workspace_bytes",
            "dt_chain_kernel_launches", "dt_decode_chains", "dt_tree_positions",
-           "dt_tree_attention", "dt_adaptive_budget", "dt_mapped_host_pointer")
+           "dt_tree_attention", "dt_adaptive_budget", "dt_mapped_host_pointer",
+           "dt_rotary_table", "dt_rotary", "dt_cache_write", "dt_cache_read", "dt_cache_commit",
+           "dt_cache_attention_workspace_bytes", "dt_cache_attention")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -54,6 +56,26 @@ class DtTreeOut(C.Structure):
 class DtOptions(C.Structure):
     _fields_ = [("spec_width", C.c_int), ("phase_events", C.POINTER(C.c_void_p)),
                 ("flags", C.c_int)]
+
+
+class DtRotaryParams(C.Structure):
+    _fields_ = [("rot", C.c_int), ("scaling", C.c_int)] + \
+        [(n, C.c_double) for n in ("base", "factor", "trained", "beta_fast", "beta_slow")]
+
+
+class DtRotation(C.Structure):
+    _fields_ = [("turns", C.c_void_p), ("rot", C.c_int), ("interleaved", C.c_int),
+                ("magnitude", C.c_float)]
+
+
+class DtHeads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("heads", C.c_int), ("stride_batch", C.c_int64),
+                ("stride_head", C.c_int64), ("stride_row", C.c_int64)]
+
+
+class DtCache(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("k", "v", "k_exp", "v_exp", "table", "status")] + \
+        [(n, C.c_int) for n in ("pages", "page", "Hkv", "dh", "dtype", "batch", "table_width")]
 
 
 class DtError(RuntimeError):
@@ -108,6 +130,20 @@ def lib():
                                         C.c_void_p]
         L.dt_tree_attention.argtypes = [C.c_void_p] * 5 + [C.c_int] * 6 + [C.c_float, C.c_void_p,
                                                                           C.c_void_p]
+        heads, cache, rot = C.POINTER(DtHeads), C.POINTER(DtCache), C.POINTER(DtRotation)
+        L.dt_rotary_table.argtypes = [C.POINTER(DtRotaryParams), C.c_void_p,
+                                      C.POINTER(C.c_double)]
+        L.dt_rotary.argtypes = [rot, C.c_void_p] + [C.c_int] * 4 + [heads] * 4 + [C.c_int,
+                                                                                  C.c_void_p]
+        L.dt_cache_write.argtypes = [cache, heads, heads, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
+                                     rot, C.c_void_p, heads, heads, C.c_void_p]
+        L.dt_cache_read.argtypes = [cache, C.c_int, C.c_int, C.c_void_p, C.c_void_p, heads, heads,
+                                    C.c_void_p]
+        L.dt_cache_commit.argtypes = [cache] + [C.c_void_p] * 3 + [C.c_int, C.c_int, C.c_void_p]
+        L.dt_cache_attention_workspace_bytes.restype = C.c_size_t
+        L.dt_cache_attention_workspace_bytes.argtypes = [cache, C.c_int, C.c_int]
+        L.dt_cache_attention.argtypes = [cache, heads, C.c_int, C.c_int] + [C.c_void_p] * 3 + \
+            [C.c_float, heads, C.c_void_p, C.c_size_t, C.c_void_p]
         _lib = L
     return _lib
 
@@ -492,3 +528,225 @@ def adaptive_budget(out: dict, N: int, c_fixed: float, c_node: float, counts=Non
     _check(lib().dt_adaptive_budget(C.byref(o), batch, int(N), float(c_fixed), float(c_node),
                                     _ptr(counts), _stream(stream)), "dt_adaptive_budget")
     return counts
+
+
+# --------------------------------- rotary positions and the paged key/value cache
+
+_TYPE16 = {torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _heads(t, what: str, heads=None, n=None, like=None) -> DtHeads:
+    """A [batch][heads][n][dh] view (last dimension dense) as a dt_heads."""
+    if t.dim() != 4 or t.stride(3) != 1:
+        raise ValueError(f"{what} must be a [batch][heads][n][dh] tensor with a dense last dimension")
+    if t.dtype not in _TYPE16 or not t.is_cuda:
+        raise ValueError(f"{what} must be a bfloat16 or float16 CUDA tensor")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device or
+                             t.shape[0] != like.shape[0] or t.shape[2:] != like.shape[2:]):
+        raise ValueError(f"{what} does not match the other tensor in type, device or shape")
+    if (heads is not None and t.shape[1] != heads) or (n is not None and t.shape[2] != n):
+        raise ValueError(f"{what} has {t.shape[1]} heads of {t.shape[2]} rows")
+    s = t.stride()
+    return DtHeads(t.data_ptr(), t.shape[1], s[0], s[1], s[2])
+
+
+def _ints(t, what: str, shape, device):
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != torch.int32 or not t.is_contiguous() or \
+            t.device != device:
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+class Rotary:
+    """Rotary positions: the table of dt_rotary_table on the device, and how it is
+    used (dt_rotation). ``scaling``: "none", "linear", "base" or "parts"."""
+
+    SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+    def __init__(self, rot: int, interleaved: bool = False, base: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, trained: float = 4096,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(self.SCALINGS)}")
+        p = DtRotaryParams(int(rot), self.SCALINGS[scaling], base, factor, trained, beta_fast,
+                           beta_slow)
+        host = (C.c_uint64 * max(1, int(rot) // 2))()
+        mag = C.c_double()
+        _check(lib().dt_rotary_table(C.byref(p), host, C.byref(mag)), "dt_rotary_table")
+        self.rot, self.interleaved, self.magnitude = int(rot), bool(interleaved), mag.value
+        self.turns = torch.frombuffer(bytearray(host), dtype=torch.int64).to(device)
+        self._struct = DtRotation(self.turns.data_ptr(), self.rot, int(self.interleaved),
+                                  self.magnitude)
+
+
+def rotary(rot: Rotary, positions, q, k=None, q_out=None, k_out=None, gradient=False, stream=None):
+    """dt_rotary: q (and k, in the same launch) [batch][heads][n][dh] turned at
+    positions [batch][n] int32. ``gradient``: the transposed rotation. Outputs
+    default to new dense tensors and may be the inputs. Returns (q_out, k_out), or
+    q_out alone without k."""
+    batch, _, n, dh = q.shape
+    x0 = _heads(q, "q")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    o0 = _heads(q_out, "q_out", q.shape[1], like=q)
+    x1 = o1 = None
+    if k is not None:
+        x1 = _heads(k, "k", like=q)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        o1 = _heads(k_out, "k_out", k.shape[1], like=q)
+    _check(lib().dt_rotary(rot._struct, _ints(positions, "positions", (batch, n), q.device), batch,
+                           n, dh, _TYPE16[q.dtype], x0, o0, x1, o1, int(gradient),
+                           _stream(stream)), "dt_rotary")
+    return q_out if k is None else (q_out, k_out)
+
+
+class PagedCache:
+    """A paged key/value cache (dt_cache): k and v [pages][Hkv][page][dh] (bfloat16,
+    float16, or uint8 / float8_e4m3fn codes with k_exp and v_exp [pages][Hkv][page]
+    uint8), table [batch][width] int32. ``status`` [batch] int32 collects the device's
+    error codes; ``check()`` reads it and raises."""
+
+    def __init__(self, k, v, table, k_exp=None, v_exp=None, status=None):
+        kinds = {torch.bfloat16: BF16, torch.float16: F16, torch.uint8: E4M3,
+                 torch.float8_e4m3fn: E4M3}
+        if k.dim() != 4 or k.dtype not in kinds or v.shape != k.shape or v.dtype != k.dtype or \
+                not (k.is_contiguous() and v.is_contiguous()) or not k.is_cuda or \
+                v.device != k.device:
+            raise ValueError("k and v must be contiguous [pages][Hkv][page][dh] CUDA tensors of "
+                             "one cache type")
+        for e in (k_exp, v_exp):
+            if (kinds[k.dtype] == E4M3) != (e is not None):
+                raise ValueError("k_exp and v_exp belong to 8-bit pages, and only to them")
+            if e is not None and (e.shape != k.shape[:3] or e.dtype != torch.uint8 or
+                                  not e.is_contiguous() or e.device != k.device):
+                raise ValueError("k_exp and v_exp must be contiguous [pages][Hkv][page] uint8 "
+                                 "tensors on the pages' device")
+        if table.dim() != 2:
+            raise ValueError("table must be [batch][width]")
+        self.k, self.v, self.table, self.k_exp, self.v_exp = k, v, table, k_exp, v_exp
+        self.device, self.batch = k.device, table.shape[0]
+        _ints(table, "table", table.shape, k.device)
+        self.status = torch.zeros(self.batch, dtype=torch.int32, device=k.device) \
+            if status is None else status
+        _ints(self.status, "status", (self.batch,), k.device)
+        pages, self.Hkv, page, self.dh = k.shape
+        self._struct = DtCache(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp), _ptr(table),
+                               _ptr(self.status), pages, page, self.Hkv, self.dh, kinds[k.dtype],
+                               self.batch, table.shape[1])
+
+    @classmethod
+    def empty(cls, pages: int, Hkv: int, page: int, dh: int, table, dtype=torch.bfloat16):
+        """A cache of unwritten pages; dtype bfloat16, float16 or float8_e4m3fn."""
+        kw = dict(device=table.device)
+        k, v = (torch.empty((pages, Hkv, page, dh), dtype=dtype, **kw) for _ in range(2))
+        ke = ve = None
+        if dtype == torch.float8_e4m3fn:
+            ke, ve = (torch.empty((pages, Hkv, page), dtype=torch.uint8, **kw) for _ in range(2))
+        return cls(k, v, table, ke, ve)
+
+    def check(self):
+        """Wait for the device and raise if a call met a bad page or timed out."""
+        bad = [(b, c) for b, c in enumerate(self.status.tolist()) if c != OK]
+        if bad:
+            raise DtError("paged cache: " + ", ".join(f"request {b}: {status_string(c)}"
+                                                      for b, c in bad))
+
+
+def _cache_rows(cache: PagedCache, t, what: str, n=None, like=None) -> DtHeads:
+    if t.shape[0] != cache.batch or t.shape[-1] != cache.dh or t.device != cache.device:
+        raise ValueError(f"{what} does not match the cache's batch, head size or device")
+    return _heads(t, what, cache.Hkv, n, like)
+
+
+def cache_write(cache: PagedCache, k, v, first, counts=None, rotary: Rotary | None = None,
+                positions=None, q=None, q_out=None, stream=None):
+    """dt_cache_write: rows of k and v [batch][Hkv][n][dh] to rows first[b].. of the
+    cache, k turned by ``rotary`` at ``positions``; with q, returns its turned rows."""
+    n = k.shape[2]
+    hk, hv = _cache_rows(cache, k, "k"), _cache_rows(cache, v, "v", like=k)
+    hq = ho = None
+    if q is not None:
+        hq = _heads(q, "q", like=k)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        ho = _heads(q_out, "q_out", q.shape[1], like=k)
+    b = (cache.batch,)
+    _check(lib().dt_cache_write(cache._struct, hk, hv, n, _TYPE16[k.dtype],
+                                _ints(first, "first", b, cache.device),
+                                _ints(counts, "counts", b, cache.device),
+                                rotary._struct if rotary is not None else None,
+                                _ints(positions, "positions", (cache.batch, n), cache.device),
+                                hq, ho, _stream(stream)), "dt_cache_write")
+    return q_out
+
+
+def cache_read(cache: PagedCache, n: int, first, counts=None, dtype=None, k_out=None, v_out=None,
+               stream=None):
+    """dt_cache_read: rows first[b] .. first[b] + counts[b] - 1 as dense k and v
+    [batch][Hkv][n][dh] (zeros behind them). dtype defaults to the cache's 16-bit
+    type, bfloat16 for an 8-bit cache."""
+    if dtype is None:
+        dtype = cache.k.dtype if cache.k.dtype in _TYPE16 else torch.bfloat16
+    shape = (cache.batch, cache.Hkv, n, cache.dh)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=cache.device)
+    hk = _cache_rows(cache, k_out, "k_out", n)
+    hv = _cache_rows(cache, v_out, "v_out", n, like=k_out)
+    b = (cache.batch,)
+    _check(lib().dt_cache_read(cache._struct, n, _TYPE16[k_out.dtype],
+                               _ints(first, "first", b, cache.device),
+                               _ints(counts, "counts", b, cache.device), hk, hv,
+                               _stream(stream)), "dt_cache_read")
+    return k_out, v_out
+
+
+def cache_commit(cache: PagedCache, first, path, lengths, n: int, stream=None):
+    """dt_cache_commit: cache row first[b] + path[b][j] to row first[b] + j for
+    j < lengths[b], in place; ``n`` is the trees' rows."""
+    b = (cache.batch,)
+    _check(lib().dt_cache_commit(cache._struct, _ints(first, "first", b, cache.device),
+                                 _ints(path, "path", (cache.batch, path.shape[-1]), cache.device),
+                                 _ints(lengths, "lengths", b, cache.device), path.shape[-1], int(n),
+                                 _stream(stream)), "dt_cache_commit")
+
+
+def cache_attention_workspace(cache: PagedCache, H: int, n: int):
+    """A workspace for cache_attention with H query heads and n rows."""
+    nbytes = lib().dt_cache_attention_workspace_bytes(cache._struct, int(H), int(n))
+    if nbytes == 0:
+        raise DtError("dt_cache_attention_workspace_bytes failed (invalid sizes or unsupported device)")
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+
+
+def cache_attention(cache: PagedCache, q, prefix_len, mask=None, counts=None, scale=None, out=None,
+                    workspace=None, stream=None):
+    """dt_cache_attention: q [batch][H][n][dh] over the cache, with the trees' mask
+    [batch][n][n] uint8 or causally (mask None). ``workspace`` (of
+    cache_attention_workspace) is allocated for the call when None. Returns out,
+    by default a new dense tensor of q's shape and type."""
+    batch, H, n, dh = q.shape
+    if batch != cache.batch or dh != cache.dh or q.device != cache.device:
+        raise ValueError("q does not match the cache's batch, head size or device")
+    if mask is not None and (tuple(mask.shape) != (batch, n, n) or not mask.is_contiguous() or
+                             mask.dtype not in (torch.uint8, torch.bool) or
+                             mask.device != q.device):
+        raise ValueError(f"mask must be a contiguous uint8 tensor of shape {(batch, n, n)}")
+    hq = _heads(q, "q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    ho = _heads(out, "out", H, like=q)
+    if workspace is None:
+        workspace = cache_attention_workspace(cache, H, n)
+    _check(lib().dt_cache_attention(cache._struct, hq, n, _TYPE16[q.dtype],
+                                    _ints(prefix_len, "prefix_len", (batch,), q.device),
+                                    _ints(counts, "counts", (batch,), q.device), _ptr(mask),
+                                    float(dh ** -0.5 if scale is None else scale), ho,
+                                    workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(),
+                                    _stream(stream)), "dt_cache_attention")
+    return out

@@ -26,6 +26,8 @@ inline size_t al(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+}  // namespace
+
 int device_sm_count(int *sms, int *smem_optin) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DT_ERR_CUDA;
@@ -39,8 +41,6 @@ int device_sm_count(int *sms, int *smem_optin) {
   if (major != 10 || minor != 3) return DT_ERR_UNSUPPORTED;  // built for sm_103a only
   return DT_OK;
 }
-
-}  // namespace
 
 int validate_dims(const dt_dims *d) {
   if (!d) return DT_ERR_INVALID_ARG;
@@ -521,6 +521,7 @@ const char *dt_status_string(int code) {
     case DT_ERR_NONFINITE: return "a base logit of the request is NaN or +inf";
     case DT_ERR_TIMEOUT: return "bounded inter-block wait expired; request output invalid";
     case DT_ERR_BAD_TEMPERATURE: return "temperature is negative or not finite";
+    case DT_ERR_BAD_PAGE: return "a cache row lies outside its page table or the pool";
     default: return "unknown status code";
   }
 }

@@ -1,0 +1,557 @@
+// dt_cache.cu -- rotary positions and the paged key/value cache: rows written
+// (turned and quantised on the way), read back, and compacted onto an accepted
+// path. All of it moves bytes: each value is read once and written once.
+//
+// Turning: y_a = m (x_a cos - x_b sin), y_b = m (x_a sin + x_b cos). The angle of pair
+// i at position p is frac(p f_i / 2 pi) turns; f_i / 2 pi is a 64-bit fraction of
+// a turn, so p times it modulo 2^64 is exact to p 2^-65 turns, where a product in
+// fp32 would be off by p 2^-25. The upper 32 bits, as a signed number in units of
+// 2^-31 half turns, go to sincospif.
+#include <cmath>
+#include <cstdint>
+
+#include "dt_cache.cuh"
+#include "dt_internal.h"
+
+namespace dt {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kLanes = 8;                     // lanes of one head row
+constexpr int kGroups = kThreads / kLanes;    // head rows in flight per block
+constexpr int kMaxHalf = 128;                 // pairs of a head, at most
+
+struct View {            // one of up to three tensors of a launch
+  const char *in;
+  char *out;             // null: the cache
+  int64_t ib, ih, ir, ob, oh, orow;   // strides in bytes
+  int heads, turned, to_v;
+};
+
+struct RowArgs {
+  View t[3];
+  int nt, heads;         // tensors, and their heads together
+  CacheView c;           // where a tensor goes to the cache
+  const int32_t *first, *counts, *positions;
+  const uint64_t *turns;
+  float mag;
+  int batch, n, dh, rot, interleaved, gradient;
+  int tokens_block, heads_block, head_blocks;
+};
+
+__device__ __forceinline__ int clamped_count(const int32_t *counts, int b, int n) {
+  return counts ? min(max(counts[b], 0), n) : n;
+}
+
+// Head rows from the tensors t[] to views or to the cache. A block takes
+// tokens_block tokens and heads_block heads of each: the angles of a token are
+// computed once for all of them. Eight lanes own a row; a lane holds chunks of VEC
+// values two at a time, chunk c of the turned part with its partner (halves: the
+// pair's other half, so a lane reads both before it writes either and a tensor can
+// be turned in place; interleaved: any other chunk). 8-bit rows need the row's
+// largest magnitude before the first code, so a lane keeps its values in registers.
+// Bound by memory: 32 bytes a lane in flight, 8 blocks an SM.
+template <int DT, bool QUANT, int VEC, int ITEMS>
+__global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_constant__ RowArgs a) {
+  extern __shared__ float s_cs[];      // [tokens_block][2][rot / 2]
+  const int tid = threadIdx.x, lane = tid & (kLanes - 1), grp = tid / kLanes;
+  const int64_t all = static_cast<int64_t>(a.batch) * a.n;
+  const int64_t tk0 = static_cast<int64_t>(blockIdx.x / a.head_blocks) * a.tokens_block;
+  const int h0 = static_cast<int>(blockIdx.x % a.head_blocks) * a.heads_block;
+  const int nh = min(a.heads_block, a.heads - h0);
+  const int ntok = static_cast<int>(min(static_cast<int64_t>(a.tokens_block), all - tk0));
+  const int half = a.rot >> 1;
+  for (int u = tid; u < ntok * half; u += kThreads) {
+    const int t = u / half, i = u - t * half;
+    const int64_t p = a.positions[tk0 + t];
+    const uint64_t frac = static_cast<uint64_t>(p) * a.turns[i];   // modulo one turn
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f, &s, &c);
+    if (a.gradient) s = -s;
+    s_cs[(2 * t) * half + i] = a.mag * c;
+    s_cs[(2 * t + 1) * half + i] = a.mag * s;
+  }
+  __syncthreads();
+  const int chunks = a.dh / VEC;
+  for (int r = grp; r < ntok * nh; r += kGroups) {
+    const int t = r / nh;
+    int h = h0 + (r - t * nh), k = 0;
+    while (k + 1 < a.nt && h >= a.t[k].heads) h -= a.t[k++].heads;
+    const View &vw = a.t[k];
+    const int64_t tk = tk0 + t;
+    const int b = static_cast<int>(tk / a.n), i = static_cast<int>(tk - static_cast<int64_t>(b) * a.n);
+    const char *in = vw.in + b * vw.ib + h * vw.ih + i * vw.ir;
+    char *out = vw.out;
+    uint8_t *expo = nullptr;
+    if (out) {
+      out += b * vw.ob + h * vw.oh + i * vw.orow;
+    } else {
+      if (i >= clamped_count(a.counts, b, a.n)) continue;
+      const int64_t row = cache_row(a.c, b, static_cast<int64_t>(a.first[b]) + i, h);
+      if (row < 0) {
+        cache_fault(a.c, b);
+        continue;
+      }
+      out = static_cast<char *>(vw.to_v ? a.c.v : a.c.k) + row * a.dh * (QUANT ? 1 : 2);
+      if (QUANT) expo = (vw.to_v ? a.c.v_exp : a.c.k_exp) + row;
+    }
+    const int pairs = vw.turned ? a.rot / (2 * VEC) : 0;      // chunk pairs of the turned part
+    const int rest = chunks - 2 * pairs, rest2 = (rest + 1) >> 1, items = pairs + rest2;
+    const float *cs = s_cs + 2 * t * half;
+    float x[ITEMS][2][VEC];
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int m = lane + it * kLanes;
+      const bool turn = m < pairs;
+      const int c0 = turn ? m : 2 * pairs + (m - pairs);
+      const int c1 = turn ? m + pairs : c0 + rest2;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int c = z ? c1 : c0;
+        uint32_t w[VEC / 2];
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) w[e] = 0u;
+        if (m < items && c < chunks) {
+          if (VEC == 8) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(in + c * 16);
+          else *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(in + c * 8);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+          const float2 f = Half16<DT>::unpack(w[e]);
+          x[it][z][2 * e] = f.x;
+          x[it][z][2 * e + 1] = f.y;
+        }
+      }
+      if (turn && !a.interleaved) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float c = cs[m * VEC + e], s = cs[half + m * VEC + e];
+          const float xa = x[it][0][e], xb = x[it][1][e];
+          x[it][0][e] = xa * c - xb * s;
+          x[it][1][e] = xa * s + xb * c;
+        }
+      } else if (turn) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int e = 0; e < VEC; e += 2) {
+            const int p = ((z ? c1 : c0) * VEC + e) >> 1;
+            const float c = cs[p], s = cs[half + p];
+            const float xa = x[it][z][e], xb = x[it][z][e + 1];
+            x[it][z][e] = xa * c - xb * s;
+            x[it][z][e + 1] = xa * s + xb * c;
+          }
+      }
+    }
+    const bool quant = QUANT && !vw.out;
+    float scale = 1.0f, top = 448.0f;
+    bool whole = true;
+    if (quant) {
+      uint32_t mx = 0;   // of magnitude bits: NaN > infinity > finite
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+        for (int e = 0; e < 2 * VEC; ++e)
+          mx = max(mx, __float_as_uint(x[it][e / VEC][e % VEC]) & 0x7fffffffu);
+#pragma unroll
+      for (int d = 1; d < kLanes; d <<= 1)
+        mx = max(mx, __shfl_xor_sync(0xffu << (threadIdx.x & 24), mx, d));
+      whole = mx < 0x7f800000u;
+      const int e = row_exponent(__uint_as_float(mx));
+      scale = exp2i(-e);
+      if (e == 120) top = 240.0f;   // 256 2^120 is no finite bf16 number
+      if (lane == 0) *expo = static_cast<uint8_t>(whole ? e + 127 : 255);
+    }
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int m = lane + it * kLanes;
+      const int c0 = m < pairs ? m : 2 * pairs + (m - pairs);
+      const int c1 = m < pairs ? m + pairs : c0 + rest2;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int c = z ? c1 : c0;
+        if (m >= items || c >= chunks) continue;
+        const float *f = x[it][z];
+        if (quant) {
+          uint32_t w[VEC / 4];
+#pragma unroll
+          for (int e = 0; e < VEC; e += 4) {
+            float q[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) q[y] = fminf(fmaxf(f[e + y] * scale, -top), top);
+            w[e / 4] = whole ? e4m3_pack2(q[0], q[1]) | (e4m3_pack2(q[2], q[3]) << 16) : 0x7f7f7f7fu;
+          }
+          if (VEC == 8) *reinterpret_cast<uint2 *>(out + c * 8) = make_uint2(w[0], w[VEC / 4 - 1]);
+          else *reinterpret_cast<uint32_t *>(out + c * 4) = w[0];
+        } else {
+          uint32_t w[VEC / 2];
+#pragma unroll
+          for (int e = 0; e < VEC / 2; ++e) w[e] = Half16<DT>::pack(f[2 * e], f[2 * e + 1]);
+          if (VEC == 8) *reinterpret_cast<uint4 *>(out + c * 16) = *reinterpret_cast<uint4 *>(w);
+          else *reinterpret_cast<uint2 *>(out + c * 8) = *reinterpret_cast<uint2 *>(w);
+        }
+      }
+    }
+  }
+}
+
+struct ReadArgs {
+  CacheView c;
+  const int32_t *first, *counts;
+  char *k, *v;
+  int64_t kb, kh, kr, vb, vh, vr;    // strides in bytes
+  int n, row_blocks;
+};
+
+constexpr int kReadRows = 64;        // rows of a block, of one head
+
+// Rows of the cache to dense views. A block takes 64 rows of one (request, head):
+// their places once into shared memory, then 8 values a lane, four rows of K and
+// of V in flight a lane.
+template <int DT, bool QUANT>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadArgs a) {
+  __shared__ int64_t s_row[kReadRows];
+  const int tid = threadIdx.x, dh = a.c.dh, chunks = dh >> 3;
+  const int bh = blockIdx.x / a.row_blocks;
+  const int i0 = static_cast<int>(blockIdx.x % a.row_blocks) * kReadRows;
+  const int b = bh / a.c.Hkv, hk = bh - b * a.c.Hkv;
+  const int count = clamped_count(a.counts, b, a.n), rows = min(kReadRows, a.n - i0);
+  if (tid < rows) {
+    int64_t row = -1;
+    if (i0 + tid < count) {
+      row = cache_row(a.c, b, static_cast<int64_t>(a.first[b]) + i0 + tid, hk);
+      if (row < 0) cache_fault(a.c, b);
+    }
+    s_row[tid] = row;
+  }
+  __syncthreads();
+  // lanes a row: the power of two at or above its 8-value chunks
+  const int lsh = chunks <= 8 ? 3 : chunks <= 16 ? 4 : 5;
+  const int c = tid & ((1 << lsh) - 1), step = kThreads >> lsh;
+  if (c >= chunks) return;
+  constexpr int kUnroll = 4;
+  for (int r0 = tid >> lsh; r0 < rows; r0 += kUnroll * step) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const char *pool = static_cast<const char *>(which ? a.c.v : a.c.k);
+      const uint8_t *expo = which ? a.c.v_exp : a.c.k_exp;
+      char *out = which ? a.v + b * a.vb + hk * a.vh : a.k + b * a.kb + hk * a.kh;
+      const int64_t stride = which ? a.vr : a.kr;
+      uint4 w[kUnroll];
+      float scale[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int r = r0 + u * step;
+        const int64_t row = r < rows ? s_row[r] : -1;
+        w[u] = make_uint4(0u, 0u, 0u, 0u);
+        scale[u] = 0.0f;
+        if (row >= 0) {
+          if (QUANT) {
+            const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(pool + row * dh) + c);
+            w[u].x = q.x;
+            w[u].y = q.y;
+            scale[u] = row_scale(expo[row]);
+          } else {
+            w[u] = __ldcs(reinterpret_cast<const uint4 *>(pool + row * dh * 2) + c);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int r = r0 + u * step;
+        if (r >= rows) break;
+        uint4 o = w[u];
+        if (QUANT) {
+          o.x = e4m3_to16<DT>(w[u].x & 0xffffu, scale[u]);
+          o.y = e4m3_to16<DT>(w[u].x >> 16, scale[u]);
+          o.z = e4m3_to16<DT>(w[u].y & 0xffffu, scale[u]);
+          o.w = e4m3_to16<DT>(w[u].y >> 16, scale[u]);
+        }
+        __stcs(reinterpret_cast<uint4 *>(out + (i0 + r) * stride) + c, o);
+      }
+    }
+  }
+}
+
+struct CommitArgs {
+  CacheView c;
+  const int32_t *first, *path, *lengths;
+  int width, n, row_bytes;
+};
+
+constexpr int kMaxPath = DT_MAX_D + 1;
+
+// One block per (request, head, K or V): all rows of the path into shared memory,
+// a barrier, then to their new places. Paths rise, but nothing relies on it.
+// Bound by latency: 16 KB or less a block.
+__global__ void __launch_bounds__(kThreads) cache_commit_kernel(const __grid_constant__ CommitArgs a) {
+  __shared__ int64_t s_from[kMaxPath], s_to[kMaxPath];
+  __shared__ uint8_t s_exp[kMaxPath];
+  extern __shared__ __align__(16) unsigned char s_rows[];   // [width][row_bytes]
+  const int tid = threadIdx.x;
+  const int which = blockIdx.x & 1, bh = blockIdx.x >> 1;
+  const int b = bh / a.c.Hkv, hk = bh - b * a.c.Hkv;
+  const int len = min(max(a.lengths[b], 0), a.width);
+  char *pool = static_cast<char *>(which ? a.c.v : a.c.k);
+  uint8_t *expo = which ? a.c.v_exp : a.c.k_exp;
+  if (tid < len) {
+    const int p = a.path[static_cast<int64_t>(b) * a.width + tid];
+    const int64_t first = a.first[b];
+    int64_t from = -1, to = -1;
+    if (p >= 0 && p < a.n && first >= 0) {
+      from = cache_row(a.c, b, first + p, hk);
+      to = cache_row(a.c, b, first + tid, hk);
+    }
+    const bool fine = from >= 0 && to >= 0;
+    if (!fine) cache_fault(a.c, b);
+    s_from[tid] = fine && from != to ? from : -1;
+    s_to[tid] = to;
+    if (expo && fine) s_exp[tid] = expo[from];
+  }
+  __syncthreads();
+  const int units = a.row_bytes >> 4;
+  for (int u = tid; u < len * units; u += kThreads) {
+    const int j = u / units, c = u - j * units;
+    if (s_from[j] >= 0)
+      reinterpret_cast<uint4 *>(s_rows)[u] =
+          reinterpret_cast<const uint4 *>(pool + s_from[j] * a.row_bytes)[c];
+  }
+  __syncthreads();
+  for (int u = tid; u < len * units; u += kThreads) {
+    const int j = u / units, c = u - j * units;
+    if (s_from[j] >= 0)
+      reinterpret_cast<uint4 *>(pool + s_to[j] * a.row_bytes)[c] =
+          reinterpret_cast<const uint4 *>(s_rows)[u];
+  }
+  if (expo && tid < len && s_from[tid] >= 0) expo[s_to[tid]] = s_exp[tid];
+}
+
+bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool al4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+template <int DT, bool QUANT>
+cudaError_t launch_rows(const RowArgs &a, cudaStream_t st) {
+  const int64_t tokens = static_cast<int64_t>(a.batch) * a.n;
+  const int64_t grid = (tokens + a.tokens_block - 1) / a.tokens_block * a.head_blocks;
+  const size_t smem = sizeof(float) * a.tokens_block * a.rot;
+  // 8-value chunks where a turned half is made of them, else 4 (rot = 8 mod 16)
+  const bool wide = a.rot % 16 == 0;
+  auto go = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
+    return cudaGetLastError();
+  };
+  if (wide)
+    return a.dh <= 128 ? go(cache_rows_kernel<DT, QUANT, 8, 1>) : go(cache_rows_kernel<DT, QUANT, 8, 2>);
+  return a.dh <= 128 ? go(cache_rows_kernel<DT, QUANT, 4, 2>) : go(cache_rows_kernel<DT, QUANT, 4, 4>);
+}
+
+// Tokens and heads of a block: where there are too few head rows to fill the GPU
+// with blocks of 32 rows (one for each group of lanes), one token's heads are cut
+// over blocks; else a block takes four tokens, so that a launch's angles are
+// computed once and its blocks stay few.
+void split_rows(RowArgs *a) {
+  const int64_t rows = static_cast<int64_t>(a->batch) * a->n * a->heads;
+  if (rows < static_cast<int64_t>(kGroups) * 2048) {
+    a->tokens_block = 1;
+    a->heads_block = a->heads < kGroups ? a->heads : kGroups;
+  } else {
+    a->tokens_block = 4;
+    a->heads_block = a->heads;
+  }
+  a->head_blocks = (a->heads + a->heads_block - 1) / a->heads_block;
+}
+
+bool set_in(View *v, const dt_heads *x) {
+  v->in = static_cast<const char *>(x->data);
+  v->ib = 2 * x->stride_batch; v->ih = 2 * x->stride_head; v->ir = 2 * x->stride_row;
+  v->heads = x->heads;
+  return true;
+}
+void set_out(View *v, const dt_heads *x) {
+  v->out = static_cast<char *>(x->data);
+  v->ob = 2 * x->stride_batch; v->oh = 2 * x->stride_head; v->orow = 2 * x->stride_row;
+}
+
+bool set_rotation(RowArgs *a, const dt_rotation *rot, const int32_t *positions, int dh) {
+  if (!rot || !positions || !al4(positions) || !rot->turns ||
+      (reinterpret_cast<uintptr_t>(rot->turns) & 7u) || rot->rot < 8 || rot->rot > dh ||
+      rot->rot % 8 || !std::isfinite(rot->magnitude))
+    return false;
+  a->turns = rot->turns;
+  a->rot = rot->rot;
+  a->interleaved = rot->interleaved != 0;
+  a->mag = rot->magnitude;
+  a->positions = positions;
+  return true;
+}
+
+constexpr int64_t kMaxTokens = int64_t{1} << 28;   // keeps every grid below 2^31
+
+}  // namespace
+
+// sizes, alignment and strides of a [batch][heads][n][dh] view
+bool heads_ok(const dt_heads *x) {
+  return x && x->data && al16(x->data) && x->heads >= 1 && x->heads <= 4096 &&
+         x->stride_batch % 8 == 0 && x->stride_head % 8 == 0 && x->stride_row % 8 == 0;
+}
+
+int check_cache(const dt_cache *c) {
+  if (!c || !c->k || !c->v || !c->table || !c->status || !al16(c->k) || !al16(c->v) ||
+      !al4(c->table) || !al4(c->status))
+    return DT_ERR_INVALID_ARG;
+  if (!(c->page == 16 || c->page == 32 || c->page == 64 || c->page == 128) || c->pages < 1 ||
+      c->Hkv < 1 || c->Hkv > 4096 || c->dh < 16 || c->dh > 256 || c->dh % 16 || c->batch < 1 ||
+      c->batch > 65535 || c->table_width < 1 || c->table_width > (1 << 24) / 16)
+    return DT_ERR_INVALID_ARG;
+  if (!(c->dtype == DT_BF16 || c->dtype == DT_F16 || c->dtype == DT_E4M3))
+    return DT_ERR_INVALID_ARG;
+  if ((c->dtype == DT_E4M3) != (c->k_exp != nullptr) || (c->dtype == DT_E4M3) != (c->v_exp != nullptr))
+    return DT_ERR_INVALID_ARG;
+  return DT_OK;
+}
+
+// the type of tensors around the cache: its own, or a 16-bit one for 8-bit rows
+bool cache_dtype_ok(const dt_cache *c, int dtype) {
+  return (dtype == DT_BF16 || dtype == DT_F16) && (c->dtype == DT_E4M3 || c->dtype == dtype);
+}
+
+}  // namespace dt
+
+extern "C" {
+
+int dt_rotary_table(const dt_rotary_params *p, uint64_t *turns, double *magnitude) {
+  if (!p || !turns || !magnitude) return DT_ERR_INVALID_ARG;
+  if (p->rot < 8 || p->rot > 2 * dt::kMaxHalf || p->rot % 8 || !std::isfinite(p->base) ||
+      !(p->base > 1.0) || !std::isfinite(p->factor) || !(p->factor >= 1.0) ||
+      p->scaling < DT_ROTARY_NONE || p->scaling > DT_ROTARY_PARTS)
+    return DT_ERR_INVALID_ARG;
+  const bool parts = p->scaling == DT_ROTARY_PARTS;
+  if (parts && (!std::isfinite(p->trained) || !(p->trained >= 1.0) || !std::isfinite(p->beta_fast) ||
+                !std::isfinite(p->beta_slow) || !(p->beta_fast > p->beta_slow)))
+    return DT_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925286766559;
+  double base = p->base;
+  if (p->scaling == DT_ROTARY_BASE) base *= std::pow(p->factor, p->rot / (p->rot - 2.0));
+  if (!std::isfinite(base)) return DT_ERR_INVALID_ARG;
+  for (int i = 0; i < p->rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / p->rot);
+    if (p->scaling == DT_ROTARY_LINEAR) f /= p->factor;
+    if (parts) {
+      double g = (p->trained * f / two_pi - p->beta_slow) / (p->beta_fast - p->beta_slow);
+      g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+      f *= g + (1.0 - g) / p->factor;
+    }
+    turns[i] = static_cast<uint64_t>(std::ldexp(f / two_pi, 64) + 0.5);   // f / 2 pi < 1/6
+  }
+  *magnitude = parts ? 1.0 + 0.1 * std::log(p->factor) : 1.0;
+  return DT_OK;
+}
+
+int dt_rotary(const dt_rotation *rot, const int32_t *positions, int batch, int n, int dh,
+              int dtype, const dt_heads *x0, const dt_heads *out0, const dt_heads *x1,
+              const dt_heads *out1, int gradient, void *stream) {
+  if (batch < 1 || batch > 65535 || n < 1 || static_cast<int64_t>(batch) * n > dt::kMaxTokens ||
+      dh < 16 || dh > 256 || dh % 16 || !(dtype == DT_BF16 || dtype == DT_F16))
+    return DT_ERR_INVALID_ARG;
+  if (!dt::heads_ok(x0) || !dt::heads_ok(out0) || x0->heads != out0->heads || !x1 != !out1)
+    return DT_ERR_INVALID_ARG;
+  if (x1 && (!dt::heads_ok(x1) || !dt::heads_ok(out1) || x1->heads != out1->heads))
+    return DT_ERR_INVALID_ARG;
+  dt::RowArgs a = {};
+  if (!dt::set_rotation(&a, rot, positions, dh)) return DT_ERR_INVALID_ARG;
+  a.gradient = gradient != 0;
+  a.batch = batch; a.n = n; a.dh = dh;
+  a.nt = x1 ? 2 : 1;
+  for (int i = 0; i < a.nt; ++i) {
+    dt::set_in(&a.t[i], i ? x1 : x0);
+    dt::set_out(&a.t[i], i ? out1 : out0);
+    a.t[i].turned = 1;
+    a.heads += a.t[i].heads;
+  }
+  dt::split_rows(&a);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == DT_BF16 ? dt::launch_rows<DT_BF16, false>(a, st)
+                                         : dt::launch_rows<DT_F16, false>(a, st);
+  return e == cudaSuccess ? DT_OK : DT_ERR_CUDA;
+}
+
+int dt_cache_write(const dt_cache *c, const dt_heads *k, const dt_heads *v, int n, int dtype,
+                   const int32_t *first, const int32_t *counts, const dt_rotation *rot,
+                   const int32_t *positions, const dt_heads *q, const dt_heads *q_out,
+                   void *stream) {
+  if (dt::check_cache(c) || !dt::cache_dtype_ok(c, dtype) || !dt::heads_ok(k) || !dt::heads_ok(v) ||
+      k->heads != c->Hkv || v->heads != c->Hkv || n < 1 ||
+      static_cast<int64_t>(c->batch) * n > dt::kMaxTokens || !first || !dt::al4(first) ||
+      !dt::al4(counts) || !rot != !positions || !q != !q_out || (q && !rot))
+    return DT_ERR_INVALID_ARG;
+  if (q && (!dt::heads_ok(q) || !dt::heads_ok(q_out) || q->heads != q_out->heads))
+    return DT_ERR_INVALID_ARG;
+  dt::RowArgs a = {};
+  if (rot && !dt::set_rotation(&a, rot, positions, c->dh)) return DT_ERR_INVALID_ARG;
+  a.c = dt::cache_view(*c);
+  a.first = first; a.counts = counts;
+  a.batch = c->batch; a.n = n; a.dh = c->dh;
+  a.nt = q ? 3 : 2;
+  dt::set_in(&a.t[0], k);
+  a.t[0].turned = rot != nullptr;
+  dt::set_in(&a.t[1], v);
+  a.t[1].to_v = 1;
+  a.heads = 2 * c->Hkv;
+  if (q) {
+    dt::set_in(&a.t[2], q);
+    dt::set_out(&a.t[2], q_out);
+    a.t[2].turned = 1;
+    a.heads += q->heads;
+  }
+  dt::split_rows(&a);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool quant = c->dtype == DT_E4M3;
+  const cudaError_t e =
+      dtype == DT_BF16 ? (quant ? dt::launch_rows<DT_BF16, true>(a, st) : dt::launch_rows<DT_BF16, false>(a, st))
+                       : (quant ? dt::launch_rows<DT_F16, true>(a, st) : dt::launch_rows<DT_F16, false>(a, st));
+  return e == cudaSuccess ? DT_OK : DT_ERR_CUDA;
+}
+
+int dt_cache_read(const dt_cache *c, int n, int dtype, const int32_t *first,
+                  const int32_t *counts, const dt_heads *k, const dt_heads *v, void *stream) {
+  if (dt::check_cache(c) || !dt::cache_dtype_ok(c, dtype) || !dt::heads_ok(k) || !dt::heads_ok(v) ||
+      k->heads != c->Hkv || v->heads != c->Hkv || n < 1 || !first || !dt::al4(first) ||
+      !dt::al4(counts))
+    return DT_ERR_INVALID_ARG;
+  const int64_t row_blocks = (static_cast<int64_t>(n) + dt::kReadRows - 1) / dt::kReadRows;
+  const int64_t grid = row_blocks * c->batch * c->Hkv;
+  if (grid > 0x7fffffff) return DT_ERR_INVALID_ARG;
+  dt::ReadArgs a;
+  a.c = dt::cache_view(*c);
+  a.first = first; a.counts = counts;
+  a.k = static_cast<char *>(k->data); a.v = static_cast<char *>(v->data);
+  a.kb = 2 * k->stride_batch; a.kh = 2 * k->stride_head; a.kr = 2 * k->stride_row;
+  a.vb = 2 * v->stride_batch; a.vh = 2 * v->stride_head; a.vr = 2 * v->stride_row;
+  a.n = n; a.row_blocks = static_cast<int>(row_blocks);
+  auto go = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(grid), dt::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return cudaGetLastError() == cudaSuccess ? DT_OK : DT_ERR_CUDA;
+  };
+  if (c->dtype != DT_E4M3) return go(dt::cache_read_kernel<DT_BF16, false>);   // a copy
+  return dtype == DT_BF16 ? go(dt::cache_read_kernel<DT_BF16, true>)
+                          : go(dt::cache_read_kernel<DT_F16, true>);
+}
+
+int dt_cache_commit(const dt_cache *c, const int32_t *first, const int32_t *path,
+                    const int32_t *lengths, int width, int n, void *stream) {
+  if (dt::check_cache(c) || !first || !path || !lengths || !dt::al4(first) || !dt::al4(path) ||
+      !dt::al4(lengths) || width < 1 || width > dt::kMaxPath || n < 1 || n > DT_MAX_N + 1)
+    return DT_ERR_INVALID_ARG;
+  const int64_t grid = 2ll * c->batch * c->Hkv;
+  dt::CommitArgs a;
+  a.c = dt::cache_view(*c);
+  a.first = first; a.path = path; a.lengths = lengths;
+  a.width = width; a.n = n;
+  a.row_bytes = c->dh * (c->dtype == DT_E4M3 ? 1 : 2);
+  dt::cache_commit_kernel<<<static_cast<unsigned>(grid), dt::kThreads, width * a.row_bytes,
+                            static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? DT_OK : DT_ERR_CUDA;
+}
+
+}  // extern "C"

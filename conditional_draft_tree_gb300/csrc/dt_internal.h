@@ -66,6 +66,8 @@ constexpr int kReqFlagNonfinite = 1;
 
 int make_plan(const dt_dims *dims, int wdtype, const dt_options *opt, Plan *p);
 int validate_dims(const dt_dims *dims);
+// SMs and opt-in shared memory of the current device; an error code on another architecture
+int device_sm_count(int *sms, int *smem_optin);
 
 // top-M over base logits -> candidate ids/values (+ optional user copy)
 cudaError_t launch_topm(const Plan &p, const float *base_logits, void *ws, int32_t *topm_out,

@@ -52,6 +52,7 @@ extern "C" {
 #define DT_ERR_NONFINITE (-4)     /* device: a base logit of the request is NaN or +inf */
 #define DT_ERR_TIMEOUT (-5)       /* device: a bounded inter-block wait expired; request output invalid */
 #define DT_ERR_BAD_TEMPERATURE (-6) /* device: temperature < 0 or not finite */
+#define DT_ERR_BAD_PAGE (-7)      /* device: a cache row outside the request's page table or the pool */
 
 /* Hard limits of this library (checked by every entry point). */
 #define DT_MAX_M 256        /* candidates per depth */
@@ -62,7 +63,9 @@ extern "C" {
 #define DT_MAX_R 1024       /* correction rank */
 #define DT_MAX_SPEC 16      /* speculative expansions per request and step */
 
-typedef enum { DT_F32 = 0, DT_BF16 = 1 } dt_dtype;
+/* DT_F16 and DT_E4M3 are types of the paged cache and of the tensors around it;
+ * weights are DT_F32 or DT_BF16. */
+typedef enum { DT_F32 = 0, DT_BF16 = 1, DT_F16 = 2, DT_E4M3 = 3 } dt_dtype;
 
 /* Problem sizes. Notation of the pages: V vocabulary, d backbone hidden size,
  * d_s GRU state size, r correction rank, D = B - 1 draft depths, M candidates per
@@ -342,6 +345,139 @@ int dt_tree_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
  * c_fixed, c_node > 0 and finite, else DT_ERR_INVALID_ARG. Asynchronous. */
 int dt_adaptive_budget(const dt_tree_out *out, int batch, int N, double c_fixed, double c_node,
                        int32_t *counts, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions: the first `rot` values of a head are turned in pairs, pair i
+ * by the angle p f_i at position p, and scaled by a magnitude:
+ *   y_a = mag (x_a cos(p f_i) - x_b sin(p f_i))
+ *   y_b = mag (x_a sin(p f_i) + x_b cos(p f_i)),     i = 0 .. rot/2 - 1
+ * with (a, b) = (i, i + rot/2), or (2i, 2i + 1) when interleaved; the other
+ * values of the head are copied. f_i = base^(-2i/rot), changed for contexts
+ * longer than the trained one by
+ *   DT_ROTARY_LINEAR  f_i / factor
+ *   DT_ROTARY_BASE    base factor^(rot / (rot - 2)) in the place of base
+ *   DT_ROTARY_PARTS   f_i (g + (1 - g) / factor), g = the pair's turns over the
+ *                     trained length, trained f_i / 2 pi, mapped linearly from
+ *                     [beta_slow, beta_fast] to [0, 1] and clamped;
+ *                     mag = 1 + 0.1 ln(factor) (1 for the other scalings)
+ *
+ * dt_rotary_table (host only): fills turns[rot/2] (host memory) with f_i / 2 pi in
+ * units of 2^-64 turns, and *magnitude. A position times such a fraction, taken
+ * modulo 2^64, is the angle's fraction of a turn, so positions of any size
+ * lose nothing. Copy the table to the device once and name it in dt_rotation.
+ * rot: a multiple of 8 in [8, 256]; base > 1; factor >= 1; trained >= 1 and
+ * beta_fast > beta_slow for DT_ROTARY_PARTS. */
+#define DT_ROTARY_NONE 0
+#define DT_ROTARY_LINEAR 1
+#define DT_ROTARY_BASE 2
+#define DT_ROTARY_PARTS 3
+typedef struct {
+  int rot, scaling;
+  double base, factor, trained, beta_fast, beta_slow;
+} dt_rotary_params;
+int dt_rotary_table(const dt_rotary_params *p, uint64_t *turns, double *magnitude);
+
+typedef struct {
+  const uint64_t *turns;   /* device, [rot/2], of dt_rotary_table */
+  int rot, interleaved;
+  float magnitude;
+} dt_rotation;
+
+/* A [batch][heads][n][dh] view: element strides of its first three dimensions
+ * (multiples of 8; the last is dense), so that heads can be read where a
+ * projection wrote them. data 16-byte aligned. */
+typedef struct {
+  void *data;
+  int heads;
+  int64_t stride_batch, stride_head, stride_row;
+} dt_heads;
+
+/* Turn one tensor, or two in one launch (x1, out1 NULL: one): out = rotation of x
+ * at positions[batch][n] (int32, device, any sign). `gradient` != 0 gives the
+ * transposed rotation instead (the angles negated, the same magnitude): the
+ * gradient with respect to x for the gradient with respect to out. dtype
+ * DT_BF16 or DT_F16; computed in fp32, rounded once. An output may be its own
+ * input (the same view) and must not overlap it otherwise. */
+int dt_rotary(const dt_rotation *rot, const int32_t *positions, int batch, int n, int dh,
+              int dtype, const dt_heads *x0, const dt_heads *out0, const dt_heads *x1,
+              const dt_heads *out1, int gradient, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key/value cache. A pool of `pages` pages of `page` slots (16, 32, 64 or
+ * 128) for each of Hkv key/value heads; k and v are [pages][Hkv][page][dh] and
+ * row `index` of request b (counted from its first token) lies in page
+ * table[b][index / page], slot index % page. dh: a multiple of 16 in [16, 256].
+ * dtype DT_BF16, DT_F16, or DT_E4M3: 8-bit codes with one exponent byte a
+ * head row in k_exp, v_exp [pages][Hkv][page] (NULL for the 16-bit types), the
+ * value being code 2^(byte - 127). The exponent is the least e in [-117, 120]
+ * with max |x| <= 448 2^e; codes are rounded to nearest even; a row that holds
+ * a NaN or an infinity is stored with byte 255 and reads back as NaN whole.
+ * Pages may be shared by requests that read them; rows are written by one
+ * request only. k and v are 16-byte aligned.
+ *
+ * status [batch] int32 (device) is the caller's, zeroed once: a call writes
+ * DT_ERR_BAD_PAGE for a request with a row outside its table or whose page
+ * number is outside the pool, and nothing else. Such rows are not written, read
+ * as zeros and are not attended to.
+ * `first` [batch] is the row index at which a call's rows start and counts
+ * [batch] (NULL: n for all) how many of its n rows a request has (clamped into
+ * [0, n]). */
+typedef struct {
+  void *k, *v;
+  uint8_t *k_exp, *v_exp;
+  const int32_t *table;    /* [batch][table_width] */
+  int32_t *status;         /* [batch] */
+  int pages, page, Hkv, dh, dtype, batch, table_width;
+} dt_cache;
+
+/* Write rows 0..counts[b]-1 of k and v (views of Hkv heads, n rows) at rows
+ * first[b].. of the cache, k turned by `rot` at positions [batch][n] first (both
+ * NULL: not turned; turned values go to the cache's type with one rounding).
+ * With rot, q may be given too: all its rows turned into q_out (as dt_rotary)
+ * in the same launch. dtype is that of k, v and q: the cache's own, or DT_BF16
+ * or DT_F16 for a DT_E4M3 cache. */
+int dt_cache_write(const dt_cache *c, const dt_heads *k, const dt_heads *v, int n, int dtype,
+                   const int32_t *first, const int32_t *counts, const dt_rotation *rot,
+                   const int32_t *positions, const dt_heads *q, const dt_heads *q_out,
+                   void *stream);
+
+/* Read rows first[b] .. first[b] + counts[b] - 1 into the views k and v (Hkv heads,
+ * n rows); the rows behind them are set to zero. dtype is that of the views: the
+ * cache's own, or DT_BF16 (exact) or DT_F16 (rounded, saturated at 65504) for a
+ * DT_E4M3 cache. */
+int dt_cache_read(const dt_cache *c, int n, int dtype, const int32_t *first,
+                  const int32_t *counts, const dt_heads *k, const dt_heads *v, void *stream);
+
+/* Compact the cache after verification: row first[b] + path[b][j] moves to row
+ * first[b] + j for j < lengths[b] (clamped into [0, width]), as if all rows were
+ * read before any is written. path [batch][width] int32 holds rows of a tree of
+ * n rows; an entry outside [0, n) is a DT_ERR_BAD_PAGE and moves nothing.
+ * width <= DT_MAX_D + 1, n <= DT_MAX_N + 1. */
+int dt_cache_commit(const dt_cache *c, const int32_t *first, const int32_t *path,
+                    const int32_t *lengths, int width, int n, void *stream);
+
+/* One attention layer over the cache (prefix and new rows both in it): row i of
+ * request b's n query rows sees the prefix_len[b] rows before them, and new row
+ * t (cache row prefix_len[b] + t), t < counts[b], iff mask[b][i][t] != 0
+ * ([batch][n][n] bytes, dt_tree_out.mask), or t <= i when mask is NULL (a chain,
+ * a chunk of a prompt, a single token):
+ *   out_i = sum_j softmax_j(scale q_i . k_j) v_j,
+ * 0 for a row that sees nothing and for rows i >= counts[b]. A row of the cache
+ * that a query row does not see does not change its result, whatever it holds.
+ * q and out are views of H heads (H a multiple of Hkv; head h reads key/value
+ * head h / (H / Hkv)) and n rows, of type dtype (DT_BF16 or DT_F16; the cache's
+ * own, or either for a DT_E4M3 cache). n <= DT_MAX_N + 1 with a mask, n <= 65536
+ * without. Products of the 16-bit values are accumulated in fp32, the softmax
+ * statistics are fp32, its weights are rounded to 16 bits for the product with v
+ * (bf16: relative 2^-9 each, as the output's own rounding).
+ * workspace: dt_cache_attention_workspace_bytes bytes, 256-byte aligned, for the
+ * partial results of requests whose keys are cut over several blocks (0 = invalid
+ * sizes). */
+size_t dt_cache_attention_workspace_bytes(const dt_cache *c, int H, int n);
+int dt_cache_attention(const dt_cache *c, const dt_heads *q, int n, int dtype,
+                       const int32_t *prefix_len, const int32_t *counts, const uint8_t *mask,
+                       float scale, const dt_heads *out, void *workspace, size_t workspace_bytes,
+                       void *stream);
 
 /* Static description of a status code. */
 const char *dt_status_string(int code);

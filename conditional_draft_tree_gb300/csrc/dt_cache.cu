@@ -406,7 +406,7 @@ int check_cache(const dt_cache *c) {
     return DT_ERR_INVALID_ARG;
   if (!(c->dtype == DT_BF16 || c->dtype == DT_F16 || c->dtype == DT_E4M3))
     return DT_ERR_INVALID_ARG;
-  if ((c->dtype == DT_E4M3) != (c->k_exp != nullptr) || (c->dtype == DT_E4M3) != (c->v_exp != nullptr))
+  if (!al16(c->k_exp) || !al16(c->v_exp) || (c->dtype == DT_E4M3) != (c->k_exp != nullptr) || (c->dtype == DT_E4M3) != (c->v_exp != nullptr))
     return DT_ERR_INVALID_ARG;
   return DT_OK;
 }

@@ -78,7 +78,7 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int BM = 64 / WK, NK = kT / WK, C8 = DH / 8;
   constexpr int RB = DH * (QUANT ? 1 : 2);      // bytes of a stored row (padded)
   extern __shared__ __align__(128) unsigned char sm[];
-  __shared__ int64_t s_warp[kNThreads / 32], s_found[2];
+  __shared__ int64_t s_scan[kNThreads / 32 + 2];
   __shared__ int s_bad, s_odd;
   unsigned char *sStage = sm;                                  // [2][K, V][kT][RB]
   unsigned char *sDeq = sStage + 4 * kT * RB;                  // [K, V][kT][DH] 16-bit
@@ -89,35 +89,20 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
   constexpr float kShift = DT == DT_F16 ? 12.0f : 0.0f;
   const int dh = a.c.dh;
 
-  Schedule<BM, kT, kNThreads> sch;
-  sch.plan(a, s_warp);
-  int64_t at = blockIdx.x * sch.chunk;
-  const int64_t stop = min(at + sch.chunk, sch.total);
-  if (at >= stop) return;
-  int b;
-  int64_t base;
-  sch.find(a, at, s_warp, s_found, &b, &base);
+  Schedule<kNThreads> sch;
+  sch.plan(a, BM, kT, s_scan);
+  Walk walk;
+  walk.at = blockIdx.x * sch.chunk;
+  walk.stop = min(walk.at + sch.chunk, sch.total);
+  if (walk.at >= walk.stop) return;
+  sch.find(a, BM, kT, walk.at, s_scan, &walk.b, &walk.base);
   int slot = 0;
+  Segment sg;
 
-  while (at < stop) {
-    // the unit at work tile `at`: request b (its first work tile is `base`)
-    Request rq = request_of(a, b);
-    int64_t per = head_tiles<BM, kT>(a, rq);
-    while (at - base >= a.c.Hkv * per) {
-      base += a.c.Hkv * per;
-      rq = request_of(a, ++b);
-      per = head_tiles<BM, kT>(a, rq);
-    }
-    const int hk = static_cast<int>((at - base) / per);
-    int64_t in_head = (at - base) - hk * per;
-    int rt = 0, tiles = unit_tiles<BM, kT>(a, rq, 0);
-    while (in_head >= tiles) {
-      in_head -= tiles;
-      tiles = unit_tiles<BM, kT>(a, rq, ++rt);
-    }
-    const int t0 = static_cast<int>(in_head);
-    const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (stop - at)));
-    const int64_t end = tile_end<BM>(a, rq, rt);
+  while (walk.next(a, BM, kT, &sg)) {
+    const int b = sg.b, hk = sg.hk, rt = sg.rt, t0 = sg.t0, t1 = sg.t1;
+    const Request rq = sg.rq;
+    const int64_t end = sg.end;
     const int rows = a.n * a.G;
 
     __syncthreads();   // the last unit's shared memory is free
@@ -341,8 +326,8 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
             make_float2(o[x][2 * y], o[x][2 * y + 1]);
     }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == tiles;
-    float *pp = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * BM * (DH + 2);
+    const bool whole = t0 == 0 && t1 == sg.tiles;
+    float *pp = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * a.slot;
     constexpr int C4 = DH / 8;
     for (int u = tid; u < BM * C4; u += kNThreads) {
       const int r = u / C4, c = u - r * C4, gr = rt * BM + r;
@@ -377,53 +362,38 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
         *reinterpret_cast<uint4 *>(a.out + b * a.ob + h * a.oh + i * a.orow + c * 16) = x;
       }
     }
-    at += t1 - t0;
     slot = 1;
   }
 }
 
 // Joins the partial results of units that were cut over blocks: one block a unit.
-template <int DT, int BM, int T, int DH>
+template <int DT>
 __global__ void __launch_bounds__(kNThreads)
-cache_attention_join_kernel(const __grid_constant__ AttnArgs a) {
-  __shared__ int64_t s_warp[kNThreads / 32], s_found[1];
+cache_attention_join_kernel(const __grid_constant__ AttnArgs a, int BM, int T, int DH) {
+  __shared__ int64_t s_scan[kNThreads / 32 + 2];
   const int tid = threadIdx.x;
   const int rt = blockIdx.x % a.row_tiles;
   const int bh = blockIdx.x / a.row_tiles, hk = bh % a.c.Hkv, b = bh / a.c.Hkv;
-  Schedule<BM, T, kNThreads> sch;
-  sch.plan(a, s_warp);
-  // first work tile of request b
-  if (a.batch <= kNThreads) {
-    if (tid == b) s_found[0] = sch.upto - sch.one;
-  } else {
-    int64_t mine = 0, all;
-    for (int x = tid; x < b; x += kNThreads) mine += a.c.Hkv * head_tiles<BM, T>(a, request_of(a, x));
-    block_scan<kNThreads>(mine, s_warp, &all);
-    if (tid == 0) s_found[0] = all;
-  }
-  __syncthreads();
+  Schedule<kNThreads> sch;
+  sch.plan(a, BM, T, s_scan);
   const Request rq = request_of(a, b);
-  int64_t u0 = s_found[0] + hk * head_tiles<BM, T>(a, rq);
-  if (a.mask) {
-    const int live = min(a.row_tiles, (rq.count * a.G + BM - 1) / BM);
-    u0 += rt <= live ? static_cast<int64_t>(rt) * unit_tiles<BM, T>(a, rq, 0)
-                     : static_cast<int64_t>(live) * unit_tiles<BM, T>(a, rq, 0) + (rt - live);
-  } else {
-    for (int x = 0; x < rt; ++x) u0 += unit_tiles<BM, T>(a, rq, x);
-  }
-  const int tiles = unit_tiles<BM, T>(a, rq, rt);
+  const int64_t u0 = sch.first_of(a, BM, T, b, s_scan) +
+                     hk * tiles_before(a, rq, a.row_tiles, BM, T) + tiles_before(a, rq, rt, BM, T);
+  const int tiles = unit_tiles(a, rq, rt, BM, T);
   const int64_t c0 = u0 / sch.chunk, c1 = (u0 + tiles - 1) / sch.chunk;
   if (c0 == c1) return;   // one block held it whole
   const float ninf = -__int_as_float(0x7f800000);
-  constexpr int C4 = DH / 4;
+  const int C4 = DH / 4;
   const int rows = a.n * a.G;
   for (int u = tid; u < BM * C4; u += kNThreads) {
     const int r = u / C4, c = u - r * C4, gr = rt * BM + r;
     if (gr >= rows || c * 4 >= a.c.dh) continue;
     float m = ninf, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t k = c0; k <= c1; ++k) {
+    for (int64_t x = c0 * a.parts; x < (c1 + 1) * a.parts; ++x) {
+      const int64_t k = a.parts == 2 ? x >> 1 : x;
       // the unit is the block's first if it reaches back to the block's first tile
-      const float *pp = a.part + (k * 2 + (u0 <= k * sch.chunk ? 0 : 1)) * BM * (DH + 2);
+      const int64_t at = (k * 2 + (u0 <= k * sch.chunk ? 0 : 1)) * a.parts + (a.parts == 2 ? x & 1 : 0);
+      const float *pp = a.part + at * a.slot;
       const float pm = pp[BM * DH + r], pl = pp[BM * DH + BM + r];
       if (pm == ninf && pl == 0.0f) continue;
       const float4 po = *reinterpret_cast<const float4 *>(pp + r * DH + c * 4);
@@ -451,10 +421,14 @@ cudaError_t launch_narrow(const AttnArgs &a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kernel<<<a.grid, kNThreads, smem, st>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cache_attention_join_kernel<DT, BM, kT, DH>
-      <<<static_cast<unsigned>(a.batch * a.c.Hkv * a.row_tiles), kNThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int DT>
+cudaError_t launch_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
+  cache_attention_join_kernel<DT>
+      <<<static_cast<unsigned>(a.batch * a.c.Hkv * a.row_tiles), kNThreads, 0, st>>>(
+          a, p.bm, p.wide ? kWideKeys : kT, p.dhp);
   return cudaGetLastError();
 }
 
@@ -472,21 +446,30 @@ cudaError_t launch_dh(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
                         : launch_bm<DT, QUANT, 256>(a, p.bm, st);
 }
 
+int64_t slot_floats(const AttnPlan &p) {
+  return (static_cast<int64_t>(p.bm) * (p.dhp + 2) + 3) / 4 * 4;
+}
+
 bool al4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
 
+// What a call launches, from its sizes and types alone.
 int attn_plan(const dt_cache &c, int H, int n, AttnPlan *p) {
   int sms = 0, smem = 0;
   const int rc = device_sm_count(&sms, &smem);
   if (rc) return rc;
   const int64_t rows = static_cast<int64_t>(n) * (H / c.Hkv);
-  p->wide = 0;
-  p->dhp = c.dh <= 64 ? 64 : c.dh <= 128 ? 128 : 256;
-  p->bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  p->row_tiles = static_cast<int>((rows + p->bm - 1) / p->bm);
-  p->grid = sms * (p->dhp == 256 ? 1 : 2);
-  p->bytes = static_cast<size_t>(p->grid) * 2 * p->bm * (p->dhp + 2) * sizeof(float);
+  *p = {};
+  if (!wide_plan(c, rows, sms, smem, p)) {
+    p->wide = 0;
+    p->parts = 1;
+    p->dhp = c.dh <= 64 ? 64 : c.dh <= 128 ? 128 : 256;
+    p->bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p->row_tiles = static_cast<int>((rows + p->bm - 1) / p->bm);
+    p->grid = sms * (p->dhp == 256 ? 1 : 2);
+  }
+  p->bytes = static_cast<size_t>(p->grid) * (p->parts == 2 ? 6 : 2) * slot_floats(*p) * sizeof(float);
   return DT_OK;
 }
 
@@ -528,11 +511,16 @@ int dt_cache_attention(const dt_cache *c, const dt_heads *q, int n, int dtype,
   a.scale_log2 = scale * 1.4426950408889634f;
   a.batch = c->batch; a.n = n; a.H = q->heads; a.G = G;
   a.row_tiles = p.row_tiles; a.grid = p.grid; a.min_tiles = 2;
+  a.slot = dt::slot_floats(p);
+  a.parts = p.parts;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool quant = c->dtype == DT_E4M3;
-  const cudaError_t e =
-      dtype == DT_BF16 ? (quant ? dt::launch_dh<DT_BF16, true>(a, p, st) : dt::launch_dh<DT_BF16, false>(a, p, st))
-                       : (quant ? dt::launch_dh<DT_F16, true>(a, p, st) : dt::launch_dh<DT_F16, false>(a, p, st));
+  cudaError_t e =
+      p.wide ? dt::launch_wide(*c, a, dtype, p, st)
+      : dtype == DT_BF16 ? (quant ? dt::launch_dh<DT_BF16, true>(a, p, st) : dt::launch_dh<DT_BF16, false>(a, p, st))
+                         : (quant ? dt::launch_dh<DT_F16, true>(a, p, st) : dt::launch_dh<DT_F16, false>(a, p, st));
+  if (e == cudaSuccess)
+    e = dtype == DT_BF16 ? dt::launch_join<DT_BF16>(a, p, st) : dt::launch_join<DT_F16>(a, p, st);
   return e == cudaSuccess ? DT_OK : DT_ERR_CUDA;
 }
 

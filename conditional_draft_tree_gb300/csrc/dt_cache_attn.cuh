@@ -24,7 +24,10 @@ struct AttnArgs {
   int64_t qb, qh, qr, ob, oh, orow;   // strides in bytes
   const int32_t *prefix, *counts;
   const uint8_t *mask;
-  float *part;           // [grid][2][BM][DH + 2]
+  float *part;           // [grid][2][parts][slot]: [BM][DH] of O, [BM] maxima, [BM] sums
+  int parts;             // 2: a block's two groups of warps have a result each; another
+                         // [grid][2][slot] behind part then passes B's to A for whole units
+  int64_t slot;          // fp32 numbers of one, a multiple of 4
   float scale_log2;      // scale times log2(e)
   int batch, n, H, G, row_tiles, grid, min_tiles;
 };
@@ -42,31 +45,30 @@ __device__ __forceinline__ Request request_of(const AttnArgs &a, int b) {
   return r;
 }
 
-// end of the keys that row tile rt may see (a tile of dead rows sees none)
-template <int BM>
-__device__ __forceinline__ int64_t tile_end(const AttnArgs &a, const Request &r, int rt) {
-  const int i0 = rt * BM / a.G;
+// end of the keys that row tile rt (of bm rows) may see (a tile of dead rows sees none)
+__device__ __forceinline__ int64_t tile_end(const AttnArgs &a, const Request &r, int rt, int bm) {
+  const int i0 = rt * bm / a.G;
   if (i0 >= r.count) return 0;
   if (a.mask) return r.pre + r.count;
-  return r.pre + min(r.count, (rt * BM + BM - 1) / a.G + 1);
+  return r.pre + min(r.count, (rt * bm + bm - 1) / a.G + 1);
 }
 
 // key tiles of the unit; at least one, whose block writes the unit's rows
-template <int BM, int T>
-__device__ __forceinline__ int unit_tiles(const AttnArgs &a, const Request &r, int rt) {
-  const int64_t e = tile_end<BM>(a, r, rt);
+__device__ __forceinline__ int unit_tiles(const AttnArgs &a, const Request &r, int rt, int bm, int T) {
+  const int64_t e = tile_end(a, r, rt, bm);
   return e > T ? static_cast<int>((e + T - 1) / T) : 1;
 }
 
-template <int BM, int T>
-__device__ __forceinline__ int64_t head_tiles(const AttnArgs &a, const Request &r) {
+// the units of one head before row tile `upto`
+__device__ __forceinline__ int64_t tiles_before(const AttnArgs &a, const Request &r, int upto, int bm,
+                                                int T) {
   int64_t w = 0;
   if (a.mask) {   // every live row tile sees the same keys
-    const int live = min(a.row_tiles, (r.count * a.G + BM - 1) / BM);
-    w = a.row_tiles - live;
-    if (live) w += static_cast<int64_t>(live) * unit_tiles<BM, T>(a, r, 0);
+    const int live = min(upto, (r.count * a.G + bm - 1) / bm);
+    w = upto - live;
+    if (live) w += static_cast<int64_t>(live) * unit_tiles(a, r, 0, bm, T);
   } else {
-    for (int rt = 0; rt < a.row_tiles; ++rt) w += unit_tiles<BM, T>(a, r, rt);
+    for (int rt = 0; rt < upto; ++rt) w += unit_tiles(a, r, rt, bm, T);
   }
   return w;
 }
@@ -93,28 +95,32 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
   return v + before;
 }
 
-// The block's place in the work. All threads of the block call both functions.
-template <int BM, int T, int THREADS>
+// The cut of all work tiles over the blocks. All threads of the block call plan() and
+// find(); s_scan: THREADS / 32 + 2 numbers of shared memory.
+template <int THREADS>
 struct Schedule {
   int64_t total, chunk;
   int64_t one;           // this thread's request's tiles where one scan covers the batch
   int64_t upto;          // inclusive sum to it
+  __device__ int64_t request_tiles(const AttnArgs &a, int b, int bm, int T) {
+    return b < a.batch ? a.c.Hkv * tiles_before(a, request_of(a, b), a.row_tiles, bm, T) : 0;
+  }
   // sizes of the whole launch
-  __device__ void plan(const AttnArgs &a, int64_t *s_warp) {
+  __device__ void plan(const AttnArgs &a, int bm, int T, int64_t *s_scan) {
     total = 0;
     for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
-      const int b = b0 + threadIdx.x;
-      one = b < a.batch ? a.c.Hkv * head_tiles<BM, T>(a, request_of(a, b)) : 0;
+      one = request_tiles(a, b0 + threadIdx.x, bm, T);
       int64_t all;
-      upto = block_scan<THREADS>(one, s_warp, &all);
+      upto = block_scan<THREADS>(one, s_scan, &all);
       total += all;
     }
     chunk = (total + a.grid - 1) / a.grid;
     if (chunk < a.min_tiles) chunk = a.min_tiles;
   }
   // request that holds work tile `at`, and the first work tile of that request
-  __device__ void find(const AttnArgs &a, int64_t at, int64_t *s_warp, int64_t *s_found, int *b,
+  __device__ void find(const AttnArgs &a, int bm, int T, int64_t at, int64_t *s_scan, int *b,
                        int64_t *start) {
+    int64_t *s_found = s_scan + THREADS / 32;
     if (a.batch <= THREADS) {
       if (at >= upto - one && at < upto) {
         s_found[0] = threadIdx.x;
@@ -123,12 +129,11 @@ struct Schedule {
     } else {
       int64_t before = 0;
       for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
-        const int t = b0 + threadIdx.x;
-        const int64_t w = t < a.batch ? a.c.Hkv * head_tiles<BM, T>(a, request_of(a, t)) : 0;
+        const int64_t w = request_tiles(a, b0 + threadIdx.x, bm, T);
         int64_t all;
-        const int64_t u = before + block_scan<THREADS>(w, s_warp, &all);
+        const int64_t u = before + block_scan<THREADS>(w, s_scan, &all);
         if (at >= u - w && at < u) {
-          s_found[0] = t;
+          s_found[0] = b0 + threadIdx.x;
           s_found[1] = u - w;
         }
         before += all;
@@ -138,6 +143,59 @@ struct Schedule {
     *b = static_cast<int>(s_found[0]);
     *start = s_found[1];
     __syncthreads();
+  }
+  // first work tile of request b
+  __device__ int64_t first_of(const AttnArgs &a, int bm, int T, int b, int64_t *s_scan) {
+    int64_t *s_found = s_scan + THREADS / 32;
+    if (a.batch <= THREADS) {
+      if (threadIdx.x == b) s_found[0] = upto - one;
+    } else {
+      int64_t mine = 0, all;
+      for (int x = threadIdx.x; x < b; x += THREADS) mine += request_tiles(a, x, bm, T);
+      block_scan<THREADS>(mine, s_scan, &all);
+      if (threadIdx.x == 0) s_found[0] = all;
+    }
+    __syncthreads();
+    return s_found[0];
+  }
+};
+
+// One unit's part that falls to a block: key tiles [t0, t1) of its `tiles`.
+struct Segment {
+  int b, hk, rt, t0, t1, tiles;
+  Request rq;
+  int64_t end;           // end of the unit's keys
+};
+
+// Walks the work tiles [at, stop) of a block, unit by unit.
+struct Walk {
+  int64_t at, stop, base;
+  int b;
+  __device__ bool next(const AttnArgs &a, int bm, int T, Segment *s) {
+    if (at >= stop) return false;
+    s->rq = request_of(a, b);
+    int64_t per = tiles_before(a, s->rq, a.row_tiles, bm, T);
+    while (at - base >= a.c.Hkv * per) {
+      base += a.c.Hkv * per;
+      s->rq = request_of(a, ++b);
+      per = tiles_before(a, s->rq, a.row_tiles, bm, T);
+    }
+    s->b = b;
+    // a 64-bit division only where it is needed
+    s->hk = (at - base) >> 31 ? static_cast<int>((at - base) / per)
+                              : static_cast<int>(static_cast<uint32_t>(at - base) / static_cast<uint32_t>(per));
+    int64_t in_head = (at - base) - s->hk * per;
+    s->rt = 0;
+    s->tiles = unit_tiles(a, s->rq, 0, bm, T);
+    while (in_head >= s->tiles) {
+      in_head -= s->tiles;
+      s->tiles = unit_tiles(a, s->rq, ++s->rt, bm, T);
+    }
+    s->t0 = static_cast<int>(in_head);
+    s->t1 = static_cast<int>(min(static_cast<int64_t>(s->tiles), in_head + (stop - at)));
+    s->end = tile_end(a, s->rq, s->rt, bm);
+    at += s->t1 - s->t0;
+    return true;
   }
 };
 
@@ -157,10 +215,14 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 struct AttnPlan {        // resolved on the host from sizes alone
-  int wide;              // the tensor-core kernel for many rows
-  int bm, dhp, row_tiles, grid;
-  size_t bytes;
+  int wide;              // dt_cache_wide.cu, else the mma.sync kernel
+  int bm, dhp, row_tiles, grid, parts;
+  int na, nb, ring, raw; // dt_cache_wide.cu: rows of its two groups, operand and raw tiles
+  size_t smem, bytes;
 };
-int attn_plan(const dt_cache &c, int H, int n, AttnPlan *p);
+constexpr int kWideKeys = 128;         // keys of a tile of dt_cache_wide.cu
+bool wide_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p);
+cudaError_t launch_wide(const dt_cache &c, const AttnArgs &a, int dtype, const AttnPlan &p,
+                        cudaStream_t st);
 
 }  // namespace dt

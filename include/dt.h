@@ -413,11 +413,13 @@ int dt_rotary(const dt_rotation *rot, const int32_t *positions, int batch, int n
  * with max |x| <= 448 2^e; codes are rounded to nearest even; a row that holds
  * a NaN or an infinity is stored with byte 255 and reads back as NaN whole.
  * Pages may be shared by requests that read them; rows are written by one
- * request only. k and v are 16-byte aligned.
+ * request only. k, v, k_exp and v_exp are 16-byte aligned. A code 0x7f or 0xff
+ * (NaN) occurs in rows of byte 255 only.
  *
  * status [batch] int32 (device) is the caller's, zeroed once: a call writes
  * DT_ERR_BAD_PAGE for a request with a row outside its table or whose page
- * number is outside the pool, and nothing else. Such rows are not written, read
+ * number is outside the pool, DT_ERR_TIMEOUT where a bounded wait of the attention
+ * kernel ran out (its output is then invalid), and nothing else. Rows on bad pages are not written, read
  * as zeros and are not attended to.
  * `first` [batch] is the row index at which a call's rows start and counts
  * [batch] (NULL: n for all) how many of its n rows a request has (clamped into

@@ -460,3 +460,19 @@ def test_pool_past_32_bit_offsets():
     gk, _ = dt.cache_read(cache, 2, pre)
     assert torch.equal(gk, k[:, :, [292, 299]])
     cache.check()
+
+
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_single_tokens_with_long_8bit_and_16bit_caches(kind, dh):
+    """Many key tiles a block, the last of them cut by the length, poison behind it."""
+    run_attention(kind, BF, 1, 4, 8, dh, 64, [8000, 7777, 4095, 513, 1, 6000], mask="tree")
+
+
+@pytest.mark.parametrize("n,G", [(1, 4), (20, 2), (30, 5), (70, 4)])
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+def test_many_short_units_a_block(n, G, kind):
+    """More units than blocks, of one to three key tiles each: a block passes from unit to
+    unit many times, and holds most of them whole."""
+    prefix = [(29 * b) % 300 for b in range(90)]
+    run_attention(kind, BF, n, G, 8, 64, 16, prefix, [1 + (b * 7) % n for b in range(90)])

@@ -3,7 +3,7 @@
 //
 // Both products are taken transposed, so that the query rows are the MMA's N side,
 // which comes in steps of 16 where the M side is 128: the rows of a unit (G heads x
-// tree rows, 4 to 224 of them) are padded to the next 16, not 128, and one kernel
+// tree rows, 4 to 192 of them) are padded to the next 16, not 128, and one kernel
 // serves single tokens and wide trees. Per tile of 128 keys and group of up to 112
 // rows: S^T = K Q^T (M = keys, K-major K tile and Q), p = 2^(x - m) by one thread a
 // key, which finds its key's scores for all rows in its TMEM lane, P^T to shared
@@ -19,11 +19,11 @@
 // registers, joined across lanes once a unit.
 //
 // Two warpgroups (A, B) take weights, so that the tensor cores work for one meanwhile.
-// Up to 112 rows: both have all rows, A the even and B the odd key tiles, and A or the
+// Up to 96 rows: both have all rows, A the even and B the odd key tiles, and A or the
 // join adds them up (an MMA takes 32 + N / 4 cycles at least, the first term for
 // reading its 128 keys: one MMA over all rows beats two over half). More rows: each
 // has half the rows, and every tile, so that a tile is read, and an 8-bit one
-// converted, once for up to 224 rows. K and V tiles alternate in a ring in the order
+// converted, once for up to 192 rows. K and V tiles alternate in a ring in the order
 // in which they are consumed (K0 K1 V0 K2 V1 ...), filled by TMA, page by page,
 // through a 128-byte swizzled tensor map; tiles of 8-bit rows land in a raw ring by
 // plain bulk copies and a third warpgroup writes their bf16 or fp16 values into the
@@ -40,11 +40,24 @@ namespace dt {
 
 namespace {
 
-constexpr int kWThreads = 512;
 constexpr int kW = kWideKeys;
 constexpr int kBlk = kW * 128;         // bytes of 128 rows of 64 16-bit values
 constexpr int kMaxRing = 8;
-constexpr int kMaxCols = 112;          // rows of a group: one sum of each in a thread's registers
+constexpr int kSegs = 4;
+constexpr int kMaxCols = 96;           // rows of a group: one sum of each in a thread's registers
+
+// Warpgroups: two for weights, two (8-bit rows) that convert, one whose warps load, issue
+// the products, find segments. Registers at launch times threads is what setmaxnreg
+// shares out: 640 x 96 >= 256 x 176 + 384 x 40, and 384 x 168 >= 256 x 200 + 128 x 96.
+template <bool QUANT> constexpr int kWThreads = QUANT ? 640 : 384;
+template <bool QUANT> constexpr int kWeightRegs = QUANT ? 176 : 200;
+template <bool QUANT> constexpr int kOtherRegs = QUANT ? 40 : 96;
+template <int N> __device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 constexpr int kOddWords = (DT_MAX_N + 32) / 32;
 constexpr long long kWaitCycles = 4000000000ll;   // about 2 s
 
@@ -58,7 +71,9 @@ struct Small {                          // behind the big buffers
   float fac[2][128];
   uint64_t full[kMaxRing], empty[kMaxRing], raw_full[kMaxRing], raw_empty[kMaxRing];
   uint64_t q_full, q_free, s_full[2], p_full[2], pv_done[2];
-  int64_t scan[kWThreads / 32 + 2];
+  int64_t scan[640 / 32 + 2];
+  Segment seg[kSegs];                   // the next segments; b < 0: no more
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint32_t odd[2][kOddWords + 1];      // tree rows whose V is not all finite; the last word: any
   uint32_t tmem;
   int fail;
@@ -171,11 +186,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 template <int DT>
 __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {   // a number beats a NaN
   uint32_t r;
@@ -183,10 +193,25 @@ __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {   // a num
   else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// largest magnitudes of two pairs of 16-bit values (signs are not kept), NaN above all
+template <int DT>
+__device__ __forceinline__ uint32_t top_abs(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (DT == DT_BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 16 weights of key gt into the group's P^T tile
+__device__ __forceinline__ void put_weights(unsigned char *sP, int gt, int c, const uint32_t (&y)[8]) {
+  unsigned char *p = sP + (c >> 2) * kBlk + gt * 128;
+  const int ch = (c & 3) * 2;
+  *reinterpret_cast<uint4 *>(p + ((ch ^ (gt & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+  *reinterpret_cast<uint4 *>(p + (((ch + 1) ^ (gt & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+}
 
-// sets bits [lo, hi) of a 128-bit set where `on`
-__device__ __forceinline__ void set_run(uint64_t (&bits)[2], int lo, int hi, bool on) {
-  if (!on || lo >= hi) return;
+// sets bits [lo, hi) of a 128-bit set
+__device__ __forceinline__ void set_run(uint64_t (&bits)[2], int lo, int hi) {
+  if (lo >= hi) return;
   const int n = hi - lo;
   const uint64_t run = n >= 64 ? ~0ull : (1ull << n) - 1;
   if (lo < 64) {
@@ -216,6 +241,58 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
   return MAX ? fmaxf(v[0], got) : v[0] + got;
 }
 
+// Sums of 8 row pairs [pair][128 keys][2] over the keys into out[16].
+__device__ __forceinline__ void sum_chunk(const float *part, float *out, int gt, int bar_id) {
+  group_sync(bar_id);
+  // 16 lanes a row pair, 8 keys each
+  const float4 *src = reinterpret_cast<const float4 *>(part + ((gt >> 4) * 128) * 2) + (gt & 15);
+  float a = 0.0f, b = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 x = src[16 * k];
+    a += x.x + x.z;
+    b += x.y + x.w;
+  }
+#pragma unroll
+  for (int m = 8; m; m >>= 1) {
+    a += __shfl_xor_sync(kFull, a, m);
+    b += __shfl_xor_sync(kFull, b, m);
+  }
+  if ((gt & 15) == 0) {
+    out[2 * (gt >> 4)] = a;
+    out[2 * (gt >> 4) + 1] = b;
+  }
+  group_sync(bar_id);
+}
+
+// New references of a group's rows: the larger of the old one and the tile's maximum,
+// taken across lanes (scores that do not count are -inf there). fac: what earlier sums
+// are to be scaled by.
+__device__ __forceinline__ void new_refs(uint32_t t_s, int n, float *wred, int gt, int lane, int bar_id,
+                                         float scale, float shift, float *neg_m, float *fac, float *m) {
+  const float ninf = -__int_as_float(0x7f800000);
+#pragma unroll 1
+  for (int c = 0; c * 16 < n; ++c) {
+    float v[16];
+    tmem_ld16(t_s + 16 * c, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] *= scale;
+    const float r = reduce16<true>(v, lane);
+    if (!(lane & 1)) wred[(gt >> 5) * 128 + 16 * c + (lane >> 1)] = r;
+  }
+  group_sync(bar_id);
+  if (gt < n) {
+    float mn = fmaxf(fmaxf(wred[gt], wred[128 + gt]), fmaxf(wred[256 + gt], wred[384 + gt]));
+    mn = fmaxf(mn, *m);
+    fac[gt] = mn == ninf ? 1.0f : fast_exp2(*m - mn);
+    // a row that has seen nothing yet: any score passes the limit
+    neg_m[gt] = mn == ninf ? 1e30f : shift - mn;
+    *m = mn;
+  }
+  group_sync(bar_id);
+}
+
 // instruction descriptor of kind::f16, M = 128, fp32 accumulation; mn: both operands
 // MN-major
 template <int DT>
@@ -225,18 +302,43 @@ __device__ __forceinline__ uint32_t idesc16(int N, bool mn) {
          (static_cast<uint32_t>(N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// two e4m3 codes, each in the upper byte of a half word, as bf16 values times 2^-120
-// times `mul` (bf16 pair): the code's exponent and mantissa bits, set in the bf16
-// fields, are the value times 2^-120 exactly, subnormal codes included
+// two of a word's four e4m3 codes (0: the lower two) as sign-extended half words
+template <int HALF>
+__device__ __forceinline__ uint32_t spread_codes(uint32_t w) {
+  uint32_t r;   // byte, its sign eight times; twice
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "n"(HALF ? 0xb3a2 : 0x9180));
+  return r;
+}
+// two codes spread over half words as bf16 values times 2^-120 times `mul` (bf16 pair): the
+// code's exponent and mantissa bits, set in the bf16 fields, are the value times 2^-120
+// exactly, subnormal codes included
 __device__ __forceinline__ uint32_t codes_bf16x2(uint32_t spread, uint32_t mul) {
-  const uint32_t r = (spread & 0x80008000u) | ((spread >> 4) & 0x07f007f0u);
+  const uint32_t r = (spread << 4) & 0x87f087f0u;
   uint32_t o;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(r), "r"(mul));
   return o;
 }
+// 16 values of row r into an operand tile, swizzled
+__device__ __forceinline__ void put_operand(unsigned char *row, int r, int c, const uint32_t (&y)[8]) {
+  unsigned char *to = row + (c >> 2) * kBlk;
+  const int z = (c & 3) * 2;
+  *reinterpret_cast<uint4 *>(to + ((z ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+  *reinterpret_cast<uint4 *>(to + (((z + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+}
+
+// a place in a ring of `size` tiles, and the parity of its barriers' phase
+struct Place {
+  uint32_t at, parity;
+  __device__ void step(uint32_t size) {
+    if (++at == size) {
+      at = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 template <int DT, bool QUANT>
-__global__ void __launch_bounds__(kWThreads, 1)
+__global__ void __launch_bounds__(kWThreads<QUANT>, 1)
 cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ WideShape w,
                             const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap) {
@@ -248,13 +350,17 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
 
   if (tid == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&ss.full[i], QUANT ? 128 : 1);
+      mbar_init(&ss.full[i], QUANT ? 256 : 1);
       mbar_init(&ss.empty[i], 1);
       mbar_init(&ss.raw_full[i], 1);
-      mbar_init(&ss.raw_empty[i], 128);
+      mbar_init(&ss.raw_empty[i], 256);
     }
     mbar_init(&ss.q_full, w.alt ? 128 : 256);
     mbar_init(&ss.q_free, 128);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&ss.seg_full[i], 1);
+      mbar_init(&ss.seg_empty[i], QUANT ? 18 : 10);   // the warps that take segments
+    }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ss.s_full[x], 1);
       mbar_init(&ss.p_full[x], 128);
@@ -263,14 +369,14 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
     ss.fail = 0;
   }
   // rows that are padding keep a reference that gives them weight 0
-  for (int i = tid; i < 256; i += kWThreads) (&ss.neg_m[0][0])[i] = ninf;
+  for (int i = tid; i < 256; i += kWThreads<QUANT>) (&ss.neg_m[0][0])[i] = ninf;
   if (warp == 0) tmem_alloc(&ss.tmem, 512);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = ss.tmem;
 
-  Schedule<kWThreads> sch;
+  Schedule<kWThreads<QUANT>> sch;
   sch.plan(a, w.bm, kW, ss.scan);
   Walk walk;
   walk.at = blockIdx.x * sch.chunk;
@@ -295,6 +401,22 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
   auto wait_warp = [&](uint64_t *bar, uint32_t parity) {
     return __all_sync(kFull, wait(bar, parity)) != 0;
   };
+  // The block's next segment. One warp finds them ahead of time (its code is long and its
+  // loads depend on each other) and ends with b < 0, in any case: every warp sees the
+  // same segments, whatever has failed.
+  uint32_t seg = 0;
+  auto next_segment = [&]() {
+    const uint32_t i = seg % kSegs, parity = (seg / kSegs) & 1;
+    bool there = false;
+    for (int k = 0; k < 4 && !there; ++k) there = mbar_wait_cycles(&ss.seg_full[i], parity);
+    __syncwarp();
+    if (!there) return false;
+    sg = ss.seg[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ss.seg_empty[i]);
+    ++seg;
+    return sg.b >= 0;
+  };
   // operand tiles of a segment of T key tiles, in ring order: K0 K1 V0 K2 V1 ... V(T-1)
   auto op_tile = [](int op, int T, bool *is_v) {
     if (op == 0) { *is_v = false; return 0; }
@@ -305,7 +427,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
 
   if (warp < 8) {
     // ------------------------------------------------ weights: groups A and B
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    more_regs<kWeightRegs<QUANT>>();
     const int X = warp >> 2, gt = tid & 127, bar_id = 1 + X;   // gt: key, lane and row of the group
     const int n = !w.alt && X ? w.nb : w.na, col0 = !w.alt && X ? w.na : 0;
     const int tstep = w.alt ? 2 : 1, tfirst = w.alt ? X : 0;
@@ -319,29 +441,36 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
     float *fac_b = reinterpret_cast<float *>(sP + 3072);
     constexpr float kShift = DT == DT_F16 ? 8.0f : 0.0f;
     const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
-    uint32_t mine = 0, ring_op = 0, seg = 0;   // tiles of this group, ring places, segments
+    // a score that counts for nothing: -inf after the scaling (0 scale: see below)
+    const float lowest = a.scale_log2 < 0.0f ? -ninf : ninf;
+    uint32_t mine = 0, ring_op = 0;            // tiles of this group, ring places
     int slot = 0;
-    while (walk.next(a, w.bm, kW, &sg)) {
+    while (next_segment()) {
+      const uint32_t si = seg - 1;
       const Request rq = sg.rq;
       const int T = sg.t1 - sg.t0, rows = a.n * a.G, row0 = sg.rt * w.bm + col0;
       const int live_rows = min(min(n, w.bm - col0), rows - row0);    // of this group
       if (tid == 0 && a.prefix[sg.b] != rq.pre) cache_fault(a.c, sg.b);
       // keys before `pre` are seen by every (live) row of the unit
-      const int64_t pre = a.mask ? rq.pre : rq.pre + sg.rt * w.bm / a.G;
-      uint32_t *odd = ss.odd[seg & 1];
+      // (row numbers fit 32 bits: a table has at most 2^20 pages of at most 128 rows)
+      const int pre = static_cast<int>(a.mask ? rq.pre : rq.pre + sg.rt * w.bm / a.G);
+      const int end = static_cast<int>(sg.end);
+      const int32_t *table = a.c.table + static_cast<int64_t>(sg.b) * a.c.width;
+      uint32_t *odd = ss.odd[si & 1];
       if (X == 0)
         for (int i = gt; i < kOddWords + 1; i += 128) odd[i] = 0u;
       // the rows of Q, K-major, 128-byte swizzle: a thread has one chunk of every
-      // eighth (sixteenth) row, four in flight
+      // eighth (sixteenth) row, eight in flight
       if (!w.alt || X == 0) {
-        if (w.alt && seg > 0) wait(&ss.q_free, (seg - 1) & 1);   // B's last scores are taken
+        if (w.alt && si > 0) wait(&ss.q_free, (si - 1) & 1);   // B's last scores are taken
         const int c = gt & (w.nblk * 8 - 1), step = 128 / (w.nblk * 8);
         const char *src = a.q + sg.b * a.qb + sg.hk * a.G * a.qh + c * 16;
         unsigned char *dst = sm + w.off_q + (c >> 3) * (w.na + w.nb) * 128 + col0 * 128;
-        for (int r0 = gt / (w.nblk * 8); r0 < n; r0 += 4 * step) {
-          uint4 x[4];
+#pragma unroll 1
+        for (int r0 = gt / (w.nblk * 8); r0 < n; r0 += 8 * step) {
+          uint4 x[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 8; ++e) {
             const int r = r0 + e * step;
             x[e] = make_uint4(0u, 0u, 0u, 0u);
             if (r < live_rows && c * 8 < dh) {
@@ -350,7 +479,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
             }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 8; ++e) {
             const int r = r0 + e * step;
             if (r < n) *reinterpret_cast<uint4 *>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[e];
           }
@@ -360,7 +489,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       } else {
         // B goes on once A has: A waits for q_free segment by segment, and a second
         // arrival of B before that would pass the phase that A waits for
-        wait(&ss.q_full, seg & 1);
+        wait(&ss.q_full, si & 1);
       }
       float m = ninf;                 // reference of row gt of the group
       uint64_t l[kMaxCols / 2];       // sums of this thread's keys' weights, two rows each
@@ -368,13 +497,14 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       for (int c = 0; c < kMaxCols / 2; ++c) l[c] = 0ull;
       // whether this thread's key of tile t is there, on a good page
       auto key_there = [&](int t) {
-        const int64_t j = static_cast<int64_t>(sg.t0 + t) * kW + gt;
-        return t < T && j < sg.end && cache_row(a.c, sg.b, j, sg.hk) >= 0;
+        const int j = (sg.t0 + t) * kW + gt, page = j >> a.c.shift;
+        return t < T && j < end && page < a.c.width &&
+               static_cast<uint32_t>(table[page]) < static_cast<uint32_t>(a.c.pages);
       };
       bool valid = key_there(tfirst);
 
       for (int t = tfirst; t < T; t += tstep, ++mine) {
-        const int64_t j = static_cast<int64_t>(sg.t0 + t) * kW + gt;
+        const int j = (sg.t0 + t) * kW + gt;
         const bool first = t == tfirst;
         const bool masked = __any_sync(kFull, !valid || j >= pre);
         uint64_t bits[2] = {0ull, 0ull};          // the rows that see this thread's key
@@ -383,19 +513,22 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
             bits[0] = bits[1] = ~0ull;
           } else {
             // tree row j - rq.pre: eight tokens' loads in flight, then each token's run of rows
-            const int tr = static_cast<int>(j - rq.pre), i0 = row0 / a.G;
+            const int tr = j - static_cast<int>(rq.pre), i0 = row0 / a.G;
             const uint8_t *mk =
                 a.mask ? a.mask + (static_cast<int64_t>(sg.b) * a.n + i0) * a.n + tr : nullptr;
             const int tokens = min((row0 + live_rows - 1) / a.G + 1, rq.count) - i0;
             for (int i = 0; i < tokens; i += 8) {
-              uint32_t v[8];
+              uint32_t v = 0;
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                v[e] = i + e < tokens && (mk ? mk[static_cast<int64_t>(i + e) * a.n] != 0 : tr <= i0 + i + e);
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                set_run(bits, max((i0 + i + e) * a.G - row0, 0),
-                        min((i0 + i + e + 1) * a.G - row0, live_rows), v[e] != 0);
+              for (int e = 0; e < 8; ++e) {
+                const bool in = i + e < tokens;
+                v |= (in && (mk ? mk[static_cast<int64_t>(i + e) * a.n] != 0 : tr <= i0 + i + e) ? 1u : 0u) << e;
+              }
+#pragma unroll 1
+              for (; v; v &= v - 1) {
+                const int e = i0 + i + __ffs(v) - 1;
+                set_run(bits, max(e * a.G - row0, 0), min((e + 1) * a.G - row0, live_rows));
+              }
             }
           }
         }
@@ -410,136 +543,118 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
           // (The slot's tile before this one is consumed by now, K(t) at the latest with
           // three places and V(t - 1) with two, so this parity is this tile's.)
           const uint32_t vop = ring_op + (t < T - 1 ? 2 * t + 2 : 2 * T - 1);
-          wait(&ss.full[vop % w.ring], (vop / w.ring) & 1);
-          unsigned char *v = sm + (vop % w.ring) * tile_bytes + gt * 128;
+          const uint32_t turn = vop / w.ring, vslot = vop - turn * w.ring;
+          wait(&ss.full[vslot], turn & 1);
+          unsigned char *v = sm + vslot * tile_bytes + gt * 128;
           bool found = false;
-          for (int kb = 0; kb < w.nblk; ++kb) {
-            uint4 *p = reinterpret_cast<uint4 *>(v + kb * kBlk);
-            uint4 x[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] = p[c ^ (gt & 7)];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint32_t *y = reinterpret_cast<uint32_t *>(&x[c]);
-              bool change = !valid;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t ex = DT == DT_BF16 ? 0x7f807f80u : 0x7c007c00u;
-                const uint32_t bad = __vcmpeq2(y[e] & ex, ex);    // 0xffff where not finite
-                if (!valid) {
-                  y[e] = 0u;
-                } else if (bad && j >= pre) {
-                  y[e] &= ~bad;
-                  change = found = true;
-                }
+          if (!valid) {
+#pragma unroll 4
+            for (int c = 0; c < 8 * w.nblk; ++c)
+              *reinterpret_cast<uint4 *>(v + (c >> 3) * kBlk + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          } else if (j >= pre) {
+            uint32_t top = 0u;          // largest magnitudes, a NaN above all
+#pragma unroll 4
+            for (int c = 0; c < 8 * w.nblk; ++c) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(v + (c >> 3) * kBlk + (((c & 7) ^ (gt & 7)) << 4));
+              top = top_abs<DT>(top_abs<DT>(top, x.x), top_abs<DT>(x.y, top_abs<DT>(x.z, x.w)));
+            }
+            const uint32_t ex = DT == DT_BF16 ? 0x7f80u : 0x7c00u;
+            if ((top & ex) == ex || ((top >> 16) & ex) == ex) {
+              found = true;
+#pragma unroll 1
+              for (int c = 0; c < 64 * w.nblk; ++c) {
+                uint16_t *x = reinterpret_cast<uint16_t *>(v + (c >> 6) * kBlk) + (c & 63);
+                if ((*x & ex) == ex) *x = 0;
               }
-              if (change) p[c ^ (gt & 7)] = x[c];
             }
           }
           if (found) {
-            // (a mask's rows, or the at most 224 that a causal unit's rows see in part)
+            // (a mask's rows, or the at most 192 that a causal unit's rows see in part)
             atomicOr(&odd[(j - pre) >> 5], 1u << ((j - pre) & 31));
             odd[kOddWords] = 1u;
           }
         }
-        valid = key_there(t + tstep);
-        int done = 0;                 // 16-row chunks whose weights are in l
-        for (int attempt = first ? 1 : 0; attempt < 2; ++attempt) {
-          if (attempt == 1) {
-            // new references: the tile's maxima across lanes
+        if (masked) {
+          // scores that do not count become -inf in place; nothing below asks again
 #pragma unroll 1
-            for (int c = 0; c * 16 < n; ++c) {
-              float v[16];
-              tmem_ld16(t_s + 16 * c, v);
-              tmem_wait_ld();
-              const uint32_t b16 =
-                  masked ? static_cast<uint32_t>((c >= 4 ? bits[1] : bits[0]) >> ((c & 3) * 16)) : 0xffffu;
+          for (int c = 0; c * 16 < n; ++c) {
+            float v[16];
+            tmem_ld16(t_s + 16 * c, v);
+            tmem_wait_ld();
+            const uint32_t b16 = static_cast<uint32_t>((c >= 4 ? bits[1] : bits[0]) >> ((c & 3) * 16));
 #pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = (b16 >> e) & 1u ? v[e] * a.scale_log2 : ninf;
-              const float r = reduce16<true>(v, lane);
-              if (!(lane & 1)) wred[(warp & 3) * 128 + 16 * c + (lane >> 1)] = r;
-            }
-            group_sync(bar_id);
-            if (gt < n) {
-              float mn = fmaxf(fmaxf(wred[gt], wred[128 + gt]), fmaxf(wred[256 + gt], wred[384 + gt]));
-              mn = fmaxf(mn, m);
-              fac[gt] = mn == ninf ? 1.0f : fast_exp2(m - mn);
-              // a row that has seen nothing yet: any score passes the limit
-              neg_m[gt] = mn == ninf ? 1e30f : kShift - mn;
-              m = mn;
-            }
-            group_sync(bar_id);
-            if (!first) {
-#pragma unroll
-              for (int c = 0; c < kMaxCols / 16; ++c) {
-                if (16 * c < n) {
-                  float o[16];
-                  tmem_ld16(t_o + 16 * c, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    const float2 f = *reinterpret_cast<const float2 *>(fac + 16 * c + 2 * e);
-                    l[8 * c + e] = mul2(l[8 * c + e], pair(f.x, f.y));
-                    o[2 * e] *= f.x;
-                    o[2 * e + 1] *= f.y;
-                  }
-                  tmem_st16(t_o + 16 * c, o);
-                }
-              }
-              tmem_wait_st();
-            }
+            for (int e = 0; e < 16; ++e) v[e] = (b16 >> e) & 1u ? v[e] : lowest;
+            tmem_st16(t_s + 16 * c, v);
           }
-          bool over = false;
+          tmem_wait_st();
+        }
+        valid = key_there(t + tstep);
+        if (first) new_refs(t_s, n, wred, gt, lane, bar_id, a.scale_log2, kShift, neg_m, fac, &m);
+        uint32_t top = 0u;            // largest weights
+        {
           float s0[16], s1[16];
           tmem_ld16(t_s, s0);
 #pragma unroll
           for (int c = 0; c < kMaxCols / 16; ++c) {
-            if (16 * c < n && !over) {
+            if (16 * c < n) {
               float *v = c & 1 ? s1 : s0;
+              const ulonglong2 *r = reinterpret_cast<const ulonglong2 *>(neg_m + 16 * c);
               tmem_wait_ld();
               if (16 * c + 16 < n) {
                 if (c & 1) tmem_ld16(t_s + 16 * c + 16, s0);
                 else tmem_ld16(t_s + 16 * c + 16, s1);
               }
-              const ulonglong2 *nm = reinterpret_cast<const ulonglong2 *>(neg_m + 16 * c);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const ulonglong2 r = nm[e];
-                unpair(fma2(pair(v[4 * e], v[4 * e + 1]), scale2, r.x), &v[4 * e], &v[4 * e + 1]);
-                unpair(fma2(pair(v[4 * e + 2], v[4 * e + 3]), scale2, r.y), &v[4 * e + 2], &v[4 * e + 3]);
-              }
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = fast_exp2(v[e]);
-              if (masked) {
-                const uint32_t b16 = static_cast<uint32_t>(bits[c >= 4] >> ((c & 3) * 16));
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = (b16 >> e) & 1u ? v[e] : 0.0f;
-              }
               uint32_t y[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = Half16<DT>::pack(v[2 * e], v[2 * e + 1]);
-              if (attempt == 0) {
-                const uint32_t top = max16x2<DT>(max16x2<DT>(max16x2<DT>(y[0], y[1]), max16x2<DT>(y[2], y[3])),
-                                                 max16x2<DT>(max16x2<DT>(y[4], y[5]), max16x2<DT>(y[6], y[7])));
-                // weights are not negative: their bits order them (2^10; fp16 2^15)
-                const uint32_t lim = DT == DT_BF16 ? 0x4480u : 0x7800u;
-                over = __any_sync(kFull, (top & 0xffffu) > lim || (top >> 16) > lim);
+              for (int e = 0; e < 8; ++e) {
+                float p0, p1;
+                unpair(fma2(pair(v[2 * e], v[2 * e + 1]), scale2, e & 1 ? r[e >> 1].y : r[e >> 1].x), &p0, &p1);
+                p0 = fast_exp2(p0);
+                p1 = fast_exp2(p1);
+                l[8 * c + e] = add2(l[8 * c + e], pair(p0, p1));
+                y[e] = Half16<DT>::pack(p0, p1);
+                top = max16x2<DT>(top, y[e]);
               }
-              if (!over) {
-                if (c >= done) {
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) l[8 * c + e] = add2(l[8 * c + e], pair(v[2 * e], v[2 * e + 1]));
-                  done = c + 1;
-                }
-                unsigned char *p = sP + (c >> 2) * kBlk + gt * 128;
-                const int ch = (c & 3) * 2;
-                *reinterpret_cast<uint4 *>(p + ((ch ^ (gt & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<uint4 *>(p + (((ch + 1) ^ (gt & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-              }
+              put_weights(sP, gt, c, y);
             }
           }
-          tmem_wait_ld();             // (a load that a stop at `over` left behind)
-          if (attempt == 0 && !group_any(bar_id, over)) break;
+        }
+        // weights are not negative: their bits order them (2^10; fp16 2^15)
+        const uint32_t lim = DT == DT_BF16 ? 0x4480u : 0x7800u;
+        if (group_any(bar_id, (top & 0xffffu) > lim || (top >> 16) > lim)) {
+          // Rare. New references; what was summed so far is scaled to them, this tile's
+          // weights are written anew. A sum past 2^100 is this tile's (what came before
+          // it is below 2^-60 of it) and may have overflowed: it starts again.
+          new_refs(t_s, n, wred, gt, lane, bar_id, a.scale_log2, kShift, neg_m, fac, &m);
+#pragma unroll
+          for (int c = 0; c < kMaxCols / 16; ++c) {
+            if (16 * c < n) {
+              float v[16];
+              if (!first) {
+                tmem_ld16(t_o + 16 * c, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] *= fac[16 * c + e];
+                tmem_st16(t_o + 16 * c, v);
+              }
+              tmem_ld16(t_s + 16 * c, v);
+              tmem_wait_ld();
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float p0 = fast_exp2(fmaf(v[2 * e], a.scale_log2, neg_m[16 * c + 2 * e]));
+                const float p1 = fast_exp2(fmaf(v[2 * e + 1], a.scale_log2, neg_m[16 * c + 2 * e + 1]));
+                float l0, l1;
+                unpair(l[8 * c + e], &l0, &l1);
+                l0 = l0 > 0x1p100f ? p0 : l0 * fac[16 * c + 2 * e];
+                l1 = l1 > 0x1p100f ? p1 : l1 * fac[16 * c + 2 * e + 1];
+                l[8 * c + e] = pair(l0, l1);
+                y[e] = Half16<DT>::pack(p0, p1);
+              }
+              put_weights(sP, gt, c, y);
+            }
+          }
+          tmem_wait_st();
         }
         fence_async_smem();
         tmem_fence_before();
@@ -551,24 +666,23 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       if (some) wait(&ss.pv_done[X], (mine - 1) & 1);
       __syncwarp();
       tmem_fence_after();
+      // (16 rows at a time through P's place: 16 lanes add up a pair of rows)
+      float *part = reinterpret_cast<float *>(sP + 4096);
 #pragma unroll
       for (int c = 0; c < kMaxCols / 16; ++c) {
         if (16 * c < n) {
-          float v[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) unpair(l[8 * c + e], &v[2 * e], &v[2 * e + 1]);
-          const float r = reduce16<false>(v, lane);
-          if (!(lane & 1)) wred[(warp & 3) * 128 + 16 * c + (lane >> 1)] = r;
+          for (int e = 0; e < 8; ++e) *reinterpret_cast<uint64_t *>(part + (e * 128 + gt) * 2) = l[8 * c + e];
+          sum_chunk(part, wred + 16 * c, gt, bar_id);
         }
       }
-      group_sync(bar_id);
       const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles, both = w.alt && whole;
       const bool leave = !whole || (both && X == 1);      // a part for the join or for A
       const int DH = 64 * w.nblk;
-      float *pp = a.part + (both ? (4ll * a.grid + 2 * blockIdx.x + (seg & 1)) * a.slot
+      float *pp = a.part + (both ? (4ll * a.grid + 2 * blockIdx.x + (si & 1)) * a.slot
                                  : ((2ll * blockIdx.x + slot) * a.parts + (w.alt ? X : 0)) * a.slot);
       if (gt < live_rows) {
-        const float sum = wred[gt] + wred[128 + gt] + wred[256 + gt] + wred[384 + gt];
+        const float sum = wred[gt];
         const int gr = row0 + gt, i = gr / a.G;
         const bool live = i < rq.count;
         if (leave) {
@@ -614,8 +728,8 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
             if (16 * c + e >= live_rows || i >= rq.count) continue;
             float add = 0.0f;
             for (int x = 0; x < 32 * kOddWords; ++x) {
-              const int64_t key = pre + x, kt = key / kW - sg.t0;
-              if (!((odd[x >> 5] >> (x & 31)) & 1u) || key >= sg.end || kt < tfirst || kt >= T ||
+              const int key = pre + x, kt = key / kW - sg.t0;
+              if (!((odd[x >> 5] >> (x & 31)) & 1u) || key >= end || kt < tfirst || kt >= T ||
                   (w.alt && (kt & 1) != X) || !sees(a, rq, sg.b, i, key))
                 continue;
               const int64_t row = cache_row(a.c, sg.b, key, sg.hk);
@@ -632,23 +746,38 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
         __syncwarp();
         // a dead row's O may hold anything: zero whatever it is
         if (d < dh) {
+          // (all reads before the first store: it might, for all the compiler knows, change them)
           if (!leave) {
+            float f[16];
+            int64_t at[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              f[e] = fac[16 * c + e];
+              at[e] = row_off[16 * c + e];
+            }
+            if (both) {
+              const float *ob = pp + 16 * c * DH + d;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                o[e] = f[e] == 0.0f ? 0.0f : o[e] * f[e];
+                f[e] = 1.0f;
+                const float fb = 16 * c + e < live_rows ? fac_b[16 * c + e] : 0.0f;
+                if (fb != 0.0f) o[e] += ob[e * DH] * fb;
+              }
+            }
             char *out = a.out + 2 * d;
-            const float *ob = pp + 16 * c * DH + d;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (16 * c + e < live_rows) {
-                const float f = fac[16 * c + e];
-                float y = f == 0.0f ? 0.0f : o[e] * f;
-                if (both && fac_b[16 * c + e] != 0.0f) y += ob[e * DH] * fac_b[16 * c + e];
-                *reinterpret_cast<uint16_t *>(out + row_off[16 * c + e]) =
-                    static_cast<uint16_t>(Half16<DT>::pack(y, 0.0f));
-              }
+              if (16 * c + e < live_rows)
+                *reinterpret_cast<uint16_t *>(out + at[e]) =
+                    static_cast<uint16_t>(Half16<DT>::pack(f[e] == 0.0f ? 0.0f : o[e] * f[e], 0.0f));
           } else {
             float *out = pp + (col0 + 16 * c) * DH + d;
 #pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = fac[16 * c + e] == 0.0f ? 0.0f : o[e];
+#pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (16 * c + e < live_rows) out[e * DH] = fac[16 * c + e] == 0.0f ? 0.0f : o[e];
+              if (16 * c + e < live_rows) out[e * DH] = o[e];
           }
         }
         __syncwarp();
@@ -658,63 +787,71 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       group_sync(bar_id);            // wred, row_off and O are free
       ring_op += 2 * T;
       slot = 1;
-      ++seg;
     }
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (QUANT) {
+  } else if (QUANT && warp < 16) {
+    fewer_regs<kOtherRegs<QUANT>>();
+    {
       // ------------------------------- 8-bit rows to the operand tiles
-      const int ct = tid & 127;
-      uint32_t op = 0;
+      // two threads a row
+      const int ct = tid & 127, half = (tid >> 7) & 1;
+      Place r = {0, 0}, o = {0, 1};     // (an operand place starts free)
       bool stop = false;
-      while (!stop && walk.next(a, w.bm, kW, &sg)) {
+      while (!stop && next_segment()) {
         const int T = sg.t1 - sg.t0;
-        for (int x = 0; x < 2 * T; ++x, ++op) {
-          const uint32_t rs = op % w.raw, os = op % w.ring;
-          if (!wait(&ss.raw_full[rs], (op / w.raw) & 1) ||
-              (op >= static_cast<uint32_t>(w.ring) && !wait(&ss.empty[os], (op / w.ring - 1) & 1))) {
+#pragma unroll 1
+        for (int x = 0; x < 2 * T; ++x) {
+          const uint32_t rs = r.at, os = o.at;
+          if (!wait(&ss.raw_full[rs], r.parity) || !wait(&ss.empty[os], o.parity)) {
             stop = true;
             break;
           }
+          r.step(w.raw);
+          o.step(w.ring);
           const unsigned char *raw = sm + w.off_raw + rs * w.raw_bytes;
-          // A thread has one row (its scale once), 16 codes at a time, starting at a chunk of
-          // its own so that eight lanes' chunks lie in eight bank groups, in the raw
-          // tile and, swizzled as K's and V's always, in the operand tile.
+          // Two threads have a row (its scale once), 16 codes at a time, chunks starting at a
+          // place of the row's own so that eight lanes' chunks lie in eight bank groups, in
+          // the raw tile and, swizzled as K's and V's always, in the operand tile.
           const uint32_t E = raw[kW * dh + ct];
           const unsigned char *src = raw + ct * dh;
           unsigned char *row = sm + os * tile_bytes + ct * 128;
-          // 2^(E - 127) 2^120 as a bf16 pair; above 2^7 in two steps
-          uint32_t mul = E == 255u ? 0x7fc0u : min(E + 120u, 254u) << 7;
-          mul |= mul << 16;
-          const bool big = E > 134u && E != 255u;
-          uint32_t more = (E - 7u) << 7;
-          more |= more << 16;
-          const float sc = row_scale(E);
-#pragma unroll 4
-          for (int i = 0; i < 8; ++i) {
-            const int c = (i + ct) & 7;
-            if (c >= dh >> 4) continue;
-            const uint4 q = *reinterpret_cast<const uint4 *>(src + c * 16);
-            const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
-            uint32_t y[8];
+          uint4 q[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (DT == DT_BF16) {
-                y[2 * e] = codes_bf16x2(__byte_perm(qw[e], 0u, 0x1404), mul);
-                y[2 * e + 1] = codes_bf16x2(__byte_perm(qw[e], 0u, 0x3424), mul);
-                if (big) {
-                  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y[2 * e]) : "r"(more));
-                  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y[2 * e + 1]) : "r"(more));
-                }
-              } else {
+          for (int i = 0; i < 4; ++i) {
+            const int c = (4 * half + i + ct) & 7;
+            if (c < dh >> 4) q[i] = *reinterpret_cast<const uint4 *>(src + c * 16);
+          }
+          if (DT == DT_BF16 && (E <= 134u || E == 255u)) {
+            // 2^(E - 127) 2^120 as a bf16 pair
+            uint32_t mul = E == 255u ? 0x7fc0u : (E + 120u) << 7;
+            mul |= mul << 16;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = (4 * half + i + ct) & 7;
+              if (c >= dh >> 4) continue;
+              const uint32_t qw[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                y[2 * e] = codes_bf16x2(spread_codes<0>(qw[e]), mul);
+                y[2 * e + 1] = codes_bf16x2(spread_codes<1>(qw[e]), mul);
+              }
+              put_operand(row, ct, c, y);
+            }
+          } else {
+            const float sc = row_scale(E);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = (4 * half + i + ct) & 7;
+              if (c >= dh >> 4) continue;
+              const uint32_t qw[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
                 y[2 * e] = e4m3_to16<DT>(qw[e] & 0xffffu, sc);
                 y[2 * e + 1] = e4m3_to16<DT>(qw[e] >> 16, sc);
               }
+              put_operand(row, ct, c, y);
             }
-            unsigned char *to = row + (c >> 2) * kBlk;
-            const int o = (c & 3) * 2;
-            *reinterpret_cast<uint4 *>(to + ((o ^ (ct & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4 *>(to + (((o + 1) ^ (ct & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
           }
           mbar_arrive(&ss.raw_empty[rs]);
           fence_async_smem();
@@ -723,24 +860,29 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 12) {
+    fewer_regs<kOtherRegs<QUANT>>();
+    const int role = warp - (QUANT ? 16 : 8);
+    if (role == 0) {
       // ---------------------------------------------------------- loads
-      uint32_t op = 0;
+      Place r = {0, 1};
+      uint32_t issued = 0;
       bool stop = false;
       const int slots = QUANT ? w.raw : w.ring;
       const int page = 1 << a.c.shift, pages = kW >> a.c.shift;
       uint64_t *full = QUANT ? ss.raw_full : ss.full, *empty = QUANT ? ss.raw_empty : ss.empty;
-      while (!stop && walk.next(a, w.bm, kW, &sg)) {
+      while (!stop && next_segment()) {
         const int T = sg.t1 - sg.t0;
-        for (int x = 0; x < 2 * T; ++x, ++op) {
+#pragma unroll 1
+        for (int x = 0; x < 2 * T; ++x) {
           bool is_v;
           const int t = sg.t0 + op_tile(x, T, &is_v);
-          const uint32_t s = op % slots;
-          if (op >= static_cast<uint32_t>(slots) && !wait_warp(&empty[s], (op / slots - 1) & 1)) {
+          const uint32_t s = r.at;
+          if (!wait_warp(&empty[s], r.parity)) {
             stop = true;
             break;
           }
+          r.step(slots);
+          ++issued;
           // lane i: page i of the tile
           const int64_t j = static_cast<int64_t>(t) * kW + (static_cast<int64_t>(lane) << a.c.shift);
           int64_t row = -1;
@@ -769,14 +911,15 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
         }
       }
       // no copy may be in flight when the block ends: wait (bounded) for the last ones
-      const uint32_t last = op < static_cast<uint32_t>(slots) ? op : slots;
-      for (uint32_t k = 1; k <= last; ++k)
-        mbar_wait_cycles(&full[(op - k) % slots], ((op - k) / slots) & 1);
-    } else if (warp == 13) {
+      for (int k = 0; k < slots; ++k, r.step(slots))
+        if (issued >= static_cast<uint32_t>(slots) || r.at < issued)
+          mbar_wait_cycles(&full[r.at], r.at < issued % slots ? (issued / slots) & 1
+                                                              : (issued / slots - 1) & 1);
+    } else if (role == 1) {
       // --------------------------------------------------------- products
       // The warp stays converged and one elected lane issues: descriptors are then
       // uniform values that need no move for each MMA.
-      uint32_t op = 0, segs = 0;
+      Place kp = {0, 0}, vp;            // the next operand tile; a V tile
       const uint32_t base = smem_u32(sm), q_blk = (w.na + w.nb) * 128;
       const uint64_t k0 = desc128(base, 16, 1024), v0 = desc128(base, w.nblk > 1 ? kBlk : 0, 1024);
       const int ks = dh >> 4, ng = w.alt ? 1 : 2;
@@ -809,30 +952,46 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
         }
         __syncwarp();
       };
-      uint32_t taken[2] = {0, 0};      // tiles of each group
-      while (!stop && walk.next(a, w.bm, kW, &sg)) {
+      uint32_t taken_a = 0, taken_b = 0;      // tiles of each group
+      while (!stop && next_segment()) {
         const int T = sg.t1 - sg.t0;
-        if (!wait_warp(&ss.q_full, segs & 1) || !wait_warp(&ss.full[op % w.ring], (op / w.ring) & 1)) break;
+        if (!wait_warp(&ss.q_full, (seg - 1) & 1) || !wait_warp(&ss.full[kp.at], kp.parity)) break;
         tmem_fence_after();
-        for (int X = 0; X < ng; ++X) scores(X, op % w.ring, X == ng - 1 ? &ss.empty[op % w.ring] : nullptr);
+#pragma unroll 1
+        for (int X = 0; X < ng; ++X) scores(X, kp.at, X == ng - 1 ? &ss.empty[kp.at] : nullptr);
+        kp.step(w.ring);
+#pragma unroll 1
         for (int t = 0; t < T && !stop; ++t) {
-          const uint32_t ko = op + 2 * t + 1, vo = op + (t < T - 1 ? 2 * t + 2 : 2 * T - 1);
-          const uint32_t kslot = ko % w.ring, vslot = vo % w.ring;
           const bool next = t + 1 < T;
-          if (next && !wait_warp(&ss.full[kslot], (ko / w.ring) & 1)) { stop = true; break; }
-          if (w.alt && next) scores((t + 1) & 1, kslot, &ss.empty[kslot]);
+          const Place k = kp;
+          if (next) kp.step(w.ring);
+          vp = kp;
+          kp.step(w.ring);
+          if (next && !wait_warp(&ss.full[k.at], k.parity)) { stop = true; break; }
+          if (w.alt && next) scores((t + 1) & 1, k.at, &ss.empty[k.at]);
+#pragma unroll 1
           for (int Y = 0; Y < ng; ++Y) {
             const int X = w.alt ? t & 1 : Y;
             const bool last = Y == ng - 1;
-            if (!wait_warp(&ss.p_full[X], taken[X]++ & 1)) { stop = true; break; }
+            if (!wait_warp(&ss.p_full[X], (X ? taken_b++ : taken_a++) & 1)) { stop = true; break; }
             tmem_fence_after();
-            if (!w.alt && next) scores(X, kslot, last ? &ss.empty[kslot] : nullptr);
-            if (Y == 0 && !wait_warp(&ss.full[vslot], (vo / w.ring) & 1)) { stop = true; break; }
-            values(X, vslot, t >= (w.alt ? 2 : 1), last ? &ss.empty[vslot] : nullptr);
+            if (!w.alt && next) scores(X, k.at, last ? &ss.empty[k.at] : nullptr);
+            if (Y == 0 && !wait_warp(&ss.full[vp.at], vp.parity)) { stop = true; break; }
+            values(X, vp.at, t >= (w.alt ? 2 : 1), last ? &ss.empty[vp.at] : nullptr);
           }
         }
-        op += 2 * T;
-        ++segs;
+      }
+    } else if (role == 2 && lane == 0) {
+      // -------------------------------------------------------- segments
+      Segment found;
+      bool more = true;
+      for (uint32_t i = 0; more; ++i) {
+        more = !*fail && walk.next(a, w.bm, kW, &found);
+        if (!more) found.b = -1;
+        // (after a failure the others go through their segments without waiting)
+        if (!mbar_wait_cycles(&ss.seg_empty[i % kSegs], ((i / kSegs) & 1) ^ 1)) *fail = 1;
+        ss.seg[i % kSegs] = found;
+        mbar_arrive(&ss.seg_full[i % kSegs]);
       }
     }
   }
@@ -895,13 +1054,13 @@ cudaError_t go(const AttnArgs &a, const WideShape &w, const AttnPlan &p, const C
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(p.smem));
   if (e != cudaSuccess) return e;
-  kernel<<<a.grid, kWThreads, p.smem, st>>>(a, w, k, v);
+  kernel<<<a.grid, kWThreads<QUANT>, p.smem, st>>>(a, w, k, v);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// Units of at most 112 rows (both groups the same) or, from 113 rows on, 224 (half the
+// Units of at most 96 rows (both groups the same) or, from 97 rows on, 192 (half the
 // rows each), as equal as they come. False where the kernel does not apply.
 bool wide_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p) {
   if (c.dh > 128 || static_cast<int64_t>(c.pages) * c.Hkv > 0x7fffffff) return false;

@@ -327,7 +327,7 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
     }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == sg.tiles;
-    float *pp = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * a.slot;
+    float *pp = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * 2 * a.slot;
     constexpr int C4 = DH / 8;
     for (int u = tid; u < BM * C4; u += kNThreads) {
       const int r = u / C4, c = u - r * C4, gr = rt * BM + r;
@@ -389,10 +389,11 @@ cache_attention_join_kernel(const __grid_constant__ AttnArgs a, int BM, int T, i
     const int r = u / C4, c = u - r * C4, gr = rt * BM + r;
     if (gr >= rows || c * 4 >= a.c.dh) continue;
     float m = ninf, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t x = c0 * a.parts; x < (c1 + 1) * a.parts; ++x) {
-      const int64_t k = a.parts == 2 ? x >> 1 : x;
+    const int parts = a.odd && rt == a.row_tiles - 1 ? 2 : 1;
+    for (int64_t x = c0 * parts; x < (c1 + 1) * parts; ++x) {
+      const int64_t k = parts == 2 ? x >> 1 : x;
       // the unit is the block's first if it reaches back to the block's first tile
-      const int64_t at = (k * 2 + (u0 <= k * sch.chunk ? 0 : 1)) * a.parts + (a.parts == 2 ? x & 1 : 0);
+      const int64_t at = (k * 2 + (u0 <= k * sch.chunk ? 0 : 1)) * 2 + (parts == 2 ? x & 1 : 0);
       const float *pp = a.part + at * a.slot;
       const float pm = pp[BM * DH + r], pl = pp[BM * DH + BM + r];
       if (pm == ninf && pl == 0.0f) continue;
@@ -463,13 +464,12 @@ int attn_plan(const dt_cache &c, int H, int n, AttnPlan *p) {
   *p = {};
   if (!wide_plan(c, rows, sms, smem, p)) {
     p->wide = 0;
-    p->parts = 1;
     p->dhp = c.dh <= 64 ? 64 : c.dh <= 128 ? 128 : 256;
     p->bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     p->row_tiles = static_cast<int>((rows + p->bm - 1) / p->bm);
     p->grid = sms * (p->dhp == 256 ? 1 : 2);
   }
-  p->bytes = static_cast<size_t>(p->grid) * (p->parts == 2 ? 6 : 2) * slot_floats(*p) * sizeof(float);
+  p->bytes = static_cast<size_t>(p->grid) * 6 * slot_floats(*p) * sizeof(float);
   return DT_OK;
 }
 
@@ -508,11 +508,12 @@ int dt_cache_attention(const dt_cache *c, const dt_heads *q, int n, int dtype,
   a.ob = 2 * out->stride_batch; a.oh = 2 * out->stride_head; a.orow = 2 * out->stride_row;
   a.prefix = prefix_len; a.counts = counts; a.mask = mask;
   a.part = static_cast<float *>(workspace);
-  a.scale_log2 = scale * 1.4426950408889634f;
+  // (a scale of zero: all weights equal, and -inf times it still -inf)
+  a.scale_log2 = scale == 0.0f ? 1e-38f : scale * 1.4426950408889634f;
   a.batch = c->batch; a.n = n; a.H = q->heads; a.G = G;
   a.row_tiles = p.row_tiles; a.grid = p.grid; a.min_tiles = 2;
   a.slot = dt::slot_floats(p);
-  a.parts = p.parts;
+  a.odd = p.odd;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool quant = c->dtype == DT_E4M3;
   cudaError_t e =

@@ -24,10 +24,12 @@ struct AttnArgs {
   int64_t qb, qh, qr, ob, oh, orow;   // strides in bytes
   const int32_t *prefix, *counts;
   const uint8_t *mask;
-  float *part;           // [grid][2][parts][slot]: [BM][DH] of O, [BM] maxima, [BM] sums
-  int parts;             // 2: a block's two groups of warps have a result each; another
-                         // [grid][2][slot] behind part then passes B's to A for whole units
-  int64_t slot;          // fp32 numbers of one, a multiple of 4
+  float *part;           // [grid][2][2][slot]: [BM][DH] of O, [BM] maxima, [BM] sums, of a
+                         // block's first or last unit, and of one of its two groups of
+                         // warps where these share a unit's rows; behind it [grid][2][slot],
+                         // which passes one group's part to the other
+  int odd;               // the last row tile's units are shared so
+  int64_t slot;          // fp32 numbers of one part, a multiple of 4
   float scale_log2;      // scale times log2(e)
   int batch, n, H, G, row_tiles, grid, min_tiles;
 };
@@ -216,11 +218,12 @@ __device__ __forceinline__ float fast_exp2(float x) {
 
 struct AttnPlan {        // resolved on the host from sizes alone
   int wide;              // dt_cache_wide.cu, else the mma.sync kernel
-  int bm, dhp, row_tiles, grid, parts;
-  int na, nb, ring, raw; // dt_cache_wide.cu: rows of its two groups, operand and raw tiles
+  int bm, dhp, row_tiles, grid;
+  int odd, ring, raw;    // dt_cache_wide.cu: the last unit is half a one; operand, raw tiles
   size_t smem, bytes;
 };
 constexpr int kWideKeys = 128;         // keys of a tile of dt_cache_wide.cu
+constexpr int kFewRows = 16;           // rows up to which the other kernel is used
 bool wide_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p);
 cudaError_t launch_wide(const dt_cache &c, const AttnArgs &a, int dtype, const AttnPlan &p,
                         cudaStream_t st);

@@ -1,33 +1,28 @@
-// dt_cache_wide.cu -- attention over the paged cache on the tcgen05 tensor cores
-// (head sizes up to 128).
+// dt_cache_wide.cu -- attention over the paged cache on the tcgen05 tensor cores, for
+// more than a few rows and head sizes up to 128.
 //
-// Both products are taken transposed, so that the query rows are the MMA's N side,
-// which comes in steps of 16 where the M side is 128: the rows of a unit (G heads x
-// tree rows, 4 to 192 of them) are padded to the next 16, not 128, and one kernel
-// serves single tokens and wide trees. Per tile of 128 keys and group of up to 112
-// rows: S^T = K Q^T (M = keys, K-major K tile and Q), p = 2^(x - m) by one thread a
-// key, which finds its key's scores for all rows in its TMEM lane, P^T to shared
-// memory ([key][row], the N side MN-major), O^T += V^T P^T (M = head dimension: the V
-// tile as it is stored, MN-major). Neither K nor V is transposed anywhere.
+// The rows of a (request, key/value head), G heads x tree rows, are cut into tiles of at
+// most 128 rows, as equal as they come; a unit is two of them (A and B), which share each
+// K and V tile of 128 keys, or the one that is left over. Per tile: S = Q K^T (Q and K
+// K-major in shared memory, S in TMEM, a thread a row), x = S scale log2(e) in one pass for
+// the row's maximum and one for its weights p = 2^(x - m), which go back to TMEM as the
+// first operand of O += P V (V as it is stored, MN-major). Maximum, sum and weights of a
+// row stay in its thread: no shuffle, no barrier, no shared memory. m follows the
+// maximum only when that has grown by 2^8 (fp16: 2^4), and only then are O and the sum
+// rescaled; any reference at most that far below the maximum gives the same quotient.
 //
-// The running maximum runs along the lanes of S^T, and is not taken for every tile:
-// a row's reference m stays until one of its weights passes 2^10 (fp16: 2^15, from
-// weights that start at 2^8), which a thread sees from its own weights; only then
-// (and for a unit's first tile) are the tile's maxima taken across lanes, O^T and the
-// sums rescaled. Any reference at most that far below the maximum gives the same
-// quotient; sums and O are fp32. Each thread sums its keys' weights row by row in
-// registers, joined across lanes once a unit.
+// What bounds it is the shared memory's 128 bytes a cycle as much as the tensor cores: an
+// MMA of 128 x 128 x 16 takes 64 cycles and reads 4 KB of each operand that is there. P
+// from TMEM halves that for the second product. (A version with both products transposed,
+// rows on the N side in steps of 16 and P^T through shared memory, was bound by it: 1.0 ms
+// where this one takes TIME_LONG for 8 trees of 129 rows at 32768 8-bit rows.)
 //
-// Two warpgroups (A, B) take weights, so that the tensor cores work for one meanwhile.
-// Up to 96 rows: both have all rows, A the even and B the odd key tiles, and A or the
-// join adds them up (an MMA takes 32 + N / 4 cycles at least, the first term for
-// reading its 128 keys: one MMA over all rows beats two over half). More rows: each
-// has half the rows, and every tile, so that a tile is read, and an 8-bit one
-// converted, once for up to 192 rows. K and V tiles alternate in a ring in the order
-// in which they are consumed (K0 K1 V0 K2 V1 ...), filled by TMA, page by page,
-// through a 128-byte swizzled tensor map; tiles of 8-bit rows land in a raw ring by
-// plain bulk copies and a third warpgroup writes their bf16 or fp16 values into the
-// operand ring.
+// While one group takes its weights the tensor cores work for the other. In a unit of a
+// single tile both groups have the same rows, A the even key tiles and B the odd ones,
+// and A or the join adds them up. K and V tiles pass through a ring in the order in which
+// they are consumed (K0 K1 V0 K2 V1 ...), filled by TMA, page by page, through a 128-byte
+// swizzled tensor map; tiles of 8-bit rows land in a raw ring by plain bulk copies and two
+// warpgroups write their bf16 or fp16 values into the operand ring.
 #include <cmath>
 #include <cstdint>
 #include <cuda.h>
@@ -44,33 +39,22 @@ constexpr int kW = kWideKeys;
 constexpr int kBlk = kW * 128;         // bytes of 128 rows of 64 16-bit values
 constexpr int kMaxRing = 8;
 constexpr int kSegs = 4;
-constexpr int kMaxCols = 96;           // rows of a group: one sum of each in a thread's registers
-
-// Warpgroups: two for weights, two (8-bit rows) that convert, one whose warps load, issue
-// the products, find segments. Registers at launch times threads is what setmaxnreg
-// shares out: 640 x 96 >= 256 x 176 + 384 x 40, and 384 x 168 >= 256 x 200 + 128 x 96.
-template <bool QUANT> constexpr int kWThreads = QUANT ? 640 : 384;
-template <bool QUANT> constexpr int kWeightRegs = QUANT ? 176 : 200;
-template <bool QUANT> constexpr int kOtherRegs = QUANT ? 40 : 96;
-template <int N> __device__ __forceinline__ void more_regs() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N> __device__ __forceinline__ void fewer_regs() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 constexpr int kOddWords = (DT_MAX_N + 32) / 32;
 constexpr long long kWaitCycles = 4000000000ll;   // about 2 s
 
+// Warpgroups: two for weights, two (8-bit rows) that convert, one whose warps load, issue
+// the products and find segments. Registers at launch times threads is what setmaxnreg
+// shares out: 640 x 96 >= 256 x 144 + 384 x 56.
+template <bool QUANT> constexpr int kWThreads = QUANT ? 640 : 384;
+
 struct WideShape {
-  int bm, na, nb, alt, ring, raw, nblk, raw_bytes;
-  int off_q, off_pa, off_pb, off_raw, off_small;
+  int tr, odd, ring, raw, nblk, raw_bytes;   // rows of a tile; whether the last unit is one tile
+  int off_q, off_raw, off_small;
 };
 
 struct Small {                          // behind the big buffers
-  float neg_m[2][128];                  // minus the reference of each row (plus the fp16 shift)
-  float fac[2][128];
   uint64_t full[kMaxRing], empty[kMaxRing], raw_full[kMaxRing], raw_empty[kMaxRing];
-  uint64_t q_full, q_free, s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full, q_free, s_full[2], p_full[2], o_done[2];
   int64_t scan[640 / 32 + 2];
   Segment seg[kSegs];                   // the next segments; b < 0: no more
   uint64_t seg_full[kSegs], seg_empty[kSegs];
@@ -149,22 +133,20 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
       : "memory");
 }
 
-// barrier of one warpgroup (id 1, 2); the second form also ORs a predicate
-__device__ __forceinline__ void group_sync(int id) {
-  asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
-__device__ __forceinline__ bool group_any(int id, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %2, 0;\n"
-      "barrier.cta.red.or.pred q, %1, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r) : "r"(id), "r"(static_cast<uint32_t>(p)) : "memory");
-  return r != 0;
-}
+
 // both warpgroups: a part of one unit handed from B to A through global memory
 __device__ __forceinline__ void pair_sync() {
   __threadfence_block();
-  asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
+  asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
+}
+// one warpgroup
+__device__ __forceinline__ void group_sync(int X) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + X) : "memory");
 }
 
 // packed pairs of fp32
@@ -186,13 +168,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-template <int DT>
-__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {   // a number beats a NaN
-  uint32_t r;
-  if (DT == DT_BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 // largest magnitudes of two pairs of 16-bit values (signs are not kept), NaN above all
 template <int DT>
 __device__ __forceinline__ uint32_t top_abs(uint32_t a, uint32_t b) {
@@ -201,105 +176,20 @@ __device__ __forceinline__ uint32_t top_abs(uint32_t a, uint32_t b) {
   else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 16 weights of key gt into the group's P^T tile
-__device__ __forceinline__ void put_weights(unsigned char *sP, int gt, int c, const uint32_t (&y)[8]) {
-  unsigned char *p = sP + (c >> 2) * kBlk + gt * 128;
-  const int ch = (c & 3) * 2;
-  *reinterpret_cast<uint4 *>(p + ((ch ^ (gt & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-  *reinterpret_cast<uint4 *>(p + (((ch + 1) ^ (gt & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-}
-
-// sets bits [lo, hi) of a 128-bit set
-__device__ __forceinline__ void set_run(uint64_t (&bits)[2], int lo, int hi) {
-  if (lo >= hi) return;
-  const int n = hi - lo;
-  const uint64_t run = n >= 64 ? ~0ull : (1ull << n) - 1;
-  if (lo < 64) {
-    bits[0] |= run << lo;
-    if (hi > 64) bits[1] |= hi >= 128 ? ~0ull : (1ull << (hi - 64)) - 1;
-  } else {
-    bits[1] |= run << (lo - 64);
-  }
-}
-
-// Reduces 16 columns across the 32 lanes of a warp (MAX: maximum, else sum): lanes
-// 2 c and 2 c + 1 end with column c.
-template <bool MAX>
-__device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
-#pragma unroll
-  for (int half = 8, m = 16; half >= 1; half >>= 1, m >>= 1) {
-    const bool up = lane & m;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < half) {
-        const float keep = up ? v[i + half] : v[i], give = up ? v[i] : v[i + half];
-        const float got = __shfl_xor_sync(kFull, give, m);
-        v[i] = MAX ? fmaxf(keep, got) : keep + got;
-      }
-  }
-  const float got = __shfl_xor_sync(kFull, v[0], 1);
-  return MAX ? fmaxf(v[0], got) : v[0] + got;
-}
-
-// Sums of 8 row pairs [pair][128 keys][2] over the keys into out[16].
-__device__ __forceinline__ void sum_chunk(const float *part, float *out, int gt, int bar_id) {
-  group_sync(bar_id);
-  // 16 lanes a row pair, 8 keys each
-  const float4 *src = reinterpret_cast<const float4 *>(part + ((gt >> 4) * 128) * 2) + (gt & 15);
-  float a = 0.0f, b = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float4 x = src[16 * k];
-    a += x.x + x.z;
-    b += x.y + x.w;
-  }
-#pragma unroll
-  for (int m = 8; m; m >>= 1) {
-    a += __shfl_xor_sync(kFull, a, m);
-    b += __shfl_xor_sync(kFull, b, m);
-  }
-  if ((gt & 15) == 0) {
-    out[2 * (gt >> 4)] = a;
-    out[2 * (gt >> 4) + 1] = b;
-  }
-  group_sync(bar_id);
-}
-
-// New references of a group's rows: the larger of the old one and the tile's maximum,
-// taken across lanes (scores that do not count are -inf there). fac: what earlier sums
-// are to be scaled by.
-__device__ __forceinline__ void new_refs(uint32_t t_s, int n, float *wred, int gt, int lane, int bar_id,
-                                         float scale, float shift, float *neg_m, float *fac, float *m) {
-  const float ninf = -__int_as_float(0x7f800000);
-#pragma unroll 1
-  for (int c = 0; c * 16 < n; ++c) {
-    float v[16];
-    tmem_ld16(t_s + 16 * c, v);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] *= scale;
-    const float r = reduce16<true>(v, lane);
-    if (!(lane & 1)) wred[(gt >> 5) * 128 + 16 * c + (lane >> 1)] = r;
-  }
-  group_sync(bar_id);
-  if (gt < n) {
-    float mn = fmaxf(fmaxf(wred[gt], wred[128 + gt]), fmaxf(wred[256 + gt], wred[384 + gt]));
-    mn = fmaxf(mn, *m);
-    fac[gt] = mn == ninf ? 1.0f : fast_exp2(*m - mn);
-    // a row that has seen nothing yet: any score passes the limit
-    neg_m[gt] = mn == ninf ? 1e30f : shift - mn;
-    *m = mn;
-  }
-  group_sync(bar_id);
-}
-
-// instruction descriptor of kind::f16, M = 128, fp32 accumulation; mn: both operands
-// MN-major
+// instruction descriptor of kind::f16, M = 128, fp32 accumulation; mn: B is MN-major
 template <int DT>
 __device__ __forceinline__ uint32_t idesc16(int N, bool mn) {
   const uint32_t f = DT == DT_BF16 ? 1u : 0u;
-  return (1u << 4) | (f << 7) | (f << 10) | (mn ? 3u << 15 : 0u) |
+  return (1u << 4) | (f << 7) | (f << 10) | (mn ? 1u << 16 : 0u) |
          (static_cast<uint32_t>(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
 }
 
 // two of a word's four e4m3 codes (0: the lower two) as sign-extended half words
@@ -345,7 +235,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
   extern __shared__ __align__(1024) unsigned char sm[];
   Small &ss = *reinterpret_cast<Small *>(sm + w.off_small);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int dh = a.c.dh, tile_bytes = w.nblk * kBlk;
+  const int dh = a.c.dh, tile_bytes = w.nblk * kBlk, bm = 2 * w.tr;
   const float ninf = -__int_as_float(0x7f800000);
 
   if (tid == 0) {
@@ -355,8 +245,8 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       mbar_init(&ss.raw_full[i], 1);
       mbar_init(&ss.raw_empty[i], 256);
     }
-    mbar_init(&ss.q_full, w.alt ? 128 : 256);
-    mbar_init(&ss.q_free, 128);
+    mbar_init(&ss.q_full, 256);
+    mbar_init(&ss.q_free, 1);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&ss.seg_full[i], 1);
       mbar_init(&ss.seg_empty[i], QUANT ? 18 : 10);   // the warps that take segments
@@ -364,12 +254,10 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ss.s_full[x], 1);
       mbar_init(&ss.p_full[x], 128);
-      mbar_init(&ss.pv_done[x], 1);
+      mbar_init(&ss.o_done[x], 1);
     }
     ss.fail = 0;
   }
-  // rows that are padding keep a reference that gives them weight 0
-  for (int i = tid; i < 256; i += kWThreads<QUANT>) (&ss.neg_m[0][0])[i] = ninf;
   if (warp == 0) tmem_alloc(&ss.tmem, 512);
   tmem_fence_before();
   __syncthreads();
@@ -377,13 +265,13 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
   const uint32_t tmem = ss.tmem;
 
   Schedule<kWThreads<QUANT>> sch;
-  sch.plan(a, w.bm, kW, ss.scan);
+  sch.plan(a, bm, kW, ss.scan);
   Walk walk;
   walk.at = blockIdx.x * sch.chunk;
   walk.stop = min(walk.at + sch.chunk, sch.total);
   walk.b = 0;
   walk.base = 0;
-  if (walk.at < walk.stop) sch.find(a, w.bm, kW, walk.at, ss.scan, &walk.b, &walk.base);
+  if (walk.at < walk.stop) sch.find(a, bm, kW, walk.at, ss.scan, &walk.b, &walk.base);
   Segment sg;
   sg.b = 0;
   volatile int *fail = &ss.fail;
@@ -417,6 +305,8 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
     ++seg;
     return sg.b >= 0;
   };
+  // a unit of a single tile of rows
+  auto single = [&]() { return w.odd && sg.rt == a.row_tiles - 1; };
   // operand tiles of a segment of T key tiles, in ring order: K0 K1 V0 K2 V1 ... V(T-1)
   auto op_tile = [](int op, int T, bool *is_v) {
     if (op == 0) { *is_v = false; return 0; }
@@ -427,127 +317,119 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
 
   if (warp < 8) {
     // ------------------------------------------------ weights: groups A and B
-    more_regs<kWeightRegs<QUANT>>();
-    const int X = warp >> 2, gt = tid & 127, bar_id = 1 + X;   // gt: key, lane and row of the group
-    const int n = !w.alt && X ? w.nb : w.na, col0 = !w.alt && X ? w.na : 0;
-    const int tstep = w.alt ? 2 : 1, tfirst = w.alt ? X : 0;
-    unsigned char *sP = sm + (X ? w.off_pb : w.off_pa);
+    if (QUANT) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    const int X = warp >> 2, gt = tid & 127;      // gt: the group's row, TMEM lane (and key)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + 128 * X + lane_off, t_o = tmem + 256 + 128 * X + lane_off;
-    float *neg_m = ss.neg_m[X], *fac = ss.fac[X];
-    // while P is not in use: [4][128] of the warps, row places [128], [128] factors of B's part
-    float *wred = reinterpret_cast<float *>(sP);
-    int64_t *row_off = reinterpret_cast<int64_t *>(sP + 2048);
-    float *fac_b = reinterpret_cast<float *>(sP + 3072);
+    // fp16 weights are scaled by 2^8, so that small ones stay normal numbers
     constexpr float kShift = DT == DT_F16 ? 8.0f : 0.0f;
-    const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
-    // a score that counts for nothing: -inf after the scaling (0 scale: see below)
-    const float lowest = a.scale_log2 < 0.0f ? -ninf : ninf;
-    uint32_t mine = 0, ring_op = 0;            // tiles of this group, ring places
+    constexpr float kGrow = DT == DT_F16 ? 4.0f : 8.0f;
+    const float scale = fabsf(a.scale_log2);
+    const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;   // the scale's sign goes to Q
+    const uint64_t scale2 = pair(scale, scale);
+    const int DH = 64 * w.nblk;
+    uint32_t mine = 0, segs_mine = 0, ring_op = 0;  // tiles, segments of this group, ring places
     int slot = 0;
     while (next_segment()) {
       const uint32_t si = seg - 1;
       const Request rq = sg.rq;
-      const int T = sg.t1 - sg.t0, rows = a.n * a.G, row0 = sg.rt * w.bm + col0;
-      const int live_rows = min(min(n, w.bm - col0), rows - row0);    // of this group
+      const bool alt = single();
+      const int T = sg.t1 - sg.t0, tstep = alt ? 2 : 1, tfirst = alt ? X : 0;
+      const int col0 = alt ? 0 : X * w.tr, row = sg.rt * bm + col0 + gt;     // stacked query row
+      const int tok = row / a.G, head = sg.hk * a.G + row - tok * a.G;
+      const bool real = gt < w.tr && row < a.n * a.G, live = real && tok < rq.count;
       if (tid == 0 && a.prefix[sg.b] != rq.pre) cache_fault(a.c, sg.b);
       // keys before `pre` are seen by every (live) row of the unit
       // (row numbers fit 32 bits: a table has at most 2^20 pages of at most 128 rows)
-      const int pre = static_cast<int>(a.mask ? rq.pre : rq.pre + sg.rt * w.bm / a.G);
-      const int end = static_cast<int>(sg.end);
+      const int pre = static_cast<int>(a.mask ? rq.pre : rq.pre + sg.rt * bm / a.G);
+      const int end = static_cast<int>(sg.end), whole_end = min(pre, end);
       const int32_t *table = a.c.table + static_cast<int64_t>(sg.b) * a.c.width;
       uint32_t *odd = ss.odd[si & 1];
       if (X == 0)
         for (int i = gt; i < kOddWords + 1; i += 128) odd[i] = 0u;
-      // the rows of Q, K-major, 128-byte swizzle: a thread has one chunk of every
-      // eighth (sixteenth) row, eight in flight
-      if (!w.alt || X == 0) {
-        if (w.alt && si > 0) wait(&ss.q_free, (si - 1) & 1);   // B's last scores are taken
-        const int c = gt & (w.nblk * 8 - 1), step = 128 / (w.nblk * 8);
-        const char *src = a.q + sg.b * a.qb + sg.hk * a.G * a.qh + c * 16;
-        unsigned char *dst = sm + w.off_q + (c >> 3) * (w.na + w.nb) * 128 + col0 * 128;
-#pragma unroll 1
-        for (int r0 = gt / (w.nblk * 8); r0 < n; r0 += 8 * step) {
+      if (si > 0) wait(&ss.q_free, (si - 1) & 1);
+      // the thread's row of Q, K-major, 128-byte swizzle
+      if (real && (!alt || X == 0)) {
+        const char *src = a.q + sg.b * a.qb + head * a.qh + tok * a.qr;
+        unsigned char *dst = sm + w.off_q + (alt ? 0 : X * tile_bytes) + gt * 128;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
           uint4 x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = r0 + e * step;
-            x[e] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < live_rows && c * 8 < dh) {
-              const int i = (row0 + r) / a.G, g = row0 + r - i * a.G;
-              x[e] = *reinterpret_cast<const uint4 *>(src + g * a.qh + i * a.qr);
-            }
-          }
+          for (int c = 0; c < 8; ++c)
+            if (kb < w.nblk && 64 * kb + 8 * c < dh) x[c] = reinterpret_cast<const uint4 *>(src)[8 * kb + c];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = r0 + e * step;
-            if (r < n) *reinterpret_cast<uint4 *>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[e];
-          }
+          for (int c = 0; c < 8; ++c)
+            if (kb < w.nblk && 64 * kb + 8 * c < dh) {
+              x[c].x ^= flip; x[c].y ^= flip; x[c].z ^= flip; x[c].w ^= flip;
+              *reinterpret_cast<uint4 *>(dst + kb * kBlk + ((c ^ (gt & 7)) << 4)) = x[c];
+            }
         }
-        fence_async_smem();
-        mbar_arrive(&ss.q_full);
-      } else {
-        // B goes on once A has: A waits for q_free segment by segment, and a second
-        // arrival of B before that would pass the phase that A waits for
-        wait(&ss.q_full, si & 1);
       }
-      float m = ninf;                 // reference of row gt of the group
-      uint64_t l[kMaxCols / 2];       // sums of this thread's keys' weights, two rows each
-#pragma unroll
-      for (int c = 0; c < kMaxCols / 2; ++c) l[c] = 0ull;
-      // whether this thread's key of tile t is there, on a good page
-      auto key_there = [&](int t) {
-        const int j = (sg.t0 + t) * kW + gt, page = j >> a.c.shift;
-        return t < T && j < end && page < a.c.width &&
-               static_cast<uint32_t>(table[page]) < static_cast<uint32_t>(a.c.pages);
+      fence_async_smem();
+      mbar_arrive(&ss.q_full);
+      float m = ninf;                       // reference of this thread's row
+      uint64_t l2[2] = {0ull, 0ull};        // its sum, in four parts
+      // whether page `lane` of key tile t is there (in lanes that have one)
+      const int pages = kW >> a.c.shift;
+      auto page_bad = [&](int t) {
+        const int page = (((sg.t0 + t) * kW) >> a.c.shift) + lane;
+        return t < T && lane < pages && (page << a.c.shift) < end &&
+               !(page < a.c.width && static_cast<uint32_t>(table[page]) < static_cast<uint32_t>(a.c.pages));
       };
-      bool valid = key_there(tfirst);
+      bool bad = page_bad(tfirst);
 
-      for (int t = tfirst; t < T; t += tstep, ++mine) {
-        const int j = (sg.t0 + t) * kW + gt;
-        const bool first = t == tfirst;
-        const bool masked = __any_sync(kFull, !valid || j >= pre);
-        uint64_t bits[2] = {0ull, 0ull};          // the rows that see this thread's key
-        if (masked && valid) {
-          if (j < pre) {
-            bits[0] = bits[1] = ~0ull;
-          } else {
-            // tree row j - rq.pre: eight tokens' loads in flight, then each token's run of rows
-            const int tr = j - static_cast<int>(rq.pre), i0 = row0 / a.G;
-            const uint8_t *mk =
-                a.mask ? a.mask + (static_cast<int64_t>(sg.b) * a.n + i0) * a.n + tr : nullptr;
-            const int tokens = min((row0 + live_rows - 1) / a.G + 1, rq.count) - i0;
-            for (int i = 0; i < tokens; i += 8) {
-              uint32_t v = 0;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const bool in = i + e < tokens;
-                v |= (in && (mk ? mk[static_cast<int64_t>(i + e) * a.n] != 0 : tr <= i0 + i + e) ? 1u : 0u) << e;
-              }
 #pragma unroll 1
-              for (; v; v &= v - 1) {
-                const int e = i0 + i + __ffs(v) - 1;
-                set_run(bits, max(e * a.G - row0, 0), min((e + 1) * a.G - row0, live_rows));
+      for (int t = tfirst; t < T; t += tstep, ++mine) {
+        const int j0 = (sg.t0 + t) * kW;
+        const uint32_t bad_pages = __ballot_sync(kFull, bad);
+        const bool masked = bad_pages != 0u || j0 + kW > whole_end;
+        bad = page_bad(t + tstep);
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};     // keys of the tile that the row sees
+        if (masked) {
+          // the warp's rows' tokens one after another, a lane a key
+          const int lo = __shfl_sync(kFull, tok, 0), hi = __shfl_sync(kFull, tok, 31);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int j = j0 + 32 * q + lane, tr = j - static_cast<int>(rq.pre);
+            const bool there = j < end && !((bad_pages >> ((32 * q + lane) >> a.c.shift)) & 1u);
+            see[q] = __ballot_sync(kFull, there);
+            if (j0 + 32 * q + 32 <= pre) continue;        // all before the tree
+            const uint32_t any = see[q];
+            const bool tree = there && tr >= 0 && tr < rq.count;
+            for (int i = lo; i <= hi; i += 4) {
+              bool v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const bool in = tree && i + e < rq.count;
+                v[e] = (there && tr < 0) ||
+                       (in && (a.mask ? a.mask[(static_cast<int64_t>(sg.b) * a.n + i + e) * a.n + tr] != 0
+                                      : tr <= i + e));
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t b = __ballot_sync(kFull, v[e]);
+                if (tok == i + e) see[q] = any & b;
               }
             }
           }
+          if (!live) see[0] = see[1] = see[2] = see[3] = 0u;
         }
         wait(&ss.s_full[X], mine & 1);
-        if (!first) wait(&ss.pv_done[X], (mine - 1) & 1);   // P is free, O is whole
         __syncwarp();
         tmem_fence_after();
-        if (w.alt && X == 1 && t + 2 >= T) mbar_arrive(&ss.q_free);
-        if ((w.alt || X == 0) && masked) {
+        if (masked && (alt || X == 0)) {
           // V rows that nobody sees become zeros, and so do values that are not finite in
-          // tree rows (zero times them is NaN): the rows that see those get them below.
-          // (The slot's tile before this one is consumed by now, K(t) at the latest with
-          // three places and V(t - 1) with two, so this parity is this tile's.)
+          // tree rows (zero times them is NaN): the rows that see those get them below. The
+          // thread takes the row of key gt. (The slot's tile before this one is consumed by
+          // now, so the parity waited for is this tile's: S of tile t is complete, and with
+          // it every product issued before, all but those of V(t - 1) and later.)
           const uint32_t vop = ring_op + (t < T - 1 ? 2 * t + 2 : 2 * T - 1);
           const uint32_t turn = vop / w.ring, vslot = vop - turn * w.ring;
           wait(&ss.full[vslot], turn & 1);
           unsigned char *v = sm + vslot * tile_bytes + gt * 128;
-          bool found = false;
-          if (!valid) {
+          const int j = j0 + gt;
+          if (j >= end || ((bad_pages >> (gt >> a.c.shift)) & 1u)) {
 #pragma unroll 4
             for (int c = 0; c < 8 * w.nblk; ++c)
               *reinterpret_cast<uint4 *>(v + (c >> 3) * kBlk + ((c & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
@@ -560,236 +442,209 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
             }
             const uint32_t ex = DT == DT_BF16 ? 0x7f80u : 0x7c00u;
             if ((top & ex) == ex || ((top >> 16) & ex) == ex) {
-              found = true;
 #pragma unroll 1
               for (int c = 0; c < 64 * w.nblk; ++c) {
                 uint16_t *x = reinterpret_cast<uint16_t *>(v + (c >> 6) * kBlk) + (c & 63);
                 if ((*x & ex) == ex) *x = 0;
               }
+              // (a mask's rows, or the at most 256 that a causal unit's rows see in part)
+              atomicOr(&odd[(j - pre) >> 5], 1u << ((j - pre) & 31));
+              odd[kOddWords] = 1u;
             }
           }
-          if (found) {
-            // (a mask's rows, or the at most 192 that a causal unit's rows see in part)
-            atomicOr(&odd[(j - pre) >> 5], 1u << ((j - pre) & 31));
-            odd[kOddWords] = 1u;
-          }
+          fence_async_smem();
         }
         if (masked) {
           // scores that do not count become -inf in place; nothing below asks again
-#pragma unroll 1
-          for (int c = 0; c * 16 < n; ++c) {
-            float v[16];
-            tmem_ld16(t_s + 16 * c, v);
-            tmem_wait_ld();
-            const uint32_t b16 = static_cast<uint32_t>((c >= 4 ? bits[1] : bits[0]) >> ((c & 3) * 16));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = (b16 >> e) & 1u ? v[e] : lowest;
-            tmem_st16(t_s + 16 * c, v);
+          for (int q = 0; q < 4; ++q) {
+            if (__all_sync(kFull, see[q] == ~0u)) continue;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              float v[16];
+              tmem_ld16(t_s + 32 * q + 16 * h, v);
+              tmem_wait_ld();
+              const uint32_t b16 = see[q] >> (16 * h);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = (b16 >> e) & 1u ? v[e] : ninf;
+              tmem_st16(t_s + 32 * q + 16 * h, v);
+            }
           }
           tmem_wait_st();
         }
-        valid = key_there(t + tstep);
-        if (first) new_refs(t_s, n, wred, gt, lane, bar_id, a.scale_log2, kShift, neg_m, fac, &m);
-        uint32_t top = 0u;            // largest weights
+        // the row's maximum
+        float top = ninf;
         {
           float s0[16], s1[16];
           tmem_ld16(t_s, s0);
 #pragma unroll
-          for (int c = 0; c < kMaxCols / 16; ++c) {
-            if (16 * c < n) {
-              float *v = c & 1 ? s1 : s0;
-              const ulonglong2 *r = reinterpret_cast<const ulonglong2 *>(neg_m + 16 * c);
-              tmem_wait_ld();
-              if (16 * c + 16 < n) {
-                if (c & 1) tmem_ld16(t_s + 16 * c + 16, s0);
-                else tmem_ld16(t_s + 16 * c + 16, s1);
-              }
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float p0, p1;
-                unpair(fma2(pair(v[2 * e], v[2 * e + 1]), scale2, e & 1 ? r[e >> 1].y : r[e >> 1].x), &p0, &p1);
-                p0 = fast_exp2(p0);
-                p1 = fast_exp2(p1);
-                l[8 * c + e] = add2(l[8 * c + e], pair(p0, p1));
-                y[e] = Half16<DT>::pack(p0, p1);
-                top = max16x2<DT>(top, y[e]);
-              }
-              put_weights(sP, gt, c, y);
+          for (int c = 0; c < 8; ++c) {
+            float *v = c & 1 ? s1 : s0;
+            tmem_wait_ld();
+            if (c < 7) {
+              if (c & 1) tmem_ld16(t_s + 16 * c + 16, s0);
+              else tmem_ld16(t_s + 16 * c + 16, s1);
             }
+            float x = fmaxf(v[0], v[1]), y = fmaxf(v[2], v[3]);    // 3-input maxima
+#pragma unroll
+            for (int e = 4; e < 16; e += 4) {
+              x = fmaxf(fmaxf(x, v[e]), v[e + 1]);
+              y = fmaxf(fmaxf(y, v[e + 2]), v[e + 3]);
+            }
+            top = fmaxf(fmaxf(top, x), y);
           }
         }
-        // weights are not negative: their bits order them (2^10; fp16 2^15)
-        const uint32_t lim = DT == DT_BF16 ? 0x4480u : 0x7800u;
-        if (group_any(bar_id, (top & 0xffffu) > lim || (top >> 16) > lim)) {
-          // Rare. New references; what was summed so far is scaled to them, this tile's
-          // weights are written anew. A sum past 2^100 is this tile's (what came before
-          // it is below 2^-60 of it) and may have overflowed: it starts again.
-          new_refs(t_s, n, wred, gt, lane, bar_id, a.scale_log2, kShift, neg_m, fac, &m);
-#pragma unroll
-          for (int c = 0; c < kMaxCols / 16; ++c) {
-            if (16 * c < n) {
-              float v[16];
-              if (!first) {
-                tmem_ld16(t_o + 16 * c, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] *= fac[16 * c + e];
-                tmem_st16(t_o + 16 * c, v);
-              }
-              tmem_ld16(t_s + 16 * c, v);
+        top *= scale;
+        const bool grow = live && (top > m + kGrow || (m == ninf && top != ninf));
+        if (__any_sync(kFull, grow)) {
+          const float f = grow ? (m == ninf ? 0.0f : fast_exp2(m - top)) : 1.0f;
+          if (grow) m = top;
+          float a0, a1, b0, b1;
+          unpair(l2[0], &a0, &a1);
+          unpair(l2[1], &b0, &b1);
+          l2[0] = pair(a0 * f, a1 * f);
+          l2[1] = pair(b0 * f, b1 * f);
+          if (t != tfirst) {
+#pragma unroll 1
+            for (int c = 0; c < dh; c += 16) {
+              float o[16];
+              tmem_ld16(t_o + c, o);
               tmem_wait_ld();
-              uint32_t y[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float p0 = fast_exp2(fmaf(v[2 * e], a.scale_log2, neg_m[16 * c + 2 * e]));
-                const float p1 = fast_exp2(fmaf(v[2 * e + 1], a.scale_log2, neg_m[16 * c + 2 * e + 1]));
-                float l0, l1;
-                unpair(l[8 * c + e], &l0, &l1);
-                l0 = l0 > 0x1p100f ? p0 : l0 * fac[16 * c + 2 * e];
-                l1 = l1 > 0x1p100f ? p1 : l1 * fac[16 * c + 2 * e + 1];
-                l[8 * c + e] = pair(l0, l1);
-                y[e] = Half16<DT>::pack(p0, p1);
-              }
-              put_weights(sP, gt, c, y);
+              for (int e = 0; e < 16; ++e) o[e] *= f;
+              tmem_st16(t_o + c, o);
             }
+            tmem_wait_st();
+          }
+        }
+        // the weights, written over the scores' first half (each chunk behind its own scores)
+        {
+          const float nm = m == ninf ? 0.0f : kShift - m;
+          const uint64_t nm2 = pair(nm, nm);
+          float s0[16], s1[16];
+          tmem_ld16(t_s, s0);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float *v = c & 1 ? s1 : s0;
+            tmem_wait_ld();
+            if (c < 7) {
+              if (c & 1) tmem_ld16(t_s + 16 * c + 16, s0);
+              else tmem_ld16(t_s + 16 * c + 16, s1);
+            }
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float p0, p1;
+              unpair(fma2(pair(v[2 * e], v[2 * e + 1]), scale2, nm2), &p0, &p1);
+              p0 = fast_exp2(p0);
+              p1 = fast_exp2(p1);
+              l2[e & 1] = add2(l2[e & 1], pair(p0, p1));
+              y[e] = Half16<DT>::pack(p0, p1);
+            }
+            // (the next chunk's scores are being read: columns 16 c + 16 on, past 8 c + 7)
+            tmem_st8(t_s + 8 * c, y);
           }
           tmem_wait_st();
         }
-        fence_async_smem();
         tmem_fence_before();
         mbar_arrive(&ss.p_full[X]);
       }
-      if (w.alt && X == 1 && T < 2) mbar_arrive(&ss.q_free);
-      // The unit's end: sums across lanes, then O^T, a lane's dimension of every row.
+      // The unit's end: O of this thread's row.
       const bool some = tfirst < T;
-      if (some) wait(&ss.pv_done[X], (mine - 1) & 1);
+      if (some) wait(&ss.o_done[X], segs_mine++ & 1);
       __syncwarp();
       tmem_fence_after();
-      // (16 rows at a time through P's place: 16 lanes add up a pair of rows)
-      float *part = reinterpret_cast<float *>(sP + 4096);
-#pragma unroll
-      for (int c = 0; c < kMaxCols / 16; ++c) {
-        if (16 * c < n) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) *reinterpret_cast<uint64_t *>(part + (e * 128 + gt) * 2) = l[8 * c + e];
-          sum_chunk(part, wred + 16 * c, gt, bar_id);
-        }
+      float sum;
+      {
+        float a0, a1, b0, b1;
+        unpair(l2[0], &a0, &a1);
+        unpair(l2[1], &b0, &b1);
+        sum = (a0 + a1) + (b0 + b1);
       }
-      const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles, both = w.alt && whole;
+      if (!live) {
+        m = ninf;
+        sum = 0.0f;
+      }
+      const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles, both = alt && whole;
       const bool leave = !whole || (both && X == 1);      // a part for the join or for A
-      const int DH = 64 * w.nblk;
       float *pp = a.part + (both ? (4ll * a.grid + 2 * blockIdx.x + (si & 1)) * a.slot
-                                 : ((2ll * blockIdx.x + slot) * a.parts + (w.alt ? X : 0)) * a.slot);
-      if (gt < live_rows) {
-        const float sum = wred[gt];
-        const int gr = row0 + gt, i = gr / a.G;
-        const bool live = i < rq.count;
-        if (leave) {
-          fac[gt] = live ? 1.0f : 0.0f;
-          pp[w.bm * DH + col0 + gt] = live ? m : ninf;
-          pp[w.bm * (DH + 1) + col0 + gt] = live ? sum : 0.0f;
-        } else {
-          row_off[gt] = sg.b * a.ob + (sg.hk * a.G + (gr - i * a.G)) * a.oh + i * a.orow;
-          if (both) {      // joined with B's part below
-            fac[gt] = m;
-            wred[gt] = sum;
-          } else {
-            fac[gt] = !live ? 0.0f : sum > 0.0f ? 1.0f / sum : sum == sum ? 0.0f : sum;
-          }
-        }
+                                 : ((2ll * blockIdx.x + slot) * 2 + (alt ? X : 0)) * a.slot);
+      if (leave && real) {
+        pp[bm * DH + col0 + gt] = m;
+        pp[bm * (DH + 1) + col0 + gt] = sum;
       }
+      float f = leave ? 1.0f : 0.0f, fb = 0.0f;           // factors of O and of B's part
       if (both && X == 0) {
         pair_sync();
-        if (gt < live_rows) {
-          const float ma = fac[gt], sa = wred[gt];
-          const float mb = pp[w.bm * DH + gt], sb = pp[w.bm * (DH + 1) + gt], mm = fmaxf(ma, mb);
-          const float fa = ma == ninf && sa == 0.0f ? 0.0f : fast_exp2(ma - mm);
-          const float fb = mb == ninf && sb == 0.0f ? 0.0f : fast_exp2(mb - mm);
-          const float all = sa * fa + sb * fb;
-          const float inv = (row0 + gt) / a.G >= rq.count ? 0.0f
-                            : all > 0.0f ? 1.0f / all : all == all ? 0.0f : all;
-          fac[gt] = fa * inv;
-          fac_b[gt] = fb * inv;
+        if (live) {
+          const float mb = pp[bm * DH + gt], sb = pp[bm * (DH + 1) + gt], mm = fmaxf(m, mb);
+          const float fa = m == ninf && sum == 0.0f ? 0.0f : fast_exp2(m - mm);
+          fb = mb == ninf && sb == 0.0f ? 0.0f : fast_exp2(mb - mm);
+          const float all = sum * fa + sb * fb;
+          const float inv = all > 0.0f ? 1.0f / all : all == all ? 0.0f : all;
+          f = fa * inv;
+          fb *= inv;
         }
+      } else if (!leave && live) {
+        f = sum > 0.0f ? 1.0f / sum : sum == sum ? 0.0f : sum;
       }
-      group_sync(bar_id);
+      if (!live) f = 0.0f;
+      group_sync(X);                        // odd[] is complete
       const bool any_odd = odd[kOddWords] != 0u;
-      const int d = (warp & 3) * 32 + lane;
+      char *out = a.out + sg.b * a.ob + head * a.oh + tok * a.orow;
+      float *po = pp + (col0 + gt) * DH;
 #pragma unroll 1
-      for (int c = 0; some && c * 16 < live_rows; ++c) {
+      for (int c = 0; c < dh; c += 16) {
         float o[16];
-        tmem_ld16(t_o + 16 * c, o);
+        tmem_ld16(t_o + c, o);
         tmem_wait_ld();
-        if (any_odd && d < dh) {       // rare: values that are not finite
+        if (any_odd && live && some) {        // rare: values that are not finite
 #pragma unroll 1
-          for (int e = 0; e < 16; ++e) {
-            const int i = (row0 + 16 * c + e) / a.G;
-            if (16 * c + e >= live_rows || i >= rq.count) continue;
-            float add = 0.0f;
-            for (int x = 0; x < 32 * kOddWords; ++x) {
-              const int key = pre + x, kt = key / kW - sg.t0;
-              if (!((odd[x >> 5] >> (x & 31)) & 1u) || key >= end || kt < tfirst || kt >= T ||
-                  (w.alt && (kt & 1) != X) || !sees(a, rq, sg.b, i, key))
-                continue;
-              const int64_t row = cache_row(a.c, sg.b, key, sg.hk);
-              if (row < 0) continue;
-              const float v = QUANT ? row_scale(a.c.v_exp[row])
-                                    : Half16<DT>::unpack(static_cast<const uint16_t *>(a.c.v)[row * dh + d]).x;
-              if (v - v != 0.0f) add += v;
-            }
-#pragma unroll
-            for (int z = 0; z < 16; ++z)
-              if (z == e) o[z] += add;
-          }
-        }
-        __syncwarp();
-        // a dead row's O may hold anything: zero whatever it is
-        if (d < dh) {
-          // (all reads before the first store: it might, for all the compiler knows, change them)
-          if (!leave) {
-            float f[16];
-            int64_t at[16];
+          for (int x = 0; x < 32 * kOddWords; ++x) {
+            const int key = pre + x, kt = key / kW - sg.t0;
+            if (!((odd[x >> 5] >> (x & 31)) & 1u) || key >= end || kt < tfirst || kt >= T ||
+                (alt && (kt & 1) != X) || !sees(a, rq, sg.b, tok, key))
+              continue;
+            const int64_t at = cache_row(a.c, sg.b, key, sg.hk);
+            if (at < 0) continue;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              f[e] = fac[16 * c + e];
-              at[e] = row_off[16 * c + e];
+              const float v = QUANT ? row_scale(a.c.v_exp[at])
+                                    : Half16<DT>::unpack(static_cast<const uint16_t *>(a.c.v)[at * dh + c + e]).x;
+              if (v - v != 0.0f) o[e] += v;
             }
-            if (both) {
-              const float *ob = pp + 16 * c * DH + d;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                o[e] = f[e] == 0.0f ? 0.0f : o[e] * f[e];
-                f[e] = 1.0f;
-                const float fb = 16 * c + e < live_rows ? fac_b[16 * c + e] : 0.0f;
-                if (fb != 0.0f) o[e] += ob[e * DH] * fb;
-              }
-            }
-            char *out = a.out + 2 * d;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (16 * c + e < live_rows)
-                *reinterpret_cast<uint16_t *>(out + at[e]) =
-                    static_cast<uint16_t>(Half16<DT>::pack(f[e] == 0.0f ? 0.0f : o[e] * f[e], 0.0f));
-          } else {
-            float *out = pp + (col0 + 16 * c) * DH + d;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = fac[16 * c + e] == 0.0f ? 0.0f : o[e];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (16 * c + e < live_rows) out[e * DH] = o[e];
           }
+        }
+        // a dead row's O may hold anything: zero whatever it is
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = f == 0.0f || !some ? 0.0f : o[e] * f;
+        if (real && leave) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4 *>(po + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else if (real) {
+          if (fb != 0.0f) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 x = *reinterpret_cast<const float4 *>(po + c + e);
+              o[e] += x.x * fb; o[e + 1] += x.y * fb; o[e + 2] += x.z * fb; o[e + 3] += x.w * fb;
+            }
+          }
+          uint32_t y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = Half16<DT>::pack(o[2 * e], o[2 * e + 1]);
+          *reinterpret_cast<uint4 *>(out + 2 * c) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4 *>(out + 2 * c + 16) = make_uint4(y[4], y[5], y[6], y[7]);
         }
         __syncwarp();
       }
       tmem_fence_before();
       if (both && X == 1) pair_sync();
-      group_sync(bar_id);            // wred, row_off and O are free
       ring_op += 2 * T;
       slot = 1;
     }
   } else if (QUANT && warp < 16) {
-    fewer_regs<kOtherRegs<QUANT>>();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     {
       // ------------------------------- 8-bit rows to the operand tiles
       // two threads a row
@@ -860,7 +715,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       }
     }
   } else {
-    fewer_regs<kOtherRegs<QUANT>>();
+    if (QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     const int role = warp - (QUANT ? 16 : 8);
     if (role == 0) {
       // ---------------------------------------------------------- loads
@@ -919,65 +774,79 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       // --------------------------------------------------------- products
       // The warp stays converged and one elected lane issues: descriptors are then
       // uniform values that need no move for each MMA.
-      Place kp = {0, 0}, vp;            // the next operand tile; a V tile
-      const uint32_t base = smem_u32(sm), q_blk = (w.na + w.nb) * 128;
-      const uint64_t k0 = desc128(base, 16, 1024), v0 = desc128(base, w.nblk > 1 ? kBlk : 0, 1024);
-      const int ks = dh >> 4, ng = w.alt ? 1 : 2;
+      const uint32_t base = smem_u32(sm);
+      const uint64_t k0 = desc128(base, 16, 1024), v0 = desc128(base, kBlk, 1024);
+      const uint32_t id_s = idesc16<DT>(kW, false), id_o = idesc16<DT>(dh, true);
+      const int ks = dh >> 4;
+      Place op = {0, 0};               // the next operand tile
+      uint32_t taken_a = 0, taken_b = 0;      // tiles of each group
       bool stop = false;
-      auto scores = [&](int X, uint32_t s, uint64_t *free) {
-        const bool second = !w.alt && X;      // the rows' second half
+      // S of group X from K tile s; `free`, `q_free`: the last reader of that tile, of Q
+      auto scores = [&](int X, bool second, uint32_t s, bool free, bool q_free) {
         const uint64_t kd = k0 + ((s * tile_bytes) >> 4);
-        const uint64_t qd = k0 + ((w.off_q + (second ? w.na * 128 : 0)) >> 4);
-        const uint32_t id = idesc16<DT>(second ? w.nb : w.na, false), to = tmem + 128 * X;
+        const uint64_t qd = k0 + ((w.off_q + (second ? tile_bytes : 0)) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (k < ks)
-              umma_bf16(to, kd + (k >> 2) * (kBlk >> 4) + (k & 3) * 2,
-                        qd + (k >> 2) * (q_blk >> 4) + (k & 3) * 2, id, k > 0);
+            if (k < ks) {
+              const int at = (k >> 2) * (kBlk >> 4) + (k & 3) * 2;
+              umma_bf16(tmem + 128 * X, qd + at, kd + at, id_s, k > 0);
+            }
           umma_commit(&ss.s_full[X]);
-          if (free) umma_commit(free);
+          if (free) umma_commit(&ss.empty[s]);
+          if (q_free) umma_commit(&ss.q_free);
         }
         __syncwarp();
       };
-      auto values = [&](int X, uint32_t s, bool more, uint64_t *free) {
+      auto values = [&](int X, uint32_t s, bool more, bool free, bool last) {
         const uint64_t vd = v0 + ((s * tile_bytes) >> 4);
-        const uint64_t pd = desc128(base + (X ? w.off_pb : w.off_pa), kBlk, 1024);
-        const uint32_t id = idesc16<DT>(!w.alt && X ? w.nb : w.na, true), to = tmem + 256 + 128 * X;
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kW / 16; ++k) umma_bf16(to, vd + k * 128, pd + k * 128, id, more || k > 0);
-          umma_commit(&ss.pv_done[X]);
-          if (free) umma_commit(free);
+          for (int k = 0; k < kW / 16; ++k)
+            umma_ts(tmem + 256 + 128 * X, tmem + 128 * X + 8 * k, vd + k * 128, id_o, more || k > 0);
+          if (last) umma_commit(&ss.o_done[X]);
+          if (free) umma_commit(&ss.empty[s]);
         }
         __syncwarp();
       };
-      uint32_t taken_a = 0, taken_b = 0;      // tiles of each group
       while (!stop && next_segment()) {
-        const int T = sg.t1 - sg.t0;
-        if (!wait_warp(&ss.q_full, (seg - 1) & 1) || !wait_warp(&ss.full[kp.at], kp.parity)) break;
+        const bool alt = single();
+        const int T = sg.t1 - sg.t0, ng = alt ? 1 : 2;
+        Place k = op, v;
+        op.step(w.ring);
+        if (!wait_warp(&ss.q_full, (seg - 1) & 1) || !wait_warp(&ss.full[k.at], k.parity)) break;
         tmem_fence_after();
-#pragma unroll 1
-        for (int X = 0; X < ng; ++X) scores(X, kp.at, X == ng - 1 ? &ss.empty[kp.at] : nullptr);
-        kp.step(w.ring);
-#pragma unroll 1
+        scores(0, false, k.at, alt, alt && T == 1);
+        if (!alt) scores(1, true, k.at, true, T == 1);
+        // `k`: the K tile of step t + 1, whose scores of groups A, B (of alternating groups:
+        // group B's, already) are issued in step t
         for (int t = 0; t < T && !stop; ++t) {
           const bool next = t + 1 < T;
-          const Place k = kp;
-          if (next) kp.step(w.ring);
-          vp = kp;
-          kp.step(w.ring);
-          if (next && !wait_warp(&ss.full[k.at], k.parity)) { stop = true; break; }
-          if (w.alt && next) scores((t + 1) & 1, k.at, &ss.empty[k.at]);
-#pragma unroll 1
-          for (int Y = 0; Y < ng; ++Y) {
-            const int X = w.alt ? t & 1 : Y;
-            const bool last = Y == ng - 1;
-            if (!wait_warp(&ss.p_full[X], (X ? taken_b++ : taken_a++) & 1)) { stop = true; break; }
+          k = op;
+          if (next) op.step(w.ring);
+          v = op;
+          op.step(w.ring);
+          if (alt) {
+            // S of tile t + 1 has a group of its own: before the weights of tile t
+            if (next) {
+              if (!wait_warp(&ss.full[k.at], k.parity)) { stop = true; break; }
+              // (from tile 2 on behind the group's last product, which read its weights)
+              scores((t + 1) & 1, false, k.at, true, t + 2 == T);
+            }
+            const int X = t & 1;
+            if (!wait_warp(&ss.p_full[X], (X ? taken_b++ : taken_a++) & 1) ||
+                !wait_warp(&ss.full[v.at], v.parity)) { stop = true; break; }
             tmem_fence_after();
-            if (!w.alt && next) scores(X, k.at, last ? &ss.empty[k.at] : nullptr);
-            if (Y == 0 && !wait_warp(&ss.full[vp.at], vp.parity)) { stop = true; break; }
-            values(X, vp.at, t >= (w.alt ? 2 : 1), last ? &ss.empty[vp.at] : nullptr);
+            values(X, v.at, t >= 2, true, t + 2 >= T);
+          } else {
+            for (int X = 0; X < ng; ++X) {
+              if (!wait_warp(&ss.p_full[X], (X ? taken_b++ : taken_a++) & 1) ||
+                  (X == 0 && !wait_warp(&ss.full[v.at], v.parity)) ||
+                  (X == 0 && next && !wait_warp(&ss.full[k.at], k.parity))) { stop = true; break; }
+              tmem_fence_after();
+              values(X, v.at, t > 0, X == 1, !next);
+              if (next) scores(X, X == 1, k.at, X == 1, X == 1 && t + 2 == T);
+            }
           }
         }
       }
@@ -986,7 +855,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       Segment found;
       bool more = true;
       for (uint32_t i = 0; more; ++i) {
-        more = !*fail && walk.next(a, w.bm, kW, &found);
+        more = !*fail && walk.next(a, bm, kW, &found);
         if (!more) found.b = -1;
         // (after a failure the others go through their segments without waiting)
         if (!mbar_wait_cycles(&ss.seg_empty[i % kSegs], ((i / kSegs) & 1) ^ 1)) *fail = 1;
@@ -1036,13 +905,11 @@ bool make_map(const dt_cache &c, const void *base, CUtensorMap *map) {
 
 WideShape wide_shape(const dt_cache &c, const AttnPlan &p) {
   WideShape w;
-  w.bm = p.bm; w.na = p.na; w.nb = p.nb; w.alt = p.parts == 2; w.ring = p.ring; w.raw = p.raw;
+  w.tr = p.bm / 2; w.odd = p.odd; w.ring = p.ring; w.raw = p.raw;
   w.nblk = c.dh > 64 ? 2 : 1;
   w.raw_bytes = kW * c.dh + kW;
   w.off_q = p.ring * w.nblk * kBlk;
-  w.off_pa = (w.off_q + (p.na + p.nb) * 128 * w.nblk + 1023) & ~1023;
-  w.off_pb = w.off_pa + (p.na + 63) / 64 * kBlk;
-  w.off_raw = w.off_pb + ((w.alt ? p.na : p.nb) + 63) / 64 * kBlk;
+  w.off_raw = w.off_q + (p.odd && p.row_tiles == 1 ? 1 : 2) * w.nblk * kBlk;
   w.off_small = w.off_raw + p.raw * w.raw_bytes;
   return w;
 }
@@ -1060,29 +927,20 @@ cudaError_t go(const AttnArgs &a, const WideShape &w, const AttnPlan &p, const C
 
 }  // namespace
 
-// Units of at most 96 rows (both groups the same) or, from 97 rows on, 192 (half the
-// rows each), as equal as they come. False where the kernel does not apply.
+// Row tiles of at most 128 rows, two a unit. False where the kernel does not apply.
 bool wide_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p) {
-  if (c.dh > 128 || static_cast<int64_t>(c.pages) * c.Hkv > 0x7fffffff) return false;
+  if (c.dh > 128 || static_cast<int64_t>(c.pages) * c.Hkv > 0x7fffffff || rows <= kFewRows) return false;
   const bool quant = c.dtype == DT_E4M3;
-  p->parts = rows <= kMaxCols ? 2 : 1;
-  const int64_t units = (rows + 2 * kMaxCols - 1) / (2 * kMaxCols);
-  p->bm = static_cast<int>((rows + units - 1) / units);
-  p->row_tiles = static_cast<int>((rows + p->bm - 1) / p->bm);
-  if (p->parts == 2) {
-    p->na = (p->bm + 15) & ~15;
-    p->nb = 0;
-  } else {
-    p->na = ((p->bm + 1) / 2 + 15) & ~15;
-    p->nb = (p->bm - p->na + 15) & ~15;
-  }
+  const int64_t tiles = (rows + 127) / 128;
+  p->bm = 2 * static_cast<int>((rows + tiles - 1) / tiles);
+  p->row_tiles = static_cast<int>((tiles + 1) / 2);
+  p->odd = static_cast<int>(tiles & 1);
   p->ring = p->raw = 0;
   const WideShape w = wide_shape(c, *p);
   const int tile = w.nblk * kBlk;
   const int room = smem - w.off_small - static_cast<int>(sizeof(Small));
   if (quant) {
-    // three operand tiles (two where the rows leave no room), the rest for raw ones
-    p->ring = p->parts == 2 || room >= 3 * tile + 2 * w.raw_bytes ? 3 : 2;
+    p->ring = 3;
     p->raw = (room - p->ring * tile) / w.raw_bytes;
     if (p->raw > kMaxRing) p->raw = kMaxRing;
     if (p->raw < 2) return false;

@@ -24,6 +24,7 @@ bool cache_dtype_ok(const dt_cache *c, int dtype);
 namespace {
 
 constexpr int kNThreads = 128;
+constexpr int kJoinThreads = 512;      // 8 rows of 256 values, 4 each
 constexpr int kT = 64;                 // keys of a tile
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -92,14 +93,14 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
   Schedule<kNThreads> sch;
   sch.plan(a, BM, kT, s_scan);
   Walk walk;
+  Segment sg;
   walk.at = blockIdx.x * sch.chunk;
   walk.stop = min(walk.at + sch.chunk, sch.total);
-  if (walk.at >= walk.stop) return;
-  sch.find(a, BM, kT, walk.at, s_scan, &walk.b, &walk.base);
-  int slot = 0;
-  Segment sg;
+  if (walk.at < walk.stop) sch.find(a, BM, kT, walk.at, s_scan, &walk.b, &walk.base);
+  bool more = walk.next(a, BM, kT, &sg);
+  if (tid == 0) walk.note_cut(a, sch.chunk, more, sg);
 
-  while (walk.next(a, BM, kT, &sg)) {
+  for (; more; more = walk.next(a, BM, kT, &sg)) {
     const int b = sg.b, hk = sg.hk, rt = sg.rt, t0 = sg.t0, t1 = sg.t1;
     const Request rq = sg.rq;
     const int64_t end = sg.end;
@@ -327,7 +328,7 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
     }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == sg.tiles;
-    float *pp = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * 2 * a.slot;
+    float *pp = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (t0 > 0 ? 0 : 1)) * 2 * a.slot;
     constexpr int C4 = DH / 8;
     for (int u = tid; u < BM * C4; u += kNThreads) {
       const int r = u / C4, c = u - r * C4, gr = rt * BM + r;
@@ -362,56 +363,52 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
         *reinterpret_cast<uint4 *>(a.out + b * a.ob + h * a.oh + i * a.orow + c * 16) = x;
       }
     }
-    slot = 1;
   }
 }
 
-// Joins the partial results of units that were cut over blocks: one block a unit.
+// Joins the partial results of units that were cut over blocks. A block for kJoinRows
+// rows of the unit that block blockIdx.x's part of the line begins within, if it is the
+// first to continue it: a thread has 4 values of a row, all parts' weights before all
+// parts' values, so that the loads wait for each other twice, not once a part.
+constexpr int kJoinRows = 8;
 template <int DT>
-__global__ void __launch_bounds__(kNThreads)
-cache_attention_join_kernel(const __grid_constant__ AttnArgs a, int BM, int T, int DH) {
-  __shared__ int64_t s_scan[kNThreads / 32 + 2];
-  const int tid = threadIdx.x;
-  const int rt = blockIdx.x % a.row_tiles;
-  const int bh = blockIdx.x / a.row_tiles, hk = bh % a.c.Hkv, b = bh / a.c.Hkv;
-  Schedule<kNThreads> sch;
-  sch.plan(a, BM, T, s_scan);
-  const Request rq = request_of(a, b);
-  const int64_t u0 = sch.first_of(a, BM, T, b, s_scan) +
-                     hk * tiles_before(a, rq, a.row_tiles, BM, T) + tiles_before(a, rq, rt, BM, T);
-  const int tiles = unit_tiles(a, rq, rt, BM, T);
-  const int64_t c0 = u0 / sch.chunk, c1 = (u0 + tiles - 1) / sch.chunk;
-  if (c0 == c1) return;   // one block held it whole
+__global__ void __launch_bounds__(kJoinThreads)
+cache_attention_join_kernel(const __grid_constant__ AttnArgs a, int BM, int DH) {
+  const int4 unit = a.cut[2 * blockIdx.x], blocks = a.cut[2 * blockIdx.x + 1];
+  if (unit.x < 0 || blocks.x + 1 != static_cast<int>(blockIdx.x)) return;
+  const int b = unit.x, hk = unit.y, rt = unit.z;
   const float ninf = -__int_as_float(0x7f800000);
-  const int C4 = DH / 4;
-  const int rows = a.n * a.G;
-  for (int u = tid; u < BM * C4; u += kNThreads) {
-    const int r = u / C4, c = u - r * C4, gr = rt * BM + r;
-    if (gr >= rows || c * 4 >= a.c.dh) continue;
-    float m = ninf, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int parts = a.odd && rt == a.row_tiles - 1 ? 2 : 1;
-    for (int64_t x = c0 * parts; x < (c1 + 1) * parts; ++x) {
-      const int64_t k = parts == 2 ? x >> 1 : x;
-      // the unit is the block's first if it reaches back to the block's first tile
-      const int64_t at = (k * 2 + (u0 <= k * sch.chunk ? 0 : 1)) * 2 + (parts == 2 ? x & 1 : 0);
-      const float *pp = a.part + at * a.slot;
-      const float pm = pp[BM * DH + r], pl = pp[BM * DH + BM + r];
-      if (pm == ninf && pl == 0.0f) continue;
-      const float4 po = *reinterpret_cast<const float4 *>(pp + r * DH + c * 4);
-      const float mn = fmaxf(m, pm);
-      const float f = m == ninf ? 0.0f : fast_exp2(m - mn), e = fast_exp2(pm - mn);
-      m = mn;
-      l = l * f + pl * e;
-      o[0] = o[0] * f + po.x * e;
-      o[1] = o[1] * f + po.y * e;
-      o[2] = o[2] * f + po.z * e;
-      o[3] = o[3] * f + po.w * e;
-    }
-    const float inv = l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
-    const int i = gr / a.G, h = hk * a.G + gr % a.G;
-    *reinterpret_cast<uint2 *>(a.out + b * a.ob + h * a.oh + i * a.orow + c * 8) =
-        make_uint2(Half16<DT>::pack(o[0] * inv, o[1] * inv), Half16<DT>::pack(o[2] * inv, o[3] * inv));
+  const int C4 = DH / 4, r = blockIdx.y * kJoinRows + threadIdx.x / C4, c = threadIdx.x % C4;
+  const int gr = rt * BM + r;
+  if (r >= min(BM, static_cast<int>(blockIdx.y + 1) * kJoinRows) || gr >= a.n * a.G || c * 4 >= a.c.dh) return;
+  // a shared unit has a part of either group of warps in a block; a block's last unit is
+  // in its second place, the one that it began within in its first
+  const int per = a.odd && rt == a.row_tiles - 1 ? 2 : 1, parts = (blocks.y - blocks.x + 1) * per;
+  auto part = [&](int x) {
+    const int k = blocks.x + (per == 2 ? x >> 1 : x), g = per == 2 ? x & 1 : 0;
+    return a.part + ((static_cast<int64_t>(k) * 2 + (k > blocks.x ? 0 : 1)) * 2 + g) * a.slot;
+  };
+  float m = ninf;
+#pragma unroll 4
+  for (int x = 0; x < parts; ++x) m = fmaxf(m, part(x)[BM * DH + r]);
+  float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int x = 0; x < parts; ++x) {
+    const float *pp = part(x);
+    const float pm = pp[BM * DH + r], pl = pp[BM * DH + BM + r];
+    const float4 po = *reinterpret_cast<const float4 *>(pp + r * DH + c * 4);
+    if (pm == ninf && pl == 0.0f) continue;     // saw nothing; its values are not written
+    const float e = fast_exp2(pm - m);
+    l += pl * e;
+    o[0] += po.x * e;
+    o[1] += po.y * e;
+    o[2] += po.z * e;
+    o[3] += po.w * e;
   }
+  const float inv = l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
+  const int i = gr / a.G, h = hk * a.G + gr - i * a.G;
+  *reinterpret_cast<uint2 *>(a.out + b * a.ob + h * a.oh + i * a.orow + c * 8) =
+      make_uint2(Half16<DT>::pack(o[0] * inv, o[1] * inv), Half16<DT>::pack(o[2] * inv, o[3] * inv));
 }
 
 template <int DT, bool QUANT, int DH, int WK>
@@ -428,8 +425,7 @@ cudaError_t launch_narrow(const AttnArgs &a, cudaStream_t st) {
 template <int DT>
 cudaError_t launch_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
   cache_attention_join_kernel<DT>
-      <<<static_cast<unsigned>(a.batch * a.c.Hkv * a.row_tiles), kNThreads, 0, st>>>(
-          a, p.bm, p.wide ? kWideKeys : kT, p.dhp);
+      <<<dim3(a.grid, (p.bm + kJoinRows - 1) / kJoinRows), kJoinRows * p.dhp / 4, 0, st>>>(a, p.bm, p.dhp);
   return cudaGetLastError();
 }
 
@@ -469,7 +465,7 @@ int attn_plan(const dt_cache &c, int H, int n, AttnPlan *p) {
     p->row_tiles = static_cast<int>((rows + p->bm - 1) / p->bm);
     p->grid = sms * (p->dhp == 256 ? 1 : 2);
   }
-  p->bytes = static_cast<size_t>(p->grid) * 6 * slot_floats(*p) * sizeof(float);
+  p->bytes = static_cast<size_t>(p->grid) * (2 * sizeof(int4) + 6 * slot_floats(*p) * sizeof(float));
   return DT_OK;
 }
 
@@ -507,13 +503,17 @@ int dt_cache_attention(const dt_cache *c, const dt_heads *q, int n, int dtype,
   a.qb = 2 * q->stride_batch; a.qh = 2 * q->stride_head; a.qr = 2 * q->stride_row;
   a.ob = 2 * out->stride_batch; a.oh = 2 * out->stride_head; a.orow = 2 * out->stride_row;
   a.prefix = prefix_len; a.counts = counts; a.mask = mask;
-  a.part = static_cast<float *>(workspace);
+  a.cut = static_cast<int4 *>(workspace);
+  a.part = reinterpret_cast<float *>(a.cut + 2 * p.grid);
   // (a scale of zero: all weights equal, and -inf times it still -inf)
   a.scale_log2 = scale == 0.0f ? 1e-38f : scale * 1.4426950408889634f;
   a.batch = c->batch; a.n = n; a.H = q->heads; a.G = G;
   a.row_tiles = p.row_tiles; a.grid = p.grid; a.min_tiles = 2;
   a.slot = dt::slot_floats(p);
   a.odd = p.odd;
+  a.weight = p.wide ? 2 : 1;
+  a.last_weight = p.wide && p.odd ? 1 : a.weight;
+  a.lead = p.wide ? dt::kWideLead : 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool quant = c->dtype == DT_E4M3;
   cudaError_t e =

@@ -4,13 +4,14 @@
 // A unit of work is (request, key/value head, tile of BM query rows); the H / Hkv
 // query heads that share a key/value head are stacked token by token, row
 // r = i G + g, so K and V are read once for all of them. A unit's keys come in
-// tiles of T. All units' tiles, in order, are cut into equal contiguous ranges,
-// one a block: lengths differ from request to request and are known on the device
-// only, and this keeps every block equally busy for any mix of them. A block writes
-// a unit that it holds whole; a unit cut over blocks leaves partial results
-// (unnormalised output, reference maximum, sum) in the workspace, at most two a
-// block, and a second launch joins them in block order: the result does not
-// depend on timing.
+// tiles of T. Units lie one after another on a line, each `lead` long (what it costs to
+// begin and end one) and then `weight` for each of its key tiles; the line is cut into
+// equal parts, one a block, and a block has the tiles that begin in its part. Lengths
+// differ from request to request and are known on the device only, and this keeps every
+// block about equally busy for any mix of them. A block writes a unit that it holds
+// whole; a unit cut over blocks leaves partial results (unnormalised output, reference
+// maximum, sum) in the workspace, at most two a block, and a second launch joins them in
+// block order: the result does not depend on timing.
 #pragma once
 
 #include "dt_cache.cuh"
@@ -32,6 +33,8 @@ struct AttnArgs {
   int64_t slot;          // fp32 numbers of one part, a multiple of 4
   float scale_log2;      // scale times log2(e)
   int batch, n, H, G, row_tiles, grid, min_tiles;
+  int weight, last_weight, lead;      // of a key tile, of one of the last row tile, of a unit
+  int4 *cut;             // [grid][2]: the unit that a block's part of the line begins within
 };
 
 struct Request {         // one request's sizes, clamped to its table
@@ -61,18 +64,26 @@ __device__ __forceinline__ int unit_tiles(const AttnArgs &a, const Request &r, i
   return e > T ? static_cast<int>((e + T - 1) / T) : 1;
 }
 
-// the units of one head before row tile `upto`
-__device__ __forceinline__ int64_t tiles_before(const AttnArgs &a, const Request &r, int upto, int bm,
-                                                int T) {
-  int64_t w = 0;
+__device__ __forceinline__ int tile_weight(const AttnArgs &a, int rt) {
+  return rt == a.row_tiles - 1 ? a.last_weight : a.weight;
+}
+
+// length of the units of one head before row tile `upto`
+__device__ __forceinline__ int64_t length_before(const AttnArgs &a, const Request &r, int upto, int bm,
+                                                 int T) {
+  int64_t len = static_cast<int64_t>(upto) * a.lead;
   if (a.mask) {   // every live row tile sees the same keys
     const int live = min(upto, (r.count * a.G + bm - 1) / bm);
-    w = upto - live;
-    if (live) w += static_cast<int64_t>(live) * unit_tiles(a, r, 0, bm, T);
+    int64_t tiles = upto - live;
+    if (live) tiles += static_cast<int64_t>(live) * unit_tiles(a, r, 0, bm, T);
+    len += tiles * a.weight;
+    if (upto == a.row_tiles)
+      len -= static_cast<int64_t>(a.weight - a.last_weight) * unit_tiles(a, r, upto - 1, bm, T);
   } else {
-    for (int rt = 0; rt < upto; ++rt) w += unit_tiles(a, r, rt, bm, T);
+    for (int rt = 0; rt < upto; ++rt)
+      len += static_cast<int64_t>(unit_tiles(a, r, rt, bm, T)) * tile_weight(a, rt);
   }
-  return w;
+  return len;
 }
 
 // inclusive sum over the block's threads (THREADS a multiple of 32); *total gets all
@@ -97,29 +108,30 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *s_warp, int64_
   return v + before;
 }
 
-// The cut of all work tiles over the blocks. All threads of the block call plan() and
-// find(); s_scan: THREADS / 32 + 2 numbers of shared memory.
+// The cut of the line over the blocks. All threads of the block call plan() and find();
+// s_scan: THREADS / 32 + 2 numbers of shared memory.
 template <int THREADS>
 struct Schedule {
   int64_t total, chunk;
-  int64_t one;           // this thread's request's tiles where one scan covers the batch
+  int64_t one;           // this thread's request's length where one scan covers the batch
   int64_t upto;          // inclusive sum to it
-  __device__ int64_t request_tiles(const AttnArgs &a, int b, int bm, int T) {
-    return b < a.batch ? a.c.Hkv * tiles_before(a, request_of(a, b), a.row_tiles, bm, T) : 0;
+  __device__ int64_t request_length(const AttnArgs &a, int b, int bm, int T) {
+    return b < a.batch ? a.c.Hkv * length_before(a, request_of(a, b), a.row_tiles, bm, T) : 0;
   }
   // sizes of the whole launch
   __device__ void plan(const AttnArgs &a, int bm, int T, int64_t *s_scan) {
     total = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
-      one = request_tiles(a, b0 + threadIdx.x, bm, T);
+      one = request_length(a, b0 + threadIdx.x, bm, T);
       int64_t all;
       upto = block_scan<THREADS>(one, s_scan, &all);
       total += all;
     }
-    chunk = (total + a.grid - 1) / a.grid;
-    if (chunk < a.min_tiles) chunk = a.min_tiles;
+    const int64_t least = static_cast<int64_t>(a.min_tiles) * a.weight + a.lead;
+    chunk = max((total + a.grid - 1) / a.grid, least);
   }
-  // request that holds work tile `at`, and the first work tile of that request
+  // request that holds place `at`, and the place where it begins
   __device__ void find(const AttnArgs &a, int bm, int T, int64_t at, int64_t *s_scan, int *b,
                        int64_t *start) {
     int64_t *s_found = s_scan + THREADS / 32;
@@ -130,8 +142,9 @@ struct Schedule {
       }
     } else {
       int64_t before = 0;
+#pragma unroll 1
       for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
-        const int64_t w = request_tiles(a, b0 + threadIdx.x, bm, T);
+        const int64_t w = request_length(a, b0 + threadIdx.x, bm, T);
         int64_t all;
         const int64_t u = before + block_scan<THREADS>(w, s_scan, &all);
         if (at >= u - w && at < u) {
@@ -146,20 +159,6 @@ struct Schedule {
     *start = s_found[1];
     __syncthreads();
   }
-  // first work tile of request b
-  __device__ int64_t first_of(const AttnArgs &a, int bm, int T, int b, int64_t *s_scan) {
-    int64_t *s_found = s_scan + THREADS / 32;
-    if (a.batch <= THREADS) {
-      if (threadIdx.x == b) s_found[0] = upto - one;
-    } else {
-      int64_t mine = 0, all;
-      for (int x = threadIdx.x; x < b; x += THREADS) mine += request_tiles(a, x, bm, T);
-      block_scan<THREADS>(mine, s_scan, &all);
-      if (threadIdx.x == 0) s_found[0] = all;
-    }
-    __syncthreads();
-    return s_found[0];
-  }
 };
 
 // One unit's part that falls to a block: key tiles [t0, t1) of its `tiles`.
@@ -167,37 +166,57 @@ struct Segment {
   int b, hk, rt, t0, t1, tiles;
   Request rq;
   int64_t end;           // end of the unit's keys
+  int64_t place;         // of the unit's first tile
 };
 
-// Walks the work tiles [at, stop) of a block, unit by unit.
+// Walks a block's part [at, stop) of the line, unit by unit.
 struct Walk {
   int64_t at, stop, base;
   int b;
   __device__ bool next(const AttnArgs &a, int bm, int T, Segment *s) {
-    if (at >= stop) return false;
-    s->rq = request_of(a, b);
-    int64_t per = tiles_before(a, s->rq, a.row_tiles, bm, T);
-    while (at - base >= a.c.Hkv * per) {
-      base += a.c.Hkv * per;
-      s->rq = request_of(a, ++b);
-      per = tiles_before(a, s->rq, a.row_tiles, bm, T);
+    while (at < stop) {
+      s->rq = request_of(a, b);
+      int64_t per = length_before(a, s->rq, a.row_tiles, bm, T);
+      while (at - base >= a.c.Hkv * per) {
+        base += a.c.Hkv * per;
+        s->rq = request_of(a, ++b);
+        per = length_before(a, s->rq, a.row_tiles, bm, T);
+      }
+      s->b = b;
+      // a 64-bit division only where it is needed
+      s->hk = (at - base) >> 31 ? static_cast<int>((at - base) / per)
+                                : static_cast<int>(static_cast<uint32_t>(at - base) / static_cast<uint32_t>(per));
+      int64_t unit = base + s->hk * per;
+      int weight, len;
+      for (s->rt = 0;; ++s->rt) {
+        s->tiles = unit_tiles(a, s->rq, s->rt, bm, T);
+        weight = tile_weight(a, s->rt);
+        len = a.lead + s->tiles * weight;
+        if (at < unit + len) break;
+        unit += len;
+      }
+      // the tiles that begin in [at, stop)
+      s->place = unit + a.lead;
+      s->t0 = at <= s->place ? 0 : static_cast<int>((at - s->place + weight - 1) / weight);
+      s->t1 = stop <= s->place ? 0
+                               : static_cast<int>(min(static_cast<int64_t>(s->tiles),
+                                                      (stop - s->place + weight - 1) / weight));
+      s->end = tile_end(a, s->rq, s->rt, bm);
+      at = unit + len;
+      if (s->t0 < s->t1) return true;
     }
-    s->b = b;
-    // a 64-bit division only where it is needed
-    s->hk = (at - base) >> 31 ? static_cast<int>((at - base) / per)
-                              : static_cast<int>(static_cast<uint32_t>(at - base) / static_cast<uint32_t>(per));
-    int64_t in_head = (at - base) - s->hk * per;
-    s->rt = 0;
-    s->tiles = unit_tiles(a, s->rq, 0, bm, T);
-    while (in_head >= s->tiles) {
-      in_head -= s->tiles;
-      s->tiles = unit_tiles(a, s->rq, ++s->rt, bm, T);
+    return false;
+  }
+  // what the join has to know of the unit that the block's part begins within
+  __device__ void note_cut(const AttnArgs &a, int64_t chunk, bool any, const Segment &s) {
+    int4 unit = make_int4(-1, 0, 0, 0), blocks = make_int4(0, 0, 0, 0);
+    if (any && s.t0 > 0) {
+      unit = make_int4(s.b, s.hk, s.rt, 0);
+      const int64_t last = s.place + static_cast<int64_t>(s.tiles - 1) * tile_weight(a, s.rt);
+      blocks = make_int4(static_cast<int>(s.place / chunk), static_cast<int>(last / chunk), 0, 0);
     }
-    s->t0 = static_cast<int>(in_head);
-    s->t1 = static_cast<int>(min(static_cast<int64_t>(s->tiles), in_head + (stop - at)));
-    s->end = tile_end(a, s->rq, s->rt, bm);
-    at += s->t1 - s->t0;
-    return true;
+    a.cut[2 * blockIdx.x] = unit;
+    a.cut[2 * blockIdx.x + 1] = blocks;
   }
 };
 
@@ -223,6 +242,7 @@ struct AttnPlan {        // resolved on the host from sizes alone
   size_t smem, bytes;
 };
 constexpr int kWideKeys = 128;         // keys of a tile of dt_cache_wide.cu
+constexpr int kWideLead = 4;           // a unit's begin and end, in half key tiles of a full unit
 constexpr int kFewRows = 16;           // rows up to which the other kernel is used
 bool wide_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p);
 cudaError_t launch_wide(const dt_cache &c, const AttnArgs &a, int dtype, const AttnPlan &p,

@@ -20,7 +20,7 @@
 // While one group takes its weights the tensor cores work for the other. In a unit of a
 // single tile both groups have the same rows, A the even key tiles and B the odd ones,
 // and A or the join adds them up. K and V tiles pass through a ring in the order in which
-// they are consumed (K0 K1 V0 K2 V1 ...), filled by TMA, page by page, through a 128-byte
+// they are consumed, filled by TMA, page by page, through a 128-byte
 // swizzled tensor map; tiles of 8-bit rows land in a raw ring by plain bulk copies and two
 // warpgroups write their bf16 or fp16 values into the operand ring.
 #include <cmath>
@@ -44,7 +44,7 @@ constexpr long long kWaitCycles = 4000000000ll;   // about 2 s
 
 // Warpgroups: two for weights, two (8-bit rows) that convert, one whose warps load, issue
 // the products and find segments. Registers at launch times threads is what setmaxnreg
-// shares out: 640 x 96 >= 256 x 144 + 384 x 56.
+// shares out: 640 x 96 >= 256 x 144 + 384 x 64.
 template <bool QUANT> constexpr int kWThreads = QUANT ? 640 : 384;
 
 struct WideShape {
@@ -240,10 +240,10 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
 
   if (tid == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&ss.full[i], QUANT ? 256 : 1);
+      mbar_init(&ss.full[i], QUANT ? 128 : 1);
       mbar_init(&ss.empty[i], 1);
       mbar_init(&ss.raw_full[i], 1);
-      mbar_init(&ss.raw_empty[i], 256);
+      mbar_init(&ss.raw_empty[i], 128);
     }
     mbar_init(&ss.q_full, 256);
     mbar_init(&ss.q_free, 1);
@@ -307,8 +307,16 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
   };
   // a unit of a single tile of rows
   auto single = [&]() { return w.odd && sg.rt == a.row_tiles - 1; };
-  // operand tiles of a segment of T key tiles, in ring order: K0 K1 V0 K2 V1 ... V(T-1)
-  auto op_tile = [](int op, int T, bool *is_v) {
+  // Operand tiles of a segment of T key tiles in ring order, which is the order in which
+  // they are consumed: K0 V0 K1 V1 ... in a unit of two row tiles, and K0 K1 V0 K2 V1 ...
+  // V(T-1) in a unit of one, where a tile's scores are taken before the weights of the one
+  // before it. (That a tile is consumed then says the same of all before it, on which the
+  // waits below rely: a barrier's parity tells two phases apart, not three.)
+  auto op_tile = [&](int op, int T, bool *is_v) {
+    if (!single()) {
+      *is_v = op & 1;
+      return op >> 1;
+    }
     if (op == 0) { *is_v = false; return 0; }
     if (op == 2 * T - 1) { *is_v = true; return T - 1; }
     *is_v = (op & 1) == 0;
@@ -329,7 +337,6 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
     const uint64_t scale2 = pair(scale, scale);
     const int DH = 64 * w.nblk;
     uint32_t mine = 0, segs_mine = 0, ring_op = 0;  // tiles, segments of this group, ring places
-    int slot = 0;
     while (next_segment()) {
       const uint32_t si = seg - 1;
       const Request rq = sg.rq;
@@ -370,48 +377,56 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       mbar_arrive(&ss.q_full);
       float m = ninf;                       // reference of this thread's row
       uint64_t l2[2] = {0ull, 0ull};        // its sum, in four parts
-      // whether page `lane` of key tile t is there (in lanes that have one)
+      // page number `lane` of key tile t, 0 in lanes that have none, -1 outside the table;
+      // loaded a tile ahead of its use
       const int pages = kW >> a.c.shift;
-      auto page_bad = [&](int t) {
+      auto page_of = [&](int t) {
         const int page = (((sg.t0 + t) * kW) >> a.c.shift) + lane;
-        return t < T && lane < pages && (page << a.c.shift) < end &&
-               !(page < a.c.width && static_cast<uint32_t>(table[page]) < static_cast<uint32_t>(a.c.pages));
+        if (t >= T || lane >= pages || (page << a.c.shift) >= end) return 0;
+        return page < a.c.width ? table[page] : -1;
       };
-      bool bad = page_bad(tfirst);
+      int entry = page_of(tfirst);
 
 #pragma unroll 1
       for (int t = tfirst; t < T; t += tstep, ++mine) {
         const int j0 = (sg.t0 + t) * kW;
-        const uint32_t bad_pages = __ballot_sync(kFull, bad);
+        const uint32_t bad_pages =
+            __ballot_sync(kFull, static_cast<uint32_t>(entry) >= static_cast<uint32_t>(a.c.pages));
         const bool masked = bad_pages != 0u || j0 + kW > whole_end;
-        bad = page_bad(t + tstep);
+        entry = page_of(t + tstep);
         uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};     // keys of the tile that the row sees
         if (masked) {
-          // the warp's rows' tokens one after another, a lane a key
-          const int lo = __shfl_sync(kFull, tok, 0), hi = __shfl_sync(kFull, tok, 31);
+          // the warp's rows' tokens, four at a time, a lane a key of each of four words
+          const int lo = __shfl_sync(kFull, tok, 0), hi = min(__shfl_sync(kFull, tok, 31), rq.count - 1);
+          const int pre0 = static_cast<int>(rq.pre);
+          bool there[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int j = j0 + 32 * q + lane, tr = j - static_cast<int>(rq.pre);
-            const bool there = j < end && !((bad_pages >> ((32 * q + lane) >> a.c.shift)) & 1u);
-            see[q] = __ballot_sync(kFull, there);
-            if (j0 + 32 * q + 32 <= pre) continue;        // all before the tree
-            const uint32_t any = see[q];
-            const bool tree = there && tr >= 0 && tr < rq.count;
-            for (int i = lo; i <= hi; i += 4) {
-              bool v[4];
+            there[q] = j0 + 32 * q + lane < end && !((bad_pages >> ((32 * q + lane) >> a.c.shift)) & 1u);
+            see[q] = __ballot_sync(kFull, there[q]);
+          }
+#pragma unroll 1
+          for (int i = lo; i <= hi; i += 4) {
+            uint32_t v = 0u;      // bit 4 q + e: key of word q seen by token i + e
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int tr = j0 + 32 * q + lane - pre0;
+              const bool tree = there[q] && tr >= 0 && tr < rq.count;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const bool in = tree && i + e < rq.count;
-                v[e] = (there && tr < 0) ||
-                       (in && (a.mask ? a.mask[(static_cast<int64_t>(sg.b) * a.n + i + e) * a.n + tr] != 0
-                                      : tr <= i + e));
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t b = __ballot_sync(kFull, v[e]);
-                if (tok == i + e) see[q] = any & b;
+                bool x = there[q] && tr < 0;
+                if (tree && i + e <= hi)
+                  x = a.mask ? a.mask[(static_cast<int64_t>(sg.b) * a.n + i + e) * a.n + tr] != 0 : tr <= i + e;
+                v |= x ? 1u << (4 * q + e) : 0u;
               }
             }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t x = __ballot_sync(kFull, (v >> (4 * q + e)) & 1u);
+                if (tok == i + e) see[q] = x;
+              }
           }
           if (!live) see[0] = see[1] = see[2] = see[3] = 0u;
         }
@@ -421,10 +436,10 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
         if (masked && (alt || X == 0)) {
           // V rows that nobody sees become zeros, and so do values that are not finite in
           // tree rows (zero times them is NaN): the rows that see those get them below. The
-          // thread takes the row of key gt. (The slot's tile before this one is consumed by
-          // now, so the parity waited for is this tile's: S of tile t is complete, and with
-          // it every product issued before, all but those of V(t - 1) and later.)
-          const uint32_t vop = ring_op + (t < T - 1 ? 2 * t + 2 : 2 * T - 1);
+          // thread takes the row of key gt. (S of tile t is complete, and with it every
+          // product issued before; the ring has at least three places, so the tile that was
+          // in this one is consumed and the parity waited for is this tile's.)
+          const uint32_t vop = ring_op + (!alt ? 2 * t + 1 : t < T - 1 ? 2 * t + 2 : 2 * T - 1);
           const uint32_t turn = vop / w.ring, vslot = vop - turn * w.ring;
           wait(&ss.full[vslot], turn & 1);
           unsigned char *v = sm + vslot * tile_bytes + gt * 128;
@@ -568,7 +583,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles, both = alt && whole;
       const bool leave = !whole || (both && X == 1);      // a part for the join or for A
       float *pp = a.part + (both ? (4ll * a.grid + 2 * blockIdx.x + (si & 1)) * a.slot
-                                 : ((2ll * blockIdx.x + slot) * 2 + (alt ? X : 0)) * a.slot);
+                                 : ((2ll * blockIdx.x + (sg.t0 > 0 ? 0 : 1)) * 2 + (alt ? X : 0)) * a.slot);
       if (leave && real) {
         pp[bm * DH + col0 + gt] = m;
         pp[bm * (DH + 1) + col0 + gt] = sum;
@@ -641,64 +656,66 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       tmem_fence_before();
       if (both && X == 1) pair_sync();
       ring_op += 2 * T;
-      slot = 1;
     }
   } else if (QUANT && warp < 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     {
       // ------------------------------- 8-bit rows to the operand tiles
-      // two threads a row
-      const int ct = tid & 127, half = (tid >> 7) & 1;
+      // one warpgroup the K tiles, the other the V tiles: a tile's waits and fences pass
+      // while the other is converted
+      const int ct = tid & 127;
+      const bool mine_v = (tid >> 7) & 1;
       Place r = {0, 0}, o = {0, 1};     // (an operand place starts free)
       bool stop = false;
       while (!stop && next_segment()) {
         const int T = sg.t1 - sg.t0;
 #pragma unroll 1
         for (int x = 0; x < 2 * T; ++x) {
-          const uint32_t rs = r.at, os = o.at;
-          if (!wait(&ss.raw_full[rs], r.parity) || !wait(&ss.empty[os], o.parity)) {
+          bool is_v;
+          op_tile(x, T, &is_v);
+          const Place rp = r, op = o;
+          const uint32_t rs = rp.at, os = op.at;
+          r.step(w.raw);
+          o.step(w.ring);
+          if (is_v != mine_v) continue;
+          // First the operand's place: it is free once the tile three before this one is
+          // consumed, which has been converted then, and all before it, so that the raw
+          // place's phase is this tile's (there are at least three raw places).
+          if (!wait(&ss.empty[os], op.parity) || !wait(&ss.raw_full[rs], rp.parity)) {
             stop = true;
             break;
           }
-          r.step(w.raw);
-          o.step(w.ring);
           const unsigned char *raw = sm + w.off_raw + rs * w.raw_bytes;
-          // Two threads have a row (its scale once), 16 codes at a time, chunks starting at a
+          // A thread has a row (its scale once), 16 codes at a time, chunks starting at a
           // place of the row's own so that eight lanes' chunks lie in eight bank groups, in
           // the raw tile and, swizzled as K's and V's always, in the operand tile.
           const uint32_t E = raw[kW * dh + ct];
           const unsigned char *src = raw + ct * dh;
           unsigned char *row = sm + os * tile_bytes + ct * 128;
-          uint4 q[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = (4 * half + i + ct) & 7;
-            if (c < dh >> 4) q[i] = *reinterpret_cast<const uint4 *>(src + c * 16);
-          }
           if (DT == DT_BF16 && (E <= 134u || E == 255u)) {
             // 2^(E - 127) 2^120 as a bf16 pair
             uint32_t mul = E == 255u ? 0x7fc0u : (E + 120u) << 7;
             mul |= mul << 16;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = (4 * half + i + ct) & 7;
+#pragma unroll 4
+            for (int i = 0; i < 8; ++i) {
+              const int c = (i + ct) & 7;
               if (c >= dh >> 4) continue;
-              const uint32_t qw[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                y[2 * e] = codes_bf16x2(spread_codes<0>(qw[e]), mul);
-                y[2 * e + 1] = codes_bf16x2(spread_codes<1>(qw[e]), mul);
-              }
+              const uint4 q = *reinterpret_cast<const uint4 *>(src + c * 16);
+              const uint32_t y[8] = {
+                  codes_bf16x2(spread_codes<0>(q.x), mul), codes_bf16x2(spread_codes<1>(q.x), mul),
+                  codes_bf16x2(spread_codes<0>(q.y), mul), codes_bf16x2(spread_codes<1>(q.y), mul),
+                  codes_bf16x2(spread_codes<0>(q.z), mul), codes_bf16x2(spread_codes<1>(q.z), mul),
+                  codes_bf16x2(spread_codes<0>(q.w), mul), codes_bf16x2(spread_codes<1>(q.w), mul)};
               put_operand(row, ct, c, y);
             }
           } else {
             const float sc = row_scale(E);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = (4 * half + i + ct) & 7;
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) {
+              const int c = (i + ct) & 7;
               if (c >= dh >> 4) continue;
-              const uint32_t qw[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+              const uint4 q = *reinterpret_cast<const uint4 *>(src + c * 16);
+              const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
               uint32_t y[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -715,7 +732,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       }
     }
   } else {
-    if (QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (QUANT) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     const int role = warp - (QUANT ? 16 : 8);
     if (role == 0) {
       // ---------------------------------------------------------- loads
@@ -811,7 +828,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       };
       while (!stop && next_segment()) {
         const bool alt = single();
-        const int T = sg.t1 - sg.t0, ng = alt ? 1 : 2;
+        const int T = sg.t1 - sg.t0;
         Place k = op, v;
         op.step(w.ring);
         if (!wait_warp(&ss.q_full, (seg - 1) & 1) || !wait_warp(&ss.full[k.at], k.parity)) break;
@@ -822,11 +839,11 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
         // group B's, already) are issued in step t
         for (int t = 0; t < T && !stop; ++t) {
           const bool next = t + 1 < T;
-          k = op;
-          if (next) op.step(w.ring);
-          v = op;
-          op.step(w.ring);
           if (alt) {
+            k = op;
+            if (next) op.step(w.ring);
+            v = op;
+            op.step(w.ring);
             // S of tile t + 1 has a group of its own: before the weights of tile t
             if (next) {
               if (!wait_warp(&ss.full[k.at], k.parity)) { stop = true; break; }
@@ -839,7 +856,11 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
             tmem_fence_after();
             values(X, v.at, t >= 2, true, t + 2 >= T);
           } else {
-            for (int X = 0; X < ng; ++X) {
+            v = op;
+            op.step(w.ring);
+            k = op;
+            if (next) op.step(w.ring);
+            for (int X = 0; X < 2; ++X) {
               if (!wait_warp(&ss.p_full[X], (X ? taken_b++ : taken_a++) & 1) ||
                   (X == 0 && !wait_warp(&ss.full[v.at], v.parity)) ||
                   (X == 0 && next && !wait_warp(&ss.full[k.at], k.parity))) { stop = true; break; }
@@ -856,6 +877,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       bool more = true;
       for (uint32_t i = 0; more; ++i) {
         more = !*fail && walk.next(a, bm, kW, &found);
+        if (i == 0) walk.note_cut(a, sch.chunk, more, found);
         if (!more) found.b = -1;
         // (after a failure the others go through their segments without waiting)
         if (!mbar_wait_cycles(&ss.seg_empty[i % kSegs], ((i / kSegs) & 1) ^ 1)) *fail = 1;
@@ -943,7 +965,7 @@ bool wide_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p) 
     p->ring = 3;
     p->raw = (room - p->ring * tile) / w.raw_bytes;
     if (p->raw > kMaxRing) p->raw = kMaxRing;
-    if (p->raw < 2) return false;
+    if (p->raw < 3) return false;
   } else {
     p->ring = room / tile < kMaxRing ? room / tile : kMaxRing;
     if (p->ring < 3) return false;

@@ -535,28 +535,40 @@ def adaptive_budget(out: dict, N: int, c_fixed: float, c_node: float, counts=Non
 _TYPE16 = {torch.bfloat16: BF16, torch.float16: F16}
 
 
-def _heads(t, what: str, heads=None, n=None, like=None) -> DtHeads:
-    """A [batch][heads][n][dh] view (last dimension dense) as a dt_heads."""
-    if t.dim() != 4 or t.stride(3) != 1:
-        raise ValueError(f"{what} must be a [batch][heads][n][dh] tensor with a dense last dimension")
-    if t.dtype not in _TYPE16 or not t.is_cuda:
-        raise ValueError(f"{what} must be a bfloat16 or float16 CUDA tensor")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device or
-                             t.shape[0] != like.shape[0] or t.shape[2:] != like.shape[2:]):
-        raise ValueError(f"{what} does not match the other tensor in type, device or shape")
-    if (heads is not None and t.shape[1] != heads) or (n is not None and t.shape[2] != n):
-        raise ValueError(f"{what} has {t.shape[1]} heads of {t.shape[2]} rows")
+def _shape(t, what: str):
+    """Shape of a [batch][heads][n][dh] tensor, its C type and device number. (These calls
+    run once a layer, so their checks are few and plain: a launch takes 2 us.)"""
+    shape, dtype, dev = t.shape, _TYPE16.get(t.dtype), t.get_device()
+    if len(shape) != 4 or dtype is None or dev < 0:
+        raise ValueError(f"{what} must be a [batch][heads][n][dh] bfloat16 or float16 CUDA tensor")
+    return shape, dtype, dev
+
+
+def _heads(t, what: str, shape, dtype, dev) -> DtHeads:
+    """A view of that shape, C type and device (last dimension dense) as a dt_heads."""
     s = t.stride()
-    return DtHeads(t.data_ptr(), t.shape[1], s[0], s[1], s[2])
+    if t.shape != shape or _TYPE16.get(t.dtype) != dtype or t.get_device() != dev or s[3] != 1:
+        raise ValueError(f"{what} must be of shape {tuple(shape)} with a dense last dimension, and of "
+                         "the other tensors' type and device")
+    return DtHeads(t.data_ptr(), shape[1], s[0], s[1], s[2])
 
 
-def _ints(t, what: str, shape, device):
+def _ints(t, what: str, shape, dev):
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != torch.int32 or not t.is_contiguous() or \
-            t.device != device:
-        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+    if t.shape != shape or t.dtype != torch.int32 or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on the "
+                         "other tensors' device")
     return t.data_ptr()
+
+
+def _dense_like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _raw_stream(stream, dev):
+    """The stream's handle: the current one of the tensors' device by default."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 class Rotary:
@@ -586,20 +598,22 @@ def rotary(rot: Rotary, positions, q, k=None, q_out=None, k_out=None, gradient=F
     positions [batch][n] int32. ``gradient``: the transposed rotation. Outputs
     default to new dense tensors and may be the inputs. Returns (q_out, k_out), or
     q_out alone without k."""
-    batch, _, n, dh = q.shape
-    x0 = _heads(q, "q")
+    shape, dtype, dev = _shape(q, "q")
+    batch, _, n, dh = shape
+    x0 = _heads(q, "q", shape, dtype, dev)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    o0 = _heads(q_out, "q_out", q.shape[1], like=q)
+        q_out = _dense_like(q)
+    o0 = _heads(q_out, "q_out", shape, dtype, dev)
     x1 = o1 = None
     if k is not None:
-        x1 = _heads(k, "k", like=q)
+        kshape = torch.Size((batch, k.shape[1], n, dh))
+        x1 = _heads(k, "k", kshape, dtype, dev)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        o1 = _heads(k_out, "k_out", k.shape[1], like=q)
-    _check(lib().dt_rotary(rot._struct, _ints(positions, "positions", (batch, n), q.device), batch,
-                           n, dh, _TYPE16[q.dtype], x0, o0, x1, o1, int(gradient),
-                           _stream(stream)), "dt_rotary")
+            k_out = _dense_like(k)
+        o1 = _heads(k_out, "k_out", kshape, dtype, dev)
+    _check(lib().dt_rotary(rot._struct, _ints(positions, "positions", (batch, n), dev), batch, n, dh,
+                           dtype, x0, o0, x1, o1, int(gradient), _raw_stream(stream, dev)),
+           "dt_rotary")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -628,10 +642,11 @@ class PagedCache:
             raise ValueError("table must be [batch][width]")
         self.k, self.v, self.table, self.k_exp, self.v_exp = k, v, table, k_exp, v_exp
         self.device, self.batch = k.device, table.shape[0]
-        _ints(table, "table", table.shape, k.device)
+        self._dev = k.get_device()
+        _ints(table, "table", table.shape, self._dev)
         self.status = torch.zeros(self.batch, dtype=torch.int32, device=k.device) \
             if status is None else status
-        _ints(self.status, "status", (self.batch,), k.device)
+        _ints(self.status, "status", (self.batch,), self._dev)
         pages, self.Hkv, page, self.dh = k.shape
         self._struct = DtCache(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp), _ptr(table),
                                _ptr(self.status), pages, page, self.Hkv, self.dh, kinds[k.dtype],
@@ -655,31 +670,27 @@ class PagedCache:
                                                       for b, c in bad))
 
 
-def _cache_rows(cache: PagedCache, t, what: str, n=None, like=None) -> DtHeads:
-    if t.shape[0] != cache.batch or t.shape[-1] != cache.dh or t.device != cache.device:
-        raise ValueError(f"{what} does not match the cache's batch, head size or device")
-    return _heads(t, what, cache.Hkv, n, like)
-
-
 def cache_write(cache: PagedCache, k, v, first, counts=None, rotary: Rotary | None = None,
                 positions=None, q=None, q_out=None, stream=None):
     """dt_cache_write: rows of k and v [batch][Hkv][n][dh] to rows first[b].. of the
     cache, k turned by ``rotary`` at ``positions``; with q, returns its turned rows."""
-    n = k.shape[2]
-    hk, hv = _cache_rows(cache, k, "k"), _cache_rows(cache, v, "v", like=k)
+    shape, dtype, dev = _shape(k, "k")
+    n, b = shape[2], (cache.batch,)
+    if shape != (cache.batch, cache.Hkv, n, cache.dh) or dev != cache._dev:
+        raise ValueError("k does not match the cache's batch, heads, head size or device")
+    hk, hv = _heads(k, "k", shape, dtype, dev), _heads(v, "v", shape, dtype, dev)
     hq = ho = None
     if q is not None:
-        hq = _heads(q, "q", like=k)
+        qshape = torch.Size((cache.batch, q.shape[1], n, cache.dh))
+        hq = _heads(q, "q", qshape, dtype, dev)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        ho = _heads(q_out, "q_out", q.shape[1], like=k)
-    b = (cache.batch,)
-    _check(lib().dt_cache_write(cache._struct, hk, hv, n, _TYPE16[k.dtype],
-                                _ints(first, "first", b, cache.device),
-                                _ints(counts, "counts", b, cache.device),
+            q_out = _dense_like(q)
+        ho = _heads(q_out, "q_out", qshape, dtype, dev)
+    _check(lib().dt_cache_write(cache._struct, hk, hv, n, dtype, _ints(first, "first", b, dev),
+                                _ints(counts, "counts", b, dev),
                                 rotary._struct if rotary is not None else None,
-                                _ints(positions, "positions", (cache.batch, n), cache.device),
-                                hq, ho, _stream(stream)), "dt_cache_write")
+                                _ints(positions, "positions", (cache.batch, n), dev),
+                                hq, ho, _raw_stream(stream, dev)), "dt_cache_write")
     return q_out
 
 
@@ -690,29 +701,28 @@ def cache_read(cache: PagedCache, n: int, first, counts=None, dtype=None, k_out=
     type, bfloat16 for an 8-bit cache."""
     if dtype is None:
         dtype = cache.k.dtype if cache.k.dtype in _TYPE16 else torch.bfloat16
-    shape = (cache.batch, cache.Hkv, n, cache.dh)
+    shape, dev = torch.Size((cache.batch, cache.Hkv, n, cache.dh)), cache._dev
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=cache.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=cache.device)
-    hk = _cache_rows(cache, k_out, "k_out", n)
-    hv = _cache_rows(cache, v_out, "v_out", n, like=k_out)
+        v_out = torch.empty(shape, dtype=k_out.dtype, device=cache.device)
+    ctype = _shape(k_out, "k_out")[1]
+    hk, hv = _heads(k_out, "k_out", shape, ctype, dev), _heads(v_out, "v_out", shape, ctype, dev)
     b = (cache.batch,)
-    _check(lib().dt_cache_read(cache._struct, n, _TYPE16[k_out.dtype],
-                               _ints(first, "first", b, cache.device),
-                               _ints(counts, "counts", b, cache.device), hk, hv,
-                               _stream(stream)), "dt_cache_read")
+    _check(lib().dt_cache_read(cache._struct, n, ctype, _ints(first, "first", b, dev),
+                               _ints(counts, "counts", b, dev), hk, hv, _raw_stream(stream, dev)),
+           "dt_cache_read")
     return k_out, v_out
 
 
 def cache_commit(cache: PagedCache, first, path, lengths, n: int, stream=None):
     """dt_cache_commit: cache row first[b] + path[b][j] to row first[b] + j for
     j < lengths[b], in place; ``n`` is the trees' rows."""
-    b = (cache.batch,)
-    _check(lib().dt_cache_commit(cache._struct, _ints(first, "first", b, cache.device),
-                                 _ints(path, "path", (cache.batch, path.shape[-1]), cache.device),
-                                 _ints(lengths, "lengths", b, cache.device), path.shape[-1], int(n),
-                                 _stream(stream)), "dt_cache_commit")
+    b, dev, width = (cache.batch,), cache._dev, path.shape[-1]
+    _check(lib().dt_cache_commit(cache._struct, _ints(first, "first", b, dev),
+                                 _ints(path, "path", (cache.batch, width), dev),
+                                 _ints(lengths, "lengths", b, dev), width, int(n),
+                                 _raw_stream(stream, dev)), "dt_cache_commit")
 
 
 def cache_attention_workspace(cache: PagedCache, H: int, n: int):
@@ -729,24 +739,26 @@ def cache_attention(cache: PagedCache, q, prefix_len, mask=None, counts=None, sc
     [batch][n][n] uint8 or causally (mask None). ``workspace`` (of
     cache_attention_workspace) is allocated for the call when None. Returns out,
     by default a new dense tensor of q's shape and type."""
-    batch, H, n, dh = q.shape
-    if batch != cache.batch or dh != cache.dh or q.device != cache.device:
+    shape, dtype, dev = _shape(q, "q")
+    batch, H, n, dh = shape
+    if batch != cache.batch or dh != cache.dh or dev != cache._dev:
         raise ValueError("q does not match the cache's batch, head size or device")
-    if mask is not None and (tuple(mask.shape) != (batch, n, n) or not mask.is_contiguous() or
+    if mask is not None and (mask.shape != (batch, n, n) or not mask.is_contiguous() or
                              mask.dtype not in (torch.uint8, torch.bool) or
-                             mask.device != q.device):
+                             mask.get_device() != dev):
         raise ValueError(f"mask must be a contiguous uint8 tensor of shape {(batch, n, n)}")
-    hq = _heads(q, "q")
+    hq = _heads(q, "q", shape, dtype, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ho = _heads(out, "out", H, like=q)
+        out = _dense_like(q)
+    ho = _heads(out, "out", shape, dtype, dev)
     if workspace is None:
         workspace = cache_attention_workspace(cache, H, n)
-    _check(lib().dt_cache_attention(cache._struct, hq, n, _TYPE16[q.dtype],
-                                    _ints(prefix_len, "prefix_len", (batch,), q.device),
-                                    _ints(counts, "counts", (batch,), q.device), _ptr(mask),
-                                    float(dh ** -0.5 if scale is None else scale), ho,
-                                    workspace.data_ptr(),
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    _check(lib().dt_cache_attention(cache._struct, hq, n, dtype,
+                                    _ints(prefix_len, "prefix_len", (batch,), dev),
+                                    _ints(counts, "counts", (batch,), dev), _ptr(mask),
+                                    dh ** -0.5 if scale is None else scale, ho, workspace.data_ptr(),
                                     workspace.numel() * workspace.element_size(),
-                                    _stream(stream)), "dt_cache_attention")
+                                    _raw_stream(stream, dev)), "dt_cache_attention")
     return out

@@ -415,10 +415,9 @@ template <int DT, bool QUANT, int DH, int WK>
 cudaError_t launch_narrow(const AttnArgs &a, cudaStream_t st) {
   constexpr int BM = 64 / WK;
   const int smem = narrow_smem<DH, QUANT>(BM);
-  auto *kernel = cache_attention_kernel<DT, QUANT, DH, WK>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem<cache_attention_kernel<DT, QUANT, DH, WK>>();
   if (e != cudaSuccess) return e;
-  kernel<<<a.grid, kNThreads, smem, st>>>(a);
+  cache_attention_kernel<DT, QUANT, DH, WK><<<a.grid, kNThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -14,6 +14,8 @@
 // block order: the result does not depend on timing.
 #pragma once
 
+#include <atomic>
+
 #include "dt_cache.cuh"
 
 namespace dt {
@@ -241,6 +243,25 @@ struct AttnPlan {        // resolved on the host from sizes alone
   int odd, ring, raw;    // dt_cache_wide.cu: the last unit is half a one; operand, raw tiles
   size_t smem, bytes;
 };
+// Opts a kernel into the device's whole shared memory, once a device (the call costs about
+// as much as a launch; always the same size, so that calls on several threads agree).
+template <auto Kernel>
+cudaError_t allow_smem() {
+  static std::atomic<bool> allowed[64] = {};
+  int dev = 0, most = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && allowed[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  cudaFuncAttributes f;
+  e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&f, Kernel);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             most - static_cast<int>(f.sharedSizeBytes));
+  if (e == cudaSuccess && dev < 64) allowed[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 constexpr int kWideKeys = 128;         // keys of a tile of dt_cache_wide.cu
 constexpr int kWideLead = 4;           // a unit's begin and end, in half key tiles of a full unit
 constexpr int kFewRows = 16;           // rows up to which the other kernel is used

@@ -939,11 +939,9 @@ WideShape wide_shape(const dt_cache &c, const AttnPlan &p) {
 template <int DT, bool QUANT>
 cudaError_t go(const AttnArgs &a, const WideShape &w, const AttnPlan &p, const CUtensorMap &k,
                const CUtensorMap &v, cudaStream_t st) {
-  auto *kernel = cache_attention_wide_kernel<DT, QUANT>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(p.smem));
+  const cudaError_t e = allow_smem<cache_attention_wide_kernel<DT, QUANT>>();
   if (e != cudaSuccess) return e;
-  kernel<<<a.grid, kWThreads<QUANT>, p.smem, st>>>(a, w, k, v);
+  cache_attention_wide_kernel<DT, QUANT><<<a.grid, kWThreads<QUANT>, p.smem, st>>>(a, w, k, v);
   return cudaGetLastError();
 }
 

@@ -1,6 +1,7 @@
 // dt_cache_attn.cu -- attention of tree, chain and single-token rows over the paged
-// cache: the kernel for any number of rows, the launch that joins partial results,
-// and the entry points.
+// cache: the kernel for head sizes above 128 (whose operands do not fit the others'
+// tiles) and pools that a tensor map cannot describe, the launch that joins partial
+// results, and the entry points.
 //
 // One pass over the keys with a running maximum: per key tile S = Q K^T, x = S scale
 // log2(e) (-inf where the row does not see the key), m' = max(m, max x),
@@ -435,13 +436,6 @@ cudaError_t launch_bm(const AttnArgs &a, int bm, cudaStream_t st) {
                     : launch_narrow<DT, QUANT, DH, 1>(a, st);
 }
 
-template <int DT, bool QUANT>
-cudaError_t launch_dh(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
-  return p.dhp == 64    ? launch_bm<DT, QUANT, 64>(a, p.bm, st)
-         : p.dhp == 128 ? launch_bm<DT, QUANT, 128>(a, p.bm, st)
-                        : launch_bm<DT, QUANT, 256>(a, p.bm, st);
-}
-
 int64_t slot_floats(const AttnPlan &p) {
   return (static_cast<int64_t>(p.bm) * (p.dhp + 2) + 3) / 4 * 4;
 }
@@ -457,12 +451,12 @@ int attn_plan(const dt_cache &c, int H, int n, AttnPlan *p) {
   if (rc) return rc;
   const int64_t rows = static_cast<int64_t>(n) * (H / c.Hkv);
   *p = {};
-  if (!wide_plan(c, rows, sms, smem, p)) {
-    p->wide = 0;
-    p->dhp = c.dh <= 64 ? 64 : c.dh <= 128 ? 128 : 256;
+  if (!few_plan(c, rows, sms, smem, p) && !wide_plan(c, rows, sms, smem, p)) {
+    *p = {};
+    p->dhp = 256;
     p->bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     p->row_tiles = static_cast<int>((rows + p->bm - 1) / p->bm);
-    p->grid = sms * (p->dhp == 256 ? 1 : 2);
+    p->grid = sms;
   }
   p->bytes = static_cast<size_t>(p->grid) * (2 * sizeof(int4) + 6 * slot_floats(*p) * sizeof(float));
   return DT_OK;
@@ -510,15 +504,17 @@ int dt_cache_attention(const dt_cache *c, const dt_heads *q, int n, int dtype,
   a.row_tiles = p.row_tiles; a.grid = p.grid; a.min_tiles = 2;
   a.slot = dt::slot_floats(p);
   a.odd = p.odd;
-  a.weight = p.wide ? 2 : 1;
-  a.last_weight = p.wide && p.odd ? 1 : a.weight;
-  a.lead = p.wide ? dt::kWideLead : 1;
+  const bool wide = p.kind == dt::AttnPlan::kWide;
+  a.weight = wide ? 2 : 1;
+  a.last_weight = wide && p.odd ? 1 : a.weight;
+  a.lead = wide ? dt::kWideLead : 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool quant = c->dtype == DT_E4M3;
   cudaError_t e =
-      p.wide ? dt::launch_wide(*c, a, dtype, p, st)
-      : dtype == DT_BF16 ? (quant ? dt::launch_dh<DT_BF16, true>(a, p, st) : dt::launch_dh<DT_BF16, false>(a, p, st))
-                         : (quant ? dt::launch_dh<DT_F16, true>(a, p, st) : dt::launch_dh<DT_F16, false>(a, p, st));
+      wide ? dt::launch_wide(*c, a, dtype, p, st)
+      : p.kind == dt::AttnPlan::kFew ? dt::launch_few(*c, a, dtype, p, st)
+      : dtype == DT_BF16 ? (quant ? dt::launch_bm<DT_BF16, true, 256>(a, p.bm, st) : dt::launch_bm<DT_BF16, false, 256>(a, p.bm, st))
+                         : (quant ? dt::launch_bm<DT_F16, true, 256>(a, p.bm, st) : dt::launch_bm<DT_F16, false, 256>(a, p.bm, st));
   if (e == cudaSuccess)
     e = dtype == DT_BF16 ? dt::launch_join<DT_BF16>(a, p, st) : dt::launch_join<DT_F16>(a, p, st);
   return e == cudaSuccess ? DT_OK : DT_ERR_CUDA;

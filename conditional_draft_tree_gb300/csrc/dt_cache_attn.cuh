@@ -15,6 +15,7 @@
 #pragma once
 
 #include <atomic>
+#include <cuda.h>
 
 #include "dt_cache.cuh"
 
@@ -238,9 +239,9 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 struct AttnPlan {        // resolved on the host from sizes alone
-  int wide;              // dt_cache_wide.cu, else the mma.sync kernel
+  enum { kAny, kWide, kFew } kind;     // dt_cache_attn.cu, dt_cache_wide.cu, dt_cache_few.cu
   int bm, dhp, row_tiles, grid;
-  int odd, ring, raw;    // dt_cache_wide.cu: the last unit is half a one; operand, raw tiles
+  int odd, ring, raw;    // dt_cache_wide.cu: the last unit is half a one; tiles, raw tiles in flight
   size_t smem, bytes;
 };
 // Opts a kernel into the device's whole shared memory, once a device (the call costs about
@@ -264,8 +265,12 @@ cudaError_t allow_smem() {
 
 constexpr int kWideKeys = 128;         // keys of a tile of dt_cache_wide.cu
 constexpr int kWideLead = 4;           // a unit's begin and end, in half key tiles of a full unit
-constexpr int kFewRows = 16;           // rows up to which the other kernel is used
+constexpr int kFewRows = 16, kFewKeys = 64;   // rows of dt_cache_few.cu, keys of its tiles
 bool wide_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p);
+bool few_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p);
+bool page_map(const dt_cache &c, const void *base, int box_rows, CUtensorMap *map);
+cudaError_t launch_few(const dt_cache &c, const AttnArgs &a, int dtype, const AttnPlan &p,
+                       cudaStream_t st);
 cudaError_t launch_wide(const dt_cache &c, const AttnArgs &a, int dtype, const AttnPlan &p,
                         cudaStream_t st);
 

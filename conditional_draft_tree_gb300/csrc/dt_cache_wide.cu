@@ -232,6 +232,10 @@ __global__ void __launch_bounds__(kWThreads<QUANT>, 1)
 cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ WideShape w,
                             const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap) {
+  // fp16 rows over 8-bit ones: V's values (as many as 2^137 apart) in bf16, where they are
+  // exact, against the weights in two bf16 terms; K's in fp16, rounded as dt_cache_read does
+  constexpr bool TWO = QUANT && DT == DT_F16;
+  constexpr int VDT = TWO ? DT_BF16 : DT;
   extern __shared__ __align__(1024) unsigned char sm[];
   Small &ss = *reinterpret_cast<Small *>(sm + w.off_small);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -330,8 +334,8 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + 128 * X + lane_off, t_o = tmem + 256 + 128 * X + lane_off;
     // fp16 weights are scaled by 2^8, so that small ones stay normal numbers
-    constexpr float kShift = DT == DT_F16 ? 8.0f : 0.0f;
-    constexpr float kGrow = DT == DT_F16 ? 4.0f : 8.0f;
+    constexpr float kShift = VDT == DT_F16 ? 8.0f : 0.0f;
+    constexpr float kGrow = VDT == DT_F16 ? 4.0f : 8.0f;
     const float scale = fabsf(a.scale_log2);
     const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;   // the scale's sign goes to Q
     const uint64_t scale2 = pair(scale, scale);
@@ -453,9 +457,9 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
 #pragma unroll 4
             for (int c = 0; c < 8 * w.nblk; ++c) {
               const uint4 x = *reinterpret_cast<const uint4 *>(v + (c >> 3) * kBlk + (((c & 7) ^ (gt & 7)) << 4));
-              top = top_abs<DT>(top_abs<DT>(top, x.x), top_abs<DT>(x.y, top_abs<DT>(x.z, x.w)));
+              top = top_abs<VDT>(top_abs<VDT>(top, x.x), top_abs<VDT>(x.y, top_abs<VDT>(x.z, x.w)));
             }
-            const uint32_t ex = DT == DT_BF16 ? 0x7f80u : 0x7c00u;
+            const uint32_t ex = VDT == DT_BF16 ? 0x7f80u : 0x7c00u;
             if ((top & ex) == ex || ((top >> 16) & ex) == ex) {
 #pragma unroll 1
               for (int c = 0; c < 64 * w.nblk; ++c) {
@@ -537,6 +541,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
           const float nm = m == ninf ? 0.0f : kShift - m;
           const uint64_t nm2 = pair(nm, nm);
           float s0[16], s1[16];
+          uint32_t lo[TWO ? 64 : 1];    // second terms, until all scores are read
           tmem_ld16(t_s, s0);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -554,11 +559,23 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
               p0 = fast_exp2(p0);
               p1 = fast_exp2(p1);
               l2[e & 1] = add2(l2[e & 1], pair(p0, p1));
-              y[e] = Half16<DT>::pack(p0, p1);
+              y[e] = Half16<VDT>::pack(p0, p1);
+              if (TWO) {
+                const float2 hi = Half16<VDT>::unpack(y[e]);
+                lo[TWO ? 8 * c + e : 0] = Half16<VDT>::pack(p0 - hi.x, p1 - hi.y);
+              }
             }
             // (the next chunk's scores are being read: columns 16 c + 16 on, past 8 c + 7)
             tmem_st8(t_s + 8 * c, y);
           }
+          if (TWO)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = lo[TWO ? 8 * c + e : 0];
+              tmem_st8(t_s + 64 + 8 * c, y);
+            }
           tmem_wait_st();
         }
         tmem_fence_before();
@@ -692,7 +709,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
           const uint32_t E = raw[kW * dh + ct];
           const unsigned char *src = raw + ct * dh;
           unsigned char *row = sm + os * tile_bytes + ct * 128;
-          if (DT == DT_BF16 && (E <= 134u || E == 255u)) {
+          if ((DT == DT_BF16 || mine_v) && (E <= 134u || E == 255u)) {
             // 2^(E - 127) 2^120 as a bf16 pair
             uint32_t mul = E == 255u ? 0x7fc0u : (E + 120u) << 7;
             mul |= mul << 16;
@@ -719,8 +736,8 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
               uint32_t y[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                y[2 * e] = e4m3_to16<DT>(qw[e] & 0xffffu, sc);
-                y[2 * e + 1] = e4m3_to16<DT>(qw[e] >> 16, sc);
+                y[2 * e] = mine_v ? e4m3_to16<VDT>(qw[e] & 0xffffu, sc) : e4m3_to16<DT>(qw[e] & 0xffffu, sc);
+                y[2 * e + 1] = mine_v ? e4m3_to16<VDT>(qw[e] >> 16, sc) : e4m3_to16<DT>(qw[e] >> 16, sc);
               }
               put_operand(row, ct, c, y);
             }
@@ -793,7 +810,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
       // uniform values that need no move for each MMA.
       const uint32_t base = smem_u32(sm);
       const uint64_t k0 = desc128(base, 16, 1024), v0 = desc128(base, kBlk, 1024);
-      const uint32_t id_s = idesc16<DT>(kW, false), id_o = idesc16<DT>(dh, true);
+      const uint32_t id_s = idesc16<DT>(kW, false), id_o = idesc16<VDT>(dh, true);
       const int ks = dh >> 4;
       Place op = {0, 0};               // the next operand tile
       uint32_t taken_a = 0, taken_b = 0;      // tiles of each group
@@ -821,6 +838,10 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
 #pragma unroll
           for (int k = 0; k < kW / 16; ++k)
             umma_ts(tmem + 256 + 128 * X, tmem + 128 * X + 8 * k, vd + k * 128, id_o, more || k > 0);
+          if (TWO)
+#pragma unroll
+            for (int k = 0; k < kW / 16; ++k)
+              umma_ts(tmem + 256 + 128 * X, tmem + 128 * X + 64 + 8 * k, vd + k * 128, id_o, true);
           if (last) umma_commit(&ss.o_done[X]);
           if (free) umma_commit(&ss.empty[s]);
         }
@@ -893,38 +914,6 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// the driver's encoder, through the runtime (the library does not link the driver)
-EncodeTiled encoder() {
-  static EncodeTiled fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) !=
-            cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
-  return fn;
-}
-
-// pages as [pages * Hkv][page][dh], a box of 64 values x one page, 128-byte swizzled
-bool make_map(const dt_cache &c, const void *base, CUtensorMap *map) {
-  EncodeTiled enc = encoder();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.dh), static_cast<cuuint64_t>(c.page),
-                              static_cast<cuuint64_t>(c.pages) * c.Hkv};
-  const cuuint64_t strides[2] = {2ull * c.dh, 2ull * c.dh * c.page};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(c.page), 1}, one[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 WideShape wide_shape(const dt_cache &c, const AttnPlan &p) {
   WideShape w;
   w.tr = p.bm / 2; w.odd = p.odd; w.ring = p.ring; w.raw = p.raw;
@@ -945,11 +934,45 @@ cudaError_t go(const AttnArgs &a, const WideShape &w, const AttnPlan &p, const C
   return cudaGetLastError();
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// the driver's encoder, through the runtime (the library does not link the driver)
+EncodeTiled encoder() {
+  static EncodeTiled fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) !=
+            cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
 }  // namespace
+
+// pages as [pages * Hkv][page][dh], a box of 128 bytes of `box_rows` rows, swizzled
+bool page_map(const dt_cache &c, const void *base, int box_rows, CUtensorMap *map) {
+  EncodeTiled enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.dh), static_cast<cuuint64_t>(c.page),
+                              static_cast<cuuint64_t>(c.pages) * c.Hkv};
+  const cuuint64_t size = c.dtype == DT_E4M3 ? 1 : 2;
+  const cuuint64_t strides[2] = {size * c.dh, size * c.dh * c.page};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Row tiles of at most 128 rows, two a unit. False where the kernel does not apply.
 bool wide_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p) {
-  if (c.dh > 128 || static_cast<int64_t>(c.pages) * c.Hkv > 0x7fffffff || rows <= kFewRows) return false;
+  if (c.dh > 128 || static_cast<int64_t>(c.pages) * c.Hkv > 0x7fffffff) return false;
   const bool quant = c.dtype == DT_E4M3;
   const int64_t tiles = (rows + 127) / 128;
   p->bm = 2 * static_cast<int>((rows + tiles - 1) / tiles);
@@ -971,7 +994,7 @@ bool wide_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p) 
   p->dhp = 64 * w.nblk;
   p->grid = sms;
   p->smem = wide_shape(c, *p).off_small + sizeof(Small);
-  p->wide = 1;
+  p->kind = AttnPlan::kWide;
   return true;
 }
 
@@ -980,7 +1003,7 @@ cudaError_t launch_wide(const dt_cache &c, const AttnArgs &a, int dtype, const A
   const WideShape w = wide_shape(c, p);
   CUtensorMap k = {}, v = {};
   const bool quant = c.dtype == DT_E4M3;
-  if (!quant && (!make_map(c, c.k, &k) || !make_map(c, c.v, &v))) return cudaErrorInvalidValue;
+  if (!quant && (!page_map(c, c.k, c.page, &k) || !page_map(c, c.v, c.page, &v))) return cudaErrorInvalidValue;
   if (dtype == DT_BF16) return quant ? go<DT_BF16, true>(a, w, p, k, v, st) : go<DT_BF16, false>(a, w, p, k, v, st);
   return quant ? go<DT_F16, true>(a, w, p, k, v, st) : go<DT_F16, false>(a, w, p, k, v, st);
 }

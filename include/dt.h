@@ -469,9 +469,10 @@ int dt_cache_commit(const dt_cache *c, const int32_t *first, const int32_t *path
  * q and out are views of H heads (H a multiple of Hkv; head h reads key/value
  * head h / (H / Hkv)) and n rows, of type dtype (DT_BF16 or DT_F16; the cache's
  * own, or either for a DT_E4M3 cache). n <= DT_MAX_N + 1 with a mask, n <= 65536
- * without. Products of the 16-bit values are accumulated in fp32, the softmax
- * statistics are fp32, its weights are rounded to 16 bits for the product with v
- * (bf16: relative 2^-9 each, as the output's own rounding).
+ * without. Products are accumulated in fp32 and the softmax statistics are fp32; its
+ * weights are rounded to the 16-bit type for the product with v (bf16: relative 2^-9
+ * each, as the output's own rounding). A DT_E4M3 cache's values are taken as they are,
+ * those of k with dtype DT_F16 as dt_cache_read gives them.
  * workspace: dt_cache_attention_workspace_bytes bytes, 256-byte aligned, for the
  * partial results of requests whose keys are cut over several blocks (0 = invalid
  * sizes). */

@@ -305,7 +305,7 @@ def tree_mask(batch, n, seed, blank=()):
 
 
 def run_attention(kind, dtype, n, G, Hkv, dh, page, prefix, counts=None, mask="tree", blank=(), seed=50,
-                  scale=None, qamp=1.0, edit=None):
+                  scale=None, qamp=1.0, edit=None, qpos=False):
     batch = len(prefix)
     rows = max(prefix) + n
     cache = R.make_cache(dt, kind, dtype, batch, rows, Hkv, page, dh, seed)
@@ -314,6 +314,8 @@ def run_attention(kind, dtype, n, G, Hkv, dh, page, prefix, counts=None, mask="t
         edit(cache)
     g = torch.Generator().manual_seed(seed + 1)
     q = (qamp * torch.randn(batch, n, Hkv * G, dh, generator=g)).to(dtype).transpose(1, 2)
+    if qpos:
+        q = q.abs()
     m = tree_mask(batch, n, seed + 2, blank) if mask == "tree" else None
     pre = torch.tensor(prefix, dtype=torch.int32)
     cnt = torch.tensor(counts, dtype=torch.int32) if counts else None
@@ -476,3 +478,53 @@ def test_many_short_units_a_block(n, G, kind):
     unit many times, and holds most of them whole."""
     prefix = [(29 * b) % 300 for b in range(90)]
     run_attention(kind, BF, n, G, 8, 64, 16, prefix, [1 + (b * 7) % n for b in range(90)])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n", [1, 40])
+def test_8bit_codes_of_every_size_count(dtype, n):
+    """Rows whose codes are the least ones beside a single large one, and rows of very
+    different scales: the values come out as they are."""
+    def edit(cache):
+        g = torch.Generator().manual_seed(7)
+        code = torch.randint(0, 8, cache.v.shape, generator=g, dtype=torch.uint8)          # 0 to 7/512
+        code |= torch.randint(0, 2, cache.v.shape, generator=g, dtype=torch.uint8) << 7     # signs
+        code[..., 3] = 0x7e                                                                # 448
+        cache.v.view(torch.uint8).copy_(code)
+        cache.v_exp.copy_(torch.randint(100, 120, cache.v_exp.shape, generator=g, dtype=torch.uint8))
+        code = torch.randint(0, 8, cache.k.shape, generator=g, dtype=torch.uint8)
+        code[..., 5] = 0x70
+        cache.k.view(torch.uint8).copy_(code)
+        cache.k_exp.copy_(torch.randint(118, 124, cache.k_exp.shape, generator=g, dtype=torch.uint8))
+    run_attention("e4m3", dtype, n, 2, 2, 128, 16, [3, 130], edit=edit)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_one_huge_value_that_hardly_counts(n):
+    """A row of 2^60 whose weight is 2^-100 and less beside ordinary rows."""
+    def edit(cache):
+        for b in range(2):
+            p = int(cache.table[b, 0])
+            cache.v_exp[p, :, 2] = 127 + 60
+            cache.k.view(torch.uint8)[p, :, 2] = 0xfe         # -448 2^-3 in every place
+            cache.k_exp[p, :, 2] = 124
+            cache.k.view(torch.uint8)[p, :, 5] = 0x78         # 256 2^-5: the row that is looked at
+            cache.k_exp[p, :, 5] = 122
+    run_attention("e4m3", BF, n, 2, 1, 64, 16, [20, 130], edit=edit, qpos=True)
+
+
+@pytest.mark.parametrize("kind,n,G", [("e4m3", 129, 4), ("e4m3", 1, 4), ("e4m3", 70, 1), ("16", 65, 4), ("16", 3, 4)])
+def test_repeated_runs_agree_bit_for_bit(kind, n, G):
+    """Long enough for every ring to turn many times, with whole units, cut ones, and tiles
+    of one and of two row tiles; no run may time out."""
+    cache = R.make_cache(dt, kind, BF, 6, 9000, 4, 64, 128, 95)
+    g = torch.Generator().manual_seed(96)
+    q = torch.randn(6, 4 * G, n, 128, generator=g).to(BF).cuda()
+    pre = torch.tensor([8800, 17, 300, 5000, 128, 2049], dtype=torch.int32).cuda()
+    ws = dt.cache_attention_workspace(cache, 4 * G, n)
+    want = dt.cache_attention(cache, q, pre, workspace=ws)
+    differ = torch.zeros((), dtype=torch.int32, device="cuda")
+    for _ in range(150):
+        differ += (dt.cache_attention(cache, q, pre, workspace=ws).view(torch.int16) != want.view(torch.int16)).any()
+    cache.check()
+    assert int(differ) == 0

@@ -5,8 +5,11 @@
 // through a ring of its own, filled by TMA through a 128-byte swizzled tensor map (16 rows
 // lie in one page): no warp waits for another before the unit's end, and about 140 KB of an SM's shared
 // memory are in flight (its share of the memory's bandwidth times latency is 45 KB). The
-// products are mma.sync m16n8k16 with the query rows on the M side; the softmax is online,
-// its reference renewed only when the maximum has grown by 2^8 (fp16: 2^4).
+// products are mma.sync m16n8k16, taken transposed: S^T = K Q^T and O^T += V^T P^T, so that
+// keys and dimensions fill the M side and eight rows are one N tile, not half an M side
+// (half the products and half the accumulators for up to eight rows; P^T becomes an operand
+// by an 8x8 transpose between lanes). The softmax is online, its reference renewed only
+// when the maximum has grown by 2^8 (fp16: 2^4).
 //
 // 8-bit rows become operands in registers. The product with K sums over dimensions in any
 // order that both sides share, so a thread takes 16 codes of a key at once, and e4m3 codes
@@ -102,7 +105,7 @@ __device__ __forceinline__ uint32_t codes_low(uint32_t w) {
   return (r << 4) & 0x87f087f0u;
 }
 
-template <int DT, bool QUANT, int DH, int RY>   // RY: rows of a thread, 1 for up to 8 rows, else 2
+template <int DT, bool QUANT, int DH, int RN>   // RN: N tiles of 8 rows
 __global__ void __launch_bounds__(kFThreads, 1)
 cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
                            const __grid_constant__ CUtensorMap kmap,
@@ -190,19 +193,16 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
     const int b = sg.b, hk = sg.hk, pre = static_cast<int>(rq.pre), end = seg_end(sg);
     const int steps = step_count(sg);
     if (tid == 0 && a.prefix[b] != rq.pre) cache_fault(a.c, b);
-    // this thread's query rows, and its part of them
-    int tok[RY], head[RY];
-    bool live[RY];
-    float row_mul[RY];
-    uint32_t q[DH / 16][4];
+    // Q^T: this thread's part of row 8 z + g; its scores are of rows 8 z + 2 t, 8 z + 2 t + 1
+    uint32_t q[DH / 16][RN][2];
+    float row_mul[RN][2];
+    int tok[RN][2];
+    bool live[RN][2];
 #pragma unroll
-    for (int y = 0; y < RY; ++y) {
-      const int r = g + 8 * y;
-      tok[y] = r / a.G;
-      head[y] = hk * a.G + r - tok[y] * a.G;
-      live[y] = r < rows && tok[y] < rq.count;
-      row_mul[y] = a.scale_log2;
-      const char *src = a.q + b * a.qb + head[y] * a.qh + tok[y] * a.qr;
+    for (int z = 0; z < RN; ++z) {
+      const int r = 8 * z + g, i = r / a.G;
+      const char *src = a.q + b * a.qb + (hk * a.G + r - i * a.G) * a.qh + i * a.qr;
+      float mul = a.scale_log2;
       uint32_t w[DH / 8];
       // 16 bytes at dimension 32 c + 8 t (a key's chunk c, t of 8 values), or 32 bytes at 64 c + 16 t
 #pragma unroll
@@ -221,38 +221,46 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
         mx = max(mx, __shfl_xor_sync(kFull, mx, 2));
         const int e = mx >= 0x7f80u || mx < 0x80u ? 0 : static_cast<int>(mx >> 7) - 127;
         const float down = exp2i(max(-e, -126)), up = e == 127 ? 0x1p126f : exp2i(max(e, -126));
-        row_mul[y] *= up;
+        mul *= up;
 #pragma unroll
         for (int c = 0; c < DH / 8; ++c) {
           const float2 f = Half16<DT_BF16>::unpack(w[c]);
           w[c] = Half16<DT_F16>::pack(f.x * down, f.y * down);
         }
       }
-      // k step s takes values 4 s' .. 4 s' + 3 of a chunk: pairs (a0, a2) of row g, (a1, a3) of g + 8
+      // k step s takes four values of a chunk: two pairs
 #pragma unroll
       for (int s = 0; s < DH / 16; ++s) {
-        q[s][y] = w[2 * s];
-        q[s][2 + y] = w[2 * s + 1];
-        if (RY == 1) q[s][1] = q[s][3] = 0u;
+        q[s][z][0] = w[2 * s];
+        q[s][z][1] = w[2 * s + 1];
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * z + 2 * t4 + e;
+        tok[z][e] = row / a.G;
+        live[z][e] = row < rows && tok[z][e] < rq.count;
+        row_mul[z][e] = __shfl_sync(kFull, mul, 4 * (2 * t4 + e));
       }
     }
-    float o[DH / 8][4];
+    float o[DH / 16][RN][4];           // dimensions 16 x + g, 16 x + g + 8 of those two rows
 #pragma unroll
-    for (int x = 0; x < DH / 8; ++x)
+    for (int x = 0; x < DH / 16; ++x)
 #pragma unroll
-      for (int y = 0; y < 4; ++y) o[x][y] = 0.0f;
-    float m[RY], l[RY];
+      for (int z = 0; z < RN; ++z)
 #pragma unroll
-    for (int y = 0; y < RY; ++y) {
-      m[y] = ninf;
-      l[y] = 0.0f;
-    }
+        for (int y = 0; y < 4; ++y) o[x][z][y] = 0.0f;
+    float m[RN][2], l[RN][2];
+#pragma unroll
+    for (int z = 0; z < RN; ++z)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[z][e] = ninf;
+        l[z][e] = 0.0f;
+      }
     int vref = -1000;                  // V's reference exponent
     const int whole_end = min(pre, end);
-    // the thread's keys of a step, 4 of each group of 16, in the order of its scores' columns
-    auto key_of = [&](int x) {
-      return 16 * (x >> 2) + (QUANT ? 4 * t4 + (x & 3) : 8 * ((x >> 1) & 1) + 2 * t4 + (x & 1));
-    };
+    // the thread's two keys of a group of 16, as rows g and g + 8 of the product
+    const int key0 = QUANT ? 4 * (g >> 1) + (g & 1) : g, key1 = key0 + (QUANT ? 2 : 8);
 
 #pragma unroll 1
     for (int k = 0; k < steps; ++k) {
@@ -265,96 +273,112 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
       __syncwarp();
       const unsigned char *sK = ring + stage_out * 2 * HS, *sV = sK + HS;
       const bool masked = j0 + SUB > whole_end || good != (1u << NG) - 1u;
-      auto there = [&](int x) { return j0 + key_of(x) < end && ((good >> (x >> 2)) & 1u); };
+      auto key_at = [&](int x) { return j0 + 16 * (x >> 1) + (x & 1 ? key1 : key0); };    // x: 2 h + which
+      auto there = [&](int x) { return key_at(x) < end && ((good >> (x >> 1)) & 1u); };
       // ------------------------------------------------------------ scores
-      float s[2 * NG][4];
+      float s[NG][RN][4];
 #pragma unroll
-      for (int x = 0; x < 2 * NG; ++x)
+      for (int h = 0; h < NG; ++h)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) s[x][y] = 0.0f;
-      if (QUANT) {
+        for (int z = 0; z < RN; ++z)
 #pragma unroll
-        for (int h = 0; h < DH / 64; ++h) {
-          uint4 c[2 * NG];
+          for (int y = 0; y < 4; ++y) s[h][z][y] = 0.0f;
 #pragma unroll
-          for (int x = 0; x < 2 * NG; ++x) {
-            const int key = 4 * (g >> 1) + (g & 1) + 2 * (x & 1);
-            c[x] = *reinterpret_cast<const uint4 *>(sK + (x >> 1) * 2048 + key * 128 +
-                                                    (((4 * h + t4) ^ (key & 7)) << 4));
-          }
+      for (int d = 0; d < (QUANT ? DH / 64 : DH / 32); ++d) {
+        uint4 c[NG][2];
 #pragma unroll
-          for (int z = 0; z < 4; ++z)
-#pragma unroll
-            for (int x = 0; x < 2 * NG; ++x) {
-              const uint32_t w = z == 0 ? c[x].x : z == 1 ? c[x].y : z == 2 ? c[x].z : c[x].w;
-              mma16<QDT>(s[x], q[4 * h + z], e4m3_f16x2(w & 0xffffu), e4m3_f16x2(w >> 16));
-            }
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < DH / 32; ++h)
+        for (int h = 0; h < NG; ++h)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int key = g + 8 * x;
-            const uint4 c = *reinterpret_cast<const uint4 *>(
-                sK + (h >> 1) * 2048 + key * 128 + (((4 * (h & 1) + t4) ^ (key & 7)) << 4));
-            mma16<QDT>(s[x], q[2 * h], c.x, c.y);
-            mma16<QDT>(s[x], q[2 * h + 1], c.z, c.w);
+            const int key = x ? key1 : key0;
+            c[h][x] = *reinterpret_cast<const uint4 *>(
+                sK + (QUANT ? h : d >> 1) * 2048 + key * 128 +
+                (((QUANT ? 4 * d + t4 : 4 * (d & 1) + t4) ^ (key & 7)) << 4));
+          }
+#pragma unroll
+        for (int i = 0; i < (QUANT ? 4 : 2); ++i)
+#pragma unroll
+          for (int h = 0; h < NG; ++h) {
+            uint32_t ka[4];            // rows g, g + 8; four values each
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint4 &v = c[h][x];
+              if (QUANT) {
+                const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+                ka[x] = e4m3_f16x2(w & 0xffffu);
+                ka[2 + x] = e4m3_f16x2(w >> 16);
+              } else {
+                ka[x] = i ? v.z : v.x;
+                ka[2 + x] = i ? v.w : v.y;
+              }
+            }
+#pragma unroll
+            for (int z = 0; z < RN; ++z) {
+              const uint32_t(&qb)[2] = q[(QUANT ? 4 : 2) * d + i][z];
+              mma16<QDT>(s[h][z], ka, qb[0], qb[1]);
+            }
           }
       }
-      uint32_t ve[NG];
-      float kmul[4 * NG];
+      uint32_t ve[2 * NG];             // V's exponent bytes of the thread's keys
+      float kmul[2 * NG];
 #pragma unroll
       for (int h = 0; h < NG; ++h) {
         if (QUANT) {
-          const uint32_t ke = *reinterpret_cast<const uint32_t *>(ss.exps[warp][stage_out] + 16 * h + 4 * t4);
-          ve[h] = *reinterpret_cast<const uint32_t *>(ss.exps[warp][stage_out] + SUB + 16 * h + 4 * t4);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) kmul[4 * h + x] = row_scale((ke >> (8 * x)) & 255u);
+          const uint8_t *e = ss.exps[warp][stage_out] + 16 * h + key0;
+          const uint32_t w = *reinterpret_cast<const uint32_t *>(e - (g & 1)) >> (8 * (g & 1));
+          const uint32_t v = *reinterpret_cast<const uint32_t *>(e + SUB - (g & 1)) >> (8 * (g & 1));
+          kmul[2 * h] = row_scale(w & 255u);
+          kmul[2 * h + 1] = row_scale((w >> 16) & 255u);
+          ve[2 * h] = v & 255u;
+          ve[2 * h + 1] = (v >> 16) & 255u;
         } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) kmul[4 * h + x] = 1.0f;
+          kmul[2 * h] = kmul[2 * h + 1] = 1.0f;
+          ve[2 * h] = ve[2 * h + 1] = 0u;
         }
       }
-      uint32_t see[RY];                // bits: keys x that row y sees
-      float mx[RY];
+      uint32_t see = ~0u;              // bit (2 h + x) 2 RN + 2 z + e: the row sees the key
+      if (masked) {
+        see = 0u;
 #pragma unroll
-      for (int y = 0; y < RY; ++y) {
-        see[y] = live[y] ? (1u << (4 * NG)) - 1u : 0u;
-        if (masked) {
-          see[y] = 0u;
+        for (int x = 0; x < 2 * NG; ++x)
 #pragma unroll
-          for (int x = 0; x < 4 * NG; ++x)
-            if (live[y] && there(x) && sees(a, rq, b, tok[y], j0 + key_of(x))) see[y] |= 1u << x;
-        }
-        mx[y] = ninf;
+          for (int z = 0; z < RN; ++z)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (live[z][e] && there(x) && sees(a, rq, b, tok[z][e], key_at(x)))
+                see |= 1u << (2 * RN * x + 2 * z + e);
       }
+      float mx[RN][2];
 #pragma unroll
-      for (int y = 0; y < RY; ++y)
+      for (int z = 0; z < RN; ++z)
 #pragma unroll
-        for (int x = 0; x < 4 * NG; ++x) {
-          float &v = s[x >> 1][2 * y + (x & 1)];
-          v *= row_mul[y] * kmul[x];
-          if (masked) v = (see[y] >> x) & 1u ? v : ninf;
-          mx[y] = fmaxf(mx[y], v);
+        for (int e = 0; e < 2; ++e) {
+          mx[z][e] = ninf;
+#pragma unroll
+          for (int x = 0; x < 2 * NG; ++x) {
+            float &v = s[x >> 1][z][2 * (x & 1) + e];
+            v *= QUANT ? row_mul[z][e] * kmul[x] : row_mul[z][e];
+            if (masked) v = (see >> (2 * RN * x + 2 * z + e)) & 1u ? v : ninf;
+            mx[z][e] = fmaxf(mx[z][e], v);
+          }
         }
       bool grow = false;
 #pragma unroll
-      for (int y = 0; y < RY; ++y) {
-        mx[y] = fmaxf(mx[y], __shfl_xor_sync(kFull, mx[y], 1));
-        mx[y] = fmaxf(mx[y], __shfl_xor_sync(kFull, mx[y], 2));
-        if (!live[y]) mx[y] = ninf;
-        grow |= mx[y] > m[y] + kGrow || (m[y] == ninf && mx[y] != ninf);
-      }
+      for (int z = 0; z < RN; ++z)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) mx[z][e] = fmaxf(mx[z][e], __shfl_xor_sync(kFull, mx[z][e], d));
+          if (!live[z][e]) mx[z][e] = ninf;
+          grow |= mx[z][e] > m[z][e] + kGrow || (m[z][e] == ninf && mx[z][e] != ninf);
+        }
       // V's reference: the step's largest exponent of a key that is there
       float vmul = 1.0f;               // of O, for a new reference
       if (QUANT) {
         int top = -1000;
 #pragma unroll
-        for (int x = 0; x < 4 * NG; ++x) {
-          const int e = static_cast<int>((ve[x >> 2] >> (8 * (x & 3))) & 255u);
-          if (e != 255 && (!masked || there(x))) top = max(top, e - 127);
-        }
+        for (int x = 0; x < 2 * NG; ++x)
+          if (ve[x] != 255u && (!masked || there(x))) top = max(top, static_cast<int>(ve[x]) - 127);
         top = __reduce_max_sync(kFull, top);
         if (top > vref + 40) {
           vmul = vref == -1000 ? 0.0f : exp2i(max(vref - top, -126));
@@ -363,119 +387,115 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
         }
       }
       if (__any_sync(kFull, grow)) {
-        float f[2] = {1.0f, 1.0f};
 #pragma unroll
-        for (int y = 0; y < RY; ++y) {
-          const bool up = mx[y] > m[y] + kGrow || (m[y] == ninf && mx[y] != ninf);
-          f[y] = !up ? 1.0f : m[y] == ninf ? 0.0f : fast_exp2(m[y] - mx[y]);
-          if (up) m[y] = mx[y];
-          l[y] *= f[y];
-          f[y] *= vmul;
-        }
+        for (int z = 0; z < RN; ++z)
 #pragma unroll
-        for (int x = 0; x < DH / 8; ++x)
+          for (int e = 0; e < 2; ++e) {
+            const bool up = mx[z][e] > m[z][e] + kGrow || (m[z][e] == ninf && mx[z][e] != ninf);
+            float f = !up ? 1.0f : m[z][e] == ninf ? 0.0f : fast_exp2(m[z][e] - mx[z][e]);
+            if (up) m[z][e] = mx[z][e];
+            l[z][e] *= f;
+            f *= vmul;
 #pragma unroll
-          for (int y = 0; y < 2 * RY; ++y) o[x][y] *= f[y >> 1];
+            for (int x = 0; x < DH / 16; ++x) {
+              o[x][z][e] *= f;
+              o[x][z][2 + e] *= f;
+            }
+          }
       }
       // ----------------------------------------------------------- weights
-      float p[2][4 * NG];
+      // p^T of 8 keys x 8 rows a register, transposed between lanes: keys 2 t, 2 t + 1 of row g
+      constexpr int PDT = QUANT ? DT_BF16 : DT;
+      uint32_t pb[NG][RN][2], pl[NG][RN][2];
 #pragma unroll
-      for (int y = 0; y < RY; ++y) {
-        const float ref = m[y] == ninf ? 0.0f : m[y] - kShift;
+      for (int x = 0; x < 2 * NG; ++x) {
+        float f = 1.0f;
+        if (QUANT)   // 2^(e - ref + 60), e at most 40 above ref; NaN rows NaN
+          f = ve[x] == 255u ? row_scale(255u) : exp2i(max(static_cast<int>(ve[x]) - 127 - vref + 60, -126));
 #pragma unroll
-        for (int x = 0; x < 4 * NG; ++x) {
-          p[y][x] = fast_exp2(s[x >> 1][2 * y + (x & 1)] - ref);
-          l[y] += p[y][x];
-        }
-      }
-      if (QUANT) {
+        for (int z = 0; z < RN; ++z) {
+          float p[2];
 #pragma unroll
-        for (int x = 0; x < 4 * NG; ++x) {
-          const uint32_t E = (ve[x >> 2] >> (8 * (x & 3))) & 255u;
-          // 2^(e - ref + 60), e at most 40 above ref; NaN rows NaN
-          const float f = E == 255u ? row_scale(E)
-                                    : exp2i(max(static_cast<int>(E) - 127 - vref + 60, -126));
-#pragma unroll
-          for (int y = 0; y < RY; ++y) {
-            p[y][x] *= f;
-            if (masked) p[y][x] = (see[y] >> x) & 1u ? p[y][x] : 0.0f;
+          for (int e = 0; e < 2; ++e) {
+            const float ref = m[z][e] == ninf ? 0.0f : m[z][e] - kShift;
+            p[e] = fast_exp2(s[x >> 1][z][2 * (x & 1) + e] - ref);
+            l[z][e] += p[e];
+            if (QUANT) p[e] *= f;
+            if (QUANT && masked) p[e] = (see >> (2 * RN * x + 2 * z + e)) & 1u ? p[e] : 0.0f;
+          }
+          const uint32_t hi = Half16<PDT>::pack(p[0], p[1]);
+          asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pb[x >> 1][z][x & 1]) : "r"(hi));
+          if (QUANT && DT == DT_F16) {   // second term
+            const float2 h2 = Half16<PDT>::unpack(hi);
+            const uint32_t lo = Half16<PDT>::pack(p[0] - h2.x, p[1] - h2.y);
+            asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pl[x >> 1][z][x & 1]) : "r"(lo));
           }
         }
       }
+      // ------------------------------------------------------------ values
       uint32_t odd = 0u;
       const uint32_t v_at = smem_u32(sV);
-      constexpr int PDT = QUANT ? DT_BF16 : DT;
 #pragma unroll
       for (int h = 0; h < NG; ++h) {
-        uint32_t pa[4], pl[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          pa[z] = pl[z] = 0u;
-          if ((z & 1) >= RY) continue;
-          const float p0 = p[z & 1][4 * h + 2 * (z >> 1)], p1 = p[z & 1][4 * h + 2 * (z >> 1) + 1];
-          pa[z] = Half16<PDT>::pack(p0, p1);
-          if (QUANT && DT == DT_F16) {   // second term
-            const float2 hi = Half16<PDT>::unpack(pa[z]);
-            pl[z] = Half16<PDT>::pack(p0 - hi.x, p1 - hi.y);
-          }
-        }
-        // ------------------------------------------------------------ values
 #pragma unroll
         for (int c = 0; c < DH / 32; ++c) {
+          uint32_t va[2][4];           // dimensions 32 c + 16 i + g, + 8; the 16 keys
           if (QUANT) {
-            uint32_t r[4];   // columns 32 c + g + 8 i: keys 4 t .. 4 t + 3
+            uint32_t r[4];             // columns 32 c + g + 8 i: keys 4 t .. 4 t + 3
             const int key = lane & 15, chunk = 2 * c + (lane >> 4);
             asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                          : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                          : "r"(v_at + h * 2048 + key * 128 + ((chunk ^ (key & 7)) << 4)));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t b0 = codes_low<0>(r[i]), b1 = codes_low<1>(r[i]);
-              mma16<PDT>(o[4 * c + i], pa, b0, b1);
-              if (DT == DT_F16) mma16<PDT>(o[4 * c + i], pl, b0, b1);
+              va[i >> 1][i & 1] = codes_low<0>(r[i]);
+              va[i >> 1][2 + (i & 1)] = codes_low<1>(r[i]);
             }
           } else {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              uint32_t r[4];
-              const int key = lane & 15, chunk = 4 * (c & 1) + 2 * i + (lane >> 4);
+              const int key = (lane & 7) + ((lane >> 4) << 3), chunk = 4 * (c & 1) + 2 * i + ((lane >> 3) & 1);
               asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                           : "=r"(va[i][0]), "=r"(va[i][1]), "=r"(va[i][2]), "=r"(va[i][3])
                            : "r"(v_at + (c >> 1) * 2048 + key * 128 + ((chunk ^ (key & 7)) << 4)));
               if (masked) {      // zero times a value that is not finite is NaN: see below
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
-                  const uint32_t x = not_finite<DT>(r[z]);
+                  const uint32_t x = not_finite<DT>(va[i][z]);
                   odd |= x;
-                  r[z] &= ~x;
+                  va[i][z] &= ~x;
                 }
               }
-              mma16<PDT>(o[4 * c + 2 * i], pa, r[0], r[1]);
-              mma16<PDT>(o[4 * c + 2 * i + 1], pa, r[2], r[3]);
             }
           }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int z = 0; z < RN; ++z) {
+              mma16<PDT>(o[2 * c + i][z], va[i], pb[h][z][0], pb[h][z][1]);
+              if (QUANT && DT == DT_F16) mma16<PDT>(o[2 * c + i][z], va[i], pl[h][z][0], pl[h][z][1]);
+            }
         }
       }
       if (!QUANT && masked && __any_sync(kFull, odd != 0u)) {
         // values that are not finite, for the rows that see them
 #pragma unroll 1
-        for (int key = 0; key < SUB && j0 + key < end && good; ++key) {
-          bool v[RY];
+        for (int key = 0; key < SUB && j0 + key < end && good; ++key)
 #pragma unroll
-          for (int y = 0; y < RY; ++y) v[y] = live[y] && sees(a, rq, b, tok[y], j0 + key);
-#pragma unroll
-          for (int x = 0; x < DH / 8; ++x)
+          for (int z = 0; z < RN; ++z)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int col = 8 * x + 2 * t4 + e;
-              const uint16_t w = *reinterpret_cast<const uint16_t *>(
-                  sV + (col >> 6) * 2048 + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4) + (col & 7) * 2);
-              if (col < dh && (not_finite<DT>(w) & 0xffffu))
+              if (!live[z][e] || !sees(a, rq, b, tok[z][e], j0 + key)) continue;
 #pragma unroll
-                for (int y = 0; y < RY; ++y)
-                  if (v[y]) o[x][2 * y + e] += Half16<DT>::unpack(w).x;
+              for (int x = 0; x < DH / 16; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int d = 16 * x + g + 8 * y;
+                  const uint16_t w = *reinterpret_cast<const uint16_t *>(
+                      sV + (d >> 6) * 2048 + key * 128 + ((((d & 63) >> 3) ^ (key & 7)) << 4) + (d & 7) * 2);
+                  if (d < dh && (not_finite<DT>(w) & 0xffffu)) o[x][z][2 * y + e] += Half16<DT>::unpack(w).x;
+                }
             }
-        }
       }
       __syncwarp();                    // the place is read
       if (++stage_out == static_cast<uint32_t>(stages)) {
@@ -493,31 +513,34 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
 
     // the warps' results together, 32 columns at a time
 #pragma unroll
-    for (int y = 0; y < RY; ++y) {
-      if (!live[y]) l[y] = 0.0f;       // (m is -inf: the row's O is not looked at)
-      l[y] += __shfl_xor_sync(kFull, l[y], 1);
-      l[y] += __shfl_xor_sync(kFull, l[y], 2);
-      if (t4 == 0) {
-        ss.m[warp][g + 8 * y] = m[y];
-        ss.l[warp][g + 8 * y] = l[y];
+    for (int z = 0; z < RN; ++z)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (!live[z][e]) l[z][e] = 0.0f;       // (m is -inf: the row's O is not looked at)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[z][e] += __shfl_xor_sync(kFull, l[z][e], d);
+        if (g == 0) {
+          ss.m[warp][8 * z + 2 * t4 + e] = m[z][e];
+          ss.l[warp][8 * z + 2 * t4 + e] = l[z][e];
+        }
       }
-    }
     const float out_mul = QUANT ? 0x1p60f : 1.0f, out_mul2 = QUANT && vref > -1000 ? exp2i(vref) : 1.0f;
     const bool whole = done.t0 == 0 && done.t1 == done.tiles;
     float *pp = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (done.t0 > 0 ? 0 : 1)) * 2 * a.slot;
     // a thread: row r, columns 4 c of a round
     const int r = tid / (kMergeCols / 4), c = tid % (kMergeCols / 4);
-    const bool mine = r < rows && r < 8 * RY;
+    const bool mine = r < rows && r < 8 * RN;
     float w[kFWarps], inv = 0.0f;
 #pragma unroll
     for (int round = 0; round < DH / kMergeCols; ++round) {
 #pragma unroll
-      for (int x = 0; x < kMergeCols / 8; ++x)
+      for (int x = 0; x < kMergeCols / 16; ++x)
 #pragma unroll
-        for (int y = 0; y < RY; ++y)
-          *reinterpret_cast<float2 *>(&ss.out[warp][g + 8 * y][8 * x + 2 * t4]) =
-              make_float2(o[kMergeCols / 8 * round + x][2 * y] * out_mul * out_mul2,
-                          o[kMergeCols / 8 * round + x][2 * y + 1] * out_mul * out_mul2);
+        for (int z = 0; z < RN; ++z)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            ss.out[warp][8 * z + 2 * t4 + (y & 1)][16 * x + g + 8 * (y >> 1)] =
+                o[kMergeCols / 16 * round + x][z][y] * out_mul * out_mul2;
       __syncthreads();
       if (mine) {
         if (round == 0) {

@@ -159,28 +159,30 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
     for (int h = 0; h < NG; ++h)
       if (static_cast<uint32_t>(entry[h]) < static_cast<uint32_t>(a.c.pages)) good |= 1u << h;
     there_in = (there_in & ~(((1u << NG) - 1u) << (NG * stage_in))) | good << (NG * stage_in);
+    uint64_t *bar = &full[stage_in];
     if (lane == 0) {
-      uint64_t *bar = &full[stage_in];
-      unsigned char *dst = ring + stage_in * 2 * HS;
       mbar_expect_tx(bar, __popc(good) * (2 * HS / NG + (QUANT ? 32 : 0)));
 #pragma unroll
-      for (int h = 0; h < NG; ++h) {
-        if (!((good >> h) & 1u)) {
-          if (entry[h] != -2) cache_fault(a.c, s.b);
-          continue;
-        }
-        const int z = entry[h] * a.c.Hkv + s.hk, y = (j + 16 * h) & ((1 << a.c.shift) - 1);
-#pragma unroll
-        for (int kb = 0; kb < HS / NG / 2048; ++kb) {
-          few_tma(dst + (h + kb) * 2048, &kmap, 64 * kb, y, z, bar);
-          few_tma(dst + HS + (h + kb) * 2048, &vmap, 64 * kb, y, z, bar);
-        }
-        if (QUANT) {
-          const int64_t row = (static_cast<int64_t>(z) << a.c.shift) + y;
-          uint8_t *e = ss.exps[warp][stage_in] + 16 * h;
-          bulk_g2s(e, a.c.k_exp + row, 16, bar);
-          bulk_g2s(e + SUB, a.c.v_exp + row, 16, bar);
-        }
+      for (int h = 0; h < NG; ++h)
+        if (entry[h] < 0 ? entry[h] != -2 : entry[h] >= a.c.pages) cache_fault(a.c, s.b);
+    }
+    __syncwarp();
+    // a lane a copy: boxes of K, of V (four of 16-bit rows, or two for each of two groups),
+    // then the exponents
+    constexpr int kBoxes = HS / NG / 2048;     // of a group's K
+    const int which = lane & 1, u = lane >> 1;
+    unsigned char *dst = ring + stage_in * 2 * HS + which * HS;
+    if (u < NG * kBoxes) {
+      const int h = u / kBoxes, kb = u % kBoxes;
+      if ((good >> h) & 1u)
+        few_tma(dst + u * 2048, which ? &vmap : &kmap, 64 * kb, (j + 16 * h) & ((1 << a.c.shift) - 1),
+                (NG == 1 || h == 0 ? entry[0] : entry[NG - 1]) * a.c.Hkv + s.hk, bar);
+    } else if (QUANT && u < 2 * NG) {
+      const int h = u - NG;
+      if ((good >> h) & 1u) {
+        const int64_t row = (static_cast<int64_t>((h == 0 ? entry[0] : entry[NG - 1]) * a.c.Hkv + s.hk) << a.c.shift) +
+                            ((j + 16 * h) & ((1 << a.c.shift) - 1));
+        bulk_g2s(ss.exps[warp][stage_in] + which * SUB + 16 * h, (which ? a.c.v_exp : a.c.k_exp) + row, 16, bar);
       }
     }
     if (++stage_in == static_cast<uint32_t>(stages)) stage_in = 0;
@@ -276,13 +278,14 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
       auto key_at = [&](int x) { return j0 + 16 * (x >> 1) + (x & 1 ? key1 : key0); };    // x: 2 h + which
       auto there = [&](int x) { return key_at(x) < end && ((good >> (x >> 1)) & 1u); };
       // ------------------------------------------------------------ scores
-      float s[NG][RN][4];
+      // (in two sums each, so that half as many products wait for one another)
+      float s[NG][RN][4], s2[NG][RN][4];
 #pragma unroll
       for (int h = 0; h < NG; ++h)
 #pragma unroll
         for (int z = 0; z < RN; ++z)
 #pragma unroll
-          for (int y = 0; y < 4; ++y) s[h][z][y] = 0.0f;
+          for (int y = 0; y < 4; ++y) s[h][z][y] = s2[h][z][y] = 0.0f;
 #pragma unroll
       for (int d = 0; d < (QUANT ? DH / 64 : DH / 32); ++d) {
         uint4 c[NG][2];
@@ -315,7 +318,7 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
 #pragma unroll
             for (int z = 0; z < RN; ++z) {
               const uint32_t(&qb)[2] = q[(QUANT ? 4 : 2) * d + i][z];
-              mma16<QDT>(s[h][z], ka, qb[0], qb[1]);
+              mma16<QDT>(i & 1 ? s2[h][z] : s[h][z], ka, qb[0], qb[1]);
             }
           }
       }
@@ -357,43 +360,47 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
 #pragma unroll
           for (int x = 0; x < 2 * NG; ++x) {
             float &v = s[x >> 1][z][2 * (x & 1) + e];
-            v *= QUANT ? row_mul[z][e] * kmul[x] : row_mul[z][e];
+            v = (v + s2[x >> 1][z][2 * (x & 1) + e]) * (QUANT ? row_mul[z][e] * kmul[x] : row_mul[z][e]);
             if (masked) v = (see >> (2 * RN * x + 2 * z + e)) & 1u ? v : ninf;
             mx[z][e] = fmaxf(mx[z][e], v);
           }
         }
+      // Does a row's maximum, or V's largest exponent of a key that is there, grow past its
+      // reference? Each lane asks for its own keys; only then are they taken across lanes.
       bool grow = false;
 #pragma unroll
       for (int z = 0; z < RN; ++z)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) mx[z][e] = fmaxf(mx[z][e], __shfl_xor_sync(kFull, mx[z][e], d));
           if (!live[z][e]) mx[z][e] = ninf;
           grow |= mx[z][e] > m[z][e] + kGrow || (m[z][e] == ninf && mx[z][e] != ninf);
         }
-      // V's reference: the step's largest exponent of a key that is there
-      float vmul = 1.0f;               // of O, for a new reference
+      int top = -1000;
       if (QUANT) {
-        int top = -1000;
 #pragma unroll
         for (int x = 0; x < 2 * NG; ++x)
           if (ve[x] != 255u && (!masked || there(x))) top = max(top, static_cast<int>(ve[x]) - 127);
-        top = __reduce_max_sync(kFull, top);
-        if (top > vref + 40) {
-          vmul = vref == -1000 ? 0.0f : exp2i(max(vref - top, -126));
-          vref = top;
-          grow = true;
-        }
+        grow |= top > vref + 40;
       }
       if (__any_sync(kFull, grow)) {
+        float vmul = 1.0f;
+        if (QUANT) {
+          top = __reduce_max_sync(kFull, top);
+          if (top > vref + 40) {
+            vmul = vref == -1000 ? 0.0f : exp2i(max(vref - top, -126));
+            vref = top;
+          }
+        }
 #pragma unroll
         for (int z = 0; z < RN; ++z)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const bool up = mx[z][e] > m[z][e] + kGrow || (m[z][e] == ninf && mx[z][e] != ninf);
-            float f = !up ? 1.0f : m[z][e] == ninf ? 0.0f : fast_exp2(m[z][e] - mx[z][e]);
-            if (up) m[z][e] = mx[z][e];
+            float t = mx[z][e];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, d));
+            const bool up = t > m[z][e] + kGrow || (m[z][e] == ninf && t != ninf);
+            float f = !up ? 1.0f : m[z][e] == ninf ? 0.0f : fast_exp2(m[z][e] - t);
+            if (up) m[z][e] = t;
             l[z][e] *= f;
             f *= vmul;
 #pragma unroll

@@ -375,6 +375,7 @@ constexpr int kJoinRows = 8;
 template <int DT>
 __global__ void __launch_bounds__(kJoinThreads)
 cache_attention_join_kernel(const __grid_constant__ AttnArgs a, int BM, int DH) {
+  cudaGridDependencySynchronize();
   const int4 unit = a.cut[2 * blockIdx.x], blocks = a.cut[2 * blockIdx.x + 1];
   if (unit.x < 0 || blocks.x + 1 != static_cast<int>(blockIdx.x)) return;
   const int b = unit.x, hk = unit.y, rt = unit.z;
@@ -424,8 +425,18 @@ cudaError_t launch_narrow(const AttnArgs &a, cudaStream_t st) {
 
 template <int DT>
 cudaError_t launch_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
-  cache_attention_join_kernel<DT>
-      <<<dim3(a.grid, (p.bm + kJoinRows - 1) / kJoinRows), kJoinRows * p.dhp / 4, 0, st>>>(a, p.bm, p.dhp);
+  // launched while the first kernel still runs; waits for its end on the device
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(a.grid, (p.bm + kJoinRows - 1) / kJoinRows);
+  config.blockDim = dim3(kJoinRows * p.dhp / 4);
+  config.stream = st;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&config, cache_attention_join_kernel<DT>, a, p.bm, p.dhp);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

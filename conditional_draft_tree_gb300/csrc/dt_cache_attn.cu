@@ -448,7 +448,7 @@ cudaError_t launch_bm(const AttnArgs &a, int bm, cudaStream_t st) {
 }
 
 int64_t slot_floats(const AttnPlan &p) {
-  return (static_cast<int64_t>(p.bm) * (p.dhp + 2) + 3) / 4 * 4;
+  return (static_cast<int64_t>(p.bm) * (p.dhp + 2) + 7) / 8 * 8;
 }
 
 bool al4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

@@ -33,7 +33,7 @@ struct AttnArgs {
                          // warps where these share a unit's rows; behind it [grid][2][slot],
                          // which passes one group's part to the other
   int odd;               // the last row tile's units are shared so
-  int64_t slot;          // fp32 numbers of one part, a multiple of 4
+  int64_t slot;          // fp32 numbers of one part, a multiple of 8
   float scale_log2;      // scale times log2(e)
   int batch, n, H, G, row_tiles, grid, min_tiles;
   int weight, last_weight, lead;      // of a key tile, of one of the last row tile, of a unit

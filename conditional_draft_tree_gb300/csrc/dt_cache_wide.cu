@@ -139,6 +139,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                : "memory");
 }
 
+// 32 bytes (aligned) of global memory
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // both warpgroups: a part of one unit handed from B to A through global memory
 __device__ __forceinline__ void pair_sync() {
   __threadfence_block();
@@ -651,9 +658,8 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[e] = f == 0.0f || !some ? 0.0f : o[e] * f;
         if (real && leave) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4 *>(po + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          store32(po + c, reinterpret_cast<uint32_t(&)[8]>(o[0]));
+          store32(po + c + 8, reinterpret_cast<uint32_t(&)[8]>(o[8]));
         } else if (real) {
           if (fb != 0.0f) {
 #pragma unroll
@@ -665,8 +671,12 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
           uint32_t y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = Half16<DT>::pack(o[2 * e], o[2 * e + 1]);
-          *reinterpret_cast<uint4 *>(out + 2 * c) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4 *>(out + 2 * c + 16) = make_uint4(y[4], y[5], y[6], y[7]);
+          if (((reinterpret_cast<uintptr_t>(a.out) | a.ob | a.oh | a.orow) & 31) == 0) {   // whole sectors
+            store32(out + 2 * c, y);
+          } else {
+            *reinterpret_cast<uint4 *>(out + 2 * c) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4 *>(out + 2 * c + 16) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
         }
         __syncwarp();
       }

@@ -7,6 +7,7 @@
 // a turn, so p times it modulo 2^64 is exact to p 2^-65 turns, where a product in
 // fp32 would be off by p 2^-25. The upper 32 bits, as a signed number in units of
 // 2^-31 half turns, go to sincospif.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -20,6 +21,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kLanes = 8;                     // lanes of one head row
 constexpr int kGroups = kThreads / kLanes;    // head rows in flight per block
+constexpr int kBlockTokens = 32;               // tokens of a block, at most
 constexpr int kMaxHalf = 128;                 // pairs of a head, at most
 
 struct View {            // one of up to three tensors of a launch
@@ -44,24 +46,108 @@ __device__ __forceinline__ int clamped_count(const int32_t *counts, int b, int n
   return counts ? min(max(counts[b], 0), n) : n;
 }
 
+// N fp32 numbers of shared memory (on a boundary of 4 N bytes, or of 16)
+template <int N>
+__device__ __forceinline__ void load_f32(const float *p, float *x) {
+  if (N % 4 == 0) {
+#pragma unroll
+    for (int e = 0; e < N / 4; ++e)
+      *reinterpret_cast<float4 *>(x + 4 * e) = reinterpret_cast<const float4 *>(p)[e];
+  } else {
+    *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(p);
+  }
+}
+
 // Head rows from the tensors t[] to views or to the cache. A block takes
-// tokens_block tokens and heads_block heads of each: the angles of a token are
-// computed once for all of them. Eight lanes own a row; a lane holds chunks of VEC
-// values two at a time, chunk c of the turned part with its partner (halves: the
-// pair's other half, so a lane reads both before it writes either and a tensor can
-// be turned in place; interleaved: any other chunk). 8-bit rows need the row's
-// largest magnitude before the first code, so a lane keeps its values in registers.
-// Bound by memory: 32 bytes a lane in flight, 8 blocks an SM.
+// tokens_block tokens and heads_block heads of each: a token's angles and its place
+// in the cache are found once for all of them. Eight lanes own a row; a lane holds
+// chunks of VEC values two at a time, chunk c of the turned part with its partner
+// (halves: the pair's other half, so a lane reads both before it writes either and a
+// tensor can be turned in place; interleaved: any other chunk). 8-bit rows need the
+// row's largest magnitude before the first code, so a lane keeps its values in
+// registers. Bound by memory: a lane's next row is loaded (its first one before the
+// angles are known) while the one before it is turned and written.
 template <int DT, bool QUANT, int VEC, int ITEMS>
 __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_constant__ RowArgs a) {
-  extern __shared__ float s_cs[];      // [tokens_block][2][rot / 2]
+  extern __shared__ __align__(16) float s_cs[];      // [tokens_block][2][rot / 2]
+  __shared__ int64_t s_row[kBlockTokens];            // of head 0; -1: no place, or no such token
   const int tid = threadIdx.x, lane = tid & (kLanes - 1), grp = tid / kLanes;
   const int64_t all = static_cast<int64_t>(a.batch) * a.n;
   const int64_t tk0 = static_cast<int64_t>(blockIdx.x / a.head_blocks) * a.tokens_block;
   const int h0 = static_cast<int>(blockIdx.x % a.head_blocks) * a.heads_block;
   const int nh = min(a.heads_block, a.heads - h0);
   const int ntok = static_cast<int>(min(static_cast<int64_t>(a.tokens_block), all - tk0));
-  const int half = a.rot >> 1;
+  const int half = a.rot >> 1, chunks = a.dh / VEC;
+  const int b0 = static_cast<int>(tk0 / a.n), i0 = static_cast<int>(tk0 - static_cast<int64_t>(b0) * a.n);
+  // the request and the row of token tk0 + t
+  auto place = [&](int t, int *b, int *i) {
+    *b = b0;
+    *i = i0 + t;
+    while (*i >= a.n) {
+      *i -= a.n;
+      ++*b;
+    }
+  };
+  // Row r of the block: its token, its tensor and head there, its chunks.
+  struct Row {
+    int t, k, h, pairs, rest2, items;
+  };
+  int rt = 0, rh = grp;                // token and head (of the block's) of the row to load
+  while (rh >= nh) {
+    rh -= nh;
+    ++rt;
+  }
+  uint32_t w[ITEMS][2][VEC / 2];
+  auto load = [&](Row *row) {
+    row->t = rt;
+    int h = h0 + rh, k = 0;
+    while (k + 1 < a.nt && h >= a.t[k].heads) h -= a.t[k++].heads;
+    const View &vw = a.t[k];
+    row->k = k;
+    row->h = h;
+    row->pairs = vw.turned ? a.rot / (2 * VEC) : 0;           // chunk pairs of the turned part
+    const int rest = chunks - 2 * row->pairs;
+    row->rest2 = (rest + 1) >> 1;
+    row->items = row->pairs + row->rest2;
+    if (rt >= ntok) return;
+    int b, i;
+    place(rt, &b, &i);
+    const char *in = vw.in + b * vw.ib + h * vw.ih + i * vw.ir;
+    const bool read = vw.out || i < clamped_count(a.counts, b, a.n);
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int m = lane + it * kLanes;
+      const int c0 = m < row->pairs ? m : 2 * row->pairs + (m - row->pairs);
+      const int c1 = m < row->pairs ? m + row->pairs : c0 + row->rest2;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int c = z ? c1 : c0;
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) w[it][z][e] = 0u;
+        if (read && m < row->items && c < chunks) {
+          if (VEC == 8) *reinterpret_cast<uint4 *>(w[it][z]) = *reinterpret_cast<const uint4 *>(in + c * 16);
+          else *reinterpret_cast<uint2 *>(w[it][z]) = *reinterpret_cast<const uint2 *>(in + c * 8);
+        }
+      }
+    }
+    rh += kGroups;
+    while (rh >= nh) {
+      rh -= nh;
+      ++rt;
+    }
+  };
+  Row next;
+  load(&next);
+  if (tid < ntok && a.c.table) {
+    int b, i;
+    place(tid, &b, &i);
+    int64_t row = -1;
+    if (i < clamped_count(a.counts, b, a.n)) {
+      row = cache_row(a.c, b, static_cast<int64_t>(a.first[b]) + i, 0);
+      if (row < 0) cache_fault(a.c, b);
+    }
+    s_row[tid] = row;
+  }
   for (int u = tid; u < ntok * half; u += kThreads) {
     const int t = u / half, i = u - t * half;
     const int64_t p = a.positions[tk0 + t];
@@ -73,79 +159,67 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
     s_cs[(2 * t + 1) * half + i] = a.mag * s;
   }
   __syncthreads();
-  const int chunks = a.dh / VEC;
-  for (int r = grp; r < ntok * nh; r += kGroups) {
-    const int t = r / nh;
-    int h = h0 + (r - t * nh), k = 0;
-    while (k + 1 < a.nt && h >= a.t[k].heads) h -= a.t[k++].heads;
-    const View &vw = a.t[k];
-    const int64_t tk = tk0 + t;
-    const int b = static_cast<int>(tk / a.n), i = static_cast<int>(tk - static_cast<int64_t>(b) * a.n);
-    const char *in = vw.in + b * vw.ib + h * vw.ih + i * vw.ir;
-    char *out = vw.out;
-    uint8_t *expo = nullptr;
-    if (out) {
-      out += b * vw.ob + h * vw.oh + i * vw.orow;
-    } else {
-      if (i >= clamped_count(a.counts, b, a.n)) continue;
-      const int64_t row = cache_row(a.c, b, static_cast<int64_t>(a.first[b]) + i, h);
-      if (row < 0) {
-        cache_fault(a.c, b);
-        continue;
-      }
-      out = static_cast<char *>(vw.to_v ? a.c.v : a.c.k) + row * a.dh * (QUANT ? 1 : 2);
-      if (QUANT) expo = (vw.to_v ? a.c.v_exp : a.c.k_exp) + row;
-    }
-    const int pairs = vw.turned ? a.rot / (2 * VEC) : 0;      // chunk pairs of the turned part
-    const int rest = chunks - 2 * pairs, rest2 = (rest + 1) >> 1, items = pairs + rest2;
-    const float *cs = s_cs + 2 * t * half;
+  while (next.t < ntok) {
+    const Row cur = next;
+    const View &vw = a.t[cur.k];
+    const int pairs = cur.pairs, rest2 = cur.rest2, items = cur.items;
     float x[ITEMS][2][VEC];
 #pragma unroll
-    for (int it = 0; it < ITEMS; ++it) {
-      const int m = lane + it * kLanes;
-      const bool turn = m < pairs;
-      const int c0 = turn ? m : 2 * pairs + (m - pairs);
-      const int c1 = turn ? m + pairs : c0 + rest2;
+    for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const int c = z ? c1 : c0;
-        uint32_t w[VEC / 2];
-#pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) w[e] = 0u;
-        if (m < items && c < chunks) {
-          if (VEC == 8) *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(in + c * 16);
-          else *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(in + c * 8);
-        }
+      for (int z = 0; z < 2; ++z)
 #pragma unroll
         for (int e = 0; e < VEC / 2; ++e) {
-          const float2 f = Half16<DT>::unpack(w[e]);
+          const float2 f = Half16<DT>::unpack(w[it][z][e]);
           x[it][z][2 * e] = f.x;
           x[it][z][2 * e + 1] = f.y;
         }
-      }
-      if (turn && !a.interleaved) {
+    load(&next);
+    char *out = vw.out;
+    uint8_t *expo = nullptr;
+    if (out) {
+      int b, i;
+      place(cur.t, &b, &i);
+      out += b * vw.ob + cur.h * vw.oh + i * vw.orow;
+    } else {
+      if (s_row[cur.t] < 0) continue;
+      const int64_t row = s_row[cur.t] + (static_cast<int64_t>(cur.h) << a.c.shift);
+      out = static_cast<char *>(vw.to_v ? a.c.v : a.c.k) + row * a.dh * (QUANT ? 1 : 2);
+      if (QUANT) expo = (vw.to_v ? a.c.v_exp : a.c.k_exp) + row;
+    }
+    const float *cs = s_cs + 2 * cur.t * half;
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int m = lane + it * kLanes;
+      if (m >= pairs) continue;
+      if (!a.interleaved) {
+        float co[VEC], si[VEC];
+        load_f32<VEC>(cs + m * VEC, co);
+        load_f32<VEC>(cs + half + m * VEC, si);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float c = cs[m * VEC + e], s = cs[half + m * VEC + e];
           const float xa = x[it][0][e], xb = x[it][1][e];
-          x[it][0][e] = xa * c - xb * s;
-          x[it][1][e] = xa * s + xb * c;
+          x[it][0][e] = xa * co[e] - xb * si[e];
+          x[it][1][e] = xa * si[e] + xb * co[e];
         }
-      } else if (turn) {
+      } else {
 #pragma unroll
-        for (int z = 0; z < 2; ++z)
+        for (int z = 0; z < 2; ++z) {
+          float co[VEC / 2], si[VEC / 2];
+          const int p = (z ? m + pairs : m) * (VEC / 2);
+          load_f32<VEC / 2>(cs + p, co);
+          load_f32<VEC / 2>(cs + half + p, si);
 #pragma unroll
-          for (int e = 0; e < VEC; e += 2) {
-            const int p = ((z ? c1 : c0) * VEC + e) >> 1;
-            const float c = cs[p], s = cs[half + p];
-            const float xa = x[it][z][e], xb = x[it][z][e + 1];
-            x[it][z][e] = xa * c - xb * s;
-            x[it][z][e + 1] = xa * s + xb * c;
+          for (int e = 0; e < VEC / 2; ++e) {
+            const float xa = x[it][z][2 * e], xb = x[it][z][2 * e + 1];
+            x[it][z][2 * e] = xa * co[e] - xb * si[e];
+            x[it][z][2 * e + 1] = xa * si[e] + xb * co[e];
           }
+        }
       }
     }
     const bool quant = QUANT && !vw.out;
-    float scale = 1.0f, top = 448.0f;
+    float scale = 1.0f;
     bool whole = true;
     if (quant) {
       uint32_t mx = 0;   // of magnitude bits: NaN > infinity > finite
@@ -160,7 +234,15 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
       whole = mx < 0x7f800000u;
       const int e = row_exponent(__uint_as_float(mx));
       scale = exp2i(-e);
-      if (e == 120) top = 240.0f;   // 256 2^120 is no finite bf16 number
+      if (e == 120) {               // 256 2^120 is no finite bf16 number
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+          for (int y = 0; y < 2 * VEC; ++y) {
+            float &f = x[it][y / VEC][y % VEC];
+            f = fminf(fmaxf(f, -240.0f * 0x1p120f), 240.0f * 0x1p120f);
+          }
+      }
       if (lane == 0) *expo = static_cast<uint8_t>(whole ? e + 127 : 255);
     }
 #pragma unroll
@@ -177,10 +259,9 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_const
           uint32_t w[VEC / 4];
 #pragma unroll
           for (int e = 0; e < VEC; e += 4) {
-            float q[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) q[y] = fminf(fmaxf(f[e + y] * scale, -top), top);
-            w[e / 4] = whole ? e4m3_pack2(q[0], q[1]) | (e4m3_pack2(q[2], q[3]) << 16) : 0x7f7f7f7fu;
+            const uint32_t y = e4m3_pack2(f[e] * scale, f[e + 1] * scale) |
+                               (e4m3_pack2(f[e + 2] * scale, f[e + 3] * scale) << 16);
+            w[e / 4] = whole ? y : 0x7f7f7f7fu;
           }
           if (VEC == 8) *reinterpret_cast<uint2 *>(out + c * 8) = make_uint2(w[0], w[VEC / 4 - 1]);
           else *reinterpret_cast<uint32_t *>(out + c * 4) = w[0];
@@ -346,20 +427,25 @@ cudaError_t launch_rows(const RowArgs &a, cudaStream_t st) {
   return a.dh <= 128 ? go(cache_rows_kernel<DT, QUANT, 4, 2>) : go(cache_rows_kernel<DT, QUANT, 4, 4>);
 }
 
-// Tokens and heads of a block: where there are too few head rows to fill the GPU
-// with blocks of 32 rows (one for each group of lanes), one token's heads are cut
-// over blocks; else a block takes four tokens, so that a launch's angles are
-// computed once and its blocks stay few.
-void split_rows(RowArgs *a) {
+// Tokens and heads of a block: where there are too few head rows to fill the GPU with
+// blocks of 32 rows (one for each group of lanes), one token's heads are cut over blocks;
+// else a block takes as many tokens (up to 32) as let all blocks run at once, four an SM,
+// so that angles and places are found once for a token and no SM waits for a last block.
+int split_rows(RowArgs *a) {
   const int64_t rows = static_cast<int64_t>(a->batch) * a->n * a->heads;
+  a->tokens_block = 1;
+  a->heads_block = a->heads;
   if (rows < static_cast<int64_t>(kGroups) * 2048) {
-    a->tokens_block = 1;
     a->heads_block = a->heads < kGroups ? a->heads : kGroups;
   } else {
-    a->tokens_block = 4;
-    a->heads_block = a->heads;
+    int sms, smem;
+    const int rc = device_sm_count(&sms, &smem);
+    if (rc) return rc;
+    const int64_t tokens = static_cast<int64_t>(a->batch) * a->n, at_once = int64_t{4} * sms;
+    a->tokens_block = static_cast<int>(std::min<int64_t>(kBlockTokens, (tokens + at_once - 1) / at_once));
   }
   a->head_blocks = (a->heads + a->heads_block - 1) / a->heads_block;
+  return DT_OK;
 }
 
 bool set_in(View *v, const dt_heads *x) {
@@ -469,7 +555,8 @@ int dt_rotary(const dt_rotation *rot, const int32_t *positions, int batch, int n
     a.t[i].turned = 1;
     a.heads += a.t[i].heads;
   }
-  dt::split_rows(&a);
+  const int rc = dt::split_rows(&a);
+  if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == DT_BF16 ? dt::launch_rows<DT_BF16, false>(a, st)
                                          : dt::launch_rows<DT_F16, false>(a, st);
@@ -504,7 +591,8 @@ int dt_cache_write(const dt_cache *c, const dt_heads *k, const dt_heads *v, int 
     a.t[2].turned = 1;
     a.heads += q->heads;
   }
-  dt::split_rows(&a);
+  const int rc = dt::split_rows(&a);
+  if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool quant = c->dtype == DT_E4M3;
   const cudaError_t e =

@@ -543,12 +543,12 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
             tmem_wait_st();
           }
         }
-        // the weights, written over the scores' first half (each chunk behind its own scores)
+        // the weights, written over the scores: 8 columns a chunk from the first on, or, of two
+        // terms, over the chunk's own 16 columns
         {
           const float nm = m == ninf ? 0.0f : kShift - m;
           const uint64_t nm2 = pair(nm, nm);
           float s0[16], s1[16];
-          uint32_t lo[TWO ? 64 : 1];    // second terms, until all scores are read
           tmem_ld16(t_s, s0);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -558,7 +558,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
               if (c & 1) tmem_ld16(t_s + 16 * c + 16, s0);
               else tmem_ld16(t_s + 16 * c + 16, s1);
             }
-            uint32_t y[8];
+            uint32_t y[8], lo[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               float p0, p1;
@@ -569,20 +569,13 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
               y[e] = Half16<VDT>::pack(p0, p1);
               if (TWO) {
                 const float2 hi = Half16<VDT>::unpack(y[e]);
-                lo[TWO ? 8 * c + e : 0] = Half16<VDT>::pack(p0 - hi.x, p1 - hi.y);
+                lo[e] = Half16<VDT>::pack(p0 - hi.x, p1 - hi.y);
               }
             }
-            // (the next chunk's scores are being read: columns 16 c + 16 on, past 8 c + 7)
-            tmem_st8(t_s + 8 * c, y);
+            // (the next chunk's scores are being read: columns 16 c + 16 on)
+            tmem_st8(t_s + (TWO ? 16 : 8) * c, y);
+            if (TWO) tmem_st8(t_s + 16 * c + 8, lo);
           }
-          if (TWO)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = lo[TWO ? 8 * c + e : 0];
-              tmem_st8(t_s + 64 + 8 * c, y);
-            }
           tmem_wait_st();
         }
         tmem_fence_before();
@@ -735,6 +728,26 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
                   codes_bf16x2(spread_codes<0>(q.w), mul), codes_bf16x2(spread_codes<1>(q.w), mul)};
               put_operand(row, ct, c, y);
             }
+          } else if (DT == DT_F16 && !mine_v && E >= 103u && E <= 134u) {
+            // 2^(E - 127) and the codes are fp16 numbers, and no product is above 448 2^7: one
+            // multiplication rounds as dt_cache_read does
+            uint32_t mul = E >= 113u ? (E - 112u) << 10 : 1u << (E - 103u);
+            mul |= mul << 16;
+            const __half2 mul2 = *reinterpret_cast<const __half2 *>(&mul);
+            auto times = [&](uint32_t two) {
+              const uint32_t f = e4m3_f16x2(two);
+              const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&f), mul2);
+              return *reinterpret_cast<const uint32_t *>(&r);
+            };
+#pragma unroll 4
+            for (int i = 0; i < 8; ++i) {
+              const int c = (i + ct) & 7;
+              if (c >= dh >> 4) continue;
+              const uint4 q = *reinterpret_cast<const uint4 *>(src + c * 16);
+              const uint32_t y[8] = {times(q.x & 0xffffu), times(q.x >> 16), times(q.y & 0xffffu), times(q.y >> 16),
+                                     times(q.z & 0xffffu), times(q.z >> 16), times(q.w & 0xffffu), times(q.w >> 16)};
+              put_operand(row, ct, c, y);
+            }
           } else {
             const float sc = row_scale(E);
 #pragma unroll 2
@@ -847,11 +860,11 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kW / 16; ++k)
-            umma_ts(tmem + 256 + 128 * X, tmem + 128 * X + 8 * k, vd + k * 128, id_o, more || k > 0);
+            umma_ts(tmem + 256 + 128 * X, tmem + 128 * X + (TWO ? 16 : 8) * k, vd + k * 128, id_o, more || k > 0);
           if (TWO)
 #pragma unroll
             for (int k = 0; k < kW / 16; ++k)
-              umma_ts(tmem + 256 + 128 * X, tmem + 128 * X + 64 + 8 * k, vd + k * 128, id_o, true);
+              umma_ts(tmem + 256 + 128 * X, tmem + 128 * X + 16 * k + 8, vd + k * 128, id_o, true);
           if (last) umma_commit(&ss.o_done[X]);
           if (free) umma_commit(&ss.empty[s]);
         }

@@ -7,7 +7,7 @@
 // log2(e) (-inf where the row does not see the key), m' = max(m, max x),
 // p = 2^(x - m'), l = l 2^(m - m') + sum p, O = O 2^(m - m') + p V; out = O / l. Sums, m, l
 // and O are fp32; p is rounded to the 16-bit type for the product with V (bf16:
-// relative 2^-9; fp16 2^-11, p scaled by 2^12 so that small weights stay normal
+// relative 2^-8; fp16 2^-11, p scaled by 2^12 so that small weights stay normal
 // numbers), l sums the unrounded p.
 #include <cmath>
 #include <cstdint>
@@ -440,11 +440,11 @@ cudaError_t launch_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <int DT, bool QUANT, int DH>
-cudaError_t launch_bm(const AttnArgs &a, int bm, cudaStream_t st) {
-  return bm == 16   ? launch_narrow<DT, QUANT, DH, 4>(a, st)
-         : bm == 32 ? launch_narrow<DT, QUANT, DH, 2>(a, st)
-                    : launch_narrow<DT, QUANT, DH, 1>(a, st);
+template <int DT, bool QUANT>
+cudaError_t launch_any(const AttnArgs &a, int bm, cudaStream_t st) {
+  return bm == 16   ? launch_narrow<DT, QUANT, 256, 4>(a, st)
+         : bm == 32 ? launch_narrow<DT, QUANT, 256, 2>(a, st)
+                    : launch_narrow<DT, QUANT, 256, 1>(a, st);
 }
 
 int64_t slot_floats(const AttnPlan &p) {
@@ -511,7 +511,7 @@ int dt_cache_attention(const dt_cache *c, const dt_heads *q, int n, int dtype,
   a.part = reinterpret_cast<float *>(a.cut + 2 * p.grid);
   // (a scale of zero: all weights equal, and -inf times it still -inf)
   a.scale_log2 = scale == 0.0f ? 1e-38f : scale * 1.4426950408889634f;
-  a.batch = c->batch; a.n = n; a.H = q->heads; a.G = G;
+  a.batch = c->batch; a.n = n; a.G = G;
   a.row_tiles = p.row_tiles; a.grid = p.grid; a.min_tiles = 2;
   a.slot = dt::slot_floats(p);
   a.odd = p.odd;
@@ -524,8 +524,8 @@ int dt_cache_attention(const dt_cache *c, const dt_heads *q, int n, int dtype,
   cudaError_t e =
       wide ? dt::launch_wide(*c, a, dtype, p, st)
       : p.kind == dt::AttnPlan::kFew ? dt::launch_few(*c, a, dtype, p, st)
-      : dtype == DT_BF16 ? (quant ? dt::launch_bm<DT_BF16, true, 256>(a, p.bm, st) : dt::launch_bm<DT_BF16, false, 256>(a, p.bm, st))
-                         : (quant ? dt::launch_bm<DT_F16, true, 256>(a, p.bm, st) : dt::launch_bm<DT_F16, false, 256>(a, p.bm, st));
+      : dtype == DT_BF16 ? (quant ? dt::launch_any<DT_BF16, true>(a, p.bm, st) : dt::launch_any<DT_BF16, false>(a, p.bm, st))
+                         : (quant ? dt::launch_any<DT_F16, true>(a, p.bm, st) : dt::launch_any<DT_F16, false>(a, p.bm, st));
   if (e == cudaSuccess)
     e = dtype == DT_BF16 ? dt::launch_join<DT_BF16>(a, p, st) : dt::launch_join<DT_F16>(a, p, st);
   return e == cudaSuccess ? DT_OK : DT_ERR_CUDA;

@@ -35,7 +35,7 @@ struct AttnArgs {
   int odd;               // the last row tile's units are shared so
   int64_t slot;          // fp32 numbers of one part, a multiple of 8
   float scale_log2;      // scale times log2(e)
-  int batch, n, H, G, row_tiles, grid, min_tiles;
+  int batch, n, G, row_tiles, grid, min_tiles;
   int weight, last_weight, lead;      // of a key tile, of one of the last row tile, of a unit
   int4 *cut;             // [grid][2]: the unit that a block's part of the line begins within
 };

@@ -66,7 +66,10 @@ __device__ __forceinline__ void load_f32(const float *p, float *x) {
 // tensor can be turned in place; interleaved: any other chunk). 8-bit rows need the
 // row's largest magnitude before the first code, so a lane keeps its values in
 // registers. Bound by memory: a lane's next row is loaded (its first one before the
-// angles are known) while the one before it is turned and written.
+// angles are known) while the one before it is turned and written. Measured, dh 128: two
+// prompts of 4099 tokens, 40 heads, fp16, 64 of 128 values turned, 33 us, 5.1 TB/s; 15009
+// tokens of 16 heads to 8-bit rows 25 us, 3.7 TB/s (scaling and packing take half of the
+// issue slots); 8 tokens 4.2 us.
 template <int DT, bool QUANT, int VEC, int ITEMS>
 __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_constant__ RowArgs a) {
   extern __shared__ __align__(16) float s_cs[];      // [tokens_block][2][rot / 2]
@@ -289,7 +292,8 @@ constexpr int kReadRows = 64;        // rows of a block, of one head
 
 // Rows of the cache to dense views. A block takes 64 rows of one (request, head):
 // their places once into shared memory, then 8 values a lane, four rows of K and
-// of V in flight a lane.
+// of V in flight a lane. Bound by memory: 8 requests of 9000 to 16385 rows, 8 heads, dh 128,
+// from 8-bit rows to bf16 119 us, 6.3 TB/s.
 template <int DT, bool QUANT>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadArgs a) {
   __shared__ int64_t s_row[kReadRows];
@@ -365,7 +369,8 @@ constexpr int kMaxPath = DT_MAX_D + 1;
 
 // One block per (request, head, K or V): all rows of the path into shared memory,
 // a barrier, then to their new places. Paths rise, but nothing relies on it.
-// Bound by latency: 16 KB or less a block.
+// Bound by latency: 16 KB or less a block; 32 paths of up to 17 rows 4.4 us, 128 16 us with
+// the rows read back.
 __global__ void __launch_bounds__(kThreads) cache_commit_kernel(const __grid_constant__ CommitArgs a) {
   __shared__ int64_t s_from[kMaxPath], s_to[kMaxPath];
   __shared__ uint8_t s_exp[kMaxPath];
@@ -431,6 +436,9 @@ cudaError_t launch_rows(const RowArgs &a, cudaStream_t st) {
 // blocks of 32 rows (one for each group of lanes), one token's heads are cut over blocks;
 // else a block takes as many tokens (up to 32) as let all blocks run at once, four an SM,
 // so that angles and places are found once for a token and no SM waits for a last block.
+// (Measured at four, five and six an SM, the latter two at fewer registers: the prompts
+// above 33, 33 and 41 us, the 8-bit rows 25.3, 26.0 and 30.5 us. Four tokens a block
+// whatever the size: 37 and 30 us.)
 int split_rows(RowArgs *a) {
   const int64_t rows = static_cast<int64_t>(a->batch) * a->n * a->heads;
   a->tokens_block = 1;

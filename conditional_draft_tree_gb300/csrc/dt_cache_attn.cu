@@ -12,8 +12,8 @@
 //
 // Products are mma.sync m16n8k16, a warp's 16 rows by the tile's keys, and the copies of
 // the next tile run during this one's. Measured at head size 256, 16 requests at 4096 keys,
-// 16 / 4 heads: single tokens 129 us (2.1 TB/s of bf16 rows; 8-bit rows 332 us), trees of 16
-// rows 287 us, of 65 rows 1.23 ms (57 TFLOP/s; 8-bit rows 2.0 ms). Bound by latency: four
+// 16 / 4 heads: single tokens 90 us (3.0 TB/s of bf16 rows; 8-bit rows 156 us), trees of 16
+// rows 244 us, of 65 rows 0.98 ms (71 TFLOP/s; 8-bit rows 1.28 ms). Bound by latency: four
 // warps a block, one block an SM at this head size, and 8-bit rows converted in between.
 #include <cmath>
 #include <cstdint>
@@ -88,6 +88,7 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ int64_t s_scan[kNThreads / 32 + 2];
   __shared__ int s_bad, s_odd;
+  __shared__ uint8_t s_exp[2][2][kT];
   unsigned char *sStage = sm;                                  // [2][K, V][kT][RB]
   unsigned char *sDeq = sStage + 4 * kT * RB;                  // [K, V][kT][DH] 16-bit
   unsigned char *sQ = sDeq + (QUANT ? 2 * kT * DH * 2 : 0);    // [BM][DH]
@@ -136,27 +137,46 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
       tok[y] = gr / a.G;
       live[y] = gr < rows && tok[y] < rq.count;
     }
+    // A warp copies 16 rows of the tile, kRows at a time: lane k < 16 looks the k-th of them
+    // up, and (8-bit rows) loads its exponents, which note() leaves in shared memory.
+    constexpr int CR = RB / 16, kRows = 32 / CR;         // 16-byte chunks of a row
+    auto row_of = [&](int k) { return (kNThreads / 32 * (k / kRows) + warp) * kRows + k % kRows; };
+    uint32_t ek = 127u, ev = 127u;
     auto stage = [&](int t) {
-      constexpr int CR = RB / 16;          // 16-byte chunks of a row
       unsigned char *sk = sStage + (t & 1) * 2 * kT * RB, *sv = sk + kT * RB;
-      for (int u = tid; u < kT * CR; u += kNThreads) {
-        const int r = u / CR, c = u - r * CR;
-        const int64_t j = static_cast<int64_t>(t) * kT + r;
-        int64_t row = -1;
-        if (j < end && c * 16 < dh * (QUANT ? 1 : 2)) {
-          row = cache_row(a.c, b, j, hk);
-          if (row < 0) {
-            s_bad = 1;
-            cache_fault(a.c, b);
-          }
+      const int64_t j = static_cast<int64_t>(t) * kT + row_of(lane & 15);
+      int64_t mine = -1;
+      if (j < end) {
+        mine = cache_row(a.c, b, j, hk);
+        if (mine < 0) {
+          s_bad = 1;
+          cache_fault(a.c, b);
         }
-        const int64_t off = row < 0 ? 0 : row * dh * (QUANT ? 1 : 2) + c * 16;
-        const uint32_t n16 = row < 0 ? 0u : 16u;
+      }
+      if (QUANT) {
+        ek = mine < 0 ? 127u : a.c.k_exp[mine];
+        ev = mine < 0 ? 127u : a.c.v_exp[mine];
+      }
+      const int c = lane % CR;
+      const bool column = c * 16 < dh * (QUANT ? 1 : 2);
+#pragma unroll
+      for (int i = 0; i < 16 / kRows; ++i) {
+        const int k = i * kRows + lane / CR, r = row_of(k);
+        const int64_t row = __shfl_sync(kFull, mine, k);
+        const bool read = row >= 0 && column;
+        const int64_t off = read ? row * dh * (QUANT ? 1 : 2) + c * 16 : 0;
+        const uint32_t n16 = read ? 16u : 0u;
         const uint32_t to = QUANT ? static_cast<uint32_t>(r * RB + c * 16) : swz<DH>(r, c);
         cp_async16(sk + to, static_cast<const char *>(a.c.k) + off, n16);
         cp_async16(sv + to, static_cast<const char *>(a.c.v) + off, n16);
       }
       cp_async_commit();
+    };
+    auto note = [&](int t) {
+      if (QUANT && lane < 16) {
+        s_exp[t & 1][0][row_of(lane)] = static_cast<uint8_t>(ek);
+        s_exp[t & 1][1][row_of(lane)] = static_cast<uint8_t>(ev);
+      }
     };
 
     float o[DH / 8][4];
@@ -167,6 +187,7 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
     float m[2] = {ninf, ninf}, l[2] = {0.0f, 0.0f};
 
     stage(t0);
+    note(t0);
     for (int t = t0; t < t1; ++t) {
       if (t + 1 < t1) {
         stage(t + 1);
@@ -179,19 +200,17 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
       unsigned char *sK = sStage + (t & 1) * 2 * kT * RB, *sV = sK + kT * RB;
       const int64_t j0 = static_cast<int64_t>(t) * kT;
       if (QUANT) {   // codes to 16-bit values
+        // (a row that is not there, or a column past dh, has codes of zero)
+#pragma unroll 4
         for (int u = tid; u < 2 * kT * C8; u += kNThreads) {
           const int which = u / (kT * C8), r = (u / C8) % kT, c = u % C8;
-          const int64_t j = j0 + r;
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          const int64_t row = j < end && c * 8 < dh ? cache_row(a.c, b, j, hk) : -1;
-          if (row >= 0) {
-            const float sc = row_scale((which ? a.c.v_exp : a.c.k_exp)[row]);
-            const uint2 q = *reinterpret_cast<const uint2 *>((which ? sV : sK) + r * RB + c * 8);
-            w.x = e4m3_to16<DT>(q.x & 0xffffu, sc);
-            w.y = e4m3_to16<DT>(q.x >> 16, sc);
-            w.z = e4m3_to16<DT>(q.y & 0xffffu, sc);
-            w.w = e4m3_to16<DT>(q.y >> 16, sc);
-          }
+          const float sc = row_scale(s_exp[t & 1][which][r]);
+          const uint2 q = *reinterpret_cast<const uint2 *>((which ? sV : sK) + r * RB + c * 8);
+          uint4 w;
+          w.x = e4m3_to16<DT>(q.x & 0xffffu, sc);
+          w.y = e4m3_to16<DT>(q.x >> 16, sc);
+          w.z = e4m3_to16<DT>(q.y & 0xffffu, sc);
+          w.w = e4m3_to16<DT>(q.y >> 16, sc);
           *reinterpret_cast<uint4 *>(sDeq + which * kT * DH * 2 + swz<DH>(r, c)) = w;
         }
         __syncthreads();
@@ -313,6 +332,7 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
             }
         }
       }
+      if (t + 1 < t1) note(t + 1);
       __syncthreads();   // the stage is free
     }
 

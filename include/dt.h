@@ -418,9 +418,9 @@ int dt_rotary(const dt_rotation *rot, const int32_t *positions, int batch, int n
  *
  * status [batch] int32 (device) is the caller's, zeroed once: a call writes
  * DT_ERR_BAD_PAGE for a request with a row outside its table or whose page
- * number is outside the pool, DT_ERR_TIMEOUT where a bounded wait of the attention
- * kernel ran out (its output is then invalid), and nothing else. Rows on bad pages are not written, read
- * as zeros and are not attended to.
+ * number is outside the pool, DT_ERR_TIMEOUT where a bounded wait of the
+ * attention kernel ran out (its output is then invalid), and nothing else. Rows
+ * on bad pages are not written, read as zeros and are not attended to.
  * `first` [batch] is the row index at which a call's rows start and counts
  * [batch] (NULL: n for all) how many of its n rows a request has (clamped into
  * [0, n]). */
@@ -470,7 +470,7 @@ int dt_cache_commit(const dt_cache *c, const int32_t *first, const int32_t *path
  * head h / (H / Hkv)) and n rows, of type dtype (DT_BF16 or DT_F16; the cache's
  * own, or either for a DT_E4M3 cache). n <= DT_MAX_N + 1 with a mask, n <= 65536
  * without. Products are accumulated in fp32 and the softmax statistics are fp32; its
- * weights are rounded to the 16-bit type for the product with v (bf16: relative 2^-9
+ * weights are rounded to the 16-bit type for the product with v (bf16: relative 2^-8
  * each, as the output's own rounding). A DT_E4M3 cache's values are taken as they are,
  * those of k with dtype DT_F16 as dt_cache_read gives them.
  * workspace: dt_cache_attention_workspace_bytes bytes, 256-byte aligned, for the

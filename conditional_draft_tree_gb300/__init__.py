@@ -8,6 +8,7 @@ every call raises: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from dataclasses import dataclass
@@ -531,6 +532,10 @@ def adaptive_budget(out: dict, N: int, c_fixed: float, c_node: float, counts=Non
 
 
 # --------------------------------- rotary positions and the paged key/value cache
+#
+# A call runs on ``stream`` (the current one when None), and the tensors that it makes belong
+# to that stream, as under torch.cuda.stream(stream): use them on another stream after waiting
+# for this one, and record_stream them there.
 
 _TYPE16 = {torch.bfloat16: BF16, torch.float16: F16}
 
@@ -562,8 +567,16 @@ def _ints(t, what: str, shape, dev):
     return t.data_ptr()
 
 
-def _dense_like(t):
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+def _made_on(stream):
+    """Where a call makes its tensors: on the stream that its kernels run on, whose part of the
+    caching allocator they then belong to. Memory of another stream's part may still be in
+    use there, and would be handed out again there while the kernels run."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _dense_like(t, stream):
+    with _made_on(stream):
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _raw_stream(stream, dev):
@@ -602,14 +615,14 @@ def rotary(rot: Rotary, positions, q, k=None, q_out=None, k_out=None, gradient=F
     batch, _, n, dh = shape
     x0 = _heads(q, "q", shape, dtype, dev)
     if q_out is None:
-        q_out = _dense_like(q)
+        q_out = _dense_like(q, stream)
     o0 = _heads(q_out, "q_out", shape, dtype, dev)
     x1 = o1 = None
     if k is not None:
         kshape = torch.Size((batch, k.shape[1], n, dh))
         x1 = _heads(k, "k", kshape, dtype, dev)
         if k_out is None:
-            k_out = _dense_like(k)
+            k_out = _dense_like(k, stream)
         o1 = _heads(k_out, "k_out", kshape, dtype, dev)
     _check(lib().dt_rotary(rot._struct, _ints(positions, "positions", (batch, n), dev), batch, n, dh,
                            dtype, x0, o0, x1, o1, int(gradient), _raw_stream(stream, dev)),
@@ -684,7 +697,7 @@ def cache_write(cache: PagedCache, k, v, first, counts=None, rotary: Rotary | No
         qshape = torch.Size((cache.batch, q.shape[1], n, cache.dh))
         hq = _heads(q, "q", qshape, dtype, dev)
         if q_out is None:
-            q_out = _dense_like(q)
+            q_out = _dense_like(q, stream)
         ho = _heads(q_out, "q_out", qshape, dtype, dev)
     _check(lib().dt_cache_write(cache._struct, hk, hv, n, dtype, _ints(first, "first", b, dev),
                                 _ints(counts, "counts", b, dev),
@@ -702,10 +715,11 @@ def cache_read(cache: PagedCache, n: int, first, counts=None, dtype=None, k_out=
     if dtype is None:
         dtype = cache.k.dtype if cache.k.dtype in _TYPE16 else torch.bfloat16
     shape, dev = torch.Size((cache.batch, cache.Hkv, n, cache.dh)), cache._dev
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=cache.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=k_out.dtype, device=cache.device)
+    with _made_on(stream):
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=cache.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=k_out.dtype, device=cache.device)
     ctype = _shape(k_out, "k_out")[1]
     hk, hv = _heads(k_out, "k_out", shape, ctype, dev), _heads(v_out, "v_out", shape, ctype, dev)
     b = (cache.batch,)
@@ -725,12 +739,13 @@ def cache_commit(cache: PagedCache, first, path, lengths, n: int, stream=None):
                                  _raw_stream(stream, dev)), "dt_cache_commit")
 
 
-def cache_attention_workspace(cache: PagedCache, H: int, n: int):
-    """A workspace for cache_attention with H query heads and n rows."""
+def cache_attention_workspace(cache: PagedCache, H: int, n: int, stream=None):
+    """A workspace for cache_attention with H query heads and n rows, for calls on ``stream``."""
     nbytes = lib().dt_cache_attention_workspace_bytes(cache._struct, int(H), int(n))
     if nbytes == 0:
         raise DtError("dt_cache_attention_workspace_bytes failed (invalid sizes or unsupported device)")
-    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    with _made_on(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
 
 
 def cache_attention(cache: PagedCache, q, prefix_len, mask=None, counts=None, scale=None, out=None,
@@ -749,10 +764,10 @@ def cache_attention(cache: PagedCache, q, prefix_len, mask=None, counts=None, sc
         raise ValueError(f"mask must be a contiguous uint8 tensor of shape {(batch, n, n)}")
     hq = _heads(q, "q", shape, dtype, dev)
     if out is None:
-        out = _dense_like(q)
+        out = _dense_like(q, stream)
     ho = _heads(out, "out", shape, dtype, dev)
     if workspace is None:
-        workspace = cache_attention_workspace(cache, H, n)
+        workspace = cache_attention_workspace(cache, H, n, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     _check(lib().dt_cache_attention(cache._struct, hq, n, dtype,

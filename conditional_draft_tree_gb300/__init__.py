@@ -580,8 +580,17 @@ def _dense_like(t, stream):
 
 
 def _raw_stream(stream, dev):
-    """The stream's handle: the current one of the tensors' device by default."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    """The stream's handle: the current one of the tensors' device by default. The library
+    launches on the thread's current device and sizes its grids for it, so that the tensors
+    and the stream have to be of that one."""
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on device {dev}, which is not the current device "
+                         "(torch.cuda.device makes it that)")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError("stream is not of the tensors' device")
+    return stream.cuda_stream
 
 
 class Rotary:
@@ -602,8 +611,17 @@ class Rotary:
         _check(lib().dt_rotary_table(C.byref(p), host, C.byref(mag)), "dt_rotary_table")
         self.rot, self.interleaved, self.magnitude = int(rot), bool(interleaved), mag.value
         self.turns = torch.frombuffer(bytearray(host), dtype=torch.int64).to(device)
+        self._dev = self.turns.get_device()
         self._struct = DtRotation(self.turns.data_ptr(), self.rot, int(self.interleaved),
                                   self.magnitude)
+
+
+def _rotation(rot: Rotary | None, dev):
+    if rot is None:
+        return None
+    if rot._dev != dev:
+        raise ValueError("the rotary table must be on the tensors' device")
+    return rot._struct
 
 
 def rotary(rot: Rotary, positions, q, k=None, q_out=None, k_out=None, gradient=False, stream=None):
@@ -613,6 +631,7 @@ def rotary(rot: Rotary, positions, q, k=None, q_out=None, k_out=None, gradient=F
     q_out alone without k."""
     shape, dtype, dev = _shape(q, "q")
     batch, _, n, dh = shape
+    table, handle = _rotation(rot, dev), _raw_stream(stream, dev)
     x0 = _heads(q, "q", shape, dtype, dev)
     if q_out is None:
         q_out = _dense_like(q, stream)
@@ -624,9 +643,8 @@ def rotary(rot: Rotary, positions, q, k=None, q_out=None, k_out=None, gradient=F
         if k_out is None:
             k_out = _dense_like(k, stream)
         o1 = _heads(k_out, "k_out", kshape, dtype, dev)
-    _check(lib().dt_rotary(rot._struct, _ints(positions, "positions", (batch, n), dev), batch, n, dh,
-                           dtype, x0, o0, x1, o1, int(gradient), _raw_stream(stream, dev)),
-           "dt_rotary")
+    _check(lib().dt_rotary(table, _ints(positions, "positions", (batch, n), dev), batch, n, dh,
+                           dtype, x0, o0, x1, o1, int(gradient), handle), "dt_rotary")
     return q_out if k is None else (q_out, k_out)
 
 
@@ -691,6 +709,7 @@ def cache_write(cache: PagedCache, k, v, first, counts=None, rotary: Rotary | No
     n, b = shape[2], (cache.batch,)
     if shape != (cache.batch, cache.Hkv, n, cache.dh) or dev != cache._dev:
         raise ValueError("k does not match the cache's batch, heads, head size or device")
+    table, handle = _rotation(rotary, dev), _raw_stream(stream, dev)
     hk, hv = _heads(k, "k", shape, dtype, dev), _heads(v, "v", shape, dtype, dev)
     hq = ho = None
     if q is not None:
@@ -700,10 +719,9 @@ def cache_write(cache: PagedCache, k, v, first, counts=None, rotary: Rotary | No
             q_out = _dense_like(q, stream)
         ho = _heads(q_out, "q_out", qshape, dtype, dev)
     _check(lib().dt_cache_write(cache._struct, hk, hv, n, dtype, _ints(first, "first", b, dev),
-                                _ints(counts, "counts", b, dev),
-                                rotary._struct if rotary is not None else None,
+                                _ints(counts, "counts", b, dev), table,
                                 _ints(positions, "positions", (cache.batch, n), dev),
-                                hq, ho, _raw_stream(stream, dev)), "dt_cache_write")
+                                hq, ho, handle), "dt_cache_write")
     return q_out
 
 
@@ -715,6 +733,7 @@ def cache_read(cache: PagedCache, n: int, first, counts=None, dtype=None, k_out=
     if dtype is None:
         dtype = cache.k.dtype if cache.k.dtype in _TYPE16 else torch.bfloat16
     shape, dev = torch.Size((cache.batch, cache.Hkv, n, cache.dh)), cache._dev
+    handle = _raw_stream(stream, dev)
     with _made_on(stream):
         if k_out is None:
             k_out = torch.empty(shape, dtype=dtype, device=cache.device)
@@ -724,8 +743,7 @@ def cache_read(cache: PagedCache, n: int, first, counts=None, dtype=None, k_out=
     hk, hv = _heads(k_out, "k_out", shape, ctype, dev), _heads(v_out, "v_out", shape, ctype, dev)
     b = (cache.batch,)
     _check(lib().dt_cache_read(cache._struct, n, ctype, _ints(first, "first", b, dev),
-                               _ints(counts, "counts", b, dev), hk, hv, _raw_stream(stream, dev)),
-           "dt_cache_read")
+                               _ints(counts, "counts", b, dev), hk, hv, handle), "dt_cache_read")
     return k_out, v_out
 
 
@@ -741,6 +759,7 @@ def cache_commit(cache: PagedCache, first, path, lengths, n: int, stream=None):
 
 def cache_attention_workspace(cache: PagedCache, H: int, n: int, stream=None):
     """A workspace for cache_attention with H query heads and n rows, for calls on ``stream``."""
+    _raw_stream(stream, cache._dev)      # the size follows the current device's SMs
     nbytes = lib().dt_cache_attention_workspace_bytes(cache._struct, int(H), int(n))
     if nbytes == 0:
         raise DtError("dt_cache_attention_workspace_bytes failed (invalid sizes or unsupported device)")
@@ -758,6 +777,7 @@ def cache_attention(cache: PagedCache, q, prefix_len, mask=None, counts=None, sc
     batch, H, n, dh = shape
     if batch != cache.batch or dh != cache.dh or dev != cache._dev:
         raise ValueError("q does not match the cache's batch, head size or device")
+    handle = _raw_stream(stream, dev)
     if mask is not None and (mask.shape != (batch, n, n) or not mask.is_contiguous() or
                              mask.dtype not in (torch.uint8, torch.bool) or
                              mask.get_device() != dev):
@@ -774,6 +794,6 @@ def cache_attention(cache: PagedCache, q, prefix_len, mask=None, counts=None, sc
                                     _ints(prefix_len, "prefix_len", (batch,), dev),
                                     _ints(counts, "counts", (batch,), dev), _ptr(mask),
                                     dh ** -0.5 if scale is None else scale, ho, workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(),
-                                    _raw_stream(stream, dev)), "dt_cache_attention")
+                                    workspace.numel() * workspace.element_size(), handle),
+           "dt_cache_attention")
     return out

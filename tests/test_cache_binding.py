@@ -123,3 +123,46 @@ def test_a_workspace_of_a_call_is_made_on_the_stream_that_uses_it(lib, monkeypat
     stream = stream_of()
     dt.cache_attention(cache_of(), heads(), ints(BATCH), out=heads(), stream=stream)
     assert [t.made_on for t in made] == [stream]
+
+
+# every entry point, on tensors of device `dev`
+ON = {
+    "rotary": lambda dev, s=None: dt.rotary(rotation(dev), ints(BATCH, N, dev=dev), heads(dev=dev), stream=s),
+    "write": lambda dev, s=None: dt.cache_write(cache_of(dev), heads(HKV, dev), heads(HKV, dev), ints(BATCH, dev=dev),
+                                                stream=s),
+    "read": lambda dev, s=None: dt.cache_read(cache_of(dev), N, ints(BATCH, dev=dev), k_out=heads(HKV, dev),
+                                              v_out=heads(HKV, dev), stream=s),
+    "commit": lambda dev, s=None: dt.cache_commit(cache_of(dev), ints(BATCH, dev=dev), ints(BATCH, 4, dev=dev),
+                                                  ints(BATCH, dev=dev), N, stream=s),
+    "attention": lambda dev, s=None: dt.cache_attention(cache_of(dev), heads(dev=dev), ints(BATCH, dev=dev), stream=s),
+    "workspace": lambda dev, s=None: dt.cache_attention_workspace(cache_of(dev), H, N, stream=s),
+}
+
+
+@pytest.mark.parametrize("call", ON)
+def test_tensors_off_the_current_device_are_refused(lib, call):
+    with pytest.raises(ValueError, match="current device"):
+        ON[call](1)
+    assert not lib.calls
+    with pytest.raises(ValueError, match="stream"):
+        ON[call](0, stream_of(1))
+    assert not lib.calls
+    ON[call](0, stream_of(0))
+    assert lib.calls
+
+
+@pytest.mark.parametrize("dev", [-1, 1])
+def test_a_rotary_table_on_another_device_is_refused(lib, dev):
+    """-1: a table left on the host, whose address a kernel cannot read."""
+    with pytest.raises(ValueError, match="rotary table"):
+        dt.rotary(rotation(dev), ints(BATCH, N), heads())
+    with pytest.raises(ValueError, match="rotary table"):
+        dt.cache_write(cache_of(), heads(HKV), heads(HKV), ints(BATCH), rotary=rotation(dev), positions=ints(BATCH, N))
+    assert not lib.calls
+
+
+def test_a_rotary_table_knows_its_device():
+    from conditional_draft_tree_gb300 import build
+    build.build()
+    r = dt.Rotary(64, device="cpu")
+    assert r._dev == r.turns.get_device() == -1

@@ -114,11 +114,11 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
     const int64_t end = sg.end;
     const int rows = a.n * a.G;
 
+    // (s_bad was last read before the barrier that ended the last unit's last tile; cleared
+    // before this one, it cannot be cleared after a warp's stage() has set it)
+    if (tid == 0) s_bad = 0;
     __syncthreads();   // the last unit's shared memory is free
-    if (tid == 0) {
-      s_bad = 0;
-      if (a.prefix[b] != rq.pre) cache_fault(a.c, b);
-    }
+    if (tid == 0 && a.prefix[b] != rq.pre) cache_fault(a.c, b);
     for (int u = tid; u < BM * C8; u += kNThreads) {
       const int r = u / C8, c = u - r * C8, gr = rt * BM + r;
       uint4 x = make_uint4(0u, 0u, 0u, 0u);

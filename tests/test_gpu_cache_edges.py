@@ -1,0 +1,85 @@
+"""Attention over the paged cache at the edges of what its kernels take: keys that are
+not there, values that are not finite or far apart in size, workspaces and streams (needs
+a GB300). Against 64-bit forms, with the tolerances of `_cache_ref.attention_slack`."""
+from __future__ import annotations
+
+import math
+import types
+
+import pytest
+import torch
+
+import _cache_ref as R
+
+pytestmark = pytest.mark.gpu
+
+dt = pytest.importorskip("conditional_draft_tree_gb300")
+
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from conditional_draft_tree_gb300 import build
+    build.build()
+
+
+def near(got, ref, slack, what=""):
+    got = got.double().cpu()
+    odd = ~torch.isfinite(ref)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), what
+    assert torch.equal(got[odd & ~torch.isnan(ref)], ref[odd & ~torch.isnan(ref)]), what
+    over = ((got - ref).abs() - slack)[~odd]
+    assert over.numel() == 0 or float(over.max()) <= 0, f"{what}: over by {float(over.max()):.3g}"
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+def queries(batch, n, H, dh, dtype, seed, amp=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (amp * torch.randn(batch, n, H, dh, generator=g)).to(dtype).transpose(1, 2)
+
+
+def place(cache, b, j):
+    """Page and slot of row j of request b."""
+    page = cache.k.shape[2]
+    return int(cache.table[b, j // page]), j % page
+
+
+@pytest.mark.parametrize("entry", [-1, -2147483648, "pages", 2147483647])
+@pytest.mark.parametrize("n,G,dh", [(1, 4, 128), (3, 4, 64), (20, 4, 128), (65, 4, 128), (1, 4, 256), (20, 2, 192), (70, 4, 256)])
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+def test_keys_on_bad_pages_are_left_out(kind, n, G, dh, entry):
+    """A bad page inside the prefix, one that holds tree rows, and one that lets a unit begin
+    with rows that are not there: reported, and the other keys attended to."""
+    keys_on_bad_pages(kind, n, G, dh, entry)
+
+
+def keys_on_bad_pages(kind, n, G, dh, entry):
+    batch, Hkv, page = 4, 2, 16
+    prefix = [200, 100, 40, 700]
+    cache = R.make_cache(dt, kind, BF, batch, max(prefix) + n, Hkv, page, dh, 300)
+    pages = cache.k.shape[0]
+    good = types.SimpleNamespace(k=cache.k, v=cache.v, k_exp=cache.k_exp, v_exp=cache.v_exp, table=cache.table.clone())
+    bad = [[5], [100 // page], [0], []]
+    for b, at in enumerate(bad):
+        for x in at:
+            cache.table[b, x] = pages if entry == "pages" else entry
+    q, scale = queries(batch, n, Hkv * G, dh, BF, 301), dh ** -0.5
+    got = dt.cache_attention(cache, q.cuda(), i32(prefix))
+    assert cache.status.tolist() == [dt.ERR_BAD_PAGE] * 3 + [dt.OK]
+    for b in range(batch):
+        keys = [j for j in range(prefix[b] + n) if j // page not in bad[b]]
+        k, v = (R.pool_rows(good, w, b, keys) for w in "kv")
+        see = torch.tensor(keys)[None] <= prefix[b] + torch.arange(n)[:, None]
+        for h in range(Hkv * G):
+            x = scale * q[b, h].double() @ k[h // G].T
+            big = scale * float((q[b, h].double().abs() @ k[h // G].abs().T).max())
+            p = torch.softmax(torch.where(see, x, -math.inf), -1)
+            p = torch.where(see.any(-1, keepdim=True), p, 0.0)        # a row that sees nothing
+            ref = p @ v[h // G]
+            near(got[b, h], ref, R.attention_slack(ref, p @ v[h // G].abs(), big, BF, dh, prefix[b] + n), f"{b} {h}")

@@ -265,6 +265,27 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// A ring of places that steps are copied into and taken from in order: where the next step
+// goes and comes from, and the parity of the phase that ends its copies. A warp that gives
+// up a wait takes no further step, issues none, and waits for the ones in flight before it
+// ends.
+struct StepRing {
+  uint32_t in, out, parity;
+  __host__ __device__ void issued(uint32_t places) {
+    if (++in == places) in = 0;
+  }
+  __host__ __device__ void taken(uint32_t places) {
+    if (++out == places) {
+      out = 0;
+      parity ^= 1u;
+    }
+  }
+  // steps in flight when step k of `steps` has not been taken
+  __host__ __device__ static int flying(int k, int steps, int places) {
+    return steps - k < places ? steps - k : places;
+  }
+};
+
 struct AttnPlan {        // resolved on the host from sizes alone
   enum { kAny, kWide, kFew } kind;     // dt_cache_attn.cu, dt_cache_wide.cu, dt_cache_few.cu
   int bm, dhp, row_tiles, grid;

@@ -141,8 +141,8 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
   if (tid == 0) walk.note_cut(a, sch.chunk, more, sg);
 
   const int rows = a.n * a.G;
-  uint32_t stage_in = 0, stage_out = 0, parity_out = 0;     // places in the ring
-  bool failed = false;
+  StepRing places = {0u, 0u, 0u};
+  int given_up = 0;                    // steps in flight behind a wait that ran out
   uint32_t there_in = 0;               // bit NG i + h: group h of 16 keys of place i is on a good page
   // the warp's step k of a segment: keys from t0 T + SUB (warp + 12 k); the number of its steps
   auto step_key = [&](const Segment &s, int k) { return s.t0 * kT + SUB * (warp + kFWarps * k); };
@@ -152,6 +152,7 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
     return left <= 0 ? 0 : (left + SUB * kFWarps - 1) / (SUB * kFWarps);
   };
   auto issue = [&](const Segment &s, int k) {
+    const uint32_t stage_in = places.in;
     const int j = step_key(s, k), end = seg_end(s);
     const int32_t *table = a.c.table + static_cast<int64_t>(s.b) * a.c.width;
     int entry[NG];
@@ -191,7 +192,7 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
         bulk_g2s(ss.exps[warp][stage_in] + which * SUB + 16 * h, (which ? a.c.v_exp : a.c.k_exp) + row, 16, bar);
       }
     }
-    if (++stage_in == static_cast<uint32_t>(stages)) stage_in = 0;
+    places.issued(stages);
   };
   if (more)
     for (int k = 0; k < min(stages, step_count(sg)); ++k) issue(sg, k);
@@ -199,7 +200,7 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
   while (more) {
     const Request rq = sg.rq;
     const int b = sg.b, hk = sg.hk, pre = static_cast<int>(rq.pre), end = seg_end(sg);
-    const int steps = step_count(sg);
+    const int steps = given_up ? 0 : step_count(sg);
     if (tid == 0 && a.prefix[b] != rq.pre) cache_fault(a.c, b);
     // Q^T: this thread's part of row 8 z + g; its scores are of rows 8 z + 2 t, 8 z + 2 t + 1
     uint32_t q[DH / 16][RN][2];
@@ -273,12 +274,13 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
 #pragma unroll 1
     for (int k = 0; k < steps; ++k) {
       const int j0 = step_key(sg, k);
+      const uint32_t stage_out = places.out;
       const uint32_t good = (there_in >> (NG * stage_out)) & ((1u << NG) - 1u);
-      if (!failed && !few_wait(&full[stage_out], parity_out)) {
-        failed = true;
+      if (!__all_sync(kFull, few_wait(&full[stage_out], places.parity))) {
+        given_up = StepRing::flying(k, steps, stages);
         a.c.status[b] = DT_ERR_TIMEOUT;
+        break;
       }
-      __syncwarp();
       const unsigned char *sK = ring + stage_out * 2 * HS, *sV = sK + HS;
       const bool masked = j0 + SUB > whole_end || good != (1u << NG) - 1u;
       auto key_at = [&](int x) { return j0 + 16 * (x >> 1) + (x & 1 ? key1 : key0); };    // x: 2 h + which
@@ -511,17 +513,14 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
             }
       }
       __syncwarp();                    // the place is read
-      if (++stage_out == static_cast<uint32_t>(stages)) {
-        stage_out = 0;
-        parity_out ^= 1u;
-      }
+      places.taken(stages);
       if (k + stages < steps) issue(sg, k + stages);
     }
 
     // The next segment's first steps are on their way while this one's end is written.
     const Segment done = sg;
     more = walk.next(a, BM, kT, &sg);
-    if (more)
+    if (more && !given_up)
       for (int k = 0; k < min(stages, step_count(sg)); ++k) issue(sg, k);
 
     // the warps' results together, 32 columns at a time
@@ -591,6 +590,12 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
       }
       __syncthreads();
     }
+  }
+  // No copy may be in flight when the block ends: after a wait that ran out, wait (bounded
+  // again) for those behind it.
+  for (; given_up > 0; --given_up) {
+    few_wait(&full[places.out], places.parity);
+    places.taken(stages);
   }
 }
 

@@ -59,7 +59,7 @@ struct WideShape {
 
 struct Small {                          // behind the big buffers
   uint64_t full[kMaxRing], empty[kMaxRing], raw_full[kMaxRing], raw_empty[kMaxRing];
-  uint64_t q_full, q_free, s_full[2], p_full[2], o_done[2];
+  uint64_t q_full, q_free, s_full[2], p_full[2], o_done[2], idle;
   int64_t scan[640 / 32 + 2];
   Segment seg[kSegs];                   // the next segments; b < 0: no more
   uint64_t seg_full[kSegs], seg_empty[kSegs];
@@ -263,6 +263,7 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
     }
     mbar_init(&ss.q_full, 256);
     mbar_init(&ss.q_free, 1);
+    mbar_init(&ss.idle, 1);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&ss.seg_full[i], 1);
       mbar_init(&ss.seg_empty[i], QUANT ? 18 : 10);   // the warps that take segments
@@ -920,6 +921,11 @@ cache_attention_wide_kernel(const __grid_constant__ AttnArgs a, const __grid_con
           }
         }
       }
+      // No product may be under way when the block gives back its tensor memory and ends,
+      // also after a wait that ran out: the last arrival follows all of them (bounded).
+      if (elect_one()) umma_commit(&ss.idle);
+      __syncwarp();
+      mbar_wait_cycles(&ss.idle, 0);
     } else if (role == 2 && lane == 0) {
       // -------------------------------------------------------- segments
       Segment found;

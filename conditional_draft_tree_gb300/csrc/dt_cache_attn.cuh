@@ -191,6 +191,13 @@ struct Schedule {
   }
 };
 
+// the head whose units, `per` long together, hold place `at` of a request's: a 64-bit
+// division only where a number needs it (2^24 stacked rows over a million keys pass 2^32)
+__host__ __device__ __forceinline__ int head_at(int64_t at, int64_t per) {
+  return (at | per) >> 32 ? static_cast<int>(at / per)
+                          : static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(per));
+}
+
 // One unit's part that falls to a block: key tiles [t0, t1) of its `tiles`.
 struct Segment {
   int b, hk, rt, t0, t1, tiles;
@@ -213,9 +220,7 @@ struct Walk {
         per = length_before(a, s->rq, a.row_tiles, bm, T);
       }
       s->b = b;
-      // a 64-bit division only where it is needed
-      s->hk = (at - base) >> 31 ? static_cast<int>((at - base) / per)
-                                : static_cast<int>(static_cast<uint32_t>(at - base) / static_cast<uint32_t>(per));
+      s->hk = head_at(at - base, per);
       int64_t unit = base + s->hk * per;
       int weight, len;
       for (s->rt = 0;; ++s->rt) {

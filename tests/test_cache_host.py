@@ -11,7 +11,7 @@ import pytest
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
-@pytest.mark.parametrize("name", ["cache_ring_check"])
+@pytest.mark.parametrize("name", ["cache_ring_check", "cache_cut_check"])
 def test_host_checks(tmp_path, name):
     nvcc = os.environ.get("NVCC") or shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
     exe = str(tmp_path / name)

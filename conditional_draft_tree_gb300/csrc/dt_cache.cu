@@ -496,7 +496,8 @@ int check_cache(const dt_cache *c) {
     return DT_ERR_INVALID_ARG;
   if (!(c->page == 16 || c->page == 32 || c->page == 64 || c->page == 128) || c->pages < 1 ||
       c->Hkv < 1 || c->Hkv > 4096 || c->dh < 16 || c->dh > 256 || c->dh % 16 || c->batch < 1 ||
-      c->batch > 65535 || c->table_width < 1 || c->table_width > (1 << 24) / 16)
+      c->batch > 65535 || c->table_width < 1 || c->table_width > (1 << 24) / 16 ||
+      static_cast<int64_t>(c->pages) * c->Hkv > 0x7fffffff)     // a tensor map's third coordinate
     return DT_ERR_INVALID_ARG;
   if (!(c->dtype == DT_BF16 || c->dtype == DT_F16 || c->dtype == DT_E4M3))
     return DT_ERR_INVALID_ARG;

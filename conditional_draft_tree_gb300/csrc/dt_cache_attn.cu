@@ -1,7 +1,6 @@
 // dt_cache_attn.cu -- attention of tree, chain and single-token rows over the paged
 // cache: the kernel for head sizes above 128 (whose operands do not fit the others'
-// tiles) and pools that a tensor map cannot describe, the launch that joins partial
-// results, and the entry points.
+// tiles), the launch that joins partial results, and the entry points.
 //
 // One pass over the keys with a running maximum: per key tile S = Q K^T, x = S scale
 // log2(e) (-inf where the row does not see the key), m' = max(m, max x),

@@ -634,7 +634,7 @@ cudaError_t go_dh(const AttnArgs &a, const AttnPlan &p, const CUtensorMap &k, co
 //              128, G 16    41.0  38.9  65.5  67.6  55.3  45.1   215   205    191   201
 // (More rows would need a third N tile and registers that are not there.)
 bool few_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p) {
-  if (c.dh > 128 || rows > kFewRows || static_cast<int64_t>(c.pages) * c.Hkv > 0x7fffffff) return false;
+  if (c.dh > 128 || rows > kFewRows) return false;
   p->kind = AttnPlan::kFew;
   p->bm = 16;
   p->row_tiles = 1;

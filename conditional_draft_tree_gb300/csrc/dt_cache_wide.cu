@@ -1008,7 +1008,7 @@ bool page_map(const dt_cache &c, const void *base, int box_rows, CUtensorMap *ma
 // kernel for any size took 0.28 ms for 32 trees of 65 rows over 512 to 1024 rows where this
 // one takes 0.10 ms, and 6.2 ms for 8 of 129 over up to 32768 8-bit rows: 0.58 ms.)
 bool wide_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p) {
-  if (c.dh > 128 || static_cast<int64_t>(c.pages) * c.Hkv > 0x7fffffff) return false;
+  if (c.dh > 128) return false;
   const bool quant = c.dtype == DT_E4M3;
   const int64_t tiles = (rows + 127) / 128;
   p->bm = 2 * static_cast<int>((rows + tiles - 1) / tiles);

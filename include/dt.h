@@ -407,6 +407,7 @@ int dt_rotary(const dt_rotation *rot, const int32_t *positions, int batch, int n
  * 128) for each of Hkv key/value heads; k and v are [pages][Hkv][page][dh] and
  * row `index` of request b (counted from its first token) lies in page
  * table[b][index / page], slot index % page. dh: a multiple of 16 in [16, 256].
+ * pages times Hkv: at most 2^31 - 1.
  * dtype DT_BF16, DT_F16, or DT_E4M3: 8-bit codes with one exponent byte a
  * head row in k_exp, v_exp [pages][Hkv][page] (NULL for the 16-bit types), the
  * value being code 2^(byte - 127). The exponent is the least e in [-117, 120]

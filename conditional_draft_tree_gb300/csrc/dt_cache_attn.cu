@@ -365,7 +365,11 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
       for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
 #pragma unroll
       for (int k = 0; k < WK; ++k) {
-        w[k] = s_m[k * BM + r] == ninf ? 0.0f : fast_exp2(s_m[k * BM + r] - mm);
+        // A row that saw nothing has -inf and 0, and its values may be anything: a row past
+        // the count has a weight of zero for every key of the prefix, zero times a value
+        // that is not finite is NaN. (A sum that is NaN is not nothing.)
+        if (s_m[k * BM + r] == ninf && s_l[k * BM + r] == 0.0f) continue;
+        w[k] = fast_exp2(s_m[k * BM + r] - mm);
         ll += w[k] * s_l[k * BM + r];
         const float *src = sO + (k * BM + r) * DH + c * 8;
 #pragma unroll

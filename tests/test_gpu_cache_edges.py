@@ -83,3 +83,32 @@ def keys_on_bad_pages(kind, n, G, dh, entry):
             p = torch.where(see.any(-1, keepdim=True), p, 0.0)        # a row that sees nothing
             ref = p @ v[h // G]
             near(got[b, h], ref, R.attention_slack(ref, p @ v[h // G].abs(), big, BF, dh, prefix[b] + n), f"{b} {h}")
+
+
+def dense(cache, prefix, counts, q, mask, scale):
+    return R.attention(cache, q, torch.tensor(prefix), mask, torch.tensor(counts) if counts is not None else None, scale)
+
+
+@pytest.mark.parametrize("n,G", [(1, 4), (20, 4), (70, 2)])
+@pytest.mark.parametrize("dh", [64, 128, 192, 256])
+@pytest.mark.parametrize("kind,dtype", [("16", BF), ("16", FP), ("e4m3", BF), ("e4m3", FP)])
+def test_rows_past_the_count_are_zero_whatever_the_prefix_holds(kind, dtype, dh, n, G):
+    """Values that are not finite in the prefix: rows that see them are NaN or infinite, rows
+    past the count are zero, in units that a block holds whole (100 keys) and in cut ones."""
+    prefix, counts = [100, 3000, 64, 700], [max(1, n - 13), max(1, n // 2), 0, n]
+    cache = R.make_cache(dt, kind, dtype, 4, max(prefix) + n, 2, 16, dh, 310)
+    for b, j, val in ((0, 10, math.nan), (1, 70, math.inf), (2, 3, -math.inf), (3, 5, math.nan)):
+        p, s = place(cache, b, j)
+        if kind == "e4m3":
+            cache.v_exp[p, :, s] = 255
+            cache.v.view(torch.uint8)[p, :, s] = 0x7f
+        else:
+            cache.v[p, 0, s, 7] = val
+            cache.v[p, 1, s, :] = val
+    q, scale = queries(4, n, 2 * G, dh, dtype, 311), dh ** -0.5
+    got = dt.cache_attention(cache, q.cuda(), i32(prefix), counts=i32(counts))
+    cache.check()
+    for b, c in enumerate(counts):
+        assert bool((got[b, :, c:] == 0).all()), b
+    ref, mass, big = dense(cache, prefix, counts, q, None, scale)
+    near(got, ref, R.attention_slack(ref, mass, big, dtype, dh, max(prefix) + n))

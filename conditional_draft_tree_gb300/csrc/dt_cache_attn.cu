@@ -7,7 +7,7 @@
 // p = 2^(x - m'), l = l 2^(m - m') + sum p, O = O 2^(m - m') + p V; out = O / l. Sums, m, l
 // and O are fp32; p is rounded to the 16-bit type for the product with V (bf16:
 // relative 2^-8; fp16 2^-11, p scaled by 2^12 so that small weights stay normal
-// numbers), l sums the unrounded p.
+// numbers; fp16 over 8-bit rows two bf16 terms), l sums the unrounded p.
 //
 // Products are mma.sync m16n8k16, a warp's 16 rows by the tile's keys, and the copies of
 // the next tile run during this one's. Measured at head size 256, 16 requests at 4096 keys,
@@ -82,6 +82,10 @@ constexpr int narrow_smem(int bm) {
 template <int DT, bool QUANT, int DH, int WK>
 __global__ void __launch_bounds__(kNThreads)
 cache_attention_kernel(const __grid_constant__ AttnArgs a) {
+  // fp16 rows over 8-bit ones: V's values (as many as 2^137 apart) in bf16, where they are
+  // exact, against the weights in two bf16 terms; K's in fp16, rounded as dt_cache_read does
+  constexpr bool TWO = QUANT && DT == DT_F16;
+  constexpr int VDT = TWO ? DT_BF16 : DT;
   constexpr int BM = 64 / WK, NK = kT / WK, C8 = DH / 8;
   constexpr int RB = DH * (QUANT ? 1 : 2);      // bytes of a stored row (padded)
   extern __shared__ __align__(128) unsigned char sm[];
@@ -94,7 +98,7 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wr = warp / WK, wk = warp % WK, g = lane >> 2, t4 = lane & 3;
   const float ninf = -__int_as_float(0x7f800000);
-  constexpr float kShift = DT == DT_F16 ? 12.0f : 0.0f;
+  constexpr float kShift = VDT == DT_F16 ? 12.0f : 0.0f;
   const int dh = a.c.dh;
 
   Schedule<kNThreads> sch;
@@ -205,11 +209,14 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
           const int which = u / (kT * C8), r = (u / C8) % kT, c = u % C8;
           const float sc = row_scale(s_exp[t & 1][which][r]);
           const uint2 q = *reinterpret_cast<const uint2 *>((which ? sV : sK) + r * RB + c * 8);
+          auto to16 = [&](uint32_t two) {
+            return TWO && which ? e4m3_to16<VDT>(two, sc) : e4m3_to16<DT>(two, sc);
+          };
           uint4 w;
-          w.x = e4m3_to16<DT>(q.x & 0xffffu, sc);
-          w.y = e4m3_to16<DT>(q.x >> 16, sc);
-          w.z = e4m3_to16<DT>(q.y & 0xffffu, sc);
-          w.w = e4m3_to16<DT>(q.y >> 16, sc);
+          w.x = to16(q.x & 0xffffu);
+          w.y = to16(q.x >> 16);
+          w.z = to16(q.y & 0xffffu);
+          w.w = to16(q.y >> 16);
           *reinterpret_cast<uint4 *>(sDeq + which * kT * DH * 2 + swz<DH>(r, c)) = w;
         }
         __syncthreads();
@@ -224,7 +231,7 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
           uint32_t *w = reinterpret_cast<uint32_t *>(sV + u * 16);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t odd = odd16<DT>(w[e]);
+            const uint32_t odd = odd16<VDT>(w[e]);
             if (odd) {
               w[e] &= ~odd;
               s_odd = 1;
@@ -293,17 +300,26 @@ cache_attention_kernel(const __grid_constant__ AttnArgs a) {
         for (int y = 0; y < 4; ++y) o[x][y] *= f[y >> 1];
 #pragma unroll
       for (int kb = 0; kb < NK / 16; ++kb) {
-        uint32_t pa[4];
-        pa[0] = Half16<DT>::pack(s[2 * kb][0], s[2 * kb][1]);
-        pa[1] = Half16<DT>::pack(s[2 * kb][2], s[2 * kb][3]);
-        pa[2] = Half16<DT>::pack(s[2 * kb + 1][0], s[2 * kb + 1][1]);
-        pa[3] = Half16<DT>::pack(s[2 * kb + 1][2], s[2 * kb + 1][3]);
+        uint32_t pa[4], pl[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p0 = s[2 * kb + (e >> 1)][2 * (e & 1)], p1 = s[2 * kb + (e >> 1)][2 * (e & 1) + 1];
+          pa[e] = Half16<VDT>::pack(p0, p1);
+          if (TWO) {
+            const float2 hi = Half16<VDT>::unpack(pa[e]);
+            pl[e] = Half16<VDT>::pack(p0 - hi.x, p1 - hi.y);
+          }
+        }
 #pragma unroll
         for (int x = 0; x < DH / 16; ++x) {
           uint32_t vb[4];
           ldsm4t(vb, v_at + swz<DH>(wk * NK + 16 * kb + (lane & 15), 2 * x + (lane >> 4)));
-          mma16816<DT>(o[2 * x], pa, vb[0], vb[1]);
-          mma16816<DT>(o[2 * x + 1], pa, vb[2], vb[3]);
+          mma16816<VDT>(o[2 * x], pa, vb[0], vb[1]);
+          mma16816<VDT>(o[2 * x + 1], pa, vb[2], vb[3]);
+          if (TWO) {
+            mma16816<VDT>(o[2 * x], pl, vb[0], vb[1]);
+            mma16816<VDT>(o[2 * x + 1], pl, vb[2], vb[3]);
+          }
         }
       }
       if (tree && s_odd) {

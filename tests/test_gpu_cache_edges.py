@@ -112,3 +112,42 @@ def test_rows_past_the_count_are_zero_whatever_the_prefix_holds(kind, dtype, dh,
         assert bool((got[b, :, c:] == 0).all()), b
     ref, mass, big = dense(cache, prefix, counts, q, None, scale)
     near(got, ref, R.attention_slack(ref, mass, big, dtype, dh, max(prefix) + n))
+
+
+@pytest.mark.parametrize("n", [1, 20, 70])
+@pytest.mark.parametrize("dh", [128, 192, 256])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_8bit_values_past_the_range_of_fp16_count_as_they_are(dtype, dh, n):
+    """A row of 448 2^12 among rows of ordinary size, each with about the same weight: the
+    result is a number of fp16, the row is not."""
+    prefix = [700, 45]
+    cache = R.make_cache(dt, "e4m3", dtype, 2, max(prefix) + n, 2, 16, dh, 320)
+    for b in range(2):
+        p, s = place(cache, b, 2)
+        cache.v.view(torch.uint8)[p, :, s] = 0x7e
+        cache.v_exp[p, :, s] = 127 + 12
+    q, scale = queries(2, n, 8, dh, dtype, 321, amp=1e-3), dh ** -0.5
+    got = dt.cache_attention(cache, q.cuda(), i32(prefix))
+    cache.check()
+    ref, mass, big = dense(cache, prefix, None, q, None, scale)
+    near(got, ref, R.attention_slack(ref, mass, big, dtype, dh, max(prefix) + n))
+
+
+@pytest.mark.parametrize("n", [1, 20, 70])
+@pytest.mark.parametrize("dh", [192, 256])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_8bit_codes_of_every_size_count_at_large_heads(dtype, dh, n):
+    """Rows whose codes are the least ones beside a single large one, of very different scales."""
+    prefix = [3, 130]
+    cache = R.make_cache(dt, "e4m3", dtype, 2, max(prefix) + n, 2, 16, dh, 330)
+    g = torch.Generator().manual_seed(331)
+    code = torch.randint(0, 8, cache.v.shape, generator=g, dtype=torch.uint8)
+    code |= torch.randint(0, 2, cache.v.shape, generator=g, dtype=torch.uint8) << 7
+    code[..., 3] = 0x7e
+    cache.v.view(torch.uint8).copy_(code)
+    cache.v_exp.copy_(torch.randint(100, 120, cache.v_exp.shape, generator=g, dtype=torch.uint8))
+    q, scale = queries(2, n, 4, dh, dtype, 332), dh ** -0.5
+    got = dt.cache_attention(cache, q.cuda(), i32(prefix))
+    cache.check()
+    ref, mass, big = dense(cache, prefix, None, q, None, scale)
+    near(got, ref, R.attention_slack(ref, mass, big, dtype, dh, max(prefix) + n))

@@ -15,7 +15,8 @@
 // order that both sides share, so a thread takes 16 codes of a key at once, and e4m3 codes
 // are exact in fp16: one conversion a pair, K's scale and the row's own (bf16 query rows are
 // scaled to fp16 by a power of two: their values lose less than 2^-24 of the row's largest)
-// multiply the score. V's codes come transposed from shared memory (8-bit ldmatrix: four
+// multiply the score (fp16 query rows: where a value is no fp16 number, K is rounded or saturated
+// as dt_cache_read does, so that a key's score does not depend on the number of rows). V's codes come transposed from shared memory (8-bit ldmatrix: four
 // consecutive keys of a column), are set in bf16 fields as they are, which makes them their
 // value times 2^-120, and 2^120 and V's scale are part of the weight: p 2^(e - ref + 60),
 // ref the largest exponent e so far (within 2^40), which keeps both in bf16's range; the
@@ -29,6 +30,7 @@
 // merge of a block's warps: 18 us for one request at 300 keys.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 
 #include "dt_cache_attn.cuh"
@@ -287,6 +289,25 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
       auto there = [&](int x) { return key_at(x) < end && ((good >> (x >> 1)) & 1u); };
       // ------------------------------------------------------------ scores
       // (in two sums each, so that half as many products wait for one another)
+      uint32_t ve[2 * NG];             // V's exponent bytes of the thread's keys
+      float kmul[2 * NG];
+      auto read_exponents = [&] {
+#pragma unroll
+        for (int h = 0; h < NG; ++h) {
+          if (QUANT) {
+            const uint8_t *e = ss.exps[warp][stage_out] + 16 * h + key0;
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(e - (g & 1)) >> (8 * (g & 1));
+            const uint32_t v = *reinterpret_cast<const uint32_t *>(e + SUB - (g & 1)) >> (8 * (g & 1));
+            kmul[2 * h] = row_scale(w & 255u);
+            kmul[2 * h + 1] = row_scale((w >> 16) & 255u);
+            ve[2 * h] = v & 255u;
+            ve[2 * h + 1] = (v >> 16) & 255u;
+          } else {
+            kmul[2 * h] = kmul[2 * h + 1] = 1.0f;
+            ve[2 * h] = ve[2 * h + 1] = 0u;
+          }
+        }
+      };
       float s[NG][RN][4], s2[NG][RN][4];
 #pragma unroll
       for (int h = 0; h < NG; ++h)
@@ -294,58 +315,66 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
         for (int z = 0; z < RN; ++z)
 #pragma unroll
           for (int y = 0; y < 4; ++y) s[h][z][y] = s2[h][z][y] = 0.0f;
+      auto products = [&](auto rounded) {
+        constexpr bool kRounded = decltype(rounded)::value;
 #pragma unroll
-      for (int d = 0; d < (QUANT ? DH / 64 : DH / 32); ++d) {
-        uint4 c[NG][2];
+        for (int d = 0; d < (QUANT ? DH / 64 : DH / 32); ++d) {
+          uint4 c[NG][2];
 #pragma unroll
-        for (int h = 0; h < NG; ++h)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int key = x ? key1 : key0;
-            c[h][x] = *reinterpret_cast<const uint4 *>(
-                sK + (QUANT ? h : d >> 1) * 2048 + key * 128 +
-                (((QUANT ? 4 * d + t4 : 4 * (d & 1) + t4) ^ (key & 7)) << 4));
-          }
-#pragma unroll
-        for (int i = 0; i < (QUANT ? 4 : 2); ++i)
-#pragma unroll
-          for (int h = 0; h < NG; ++h) {
-            uint32_t ka[4];            // rows g, g + 8; four values each
+          for (int h = 0; h < NG; ++h)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint4 &v = c[h][x];
-              if (QUANT) {
-                const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-                ka[x] = e4m3_f16x2(w & 0xffffu);
-                ka[2 + x] = e4m3_f16x2(w >> 16);
-              } else {
-                ka[x] = i ? v.z : v.x;
-                ka[2 + x] = i ? v.w : v.y;
+              const int key = x ? key1 : key0;
+              c[h][x] = *reinterpret_cast<const uint4 *>(
+                  sK + (QUANT ? h : d >> 1) * 2048 + key * 128 +
+                  (((QUANT ? 4 * d + t4 : 4 * (d & 1) + t4) ^ (key & 7)) << 4));
+            }
+#pragma unroll
+          for (int i = 0; i < (QUANT ? 4 : 2); ++i)
+#pragma unroll
+            for (int h = 0; h < NG; ++h) {
+              uint32_t ka[4];            // rows g, g + 8; four values each
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint4 &v = c[h][x];
+                if (QUANT) {
+                  const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+                  if (kRounded) {
+                    ka[x] = e4m3_to16<DT_F16>(w & 0xffffu, kmul[2 * h + x]);
+                    ka[2 + x] = e4m3_to16<DT_F16>(w >> 16, kmul[2 * h + x]);
+                  } else {
+                    ka[x] = e4m3_f16x2(w & 0xffffu);
+                    ka[2 + x] = e4m3_f16x2(w >> 16);
+                  }
+                } else {
+                  ka[x] = i ? v.z : v.x;
+                  ka[2 + x] = i ? v.w : v.y;
+                }
+              }
+#pragma unroll
+              for (int z = 0; z < RN; ++z) {
+                const uint32_t(&qb)[2] = q[(QUANT ? 4 : 2) * d + i][z];
+                mma16<QDT>(i & 1 ? s2[h][z] : s[h][z], ka, qb[0], qb[1]);
               }
             }
-#pragma unroll
-            for (int z = 0; z < RN; ++z) {
-              const uint32_t(&qb)[2] = q[(QUANT ? 4 : 2) * d + i][z];
-              mma16<QDT>(i & 1 ? s2[h][z] : s[h][z], ka, qb[0], qb[1]);
-            }
-          }
-      }
-      uint32_t ve[2 * NG];             // V's exponent bytes of the thread's keys
-      float kmul[2 * NG];
-#pragma unroll
-      for (int h = 0; h < NG; ++h) {
-        if (QUANT) {
-          const uint8_t *e = ss.exps[warp][stage_out] + 16 * h + key0;
-          const uint32_t w = *reinterpret_cast<const uint32_t *>(e - (g & 1)) >> (8 * (g & 1));
-          const uint32_t v = *reinterpret_cast<const uint32_t *>(e + SUB - (g & 1)) >> (8 * (g & 1));
-          kmul[2 * h] = row_scale(w & 255u);
-          kmul[2 * h + 1] = row_scale((w >> 16) & 255u);
-          ve[2 * h] = v & 255u;
-          ve[2 * h + 1] = (v >> 16) & 255u;
-        } else {
-          kmul[2 * h] = kmul[2 * h + 1] = 1.0f;
-          ve[2 * h] = ve[2 * h + 1] = 0u;
         }
+      };
+      if (DT == DT_F16 && QUANT) {
+        // rows of which fp16 rounds or saturates a value: as dt_cache_read gives them
+        read_exponents();
+        bool odd_scale = false;
+#pragma unroll
+        for (int x = 0; x < 2 * NG; ++x) odd_scale |= kmul[x] < 0x1p-15f || kmul[x] > 0x1p7f;
+        if (__any_sync(kFull, odd_scale)) {
+          products(std::true_type{});
+#pragma unroll
+          for (int x = 0; x < 2 * NG; ++x) kmul[x] = 1.0f;
+        } else {
+          products(std::false_type{});
+        }
+      } else {
+        products(std::false_type{});
+        read_exponents();
       }
       uint32_t see = ~0u;              // bit (2 h + x) 2 RN + 2 z + e: the row sees the key
       if (masked) {

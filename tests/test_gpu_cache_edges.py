@@ -151,3 +151,23 @@ def test_8bit_codes_of_every_size_count_at_large_heads(dtype, dh, n):
     cache.check()
     ref, mass, big = dense(cache, prefix, None, q, None, scale)
     near(got, ref, R.attention_slack(ref, mass, big, dtype, dh, max(prefix) + n))
+
+
+@pytest.mark.parametrize("n", [1, 3, 20])
+@pytest.mark.parametrize("dh", [64, 128, 256])
+@pytest.mark.parametrize("low,high,amp,scale", [(127 + 9, 127 + 11, 1e-4, 0.05), (92, 106, 30.0, 1024.0), (96, 142, 1e-3, 0.5)])
+def test_fp16_scores_take_8bit_keys_as_they_are_read(low, high, amp, scale, dh, n, monkeypatch):
+    """Keys past fp16's largest number, below its least step, and both: the scores are those of
+    the keys that dt_cache_read gives in fp16, however many rows there are."""
+    prefix = [300, 17]
+    cache = R.make_cache(dt, "e4m3", FP, 2, max(prefix) + n, 2, 16, dh, 340)
+    g = torch.Generator().manual_seed(341)
+    cache.k_exp.copy_(torch.randint(low, high + 1, cache.k_exp.shape, generator=g, dtype=torch.uint8))
+    q = queries(2, n, 8, dh, FP, 342, amp=amp)
+    got = dt.cache_attention(cache, q.cuda(), i32(prefix), scale=scale)
+    cache.check()
+    rows = R.pool_rows
+    monkeypatch.setattr(R, "pool_rows", lambda c, which, b, at: rows(c, which, b, at) if which == "v" else
+                        rows(c, which, b, at).clamp(-65504, 65504).to(FP).double())
+    ref, mass, big = dense(cache, prefix, None, q, None, scale)
+    near(got, ref, R.attention_slack(ref, mass, big, FP, dh, max(prefix) + n))

@@ -162,7 +162,7 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
 #pragma unroll
     for (int h = 0; h < NG; ++h) {
       const int page = (j + 16 * h) >> a.c.shift;
-      entry[h] = j + 16 * h < end ? (page < a.c.width ? table[page] : -1) : -2;
+      entry[h] = j + 16 * h < end && page < a.c.width ? table[page] : -1;
     }
 #pragma unroll
     for (int h = 0; h < NG; ++h)
@@ -173,7 +173,7 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
       mbar_expect_tx(bar, __popc(good) * (2 * HS / NG + (QUANT ? 32 : 0)));
 #pragma unroll
       for (int h = 0; h < NG; ++h)
-        if (entry[h] < 0 ? entry[h] != -2 : entry[h] >= a.c.pages) cache_fault(a.c, s.b);
+        if (j + 16 * h < end && !((good >> h) & 1u)) cache_fault(a.c, s.b);
     }
     __syncwarp();
     // a lane a copy: boxes of K, of V (four of 16-bit rows, or two for each of two groups),

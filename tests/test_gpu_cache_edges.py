@@ -171,3 +171,9 @@ def test_fp16_scores_take_8bit_keys_as_they_are_read(low, high, amp, scale, dh, 
                         rows(c, which, b, at).clamp(-65504, 65504).to(FP).double())
     ref, mass, big = dense(cache, prefix, None, q, None, scale)
     near(got, ref, R.attention_slack(ref, mass, big, FP, dh, max(prefix) + n))
+
+
+@pytest.mark.parametrize("n,G,dh", [(1, 4, 128), (3, 4, 64), (20, 4, 128), (1, 4, 256)])
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+def test_a_table_entry_of_minus_two_is_a_bad_page_too(kind, n, G, dh):
+    keys_on_bad_pages(kind, n, G, dh, -2)

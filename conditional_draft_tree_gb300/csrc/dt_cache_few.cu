@@ -397,7 +397,9 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
 #pragma unroll
           for (int x = 0; x < 2 * NG; ++x) {
             float &v = s[x >> 1][z][2 * (x & 1) + e];
-            v = (v + s2[x >> 1][z][2 * (x & 1) + e]) * (QUANT ? row_mul[z][e] * kmul[x] : row_mul[z][e]);
+            // (one scale after the other: their product may be no fp32 number where the score is)
+            v = (v + s2[x >> 1][z][2 * (x & 1) + e]) * row_mul[z][e];
+            if (QUANT) v *= kmul[x];
             if (masked) v = (see >> (2 * RN * x + 2 * z + e)) & 1u ? v : ninf;
             mx[z][e] = fmaxf(mx[z][e], v);
           }

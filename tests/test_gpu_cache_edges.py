@@ -177,3 +177,22 @@ def test_fp16_scores_take_8bit_keys_as_they_are_read(low, high, amp, scale, dh, 
 @pytest.mark.parametrize("kind", ["16", "e4m3"])
 def test_a_table_entry_of_minus_two_is_a_bad_page_too(kind, n, G, dh):
     keys_on_bad_pages(kind, n, G, dh, -2)
+
+
+@pytest.mark.parametrize("n", [1, 3, 20])
+def test_a_score_of_zero_between_huge_vectors_is_zero(n):
+    """q holds 2^60 in one place, a key 2^80 in another: their scales' product is no fp32 number,
+    the score is zero."""
+    dh = 128
+    cache = R.make_cache(dt, "e4m3", BF, 2, 80, 2, 16, dh, 370)
+    cache.k.view(torch.uint8)[..., 0] = 0
+    p, s = place(cache, 0, 4)
+    cache.k_exp[p, :, s] = 127 + 72
+    cache.k.view(torch.uint8)[p, :, s, :] = 0
+    cache.k.view(torch.uint8)[p, :, s, 1] = 0x7e
+    q = torch.zeros(2, 8, n, dh, dtype=BF)
+    q[..., 0] = 2.0 ** 60
+    got = dt.cache_attention(cache, q.cuda(), i32([30, 40]))
+    cache.check()
+    ref, mass, _ = dense(cache, [30, 40], None, q, None, dh ** -0.5)
+    near(got, ref, R.attention_slack(ref, mass, 0.0, BF, dh, 80))

@@ -15,13 +15,18 @@
 // order that both sides share, so a thread takes 16 codes of a key at once, and e4m3 codes
 // are exact in fp16: one conversion a pair, K's scale and the row's own (bf16 query rows are
 // scaled to fp16 by a power of two: their values lose less than 2^-24 of the row's largest)
-// multiply the score (fp16 query rows: where a value is no fp16 number, K is rounded or saturated
-// as dt_cache_read does, so that a key's score does not depend on the number of rows). V's codes come transposed from shared memory (8-bit ldmatrix: four
-// consecutive keys of a column), are set in bf16 fields as they are, which makes them their
-// value times 2^-120, and 2^120 and V's scale are part of the weight: p 2^(e - ref + 60),
-// ref the largest exponent e so far (within 2^40), which keeps both in bf16's range; the
-// result has that power of two taken out. fp16 results need weights of more than bf16's 8
-// bits: two terms.
+// multiply the score. (fp16 query rows: where a value is no fp16 number, K is rounded or
+// saturated as dt_cache_read does, so that a key's score does not depend on the number of
+// rows.) V's codes come transposed from shared memory (8-bit ldmatrix: four consecutive
+// keys of a column) and are set in bf16 fields as they are, which makes them their value
+// times 2^-120. V's scale 2^e is part of the weight: 2^(x + e - M + 60) for a score x (a
+// power of two's exponent, as the references are), where M = m + a whole number is a
+// reference of the row's own for x + e, as m is for x: the largest term of O is near it
+// however scores and scales are mixed, and keys that a row does not see leave its result
+// alone. (One reference exponent a warp, of all its keys, lost what was 2^-80 of it: a row of
+// 2^100 that nobody saw made the others' results zero. The second exponential costs no time:
+// 32 tokens at 8192 keys 135 us before, 133 us now.) The result has that power of two taken
+// out. fp16 results need weights of more than bf16's 8 bits: two terms.
 //
 // Measured, 32 / 8 heads, dh 128, 32 single tokens at 8192 keys: 8-bit rows 137 us, 3.9 TB/s
 // of cache rows; 16-bit rows 203 us, 5.3 TB/s (of 6.8 that a copy reaches). For 8-bit rows a
@@ -260,15 +265,15 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
       for (int z = 0; z < RN; ++z)
 #pragma unroll
         for (int y = 0; y < 4; ++y) o[x][z][y] = 0.0f;
-    float m[RN][2], l[RN][2];
+    // references and sums; (8-bit rows) O's reference is m + od, od a whole number
+    float m[RN][2], l[RN][2], od[RN][2];
 #pragma unroll
     for (int z = 0; z < RN; ++z)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         m[z][e] = ninf;
-        l[z][e] = 0.0f;
+        l[z][e] = od[z][e] = 0.0f;
       }
-    int vref = -1000;                  // V's reference exponent
     const int whole_end = min(pre, end);
     // the thread's two keys of a group of 16, as rows g and g + 8 of the product
     const int key0 = QUANT ? 4 * (g >> 1) + (g & 1) : g, key1 = key0 + (QUANT ? 2 : 8);
@@ -388,12 +393,18 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
               if (live[z][e] && there(x) && sees(a, rq, b, tok[z][e], key_at(x)))
                 see |= 1u << (2 * RN * x + 2 * z + e);
       }
-      float mx[RN][2];
+      // V's exponents as numbers (a row of 255: NaN), which go to the weights' exponents
+      float vx[2 * NG];
+#pragma unroll
+      for (int x = 0; x < 2 * NG; ++x)
+        vx[x] = ve[x] == 255u ? row_scale(255u) : static_cast<float>(static_cast<int>(ve[x]) - 127);
+      // largest scores, and largest sums of a score and its V's exponent
+      float mx[RN][2], mo[RN][2];
 #pragma unroll
       for (int z = 0; z < RN; ++z)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[z][e] = ninf;
+          mx[z][e] = mo[z][e] = ninf;
 #pragma unroll
           for (int x = 0; x < 2 * NG; ++x) {
             float &v = s[x >> 1][z][2 * (x & 1) + e];
@@ -402,46 +413,43 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
             if (QUANT) v *= kmul[x];
             if (masked) v = (see >> (2 * RN * x + 2 * z + e)) & 1u ? v : ninf;
             mx[z][e] = fmaxf(mx[z][e], v);
+            if (QUANT) mo[z][e] = fmaxf(mo[z][e], v + vx[x]);
           }
         }
-      // Does a row's maximum, or V's largest exponent of a key that is there, grow past its
-      // reference? Each lane asks for its own keys; only then are they taken across lanes.
+      // Does a row's maximum grow past its reference, or that sum past O's? Each lane asks
+      // for its own keys; only then are they taken across lanes.
       bool grow = false;
 #pragma unroll
       for (int z = 0; z < RN; ++z)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          if (!live[z][e]) mx[z][e] = ninf;
+          if (!live[z][e]) mx[z][e] = mo[z][e] = ninf;
           grow |= mx[z][e] > m[z][e] + kGrow || (m[z][e] == ninf && mx[z][e] != ninf);
+          if (QUANT) grow |= mo[z][e] > m[z][e] + od[z][e] + kGrow;
         }
-      int top = -1000;
-      if (QUANT) {
-#pragma unroll
-        for (int x = 0; x < 2 * NG; ++x)
-          if (ve[x] != 255u && (!masked || there(x))) top = max(top, static_cast<int>(ve[x]) - 127);
-        grow |= top > vref + 40;
-      }
       if (__any_sync(kFull, grow)) {
-        float vmul = 1.0f;
-        if (QUANT) {
-          top = __reduce_max_sync(kFull, top);
-          if (top > vref + 40) {
-            vmul = vref == -1000 ? 0.0f : exp2i(max(vref - top, -126));
-            vref = top;
-          }
-        }
 #pragma unroll
         for (int z = 0; z < RN; ++z)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float t = mx[z][e];
+            float t = mx[z][e], to = mo[z][e];
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, d));
-            const bool up = t > m[z][e] + kGrow || (m[z][e] == ninf && t != ninf);
-            float f = !up ? 1.0f : m[z][e] == ninf ? 0.0f : fast_exp2(m[z][e] - t);
+            for (int x = 4; x < 32; x <<= 1) {
+              t = fmaxf(t, __shfl_xor_sync(kFull, t, x));
+              if (QUANT) to = fmaxf(to, __shfl_xor_sync(kFull, to, x));
+            }
+            const bool first = m[z][e] == ninf, up = t > m[z][e] + kGrow || (first && t != ninf);
+            const float old = m[z][e], shift = up ? old - t : 0.0f;
             if (up) m[z][e] = t;
+            float f = first ? 0.0f : fast_exp2(shift);
             l[z][e] *= f;
-            f *= vmul;
+            if (QUANT) {
+              // (within 180 for any scores and exponents that are numbers)
+              const float from = old + od[z][e], ref = first || to > from + kGrow ? to : from;
+              const float dn = fminf(fmaxf(rintf(ref - m[z][e]), -180.0f), 180.0f);
+              f = first ? 0.0f : fast_exp2(shift + (od[z][e] - dn));
+              od[z][e] = dn;
+            }
 #pragma unroll
             for (int x = 0; x < DH / 16; ++x) {
               o[x][z][e] *= f;
@@ -455,18 +463,16 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
       uint32_t pb[NG][RN][2], pl[NG][RN][2];
 #pragma unroll
       for (int x = 0; x < 2 * NG; ++x) {
-        float f = 1.0f;
-        if (QUANT)   // 2^(e - ref + 60), e at most 40 above ref; NaN rows NaN
-          f = ve[x] == 255u ? row_scale(255u) : exp2i(max(static_cast<int>(ve[x]) - 127 - vref + 60, -126));
 #pragma unroll
         for (int z = 0; z < RN; ++z) {
           float p[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float ref = m[z][e] == ninf ? 0.0f : m[z][e] - kShift;
-            p[e] = fast_exp2(s[x >> 1][z][2 * (x & 1) + e] - ref);
+            const float a2 = s[x >> 1][z][2 * (x & 1) + e] - ref;
+            p[e] = fast_exp2(a2);
             l[z][e] += p[e];
-            if (QUANT) p[e] *= f;
+            if (QUANT) p[e] = fast_exp2(a2 + (vx[x] - od[z][e] + 60.0f));
             if (QUANT && masked) p[e] = (see >> (2 * RN * x + 2 * z + e)) & 1u ? p[e] : 0.0f;
           }
           const uint32_t hi = Half16<PDT>::pack(p[0], p[1]);
@@ -561,13 +567,22 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
       for (int e = 0; e < 2; ++e) {
         if (!live[z][e]) l[z][e] = 0.0f;       // (m is -inf: the row's O is not looked at)
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[z][e] += __shfl_xor_sync(kFull, l[z][e], d);
+        for (int x = 4; x < 32; x <<= 1) l[z][e] += __shfl_xor_sync(kFull, l[z][e], x);
         if (g == 0) {
           ss.m[warp][8 * z + 2 * t4 + e] = m[z][e];
           ss.l[warp][8 * z + 2 * t4 + e] = l[z][e];
         }
       }
-    const float out_mul = QUANT ? 0x1p60f : 1.0f, out_mul2 = QUANT && vref > -1000 ? exp2i(vref) : 1.0f;
+    // (8-bit rows) 2^(60 + d) in two factors
+    float mul0[RN][2], mul1[RN][2];
+#pragma unroll
+    for (int z = 0; z < RN; ++z)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int dn = static_cast<int>(od[z][e]), part = dn / 2;
+        mul0[z][e] = QUANT ? exp2i(30 + part) : 1.0f;
+        mul1[z][e] = QUANT ? exp2i(30 + dn - part) : 1.0f;
+      }
     const bool whole = done.t0 == 0 && done.t1 == done.tiles;
     float *pp = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (done.t0 > 0 ? 0 : 1)) * 2 * a.slot;
     // a thread: row r, columns 4 c of a round
@@ -583,7 +598,7 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
 #pragma unroll
           for (int y = 0; y < 4; ++y)
             ss.out[warp][8 * z + 2 * t4 + (y & 1)][16 * x + g + 8 * (y >> 1)] =
-                o[kMergeCols / 16 * round + x][z][y] * out_mul * out_mul2;
+                o[kMergeCols / 16 * round + x][z][y] * mul0[z][y & 1] * mul1[z][y & 1];
       __syncthreads();
       if (mine) {
         if (round == 0) {

@@ -196,3 +196,58 @@ def test_a_score_of_zero_between_huge_vectors_is_zero(n):
     cache.check()
     ref, mass, _ = dense(cache, [30, 40], None, q, None, dh ** -0.5)
     near(got, ref, R.attention_slack(ref, mass, 0.0, BF, dh, 80))
+
+
+@pytest.mark.parametrize("n,G", [(3, 2), (4, 4), (20, 2)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_a_huge_value_that_is_not_seen_changes_nothing(dtype, n, G):
+    """Row 1 of a tree of siblings holds 2^100 and more; the others' results are as without it."""
+    cache = R.make_cache(dt, "e4m3", dtype, 2, 60 + n, 2, 16, 128, 350)
+    prefix = [5, 60]
+    q, scale = queries(2, n, 2 * G, 128, dtype, 351), 128 ** -0.5
+    mask = torch.eye(n, dtype=torch.uint8)[None].repeat(2, 1, 1)
+    mask[:, :, 0] = 1
+    results = []
+    for e in (120, 127 + 100):
+        for b in range(2):
+            p, s = place(cache, b, prefix[b] + 1)
+            cache.v_exp[p, :, s] = e
+        results.append(dt.cache_attention(cache, q.cuda(), i32(prefix), mask=mask.cuda()))
+    cache.check()
+    ref, mass, big = dense(cache, prefix, None, q, mask, scale)
+    others = [i for i in range(n) if i != 1]
+    slack = R.attention_slack(ref, mass, big, dtype, 128, 60 + n)
+    near(results[1][:, :, others], ref[:, :, others], slack[:, :, others])
+    assert torch.equal(results[0][:, :, others], results[1][:, :, others])
+
+
+@pytest.mark.parametrize("n,G", [(1, 4), (2, 8), (20, 1)])
+@pytest.mark.parametrize("batch,length", [(2, 90), (24, 3000)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_huge_values_of_little_weight_beside_ordinary_ones(dtype, batch, length, n, G):
+    """Scores of 0, -30 and -64 (powers of e), values of about e^0, e^30 and e^64 with them, in
+    any order: each kind gives about as much of the result. A warp of the kernel for a few
+    rows meets them in one step (90 keys) and over many (3000 keys of 24 requests)."""
+    dh, Hkv = 64, 8
+    cache = R.make_cache(dt, "e4m3", dtype, batch, length + n, Hkv, 64, dh, 360)
+    g = torch.Generator().manual_seed(361)
+    shape = cache.k_exp.shape
+    what = torch.multinomial(torch.tensor([1.0, 5.0, 94.0]), shape.numel(), replacement=True, generator=g).view(shape)
+    # q is 1 everywhere, scale 1/8: the score of a row of 64 values x is 8 x
+    x = torch.tensor([0.0, -3.75, -8.0])[what]
+    cache.k.view(torch.uint8).copy_(R.quantise(x[..., None].expand(cache.k.shape).contiguous().to(BF))[0])
+    cache.k_exp.copy_(R.quantise(x[..., None].expand(cache.k.shape).contiguous().to(BF))[1])
+    e = cache.v_exp.cpu().int() + torch.tensor([0, 43 - 3, 92 - 7])[what]
+    cache.v_exp.copy_(e.to(torch.uint8))
+    q = torch.ones(batch, Hkv * G, n, dh, dtype=dtype)
+    prefix = [length - 7 * b for b in range(batch)]
+    got = dt.cache_attention(cache, q.cuda(), i32(prefix), scale=0.125)
+    cache.check()
+    some = [0, batch - 1]
+    for b in some:
+        one = types.SimpleNamespace(k=cache.k, v=cache.v, k_exp=cache.k_exp, v_exp=cache.v_exp,
+                                    table=cache.table[b:b + 1], Hkv=Hkv)
+        ref, mass, big = dense(one, prefix[b:b + 1], None, q[b:b + 1], None, 0.125)
+        if dtype == FP:         # a result past the type's largest number is rounded to infinity
+            ref = torch.where(ref.abs() < 65520, ref, ref.sign() * math.inf)
+        near(got[b:b + 1], ref, R.attention_slack(ref, mass, big, dtype, dh, length + n))

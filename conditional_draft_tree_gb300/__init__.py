@@ -758,7 +758,7 @@ def cache_commit(cache: PagedCache, first, path, lengths, n: int, stream=None):
 
 
 def cache_attention_workspace(cache: PagedCache, H: int, n: int, stream=None):
-    """A workspace for cache_attention with H query heads and n rows, for calls on ``stream``."""
+    """A workspace for cache_attention with up to H query heads and n rows, for calls on ``stream``."""
     _raw_stream(stream, cache._dev)      # the size follows the current device's SMs
     nbytes = lib().dt_cache_attention_workspace_bytes(cache._struct, int(H), int(n))
     if nbytes == 0:

@@ -14,6 +14,7 @@
 // 16 / 4 heads: single tokens 90 us (3.0 TB/s of bf16 rows; 8-bit rows 156 us), trees of 16
 // rows 244 us, of 65 rows 0.98 ms (71 TFLOP/s; 8-bit rows 1.28 ms). Bound by latency: four
 // warps a block, one block an SM at this head size, and 8-bit rows converted in between.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -497,6 +498,9 @@ cudaError_t launch_any(const AttnArgs &a, int bm, cudaStream_t st) {
 int64_t slot_floats(const AttnPlan &p) {
   return (static_cast<int64_t>(p.bm) * (p.dhp + 2) + 7) / 8 * 8;
 }
+size_t plan_bytes(const AttnPlan &p) {
+  return static_cast<size_t>(p.grid) * (2 * sizeof(int4) + 6 * slot_floats(p) * sizeof(float));
+}
 
 bool al4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -516,7 +520,7 @@ int attn_plan(const dt_cache &c, int H, int n, AttnPlan *p) {
     p->row_tiles = static_cast<int>((rows + p->bm - 1) / p->bm);
     p->grid = sms;
   }
-  p->bytes = static_cast<size_t>(p->grid) * (2 * sizeof(int4) + 6 * slot_floats(*p) * sizeof(float));
+  p->bytes = plan_bytes(*p);
   return DT_OK;
 }
 
@@ -528,7 +532,12 @@ size_t dt_cache_attention_workspace_bytes(const dt_cache *c, int H, int n) {
   dt::AttnPlan p;
   if (dt::check_cache(c) || H < 1 || H % c->Hkv || n < 1 || n > 65536 || dt::attn_plan(*c, H, n, &p))
     return 0;
-  return p.bytes;
+  // Units of two row tiles are as long as the rows divide: 65 x 4 stacked rows take units of
+  // 174, 64 x 4 take 256. The size is that of the largest that so many rows or fewer take, so
+  // that a workspace serves every smaller call.
+  if (p.kind == dt::AttnPlan::kWide)
+    p.bm = 2 * static_cast<int>(std::min<int64_t>(static_cast<int64_t>(n) * (H / c->Hkv), 128));
+  return dt::plan_bytes(p);
 }
 
 int dt_cache_attention(const dt_cache *c, const dt_heads *q, int n, int dtype,

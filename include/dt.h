@@ -476,7 +476,8 @@ int dt_cache_commit(const dt_cache *c, const int32_t *first, const int32_t *path
  * those of k with dtype DT_F16 as dt_cache_read gives them.
  * workspace: dt_cache_attention_workspace_bytes bytes, 256-byte aligned, for the
  * partial results of requests whose keys are cut over several blocks (0 = invalid
- * sizes). */
+ * sizes). The size for H heads and n rows serves every call on the cache with as many
+ * heads and rows or fewer. */
 size_t dt_cache_attention_workspace_bytes(const dt_cache *c, int H, int n);
 int dt_cache_attention(const dt_cache *c, const dt_heads *q, int n, int dtype,
                        const int32_t *prefix_len, const int32_t *counts, const uint8_t *mask,

@@ -251,3 +251,19 @@ def test_huge_values_of_little_weight_beside_ordinary_ones(dtype, batch, length,
         if dtype == FP:         # a result past the type's largest number is rounded to infinity
             ref = torch.where(ref.abs() < 65520, ref, ref.sign() * math.inf)
         near(got[b:b + 1], ref, R.attention_slack(ref, mass, big, dtype, dh, length + n))
+
+
+@pytest.mark.parametrize("H,Hkv,dh", [(32, 8, 128), (8, 8, 64), (40, 8, 128), (16, 4, 256), (64, 4, 96)])
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+def test_a_workspace_serves_any_smaller_call(kind, H, Hkv, dh):
+    cache = R.make_cache(dt, kind, BF, 3, 600, Hkv, 32, dh, 380)
+    L = dt.lib()
+    sizes = [L.dt_cache_attention_workspace_bytes(cache._struct, H, n) for n in range(1, 300)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:])) and sizes[0] > 0
+    assert all(L.dt_cache_attention_workspace_bytes(cache._struct, h, 33) <= sizes[32] for h in range(Hkv, H + 1, Hkv))
+    ws = dt.cache_attention_workspace(cache, H, 65)
+    prefix = i32([500, 3, 130])
+    for n in (65, 64, 33, 32, 17, 5, 1):
+        q = queries(3, n, H, dh, BF, 381).cuda()
+        assert torch.equal(dt.cache_attention(cache, q, prefix, workspace=ws), dt.cache_attention(cache, q, prefix))
+    cache.check()

@@ -35,7 +35,6 @@
 // merge of a block's warps: 18 us for one request at 300 keys.
 #include <cmath>
 #include <cstdint>
-#include <type_traits>
 #include <cuda.h>
 
 #include "dt_cache_attn.cuh"
@@ -294,25 +293,6 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
       auto there = [&](int x) { return key_at(x) < end && ((good >> (x >> 1)) & 1u); };
       // ------------------------------------------------------------ scores
       // (in two sums each, so that half as many products wait for one another)
-      uint32_t ve[2 * NG];             // V's exponent bytes of the thread's keys
-      float kmul[2 * NG];
-      auto read_exponents = [&] {
-#pragma unroll
-        for (int h = 0; h < NG; ++h) {
-          if (QUANT) {
-            const uint8_t *e = ss.exps[warp][stage_out] + 16 * h + key0;
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(e - (g & 1)) >> (8 * (g & 1));
-            const uint32_t v = *reinterpret_cast<const uint32_t *>(e + SUB - (g & 1)) >> (8 * (g & 1));
-            kmul[2 * h] = row_scale(w & 255u);
-            kmul[2 * h + 1] = row_scale((w >> 16) & 255u);
-            ve[2 * h] = v & 255u;
-            ve[2 * h + 1] = (v >> 16) & 255u;
-          } else {
-            kmul[2 * h] = kmul[2 * h + 1] = 1.0f;
-            ve[2 * h] = ve[2 * h + 1] = 0u;
-          }
-        }
-      };
       float s[NG][RN][4], s2[NG][RN][4];
 #pragma unroll
       for (int h = 0; h < NG; ++h)
@@ -320,66 +300,111 @@ cache_attention_few_kernel(const __grid_constant__ AttnArgs a, int stages,
         for (int z = 0; z < RN; ++z)
 #pragma unroll
           for (int y = 0; y < 4; ++y) s[h][z][y] = s2[h][z][y] = 0.0f;
-      auto products = [&](auto rounded) {
-        constexpr bool kRounded = decltype(rounded)::value;
 #pragma unroll
-        for (int d = 0; d < (QUANT ? DH / 64 : DH / 32); ++d) {
-          uint4 c[NG][2];
+      for (int d = 0; d < (QUANT ? DH / 64 : DH / 32); ++d) {
+        uint4 c[NG][2];
 #pragma unroll
-          for (int h = 0; h < NG; ++h)
+        for (int h = 0; h < NG; ++h)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int key = x ? key1 : key0;
+            c[h][x] = *reinterpret_cast<const uint4 *>(
+                sK + (QUANT ? h : d >> 1) * 2048 + key * 128 +
+                (((QUANT ? 4 * d + t4 : 4 * (d & 1) + t4) ^ (key & 7)) << 4));
+          }
+#pragma unroll
+        for (int i = 0; i < (QUANT ? 4 : 2); ++i)
+#pragma unroll
+          for (int h = 0; h < NG; ++h) {
+            uint32_t ka[4];            // rows g, g + 8; four values each
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const int key = x ? key1 : key0;
-              c[h][x] = *reinterpret_cast<const uint4 *>(
-                  sK + (QUANT ? h : d >> 1) * 2048 + key * 128 +
-                  (((QUANT ? 4 * d + t4 : 4 * (d & 1) + t4) ^ (key & 7)) << 4));
+              const uint4 &v = c[h][x];
+              if (QUANT) {
+                const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+                ka[x] = e4m3_f16x2(w & 0xffffu);
+                ka[2 + x] = e4m3_f16x2(w >> 16);
+              } else {
+                ka[x] = i ? v.z : v.x;
+                ka[2 + x] = i ? v.w : v.y;
+              }
             }
 #pragma unroll
-          for (int i = 0; i < (QUANT ? 4 : 2); ++i)
+            for (int z = 0; z < RN; ++z) {
+              const uint32_t(&qb)[2] = q[(QUANT ? 4 : 2) * d + i][z];
+              mma16<QDT>(i & 1 ? s2[h][z] : s[h][z], ka, qb[0], qb[1]);
+            }
+          }
+      }
+      uint32_t ve[2 * NG];             // V's exponent bytes of the thread's keys
+      float kmul[2 * NG];
 #pragma unroll
-            for (int h = 0; h < NG; ++h) {
-              uint32_t ka[4];            // rows g, g + 8; four values each
+      for (int h = 0; h < NG; ++h) {
+        if (QUANT) {
+          const uint8_t *e = ss.exps[warp][stage_out] + 16 * h + key0;
+          const uint32_t w = *reinterpret_cast<const uint32_t *>(e - (g & 1)) >> (8 * (g & 1));
+          const uint32_t v = *reinterpret_cast<const uint32_t *>(e + SUB - (g & 1)) >> (8 * (g & 1));
+          kmul[2 * h] = row_scale(w & 255u);
+          kmul[2 * h + 1] = row_scale((w >> 16) & 255u);
+          ve[2 * h] = v & 255u;
+          ve[2 * h + 1] = (v >> 16) & 255u;
+        } else {
+          kmul[2 * h] = kmul[2 * h + 1] = 1.0f;
+          ve[2 * h] = ve[2 * h + 1] = 0u;
+        }
+      }
+      if (QUANT && DT == DT_F16) {
+        // Scales of which fp16 rounds or saturates a value: the scores of the keys as
+        // dt_cache_read gives them, in a short loop that reads Q again. (One token at 300 keys
+        // takes 22 us, 21 without this, 26 with a second copy of the products above.)
+        bool odd = false;
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint4 &v = c[h][x];
-                if (QUANT) {
-                  const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-                  if (kRounded) {
-                    ka[x] = e4m3_to16<DT_F16>(w & 0xffffu, kmul[2 * h + x]);
-                    ka[2 + x] = e4m3_to16<DT_F16>(w >> 16, kmul[2 * h + x]);
-                  } else {
-                    ka[x] = e4m3_f16x2(w & 0xffffu);
-                    ka[2 + x] = e4m3_f16x2(w >> 16);
-                  }
-                } else {
-                  ka[x] = i ? v.z : v.x;
-                  ka[2 + x] = i ? v.w : v.y;
-                }
-              }
+        for (int x = 0; x < 2 * NG; ++x) odd |= kmul[x] < 0x1p-15f || kmul[x] > 0x1p7f;
+        if (__any_sync(kFull, odd)) {
+          odd = false;
+#pragma unroll
+          for (int x = 0; x < 2 * NG; ++x) {
+            if (kmul[x] < 0x1p-33f) kmul[x] = 0.0f;      // below half of fp16's least step: zeros
+            odd |= kmul[x] > 0.0f && (kmul[x] < 0x1p-15f || kmul[x] > 0x1p7f);
+          }
+          if (__any_sync(kFull, odd)) {
+#pragma unroll
+            for (int h = 0; h < NG; ++h)
+#pragma unroll
+              for (int z = 0; z < RN; ++z)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) s[h][z][y] = s2[h][z][y] = 0.0f;
+#pragma unroll 1
+            for (int k16 = 0; k16 < DH / 16; ++k16) {    // four values of each of four lanes
+              const int at = 64 * (k16 >> 2) + 16 * t4 + 4 * (k16 & 3);
+              uint2 qw[RN];
 #pragma unroll
               for (int z = 0; z < RN; ++z) {
-                const uint32_t(&qb)[2] = q[(QUANT ? 4 : 2) * d + i][z];
-                mma16<QDT>(i & 1 ? s2[h][z] : s[h][z], ka, qb[0], qb[1]);
+                const int r = 8 * z + g, i = r / a.G;
+                qw[z] = make_uint2(0u, 0u);
+                if (r < rows && at < dh)
+                  qw[z] = *reinterpret_cast<const uint2 *>(a.q + b * a.qb + (hk * a.G + r - i * a.G) * a.qh +
+                                                           i * a.qr + 2 * at);
+              }
+#pragma unroll
+              for (int h = 0; h < NG; ++h) {
+                uint32_t ka[4];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const int key = x ? key1 : key0;
+                  const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                      sK + h * 2048 + key * 128 + (((at >> 4) ^ (key & 7)) << 4) + (at & 15));
+                  ka[x] = e4m3_to16<DT_F16>(w & 0xffffu, kmul[2 * h + x]);
+                  ka[2 + x] = e4m3_to16<DT_F16>(w >> 16, kmul[2 * h + x]);
+                }
+#pragma unroll
+                for (int z = 0; z < RN; ++z) mma16<DT_F16>(s[h][z], ka, qw[z].x, qw[z].y);
               }
             }
-        }
-      };
-      if (DT == DT_F16 && QUANT) {
-        // rows of which fp16 rounds or saturates a value: as dt_cache_read gives them
-        read_exponents();
-        bool odd_scale = false;
 #pragma unroll
-        for (int x = 0; x < 2 * NG; ++x) odd_scale |= kmul[x] < 0x1p-15f || kmul[x] > 0x1p7f;
-        if (__any_sync(kFull, odd_scale)) {
-          products(std::true_type{});
-#pragma unroll
-          for (int x = 0; x < 2 * NG; ++x) kmul[x] = 1.0f;
-        } else {
-          products(std::false_type{});
+            for (int x = 0; x < 2 * NG; ++x) kmul[x] = 1.0f;
+          }
         }
-      } else {
-        products(std::false_type{});
-        read_exponents();
       }
       uint32_t see = ~0u;              // bit (2 h + x) 2 RN + 2 z + e: the row sees the key
       if (masked) {

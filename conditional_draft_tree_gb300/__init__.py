@@ -567,14 +567,19 @@ def _ints(t, what: str, shape, dev):
     return t.data_ptr()
 
 
+_CURRENT = contextlib.nullcontext()
+
+
 def _made_on(stream):
     """Where a call makes its tensors: on the stream that its kernels run on, whose part of the
     caching allocator they then belong to. Memory of another stream's part may still be in
     use there, and would be handed out again there while the kernels run."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return torch.cuda.stream(stream) if stream is not None else _CURRENT
 
 
 def _dense_like(t, stream):
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     with _made_on(stream):
         return torch.empty_like(t, memory_format=torch.contiguous_format)
 

@@ -11,9 +11,10 @@
 //
 // Products are mma.sync m16n8k16, a warp's 16 rows by the tile's keys, and the copies of
 // the next tile run during this one's. Measured at head size 256, 16 requests at 4096 keys,
-// 16 / 4 heads: single tokens 90 us (3.0 TB/s of bf16 rows; 8-bit rows 156 us), trees of 16
-// rows 244 us, of 65 rows 0.98 ms (71 TFLOP/s; 8-bit rows 1.28 ms). Bound by latency: four
-// warps a block, one block an SM at this head size, and 8-bit rows converted in between.
+// 16 / 4 heads: single tokens 92 us (2.9 TB/s of bf16 rows; 8-bit rows 158 us, with fp16
+// queries, whose weights are two products, 205 us), trees of 16 rows 242 us, of 65 rows 0.97 ms
+// (72 TFLOP/s; 8-bit rows 1.20 ms, 1.53 ms). Bound by latency: four warps a block, one block
+// an SM at this head size, and 8-bit rows converted in between.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

@@ -28,11 +28,11 @@
 // 32 tokens at 8192 keys 135 us before, 133 us now.) The result has that power of two taken
 // out. fp16 results need weights of more than bf16's 8 bits: two terms.
 //
-// Measured, 32 / 8 heads, dh 128, 32 single tokens at 8192 keys: 8-bit rows 137 us, 3.9 TB/s
-// of cache rows; 16-bit rows 203 us, 5.3 TB/s (of 6.8 that a copy reaches). For 8-bit rows a
+// Measured, 32 / 8 heads, dh 128, 32 single tokens at 8192 keys: 8-bit rows 133 us, 4.1 TB/s
+// of cache rows; 16-bit rows 205 us, 5.2 TB/s (of 6.8 that a copy reaches). For 8-bit rows a
 // scheduler's three warps take about 1800 cycles for their steps of 32 keys, where memory
 // would deliver them in 1400: conversions and products wait on each other; short caches are bound by a launch, its cut and the
-// merge of a block's warps: 18 us for one request at 300 keys.
+// merge of a block's warps: 22 us for one request at 300 keys.
 #include <cmath>
 #include <cstdint>
 #include <cuda.h>
@@ -695,15 +695,21 @@ cudaError_t go_dh(const AttnArgs &a, const AttnPlan &p, const CUtensorMap &k, co
 
 // For units of one row tile of at most 16 rows. False where the kernel does not apply.
 // Sixteen, measured against the tcgen05 kernel (us, that one second; single tokens of G
-// heads; batch x keys; head size):
-//                            1 x 300     1 x 32768    8 x 2048   32 x 8192   128 x 1024
-//   bf16 rows, 64,  G 8     14.3  32.7  36.9  43.0  28.7  34.8   123   152     86   121
-//              64,  G 16    20.5  32.8  47.1  63.5  32.8  36.9   123   152    107   121
-//              128, G 8     18.4  35.3  43.0  47.1  36.9  43.0   197   197    123   150
-//              128, G 16    26.6  36.9  57.3  63.6  47.1  43.0   215   201    162   156
-//   8-bit rows, 128, G 8    22.5  38.9  45.1  49.2  38.9  43.0   137   201    119   193
-//              128, G 16    41.0  38.9  65.5  67.6  55.3  45.1   215   205    191   201
-// (More rows would need a third N tile and registers that are not there.)
+// heads, 8 key/value heads; requests x keys; head size), with the ratio of the two in the mean:
+//                              1 x 300  1 x 32768  8 x 2048  32 x 8192  128 x 1024
+//   bf16, 16-bit  64,  G 8     14  31    37  51     29  37   122  152     86  121   0.68
+//                 64,  G 16    29  31    45  57     32  37   123  152    103  121   0.85
+//                 128, G 8     22  33    57  68     39  44   205  199    124  150   0.85
+//                 128, G 9     43  35    70  70     45  45   214  200    158  152   1.07
+//                 128, G 16    25  35    70  72     45  45   217  202    161  156   0.95
+//   bf16, 8-bit   64,  G 16    27  37    49  62     38  43   141  201    125  176   0.76
+//                 128, G 8     22  41    51  62     37  45   131  204    114  195   0.67
+//                 128, G 9     39  41    71  64     53  45   197  206    180  200   1.01
+//                 128, G 16    39  41    70  68     53  47   197  206    182  204   0.99
+//   fp16, 8-bit   128, G 8     22  45    51  71     37  51   134  248    115  255   0.58
+//                 128, G 16    37  47    76  76     55  53   237  250    204  269   0.90
+// (fp16 over 16-bit rows as bf16.) Nine to sixteen rows at head sizes above 64 are about
+// even: their second N tile spills 160 to 480 bytes a thread. More rows would need a third.
 bool few_plan(const dt_cache &c, int64_t rows, int sms, int smem, AttnPlan *p) {
   if (c.dh > 128 || rows > kFewRows) return false;
   p->kind = AttnPlan::kFew;

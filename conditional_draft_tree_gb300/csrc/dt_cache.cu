@@ -4,9 +4,10 @@
 //
 // Turning: y_a = m (x_a cos - x_b sin), y_b = m (x_a sin + x_b cos). The angle of pair
 // i at position p is frac(p f_i / 2 pi) turns; f_i / 2 pi is a 64-bit fraction of
-// a turn, so p times it modulo 2^64 is exact to p 2^-65 turns, where a product in
-// fp32 would be off by p 2^-25. The upper 32 bits, as a signed number in units of
-// 2^-31 half turns, go to sincospif.
+// a turn, and p times it modulo 2^64 is exact, where a product in fp32 would be off by
+// p 2^-25 turns: what is left is the table's own error, below p 2^-55 (it is computed in
+// double precision). The upper 32 bits, as a signed number in units of 2^-31 half turns,
+// go to sincospif.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

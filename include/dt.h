@@ -363,8 +363,11 @@ int dt_adaptive_budget(const dt_tree_out *out, int batch, int N, double c_fixed,
  *
  * dt_rotary_table (host only): fills turns[rot/2] (host memory) with f_i / 2 pi in
  * units of 2^-64 turns, and *magnitude. A position times such a fraction, taken
- * modulo 2^64, is the angle's fraction of a turn, so positions of any size
- * lose nothing. Copy the table to the device once and name it in dt_rotation.
+ * modulo 2^64, is the angle's fraction of a turn: the product is exact at any
+ * position p, and the angle within p 2^-55 turns (the table is computed in double
+ * precision). Copy the table to the device once and name it in dt_rotation. A table
+ * of other frequencies (a model that ramps over a pair's index, not over its turns)
+ * and another magnitude are the caller's to fill in.
  * rot: a multiple of 8 in [8, 256]; base > 1; factor >= 1; trained >= 1 and
  * beta_fast > beta_slow for DT_ROTARY_PARTS. */
 #define DT_ROTARY_NONE 0
@@ -472,8 +475,10 @@ int dt_cache_commit(const dt_cache *c, const int32_t *first, const int32_t *path
  * own, or either for a DT_E4M3 cache). n <= DT_MAX_N + 1 with a mask, n <= 65536
  * without. Products are accumulated in fp32 and the softmax statistics are fp32; its
  * weights are rounded to the 16-bit type for the product with v (bf16: relative 2^-8
- * each, as the output's own rounding). A DT_E4M3 cache's values are taken as they are,
- * those of k with dtype DT_F16 as dt_cache_read gives them.
+ * each, as the output's own rounding; dt_tree_attention takes two bf16 terms and is
+ * that much closer). A DT_E4M3 cache's values are taken as they are (with dtype
+ * DT_F16 against weights of two bf16 terms), those of k with dtype DT_F16 as
+ * dt_cache_read gives them.
  * workspace: dt_cache_attention_workspace_bytes bytes, 256-byte aligned, for the
  * partial results of requests whose keys are cut over several blocks (0 = invalid
  * sizes). The size for H heads and n rows serves every call on the cache with as many

@@ -193,3 +193,9 @@ def test_large_heads_repeat_bit_for_bit():
     for _ in range(30):
         assert torch.equal(dt.cache_attention(cache, q, pre), want)
     cache.check()
+
+
+@pytest.mark.parametrize("kind,n,G,dh", [("16", 20, 2, 64), ("e4m3", 20, 2, 128), ("16", 3, 2, 192), ("e4m3", 20, 2, 256)])
+def test_more_requests_than_a_warp_adds_up(kind, n, G, dh):
+    """Above 128 requests a block finds its part of the work with all its threads."""
+    attend(kind, BF, n, G, 1, dh, [(37 * b) % 90 for b in range(300)], [1 + (b * 7) % n for b in range(300)])

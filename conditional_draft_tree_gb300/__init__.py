@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(HERE, "libdt.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA = 0, -1, -2, -3
 ERR_NONFINITE, ERR_TIMEOUT, ERR_BAD_TEMPERATURE, ERR_BAD_PAGE = -4, -5, -6, -7
+ERR_NO_PAGES, ERR_BAD_INDEX = -8, -9
 F32, BF16, F16, E4M3 = 0, 1, 2, 3
 NUM_PHASE_EVENTS = 4
 OPT_TEST_BARRIER_TIMEOUT = 2  # dt_options.flags: failure-detection test hook
@@ -35,7 +36,9 @@ EXPORTS = ("dt_abi_version", "dt_status_string", "dt_prepared_bytes", "dt_prepar
            "dt_chain_kernel_launches", "dt_decode_chains", "dt_tree_positions",
            "dt_tree_attention", "dt_adaptive_budget", "dt_mapped_host_pointer",
            "dt_rotary_table", "dt_rotary", "dt_cache_write", "dt_cache_read", "dt_cache_commit",
-           "dt_cache_attention_workspace_bytes", "dt_cache_attention")
+           "dt_cache_attention_workspace_bytes", "dt_cache_attention", "dt_cache_reserve",
+           "dt_cache_slots", "dt_rms_norm", "dt_quantize_rows", "dt_project_workspace_bytes",
+           "dt_project")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -77,6 +80,24 @@ class DtHeads(C.Structure):
 class DtCache(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("k", "v", "k_exp", "v_exp", "table", "status")] + \
         [(n, C.c_int) for n in ("pages", "page", "Hkv", "dh", "dtype", "batch", "table_width")]
+
+
+class DtPagePool(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("held", "free_pages", "state")]
+
+
+class DtRows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("stride_outer", C.c_int64), ("stride_inner", C.c_int64)]
+
+
+class DtMatrix(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("exps", C.c_void_p), ("ld", C.c_int64)] + \
+        [(n, C.c_int) for n in ("O", "K", "dtype")]
+
+
+class DtAdapters(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("down", "up", "scale")] + \
+        [(n, C.c_int) for n in ("count", "rank")]
 
 
 class DtError(RuntimeError):
@@ -145,6 +166,15 @@ def lib():
         L.dt_cache_attention_workspace_bytes.argtypes = [cache, C.c_int, C.c_int]
         L.dt_cache_attention.argtypes = [cache, heads, C.c_int, C.c_int] + [C.c_void_p] * 3 + \
             [C.c_float, heads, C.c_void_p, C.c_size_t, C.c_void_p]
+        rows, v, i, n64 = C.POINTER(DtRows), C.c_void_p, C.c_int, C.c_int64
+        L.dt_cache_reserve.argtypes = [cache, C.POINTER(DtPagePool), v, v]
+        L.dt_cache_slots.argtypes = [cache, i, v, v, v, v, v]
+        L.dt_rms_norm.argtypes = [rows] * 4 + [v] * 3 + [C.c_float] * 2 + [i] * 4 + [v]
+        L.dt_quantize_rows.argtypes = [rows, v, v] + [i] * 4 + [v]
+        L.dt_project_workspace_bytes.restype = C.c_size_t
+        L.dt_project_workspace_bytes.argtypes = [i] * 3
+        L.dt_project.argtypes = [C.POINTER(DtMatrix), v, n64, v, i, i, i, C.POINTER(DtAdapters), v, v,
+                                 n64, v, n64, v, v, C.c_size_t, v]
         _lib = L
     return _lib
 
@@ -801,4 +831,294 @@ def cache_attention(cache: PagedCache, q, prefix_len, mask=None, counts=None, sc
                                     dh ** -0.5 if scale is None else scale, ho, workspace.data_ptr(),
                                     workspace.numel() * workspace.element_size(), handle),
            "dt_cache_attention")
+    return out
+
+
+# --------------------------- page tables, norms and projections around the cache's layers
+
+class PagePool:
+    """The free pages of ``cache`` and how many entries of its table row each request holds
+    (dt_page_pool): held [batch] int32, free_pages [pages] int32 (the first state[0] are free),
+    state [2] int32. ``PagePool.all_free(cache)`` begins with every page free and empty tables.
+    Requests' pages are their own: a page that two rows of the table name is not for this class."""
+
+    def __init__(self, cache: PagedCache, held, free_pages, state):
+        dev = cache._dev
+        self.cache, self.held, self.free_pages, self.state = cache, held, free_pages, state
+        pages = cache._struct.pages
+        for t in (held, free_pages, state):
+            if t is None:
+                raise ValueError("held, free_pages and state are needed")
+        self._struct = DtPagePool(_ints(held, "held", (cache.batch,), dev),
+                                  _ints(free_pages, "free_pages", (pages,), dev),
+                                  _ints(state, "state", (2,), dev))
+
+    @classmethod
+    def all_free(cls, cache: PagedCache):
+        """A pool of nothing but free pages (taken in rising order); the cache's table is set to -1."""
+        pages = cache._struct.pages
+        cache.table.fill_(-1)
+        free = torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=cache.device)
+        held = torch.zeros(cache.batch, dtype=torch.int32, device=cache.device)
+        return cls(cache, held, free, torch.tensor([pages, 0], dtype=torch.int32, device=cache.device))
+
+
+def cache_reserve(pool: PagePool, lengths, stream=None):
+    """dt_cache_reserve: the pages for lengths[b] rows of every request ([batch] int32), taken
+    from the pool or given back to it; the cache's table, ``pool.held`` and the free pages change.
+    A request that the pool has too few pages for gets none, which ``cache.check()`` reports."""
+    cache = pool.cache
+    handle = _raw_stream(stream, cache._dev)
+    if lengths is None:
+        raise ValueError("lengths are needed")
+    _check(lib().dt_cache_reserve(cache._struct, pool._struct,
+                                  _ints(lengths, "lengths", (cache.batch,), cache._dev), handle),
+           "dt_cache_reserve")
+
+
+def cache_slots(cache: PagedCache, n: int, first, counts=None, slots=None, positions=None, stream=None):
+    """dt_cache_slots: for rows first[b] .. first[b] + counts[b] - 1 their places in the pool
+    (page * page size + row in the page, [batch][n] int64) and their positions ([batch][n] int32);
+    -1 behind them. Returns (slots, positions)."""
+    dev, b = cache._dev, (cache.batch,)
+    handle = _raw_stream(stream, dev)
+    shape = torch.Size((cache.batch, n))
+    with _made_on(stream):
+        if slots is None:
+            slots = torch.empty(shape, dtype=torch.int64, device=cache.device)
+        if positions is None:
+            positions = torch.empty(shape, dtype=torch.int32, device=cache.device)
+    if slots.shape != shape or slots.dtype != torch.int64 or not slots.is_contiguous() or \
+            slots.get_device() != dev:
+        raise ValueError(f"slots must be a contiguous int64 tensor of shape {tuple(shape)} on the cache's device")
+    if first is None:
+        raise ValueError("first is needed")
+    _check(lib().dt_cache_slots(cache._struct, int(n), _ints(first, "first", b, dev),
+                                _ints(counts, "counts", b, dev), slots.data_ptr(),
+                                _ints(positions, "positions", shape, dev), handle), "dt_cache_slots")
+    return slots, positions
+
+
+class Rows8:
+    """8-bit rows: e4m3 codes [...][d] (float8_e4m3fn or uint8, dense rows) and the exponent byte of
+    each row, exps [...] uint8; a row's values are code * 2^(exps - 127), all NaN for exps 255."""
+
+    def __init__(self, codes, exps):
+        if codes.dtype not in (torch.float8_e4m3fn, torch.uint8) or codes.dim() < 2 or \
+                codes.get_device() < 0 or codes.stride(-1) != 1:
+            raise ValueError("codes must be a [...][d] float8_e4m3fn or uint8 CUDA tensor with a dense last "
+                             "dimension")
+        if exps.shape != codes.shape[:-1] or exps.dtype != torch.uint8 or not exps.is_contiguous() or \
+                exps.get_device() != codes.get_device():
+            raise ValueError("exps must be a contiguous uint8 tensor, one a row, on the codes' device")
+        self.codes, self.exps, self.shape = codes, exps, codes.shape
+
+    def values(self, dtype=torch.float32):
+        """The rows' values (plain torch operations, for looking at them)."""
+        e = self.exps.to(torch.int32)
+        scale = torch.ldexp(torch.ones((), device=e.device), e - 127)
+        x = self.codes.view(torch.float8_e4m3fn).float() * scale[..., None]
+        return torch.where((e == 255)[..., None], float("nan"), x).to(dtype)
+
+
+def _row_view(t, what: str, dtype=None, dev=None, shape=None):
+    """A [...][d] tensor as a dt_rows of two outer dimensions: its rows lie at one stride within
+    the second-last dimension and at one within those before it. Returns the view and its sizes."""
+    kind = _TYPE16.get(t.dtype)
+    if kind is None or t.get_device() < 0 or (dtype is not None and (kind != dtype or t.get_device() != dev or
+                                                                       t.shape != shape)):
+        raise ValueError(f"{what} must be a bfloat16 or float16 CUDA tensor" +
+                         ("" if dtype is None else " of the rows' shape, type and device"))
+    size, s = t.shape, t.stride()
+    if len(size) < 2 or s[-1] != 1:
+        raise ValueError(f"{what} must be [...][d] with a dense last dimension")
+    outer, step = 1, 0
+    for n, st in zip(reversed(size[:-2]), reversed(s[:-2])):
+        if n == 1:
+            continue
+        if outer == 1:
+            step = st
+        elif st != step * outer:
+            raise ValueError(f"{what}'s rows must lie at two strides: one within the second-last dimension, one "
+                             "across those before it")
+        outer *= n
+    return DtRows(t.data_ptr(), step, s[-2]), outer, size[-2], size[-1], kind
+
+
+class Norm:
+    """A root-mean-square norm: weight [d] (bfloat16 or float16, or None), eps, and ``offset``
+    added to the weight (1 where a model stores it that way)."""
+
+    def __init__(self, weight, eps: float = 1e-6, offset: float = 0.0):
+        if weight is not None and (weight.dim() != 1 or weight.dtype not in _TYPE16 or
+                                   not weight.is_contiguous() or weight.get_device() < 0):
+            raise ValueError("weight must be a contiguous [d] bfloat16 or float16 CUDA tensor")
+        self.weight, self.eps, self.offset = weight, float(eps), float(offset)
+
+
+def _codes_like(x, stream):
+    with _made_on(stream):
+        return (torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device),
+                torch.empty(x.shape[:-1], dtype=torch.uint8, device=x.device))
+
+
+def rms_norm(norm: Norm, x, residual=None, kind: str = "16", out=None, total=None, stream=None):
+    """dt_rms_norm of the rows x [...][d], of x + residual where that is given. ``kind``: "16" (a
+    tensor of x's type), "e4m3" (a Rows8), or "both" ((tensor, Rows8), from the same fp32 values).
+    Returns that, and with ``residual`` also the sum: (y, total). ``total`` and ``out`` may be
+    x or residual."""
+    if kind not in ("16", "e4m3", "both"):
+        raise ValueError('kind must be "16", "e4m3" or "both"')
+    vx, outer, inner, d, dtype = _row_view(x, "x")
+    dev, shape, w = x.get_device(), x.shape, norm.weight
+    handle = _raw_stream(stream, dev)
+    if w is not None and (w.shape[0] != d or _TYPE16[w.dtype] != dtype or w.get_device() != dev):
+        raise ValueError("the norm's weight must have one value a column, of the rows' type and device")
+    vr = vt = vo = codes = exps = None
+    if residual is not None:
+        vr = _row_view(residual, "residual", dtype, dev, shape)[0]
+        if total is None:
+            total = _dense_like(x, stream)
+        vt = _row_view(total, "total", dtype, dev, shape)[0]
+    elif total is not None:
+        raise ValueError("total is the sum of x and residual: residual is needed")
+    if kind != "e4m3":
+        if out is None:
+            out = _dense_like(x, stream)
+        vo = _row_view(out, "out", dtype, dev, shape)[0]
+    elif out is not None:
+        raise ValueError('out is for kind "16" or "both"')
+    if kind != "16":
+        codes, exps = _codes_like(x, stream)
+    _check(lib().dt_rms_norm(vx, vr, vt, vo, _ptr(codes), _ptr(exps), _ptr(w), norm.offset, norm.eps,
+                             outer, inner, d, dtype, handle), "dt_rms_norm")
+    y = out if kind == "16" else Rows8(codes, exps) if kind == "e4m3" else (out, Rows8(codes, exps))
+    return y if residual is None else (y, total)
+
+
+def quantize_rows(x, stream=None):
+    """dt_quantize_rows: the rows x [...][d] as a Rows8 (a weight matrix, or a projection's input
+    that comes from no norm)."""
+    vx, outer, inner, d, dtype = _row_view(x, "x")
+    handle = _raw_stream(stream, x.get_device())
+    codes, exps = _codes_like(x, stream)
+    _check(lib().dt_quantize_rows(vx, codes.data_ptr(), exps.data_ptr(), outer, inner, d, dtype, handle),
+           "dt_quantize_rows")
+    return Rows8(codes, exps)
+
+
+class Projection:
+    """A shared weight matrix W [O][K]: a bfloat16 or float16 tensor, or a Rows8 for 8-bit
+    projections. ``status`` collects the device's error codes of its calls; ``check()`` reads it
+    and raises."""
+
+    def __init__(self, weight):
+        t, exps = (weight.codes, weight.exps) if isinstance(weight, Rows8) else (weight, None)
+        if t.dim() != 2 or t.get_device() < 0 or t.stride(1) != 1 or (exps is None and t.dtype not in _TYPE16):
+            raise ValueError("weight must be a [O][K] bfloat16 or float16 CUDA tensor with dense rows, or a Rows8")
+        self.weight, self.O, self.K, self.device = weight, t.shape[0], t.shape[1], t.device
+        self._dev, self._type = t.get_device(), E4M3 if exps is not None else _TYPE16[t.dtype]
+        self.status = torch.zeros(1, dtype=torch.int32, device=t.device)
+        self._struct = DtMatrix(t.data_ptr(), _ptr(exps), max(t.stride(0), self.K) if self.O == 1 else t.stride(0),
+                                self.O, self.K, self._type)
+
+    def check(self):
+        """Wait for the device and raise if a call met a bad adapter index or timed out."""
+        code = int(self.status)
+        if code != OK:
+            raise DtError(f"projection: {status_string(code)}")
+
+
+class Adapters:
+    """Low-rank adapters of one projection: down [count][rank][K], up [count][O][rank] (bfloat16 or
+    float16, dense) and scale [count] fp32 (ones when None). Adapters of lower ranks are padded
+    with zeros."""
+
+    def __init__(self, down, up, scale=None):
+        dev = down.get_device()
+        if down.dim() != 3 or up.dim() != 3 or down.dtype not in _TYPE16 or up.dtype != down.dtype or dev < 0 or \
+                up.get_device() != dev or not (down.is_contiguous() and up.is_contiguous()) or \
+                up.shape[0] != down.shape[0] or up.shape[2] != down.shape[1]:
+            raise ValueError("down [count][rank][K] and up [count][O][rank] must be contiguous CUDA tensors of one "
+                             "16-bit type")
+        if scale is not None and (scale.shape != down.shape[:1] or scale.dtype != torch.float32 or
+                                  not scale.is_contiguous() or scale.get_device() != dev):
+            raise ValueError("scale must be a contiguous [count] float32 tensor on the adapters' device")
+        self.down, self.up, self.scale = down, up, scale
+        self.count, self.rank, self.K, self.O = down.shape[0], down.shape[1], down.shape[2], up.shape[1]
+        self._dev, self._type = dev, _TYPE16[down.dtype]
+        self._struct = DtAdapters(down.data_ptr(), up.data_ptr(), _ptr(scale), self.count, self.rank)
+
+
+def project_workspace(projection: Projection, batch: int, n: int, adapters: Adapters | None, stream=None):
+    """A workspace for project with up to ``batch`` requests of n rows, for calls on ``stream`` (None
+    without adapters)."""
+    _raw_stream(stream, projection._dev)
+    if adapters is None:
+        return None
+    nbytes = lib().dt_project_workspace_bytes(int(batch), int(n), adapters.rank)
+    if nbytes == 0:
+        raise DtError("dt_project_workspace_bytes failed (invalid sizes)")
+    with _made_on(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=projection.device)
+
+
+def _flat_rows(t, what: str, batch: int, n: int):
+    """Stride of the rows of a [batch][n][d] tensor, which lie at one."""
+    s = t.stride()
+    if s[2] != 1 or (batch > 1 and n > 1 and s[0] != n * s[1]):
+        raise ValueError(f"{what}'s rows must be dense and lie at one stride")
+    return s[1] if n > 1 else s[0] if batch > 1 else max(s[0], s[1], t.shape[2])
+
+
+def project(projection: Projection, x, adapters: Adapters | None = None, index=None, x16=None, dtype=None,
+            out=None, workspace=None, stream=None):
+    """dt_project: y [batch][n][O] = x W^T, and for requests with an adapter (index [batch] int32,
+    negative: none) scale (x A^T) B^T beside it. x: [batch][n][K] of the weight's type, or a Rows8 for
+    an 8-bit weight; then ``x16``, the same rows in 16 bits, is what the adapters see, and
+    ``dtype`` the result's type (that of out, x16 or the adapters, or bfloat16). ``workspace`` (of
+    project_workspace) is allocated for the call when None and needed."""
+    p, dev = projection, projection._dev
+    t, exps = (x.codes, x.exps) if isinstance(x, Rows8) else (x, None)
+    if t.dim() != 3 or t.shape[2] != p.K or t.get_device() != dev or (exps is not None) != (p._type == E4M3):
+        raise ValueError("x must be [batch][n][K] rows on the weight's device, a Rows8 for an 8-bit weight only")
+    batch, n, K = t.shape
+    handle = _raw_stream(stream, dev)
+    if exps is None:
+        if _TYPE16.get(t.dtype) != p._type:
+            raise ValueError("x must have the weight's type")
+        dtype = t.dtype
+    elif dtype is None:
+        dtype = out.dtype if out is not None else x16.dtype if x16 is not None else torch.bfloat16
+    kind = _TYPE16.get(dtype)
+    if kind is None:
+        raise ValueError("dtype must be bfloat16 or float16")
+    ldx16, set_struct = 0, None
+    if adapters is not None:
+        if adapters._dev != dev or adapters._type != kind or adapters.K != K or adapters.O != p.O:
+            raise ValueError("the adapters must match the weight's sizes and device and the result's type")
+        if index is None:
+            raise ValueError("adapters need an index of each request's")
+        set_struct = adapters._struct
+        if exps is not None:
+            if x16 is None or x16.shape != t.shape or x16.dtype != dtype or x16.get_device() != dev:
+                raise ValueError("adapters beside an 8-bit weight need x16, the rows in the result's type")
+            ldx16 = _flat_rows(x16, "x16", batch, n)
+        if workspace is None:
+            workspace = project_workspace(p, batch, n, adapters, stream)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the weight's device")
+    elif index is not None:
+        raise ValueError("an index needs adapters")
+    if out is None:
+        with _made_on(stream):
+            out = torch.empty((batch, n, p.O), dtype=dtype, device=p.device)
+    elif out.shape != (batch, n, p.O) or out.dtype != dtype or out.get_device() != dev:
+        raise ValueError("out must be [batch][n][O] of the result's type, on the weight's device")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().dt_project(p._struct, t.data_ptr(), _flat_rows(t, "x", batch, n), _ptr(exps), batch, n, kind,
+                            set_struct, _ints(index, "index", (batch,), dev),
+                            x16.data_ptr() if ldx16 else None, ldx16, out.data_ptr(),
+                            _flat_rows(out, "out", batch, n), p.status.data_ptr(), _ptr(workspace), ws_bytes,
+                            handle), "dt_project")
     return out

@@ -522,6 +522,8 @@ const char *dt_status_string(int code) {
     case DT_ERR_TIMEOUT: return "bounded inter-block wait expired; request output invalid";
     case DT_ERR_BAD_TEMPERATURE: return "temperature is negative or not finite";
     case DT_ERR_BAD_PAGE: return "a cache row lies outside its page table or the pool";
+    case DT_ERR_NO_PAGES: return "the pool has too few free pages";
+    case DT_ERR_BAD_INDEX: return "an adapter index is not below the number of adapters";
     default: return "unknown status code";
   }
 }

@@ -53,6 +53,8 @@ extern "C" {
 #define DT_ERR_TIMEOUT (-5)       /* device: a bounded inter-block wait expired; request output invalid */
 #define DT_ERR_BAD_TEMPERATURE (-6) /* device: temperature < 0 or not finite */
 #define DT_ERR_BAD_PAGE (-7)      /* device: a cache row outside the request's page table or the pool */
+#define DT_ERR_NO_PAGES (-8)      /* device: the pool has too few free pages for the request */
+#define DT_ERR_BAD_INDEX (-9)     /* device: a request's adapter index at or above their number */
 
 /* Hard limits of this library (checked by every entry point). */
 #define DT_MAX_M 256        /* candidates per depth */
@@ -64,7 +66,7 @@ extern "C" {
 #define DT_MAX_SPEC 16      /* speculative expansions per request and step */
 
 /* DT_F16 and DT_E4M3 are types of the paged cache and of the tensors around it;
- * weights are DT_F32 or DT_BF16. */
+ * a head's weights (dt_weights) are DT_F32 or DT_BF16. */
 typedef enum { DT_F32 = 0, DT_BF16 = 1, DT_F16 = 2, DT_E4M3 = 3 } dt_dtype;
 
 /* Problem sizes. Notation of the pages: V vocabulary, d backbone hidden size,
@@ -488,6 +490,108 @@ int dt_cache_attention(const dt_cache *c, const dt_heads *q, int n, int dtype,
                        const int32_t *prefix_len, const int32_t *counts, const uint8_t *mask,
                        float scale, const dt_heads *out, void *workspace, size_t workspace_bytes,
                        void *stream);
+
+/* ------------------------------------------------------------------------
+ * Page tables and slot maps from lengths. A pool's free pages are a stack on the
+ * device: `free_pages` [c->pages] int32, of which the first state[0] count; `held`
+ * [batch] int32 is how many entries of its table row each request holds. The caller
+ * fills them in once (all pages free: any order of 0 .. pages - 1, state[0] = pages,
+ * held zero, tables -1); state[1] is the library's own, zeroed once. A page that is
+ * held or free is so once: pages that requests share are not for these calls.
+ *
+ * dt_cache_reserve: request b gets the pages for lengths[b] rows,
+ * need = ceil(max(lengths[b], 0) / page). First every request that holds more than it
+ * needs gives back its table's last pages, the last request and its last page first;
+ * then those that hold fewer take pages from the end of the stack, the first request
+ * first, in the order of its table. Calls with the lengths of before undo each other
+ * exactly. Table entries that are given back become -1 (c->table is written); free_pages
+ * behind the count keeps what it held. Requests are served in order: one whose pages,
+ * with those that earlier requests ask for, are more than the stack holds gets none
+ * (DT_ERR_NO_PAGES in its status, held and table unchanged). One that needs more than
+ * table_width pages keeps what it has (DT_ERR_BAD_PAGE). batch <= 16384. Calls on the same
+ * pool must not overlap.
+ *
+ * dt_cache_slots: where rows lie and what their positions are: for i < counts[b] (NULL:
+ * n) slots[b][i] = table[b][(first[b] + i) / page] page + (first[b] + i) % page and
+ * positions[b][i] = first[b] + i; -1 for both behind them. A row outside the table or
+ * on a page outside the pool gets slot -1 (DT_ERR_BAD_PAGE). slots [batch][n] int64,
+ * positions [batch][n] int32 (either may be NULL). */
+typedef struct {
+  int32_t *held;         /* [batch] */
+  int32_t *free_pages;   /* [pages] */
+  int32_t *state;        /* [2]: free pages, 0 */
+} dt_page_pool;
+int dt_cache_reserve(const dt_cache *c, const dt_page_pool *pool, const int32_t *lengths,
+                     void *stream);
+int dt_cache_slots(const dt_cache *c, int n, const int32_t *first, const int32_t *counts,
+                   int64_t *slots, int32_t *positions, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Rows of d values: a [outer][inner][d] view with element strides (any; the last
+ * dimension is dense), so that the heads of a projection's output are rows too.
+ * 8-bit rows are those of the paged cache: e4m3 codes [rows][d] and an exponent byte
+ * a row (bias 127), the least e in [-117, 120] with max |y| <= 448 2^e; a row with a
+ * NaN or an infinity has byte 255 and codes 0x7f.
+ *
+ * dt_rms_norm: t = x + residual, y_i = t_i (offset + weight_i) / sqrt(mean(t^2) + eps),
+ * computed in fp32. total (with residual only) gets t, out gets y, rounded once each;
+ * codes and exps get y in 8 bits, taken from fp32. out, or codes and exps, may be NULL,
+ * not both. weight [d] has the rows' type (NULL: ones). An output may be one of the inputs
+ * (the same view), and must not overlap them otherwise; codes and exps are buffers of
+ * their own. d in [1, 32768], dtype DT_BF16 or DT_F16, eps >= 1e-30. Rows of a multiple
+ * of 8 values on 16-byte boundaries are moved 16 bytes at a time, others value by value.
+ *
+ * dt_quantize_rows: x itself in 8 bits. */
+typedef struct {
+  void *data;
+  int64_t stride_outer, stride_inner;
+} dt_rows;
+int dt_rms_norm(const dt_rows *x, const dt_rows *residual, const dt_rows *total,
+                const dt_rows *out, uint8_t *codes, uint8_t *exps, const void *weight,
+                float offset, float eps, int outer, int inner, int d, int dtype, void *stream);
+int dt_quantize_rows(const dt_rows *x, uint8_t *codes, uint8_t *exps, int outer, int inner,
+                     int d, int dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A projection that many requests share, and low-rank adapters of their own beside
+ * it: for row i of request b, with a = index[b],
+ *   y = x W^T + scale[a] (x A_a^T) B_a^T,
+ * the second term only where 0 <= a < adapters->count (a negative index: no adapter; one at or
+ * above count: none, and DT_ERR_BAD_INDEX in *status). Products are accumulated in fp32; x A^T, times
+ * the scale, is rounded to dtype (and so overflows where dtype does) before the
+ * product with B, y once.
+ *   w      W [O][K], dtype 16-bit or DT_E4M3 with exps [O] (8-bit rows); data 16-byte
+ *          aligned, row stride ld elements, a multiple of 16 bytes
+ *   x      [batch n][K] rows, of w's type: dtype itself, or 8-bit rows with x_exps
+ *          [batch n]; 16-byte aligned, row stride ldx, a multiple of 16 bytes
+ *   x16    the rows that the adapters see, for 8-bit weights with adapters (dt_rms_norm
+ *          gives both); NULL otherwise
+ *   y      [batch n][O] of type dtype (DT_BF16 or DT_F16), row stride ldy >= O, any; must
+ *          not overlap the inputs
+ *   A (down) [count][rank][K], B (up) [count][O][rank], dense, dtype, 16-byte aligned;
+ *          scale [count] fp32 (NULL: ones); adapters NULL: none
+ *   index  [batch] int32; with adapters only
+ *   status one int32 of the caller's, zeroed once: DT_ERR_BAD_INDEX, DT_ERR_TIMEOUT
+ * K: a multiple of 16 in [16, 65536]; O in [1, 2^24]; rank: a multiple of 16 in [16, 128];
+ * batch in [1, 65535], batch n <= 2^24. workspace: dt_project_workspace_bytes bytes,
+ * 256-byte aligned, for x A^T (may be 0: NULL without adapters); the size for a batch, n and
+ * rank serves smaller ones. Sums run in an order fixed by the sizes: results repeat. */
+typedef struct {
+  const void *data;
+  const uint8_t *exps;
+  int64_t ld;
+  int O, K, dtype;
+} dt_matrix;
+typedef struct {
+  const void *down, *up;
+  const float *scale;
+  int count, rank;
+} dt_adapters;
+size_t dt_project_workspace_bytes(int batch, int n, int rank);
+int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_exps, int batch,
+               int n, int dtype, const dt_adapters *adapters, const int32_t *index,
+               const void *x16, int64_t ldx16, void *y, int64_t ldy, int32_t *status,
+               void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static description of a status code. */
 const char *dt_status_string(int code);

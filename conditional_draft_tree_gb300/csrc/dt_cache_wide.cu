@@ -45,7 +45,6 @@ constexpr int kBlk = kW * 128;         // bytes of 128 rows of 64 16-bit values
 constexpr int kMaxRing = 8;
 constexpr int kSegs = 4;
 constexpr int kOddWords = (DT_MAX_N + 32) / 32;
-constexpr long long kWaitCycles = 4000000000ll;   // about 2 s
 
 // Warpgroups: two for weights, two (8-bit rows) that convert, one whose warps load, issue
 // the products and find segments. Registers at launch times threads is what setmaxnreg
@@ -67,40 +66,6 @@ struct Small {                          // behind the big buffers
   uint32_t tmem;
   int fail;
 };
-
-// Bounded wait for a phase. The limit is in SM cycles: a read of the clock register
-// costs a few cycles, of the global timer about a microsecond, which every wait that
-// is not over at once would pay.
-__device__ __forceinline__ bool mbar_wait_cycles(uint64_t *bar, uint32_t parity) {
-  const uint32_t at = smem_u32(bar);
-  long long t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(at), "r"(parity)
-        : "memory");
-    if (done) return true;
-    const long long t = clock64();
-    if (it == 0) t0 = t;
-    else if (t - t0 > kWaitCycles) return false;
-  }
-}
-
-// 128-byte swizzled operand descriptor; its address field counts 16-byte units, so an
-// operand further on is a plain addition
-__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return umma_desc(addr, lbo, sbo) | (2ull << 61);
-}
-
-// true in one lane of a converged warp
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
-  return r != 0;
-}
 
 __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
                                        uint64_t *bar) {
@@ -988,6 +953,20 @@ EncodeTiled encoder() {
 }
 
 }  // namespace
+
+bool matrix_map(const void *base, int size, int64_t cols, int64_t rows, int64_t row_bytes, int box_cols,
+                int box_rows, CUtensorMap *map) {
+  EncodeTiled enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t one[2] = {1, 1};
+  return enc(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base),
+             dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_cols * size == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // pages as [pages * Hkv][page][dh], a box of 128 bytes of `box_rows` rows, swizzled
 bool page_map(const dt_cache &c, const void *base, int box_rows, CUtensorMap *map) {

@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/dt.h"
@@ -68,6 +69,11 @@ int make_plan(const dt_dims *dims, int wdtype, const dt_options *opt, Plan *p);
 int validate_dims(const dt_dims *dims);
 // SMs and opt-in shared memory of the current device; an error code on another architecture
 int device_sm_count(int *sms, int *smem_optin);
+
+// [rows][cols] of 1- or 2-byte values, row_bytes apart (a multiple of 16), in boxes of box_rows rows of
+// 32 or 128 bytes, swizzled by as much; what lies outside reads as zero. False where it cannot be made.
+bool matrix_map(const void *base, int size, int64_t cols, int64_t rows, int64_t row_bytes, int box_cols,
+                int box_rows, CUtensorMap *map);
 
 // top-M over base logits -> candidate ids/values (+ optional user copy)
 cudaError_t launch_topm(const Plan &p, const float *base_logits, void *ws, int32_t *topm_out,

@@ -1,113 +1,867 @@
 // dt_project.cu -- a projection that many requests share, with low-rank adapters of their
-// own beside it: y = x W^T + scale_a (x A_a^T) B_a^T for the rows of a request with adapter a.
+// own beside it, on the tcgen05 tensor cores: y = x W^T + scale_a (x A_a^T) B_a^T for the rows of
+// a request with adapter a.
+//
+// The MMA's M side is 128 rows of W (256 in a pair of blocks), its N side a tile of up to 256 token
+// rows, so that one form serves single tokens and long prompts. K goes by in slabs of 128
+// bytes a row (64 16-bit values or 128 codes) through a ring that TMA fills. The adapters are more of
+// K: for the distinct adapters of a tile's rows one after the other, B_a beside W and, beside x, the
+// rows u = scale x A_a^T with zeros in the rows of other requests, so the shared and the own
+// products meet in one accumulator and B_a is read once a tile, however its requests lie. (8-bit
+// rows: in an accumulator of their own, as the shared one is scaled at the end.) u comes from a
+// launch before, which stacks the A_a of a tile's adapters on the M side; the projection begins
+// beside it and waits for it only where it reads u.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
+#include <type_traits>
 
-#include "dt_cache.cuh"
+#include "dt_cache_attn.cuh"
 #include "dt_internal.h"
+#include "dt_umma.cuh"
 
 namespace dt {
 
 namespace {
 
+constexpr int kOuts = 128;             // rows of W of a block's tile: lanes of TMEM
+constexpr int kSlabA = kOuts * 128;    // bytes of a slab of them
+constexpr int kPiece = kOuts * 32;     // bytes of 16 values of B_a for as many rows
+constexpr int kMaxTokens = 256;        // rows of x of a tile
+constexpr int kMaxStages = 12;
+constexpr int kMaxSplit = 8;           // blocks that share a tile's K: a cluster
+
 struct ProjectArgs {
-  const char *w, *x, *x16, *down, *up;
   const uint8_t *w_exps, *x_exps;
   const float *scale;
   const int32_t *index;
   char *y;
   uint16_t *u;           // [rows][rank]: scale x A^T, rounded
   int32_t *status;
-  int64_t ldw, ldx, ldx16, ldy;    // in bytes
+  int64_t ldy;           // in bytes
   int rows, n, O, K, count, rank;
 };
 
-template <int DT>
-__device__ __forceinline__ float value16(const char *p, int64_t i) {
-  const uint32_t v = *reinterpret_cast<const uint16_t *>(p + 2 * i);
-  return Half16<DT>::unpack(v).x;
+struct ProjectShape {
+  int nt, stages, buffers;        // rows of x of a tile; places of the ring; accumulators
+  int tiles_o, tiles, split;      // tiles along the outputs, all; blocks that share a tile
+  int off_small;
+};
+
+// The distinct adapters of a tile's requests, in the order in which they first occur.
+struct AdapterList {
+  int count, first;               // first: the request of the tile's first row
+  int ids[kMaxTokens];
+  int16_t slot[kMaxTokens];       // place in ids of each request's, -1: it has none
+};
+
+struct ListScratch {
+  int4 ad[kMaxTokens / 4];
+  int counts[8];
+};
+
+struct Small {                    // behind the ring
+  uint64_t full[kMaxStages], empty[kMaxStages], u_go[kMaxStages], u_full[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2], list_full[2], list_empty[2], idle;
+  AdapterList list[2];
+  ListScratch scratch;
+  uint32_t tmem;
+  int fail;
+};
+
+// ------------------------------------------------------------ clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
 }
-__device__ __forceinline__ float value8(const char *p, int64_t i) {
-  return Half16<DT_F16>::unpack(e4m3_f16x2(*reinterpret_cast<const uint8_t *>(p + i))).x;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// the address of block `rank`'s copy of a shared variable
+__device__ __forceinline__ uint32_t peer_address(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float load_peer(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void arrive_peer(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// u = scale x A^T of a row, a warp for each of the adapter's ranks in turn.
-template <int DT>
-__global__ void __launch_bounds__(256) adapter_down_kernel(const __grid_constant__ ProjectArgs a) {
-  const int row = blockIdx.x, lane = threadIdx.x & 31;
-  const int at = a.index[row / a.n];
-  if (at >= a.count && threadIdx.x == 0) *a.status = DT_ERR_BAD_INDEX;
-  if (at < 0 || at >= a.count) return;
-  const char *x = a.x16 + row * a.ldx16;
-  for (int j = threadIdx.x >> 5; j < a.rank; j += 8) {
-    const char *d = a.down + 2 * (static_cast<int64_t>(at) * a.rank + j) * a.K;
-    float s = 0.0f;
-    for (int k = lane; k < a.K; k += 32) s += value16<DT>(x, k) * value16<DT>(d, k);
-    s = warp_sum(s) * (a.scale ? a.scale[at] : 1.0f);
-    if (lane == 0) a.u[static_cast<int64_t>(row) * a.rank + j] = static_cast<uint16_t>(Half16<DT>::pack(s, 0.0f));
+// ------------------------------------------------- one block, or a pair (CG = 2)
+
+template <int CG>
+__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+  if (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_take(uint32_t *dst) {
+  if (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, 512);
   }
 }
+template <int CG>
+__device__ __forceinline__ void tmem_give(uint32_t taddr) {
+  if (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+  else
+    tmem_dealloc(taddr, 512);
+}
 
-// 64 rows x 64 outputs a block, 4 x 4 a thread, 32 values of K at a time.
+// D[tmem] (+)= A[smem] * B[smem]^T; E8: e4m3 operands, 32 values of K, else 16
+template <int CG, bool E8>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+#define DT_MMA(group, kind)                                                                      \
+  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"                                       \
+               "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n}\n" ::"r"(d), \
+               "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))                       \
+               : "memory")
+  if (CG == 2) {
+    if (E8) DT_MMA("2", "f8f6f4");
+    else DT_MMA("2", "f16");
+  } else {
+    if (E8) DT_MMA("1", "f8f6f4");
+    else DT_MMA("1", "f16");
+  }
+#undef DT_MMA
+}
+
+// one arrival on the barrier (in a pair: on both blocks') once all products so far are done
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  if (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    umma_commit(bar);
+}
+
+// instruction descriptor: fp32 accumulation, both operands K-major
 template <int DT, bool E8>
-__global__ void __launch_bounds__(256) project_kernel(const __grid_constant__ ProjectArgs a) {
-  __shared__ float s_x[32][65], s_w[32][65];
-  const int tid = threadIdx.x, r0 = blockIdx.y * 64, o0 = blockIdx.x * 64;
-  const int ty = tid / 16, tx = tid % 16;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += 32) {
-    for (int i = tid; i < 64 * 32; i += 256) {
-      const int r = i / 32, k = i % 32;
-      float x = 0.0f, w = 0.0f;
-      if (k0 + k < a.K && r0 + r < a.rows) {
-        const char *p = a.x + (r0 + r) * a.ldx;
-        x = E8 ? value8(p, k0 + k) : value16<DT>(p, k0 + k);
-      }
-      if (k0 + k < a.K && o0 + r < a.O) {
-        const char *p = a.w + (o0 + r) * a.ldw;
-        w = E8 ? value8(p, k0 + k) : value16<DT>(p, k0 + k);
-      }
-      s_x[k][r] = x;
-      s_w[k][r] = w;
-    }
-    __syncthreads();
-    for (int k = 0; k < 32; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += s_x[k][ty + 16 * i] * s_w[k][tx + 16 * j];
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + ty + 16 * i, o = o0 + tx + 16 * j;
-      if (r >= a.rows || o >= a.O) continue;
-      float y = acc[i][j];
-      if (E8) y = y * row_scale(a.x_exps[r]) * row_scale(a.w_exps[o]);
-      const int at = a.index ? a.index[r / a.n] : -1;
-      if (at >= 0 && at < a.count) {
-        const char *up = a.up + 2 * (static_cast<int64_t>(at) * a.O + o) * a.rank;
-        for (int k = 0; k < a.rank; ++k)
-          y += value16<DT>(reinterpret_cast<const char *>(a.u + static_cast<int64_t>(r) * a.rank), k) * value16<DT>(up, k);
-      }
-      *reinterpret_cast<uint16_t *>(a.y + r * a.ldy + 2 * o) = static_cast<uint16_t>(Half16<DT>::pack(y, 0.0f));
-    }
+__device__ __forceinline__ uint32_t descriptor(int M, int N) {
+  const uint32_t f = !E8 && DT == DT_BF16 ? 1u : 0u;     // e4m3 and fp16: 0
+  return (1u << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
 }
+// operands in rows of 128 or 32 bytes, swizzled by as much
+__device__ __forceinline__ uint64_t rows128(uint32_t addr) { return umma_desc(addr, 16, 1024) | (2ull << 61); }
+__device__ __forceinline__ uint64_t rows32(uint32_t addr) { return umma_desc(addr, 16, 256) | (6ull << 61); }
+
+// Bounded wait for a phase whose arrivals may come from another block of the cluster.
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity) {
+  const uint32_t at = smem_u32(bar);
+  long long t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (done) return true;
+    const long long t = clock64();
+    if (it == 0) t0 = t;
+    else if (t - t0 > kWaitCycles) return false;
+  }
+}
+
+// 16 fp32 columns of this thread's TMEM lane
+__device__ __forceinline__ void load16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// a place in a ring of `size` stages, and the parity of its barriers' phase
+struct Place {
+  uint32_t at, parity;
+  __device__ void step(uint32_t size) {
+    if (++at == size) {
+      at = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// The list for the rows [t0, t1), by 128 threads that meet at barrier `bar`. A request's adapter is
+// compared with those of the tile's requests before it (256 at most), four at a time.
+__device__ void list_adapters(const ProjectArgs &a, int t0, int t1, AdapterList &list, ListScratch &z, int tid,
+                              int bar) {
+  const int b0 = t0 / a.n, nb = (t1 - 1) / a.n - b0 + 1, lane = tid & 31, warp = tid >> 5;
+  int *ad = reinterpret_cast<int *>(z.ad);
+  auto meet = [&]() { asm volatile("barrier.cta.sync %0, 128;" ::"r"(bar) : "memory"); };
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = tid + 128 * k;
+    int at = -1;
+    if (i < nb) {
+      at = a.index[b0 + i];
+      if (at >= a.count) {
+        *a.status = DT_ERR_BAD_INDEX;
+        at = -1;
+      }
+    }
+    ad[i] = at < 0 ? -1 : at;
+  }
+  meet();
+  int same[2];
+  unsigned votes[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = tid + 128 * k, at = ad[i];
+    int j = i;                                  // the first request with this adapter
+    if (at >= 0)
+      for (int q = i / 4; q >= 0; --q) {
+        const int4 v = z.ad[q];
+        if (v.w == at && 4 * q + 3 <= i) j = 4 * q + 3;
+        if (v.z == at && 4 * q + 2 <= i) j = 4 * q + 2;
+        if (v.y == at && 4 * q + 1 <= i) j = 4 * q + 1;
+        if (v.x == at && 4 * q <= i) j = 4 * q;
+      }
+    same[k] = at < 0 ? -1 : j;
+    votes[k] = __ballot_sync(kFull, same[k] == i);
+    if (lane == 0) z.counts[4 * k + warp] = __popc(votes[k]);
+  }
+  meet();
+  int slot[2] = {-1, -1};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = tid + 128 * k;
+    if (same[k] == i) {
+      slot[k] = __popc(votes[k] & ((1u << lane) - 1u));
+      for (int w = 0; w < 4 * k + warp; ++w) slot[k] += z.counts[w];
+      list.ids[slot[k]] = ad[i];
+      list.slot[i] = static_cast<int16_t>(slot[k]);
+    } else if (same[k] < 0) {
+      list.slot[i] = -1;
+    }
+  }
+  if (tid == 0) {
+    int all = 0;
+    for (int w = 0; w < 8; ++w) all += z.counts[w];
+    list.count = all;
+    list.first = b0;
+  }
+  meet();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = tid + 128 * k;
+    if (same[k] >= 0 && same[k] != i) list.slot[i] = list.slot[same[k]];
+  }
+  meet();
+}
+
+// Sums of the cluster's partial accumulators: each block has its own, [columns][128], at `own` in
+// shared memory; this block's share of the columns goes to put(column, sum), a thread a lane,
+// the blocks' terms in their order.
+template <typename Put>
+__device__ __forceinline__ void sum_columns(const float *own, int columns, int split, int rank, int lane, Put put) {
+  const int c0 = columns * rank / split, c1 = columns * (rank + 1) / split;
+  uint32_t at[kMaxSplit];
+#pragma unroll
+  for (int q = 0; q < kMaxSplit; ++q)
+    at[q] = q < split ? peer_address(smem_u32(own), q) + 4 * lane : 0u;
+  for (int c = c0; c < c1; c += 4) {
+    float v[4] = {};
+#pragma unroll
+    for (int q = 0; q < kMaxSplit; ++q)
+      if (q < split)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < c1) v[e] += load_peer(at[q] + (c + e) * 512);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < c1) put(c + e, v[e]);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint16_t round16(float v) {
+  return static_cast<uint16_t>(Half16<DT>::pack(v, 0.0f));
+}
+
+// v 2^e for any e in [-254, 256], without overflow or underflow on the way
+__device__ __forceinline__ float times_power(float v, int e) {
+  const int h = e >> 1;
+  return v * __uint_as_float(static_cast<uint32_t>(h + 127) << 23) *
+         __uint_as_float(static_cast<uint32_t>(e - h + 127) << 23);
+}
+
+// u = scale x A^T: 128 stacked rows of A_a (the slots [m spt, m spt + spt) of a token tile's list)
+// times nt rows of x, K shared by the blocks of a cluster. Warps 0-3: the list, and the
+// accumulator's rows to u; 4: TMA; 5: products.
+template <int DT>
+__global__ void __launch_bounds__(192, 1)
+adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ ProjectShape w,
+                    const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap xmap) {
+  extern __shared__ __align__(1024) unsigned char sm[];
+  Small &ss = *reinterpret_cast<Small *>(sm + w.off_small);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int split = w.split, rank = static_cast<int>(blockIdx.x) % split, tile = blockIdx.x / split;
+  const int spt = kOuts / a.rank, m = tile % w.tiles_o;
+  const int t0 = tile / w.tiles_o * w.nt, t1 = min(t0 + w.nt, a.rows);
+  AdapterList &list = ss.list[0];
+  if (warp < 4) list_adapters(a, t0, t1, list, ss.scratch, tid, 1);
+  if (tid == 0) {
+    for (int i = 0; i < w.stages; ++i) {
+      mbar_init(&ss.full[i], 1);
+      mbar_init(&ss.empty[i], 1);
+    }
+    mbar_init(&ss.acc_full[0], 1);
+    ss.fail = 0;
+  }
+  __syncthreads();
+  const int slots = min(list.count - m * spt, spt);
+  if (slots <= 0) return;                       // all blocks of the cluster alike
+  if (warp == 5) tmem_alloc(&ss.tmem, 256);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = ss.tmem;
+  const int steps = (2 * a.K + 127) / 128, k0 = steps * rank / split, k1 = steps * (rank + 1) / split;
+  const int stage = kSlabA + w.nt * 128;
+  volatile int *fail = &ss.fail;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (*fail) return false;
+    if (mbar_wait_cycles(bar, parity)) return true;
+    *fail = 1;
+    *a.status = DT_ERR_TIMEOUT;
+    return false;
+  };
+  Place p = {0, 0};
+  if (warp == 4 && lane == 0) {
+    int s = k0;
+    for (; s < k1 && wait(&ss.empty[p.at], p.parity ^ 1u); ++s) {
+      unsigned char *to = sm + p.at * stage;
+      const uint32_t bar = smem_u32(&ss.full[p.at]);
+      mbar_expect_tx(&ss.full[p.at], (slots * a.rank + w.nt) * 128);
+      for (int i = 0; i < slots; ++i)
+        tma_2d<1>(to + i * a.rank * 128, &dmap, s * 64, list.ids[m * spt + i] * a.rank, bar);
+      tma_2d<1>(to + kSlabA, &xmap, s * 64, t0, bar);
+      p.step(w.stages);
+    }
+    if (*fail)       // nothing may land in memory that the block has given up
+      for (int i = max(s - w.stages, k0); i < s; ++i)
+        mbar_wait_cycles(&ss.full[(i - k0) % w.stages], ((i - k0) / w.stages) & 1);
+  } else if (warp == 5 && lane == 0) {
+    const uint32_t idesc = descriptor<DT, false>(kOuts, w.nt);
+    for (int s = k0; s < k1 && wait(&ss.full[p.at], p.parity); ++s) {
+      tmem_fence_after();
+      const uint32_t at = smem_u32(sm + p.at * stage);
+      const int parts = min(4, (a.K - s * 64 + 15) / 16);
+      for (int i = 0; i < parts; ++i)
+        mma<1, false>(tmem, rows128(at) + 2 * i, rows128(at + kSlabA) + 2 * i, idesc, s > k0 || i > 0);
+      commit<1>(&ss.empty[p.at]);
+      p.step(w.stages);
+    }
+    commit<1>(&ss.acc_full[0]);
+    if (*fail) mbar_wait_cycles(&ss.acc_full[0], 0);
+  }
+  if (warp < 4) {
+    __syncwarp();
+    wait(&ss.acc_full[0], 0);
+    tmem_fence_after();
+    float *own = reinterpret_cast<float *>(sm);
+    const int slot = tid / a.rank, j = tid - slot * a.rank;
+    const bool live = slot < slots;
+    const int id = live ? list.ids[m * spt + slot] : 0;
+    const float scale = live && a.scale ? a.scale[id] : 1.0f;
+    auto put = [&](int c, float v) {
+      const int t = t0 + c;
+      if (live && t < t1 && list.slot[t / a.n - list.first] == m * spt + slot)
+        a.u[static_cast<int64_t>(t) * a.rank + j] = round16<DT>(v * scale);
+    };
+    for (int c = 0; c < w.nt; c += 16) {
+      float v[16];
+      load16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if (split == 1) put(c + e, v[e]);
+        else own[(c + e) * 128 + tid] = v[e];
+      }
+    }
+    tmem_fence_before();
+    if (split > 1) {
+      cluster_sync();
+      sum_columns(own, w.nt, split, rank, tid, put);
+    }
+  } else if (split > 1) {
+    __syncwarp();
+    cluster_sync();
+  }
+  __syncthreads();
+  if (split > 1) cluster_sync();                // its sums have been read
+  tmem_fence_after();
+  if (warp == 5) tmem_dealloc(tmem, 256);
+}
+
+// The projection. Warps 0-3: accumulators to y (a thread an output); 4: TMA; 5: products; 6-9 (AD): the
+// adapters' list, and their u rows into the ring. In a pair (CG = 2) each block holds its 128
+// rows of W and half of the tile's rows of x, and the first one issues the products of both.
+template <int DT, bool E8, bool AD, int CG>
+__global__ void __launch_bounds__(AD ? 320 : 192, 1)
+project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ ProjectShape w,
+               const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+               const __grid_constant__ CUtensorMap umap) {
+  extern __shared__ __align__(1024) unsigned char sm[];
+  Small &ss = *reinterpret_cast<Small *>(sm + w.off_small);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int size = CG == 2 ? 2 : w.split;                 // blocks of a cluster
+  const int crank = size > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int split = CG == 2 ? 1 : w.split, rank = CG == 2 ? 0 : crank;
+  const int pair = CG == 2 ? crank : 0;
+  const int mine = w.nt / CG;                             // rows of x in this block's memory
+  const int stage = kSlabA + mine * 128;
+  const int first = blockIdx.x / size, step = gridDim.x / size;
+  const int kbytes = E8 ? a.K : 2 * a.K, steps = (kbytes + 127) / 128;
+  const int k0 = steps * rank / split, k1 = steps * (rank + 1) / split;
+  constexpr int kValues = E8 ? 128 : 64;                  // of a slab's row
+
+  if (tid == 0) {
+    for (int i = 0; i < w.stages; ++i) {
+      mbar_init(&ss.full[i], 1);
+      mbar_init(&ss.empty[i], 1);
+      mbar_init(&ss.u_go[i], 1);
+      mbar_init(&ss.u_full[i], 128 * CG);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ss.acc_full[i], 1);
+      mbar_init(&ss.acc_empty[i], 128 * CG);
+      mbar_init(&ss.list_full[i], 128);
+      mbar_init(&ss.list_empty[i], E8 ? 6 : 2);
+    }
+    mbar_init(&ss.idle, 1);
+    ss.fail = 0;
+  }
+  if (warp == 5) tmem_take<CG>(&ss.tmem);
+  tmem_fence_before();
+  __syncthreads();
+  if (size > 1) cluster_sync();
+  tmem_fence_after();
+  const uint32_t tmem = ss.tmem;
+  volatile int *fail = &ss.fail;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (*fail) return false;
+    if (CG == 2 ? wait_cluster(bar, parity) : mbar_wait_cycles(bar, parity)) return true;
+    *fail = 1;
+    *a.status = DT_ERR_TIMEOUT;
+    return false;
+  };
+  // the barrier of the block that issues the products
+  auto first_block = [&](uint64_t *bar) { return CG == 2 ? peer_address(smem_u32(bar), 0) : smem_u32(bar); };
+  auto arrive_first = [&](uint64_t *bar) {
+    if (CG == 2) arrive_peer(first_block(bar));
+    else mbar_arrive(bar);
+  };
+  // the adapters' part of K in pieces of 16, four a stage; this block's stages of them
+  auto pieces_of = [&](const AdapterList &l) { return l.count * (a.rank >> 4); };
+  auto share = [&](int pieces, int *q0, int *q1) {
+    const int n = (pieces + 3) >> 2;
+    *q0 = n * rank / split;
+    *q1 = n * (rank + 1) / split;
+  };
+
+  if (warp == 4 && lane == 0) {
+    Place p = {0, 0};
+    uint32_t issued = 0;
+    bool go = true;
+    for (int t = first, i = 0; t < w.tiles && go; t += step, ++i) {
+      const int o0 = (t % w.tiles_o * CG + pair) * kOuts, x0 = t / w.tiles_o * w.nt + pair * mine;
+      for (int s = k0; s < k1 && go; ++s) {
+        if (!(go = wait(&ss.empty[p.at], p.parity ^ 1u))) break;
+        unsigned char *to = sm + p.at * stage;
+        const uint32_t bar = first_block(&ss.full[p.at]);
+        if (pair == 0) mbar_expect_tx(&ss.full[p.at], CG * stage);
+        tma_2d<CG>(to, &wmap, s * kValues, o0, bar);
+        tma_2d<CG>(to + kSlabA, &xmap, s * kValues, x0, bar);
+        p.step(w.stages);
+        ++issued;
+      }
+      if (!AD || !go) continue;
+      if (!(go = wait(&ss.list_full[i & 1], (i >> 1) & 1))) break;
+      const AdapterList &l = ss.list[i & 1];
+      const int pieces = pieces_of(l), per = a.rank >> 4;
+      int q0, q1;
+      share(pieces, &q0, &q1);
+      for (int q = q0; q < q1; ++q) {
+        if (!(go = wait(&ss.empty[p.at], p.parity ^ 1u))) break;
+        mbar_arrive(&ss.u_go[p.at]);
+        unsigned char *to = sm + p.at * stage;
+        const uint32_t bar = first_block(&ss.full[p.at]);
+        const int here = min(4, pieces - 4 * q);
+        if (pair == 0) mbar_expect_tx(&ss.full[p.at], CG * here * kPiece);
+        for (int k = 0; k < here; ++k) {
+          const int u = (4 * q + k) / per, j = (4 * q + k - u * per) * 16;
+          tma_2d<CG>(to + k * kPiece, &umap, j, l.ids[u] * a.O + o0, bar);
+        }
+        p.step(w.stages);
+        ++issued;
+      }
+      mbar_arrive(&ss.list_empty[i & 1]);
+    }
+    if (*fail && pair == 0)    // nothing may land in memory that the block has given up
+      for (uint32_t k = issued > static_cast<uint32_t>(w.stages) ? issued - w.stages : 0; k < issued; ++k)
+        mbar_wait_cycles(&ss.full[k % w.stages], (k / w.stages) & 1u);
+  } else if (warp == 5 && lane == 0) {
+    const uint32_t idesc = descriptor<DT, E8>(kOuts * CG, w.nt), idesc16 = descriptor<DT, false>(kOuts * CG, w.nt);
+    Place p = {0, 0};
+    uint32_t phases = 0;                       // of u_full, a bit a stage
+    bool go = true;
+    for (int t = first, i = 0; t < w.tiles && go; t += step, ++i) {
+      const int buf = w.buffers == 2 ? i & 1 : 0, turn = w.buffers == 2 ? i >> 1 : i;
+      const uint32_t acc = tmem + buf * w.nt;
+      if (pair == 0) {
+        if (!(go = wait(&ss.acc_empty[buf], (turn & 1) ^ 1))) break;
+        tmem_fence_after();
+        for (int s = k0; s < k1; ++s) {
+          if (!(go = wait(&ss.full[p.at], p.parity))) break;
+          tmem_fence_after();
+          const uint32_t at = smem_u32(sm + p.at * stage);
+          const int parts = min(4, (kbytes - s * 128 + 31) / 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < parts)
+              mma<CG, E8>(acc, rows128(at) + 2 * k, rows128(at + kSlabA) + 2 * k, idesc, s > k0 || k > 0);
+          commit<CG>(&ss.empty[p.at]);
+          p.step(w.stages);
+        }
+        if (!go) break;
+      }
+      if (AD) {
+        if (!(go = wait(&ss.list_full[i & 1], (i >> 1) & 1))) break;
+        const int pieces = pieces_of(ss.list[i & 1]);
+        int q0, q1;
+        share(pieces, &q0, &q1);
+        if (pair == 0) {
+          // the adapters' own accumulator is the only one: the tile before has to have read it
+          if (E8 && w.buffers == 2 && i > 0 && q0 < q1) {
+            if (!(go = wait(&ss.acc_empty[(i - 1) & 1], ((i - 1) >> 1) & 1))) break;
+            tmem_fence_after();
+          }
+          const uint32_t to = E8 ? tmem + w.buffers * w.nt : acc;
+          for (int q = q0; q < q1; ++q) {
+            if (!(go = wait(&ss.full[p.at], p.parity) && wait(&ss.u_full[p.at], (phases >> p.at) & 1u))) break;
+            phases ^= 1u << p.at;
+            tmem_fence_after();
+            const uint32_t at = smem_u32(sm + p.at * stage);
+            const int here = min(4, pieces - 4 * q);
+            for (int k = 0; k < here; ++k)
+              mma<CG, false>(to, rows32(at + k * kPiece), rows32(at + kSlabA + k * mine * 32), idesc16,
+                             !E8 || q > q0 || k > 0);
+            commit<CG>(&ss.empty[p.at]);
+            p.step(w.stages);
+          }
+          if (!go) break;
+        }
+        mbar_arrive(&ss.list_empty[i & 1]);
+      }
+      if (pair == 0) commit<CG>(&ss.acc_full[buf]);
+    }
+    if (*fail && pair == 0) {
+      commit<CG>(&ss.idle);
+      mbar_wait_cycles(&ss.idle, 0);
+    }
+  } else if (AD && warp >= 6) {
+    const int id = tid - 192;
+    uint32_t at = 0, phases = 0;               // stage of the ring; phases of u_go
+    // (these warps meet for the lists: they go through all tiles, whatever has failed)
+    for (int t = first, i = 0; t < w.tiles; t += step, ++i) {
+      AdapterList &l = ss.list[i & 1];
+      const int tt = t / w.tiles_o * w.nt, x0 = tt + pair * mine;
+      bool go = wait(&ss.list_empty[i & 1], ((i >> 1) & 1) ^ 1);
+      list_adapters(a, tt, min(tt + w.nt, a.rows), l, ss.scratch, id, 1);
+      mbar_arrive(&ss.list_full[i & 1]);
+      if (i == 0) cudaGridDependencySynchronize();        // u is there
+      const int pieces = pieces_of(l), per = a.rank >> 4;
+      int q0, q1, slot[2];
+      const uint16_t *u[2];
+      share(pieces, &q0, &q1);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = id + 128 * k, row = x0 + r;
+        slot[k] = r < mine && row < a.rows ? l.slot[row / a.n - l.first] : -1;
+        u[k] = a.u + static_cast<int64_t>(row) * a.rank;
+      }
+      at = (at + (k1 - k0)) % w.stages;
+      for (int q = q0; q < q1 && go; ++q) {
+        if (!(go = wait(&ss.u_go[at], (phases >> at) & 1u))) break;
+        phases ^= 1u << at;
+        unsigned char *to = sm + at * stage + kSlabA;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = id + 128 * k;
+          if (r >= mine) break;
+          uint4 v[4][2];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int piece = 4 * q + z, s = piece / per, j = (piece - s * per) * 16;
+            v[z][0] = v[z][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (piece < pieces && s == slot[k]) {
+              v[z][0] = *reinterpret_cast<const uint4 *>(u[k] + j);
+              v[z][1] = *reinterpret_cast<const uint4 *>(u[k] + j + 8);
+            }
+          }
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            unsigned char *row = to + z * mine * 32 + r * 32;
+            const int turn = (r >> 2) & 1;
+            *reinterpret_cast<uint4 *>(row + 16 * turn) = v[z][0];
+            *reinterpret_cast<uint4 *>(row + 16 * (turn ^ 1)) = v[z][1];
+          }
+        }
+        fence_async_smem();
+        arrive_first(&ss.u_full[at]);
+        if (++at == static_cast<uint32_t>(w.stages)) at = 0;
+      }
+    }
+  } else if (warp < 4) {
+    bool go = true;
+    for (int t = first, i = 0; t < w.tiles && go; t += step, ++i) {
+      const int buf = w.buffers == 2 ? i & 1 : 0, turn = w.buffers == 2 ? i >> 1 : i;
+      const int o = (t % w.tiles_o * CG + pair) * kOuts + tid, t0 = t / w.tiles_o * w.nt;
+      bool both = false;                       // the adapters have something in their accumulator
+      if (AD && E8) {
+        go = __all_sync(kFull, wait(&ss.list_full[i & 1], (i >> 1) & 1));
+        int q0 = 0, q1 = 0;
+        if (go) share(pieces_of(ss.list[i & 1]), &q0, &q1);
+        both = q0 < q1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ss.list_empty[i & 1]);
+      }
+      go = __all_sync(kFull, go && wait(&ss.acc_full[buf], turn & 1));
+      tmem_fence_after();
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+      const int wexp = E8 && o < a.O ? a.w_exps[o] - 127 : 0;
+      float *own = reinterpret_cast<float *>(sm);
+      char *y = a.y + static_cast<int64_t>(t0) * a.ldy + 2 * static_cast<int64_t>(o);
+      const int rows = min(w.nt, a.rows - t0);
+      auto put = [&](int c, float v) {
+        if (c < rows && o < a.O) *reinterpret_cast<uint16_t *>(y + c * a.ldy) = round16<DT>(v);
+      };
+      for (int c = 0; c < w.nt && go; c += 16) {
+        float v[16], z[16];
+        load16(lanes + buf * w.nt + c, v);
+        if (AD && E8 && both) load16(lanes + w.buffers * w.nt + c, z);
+        const int xexp = E8 ? (t0 + c + (lane & 15) < a.rows ? a.x_exps[t0 + c + (lane & 15)] : 127) - 127 : 0;
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (E8) {
+            v[e] = times_power(v[e], wexp + __shfl_sync(kFull, xexp, e));
+            if (AD && both) v[e] += z[e];
+          }
+          if (split == 1) put(c + e, v[e]);
+          else own[(c + e) * 128 + tid] = v[e];
+        }
+      }
+      tmem_fence_before();
+      arrive_first(&ss.acc_empty[buf]);
+      if (split > 1) {
+        cluster_sync();
+        sum_columns(own, w.nt, split, rank, tid, put);
+      }
+    }
+  }
+  if (split > 1 && warp >= 4) {
+    __syncwarp();
+    cluster_sync();
+  }
+  __syncthreads();
+  if (size > 1) cluster_sync();          // no block ends while another may still read or signal it
+  tmem_fence_after();
+  if (warp == 5) tmem_give<CG>(tmem);
+}
+
+// ------------------------------------------------------------ plans
+
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+int stages_of(int smem, int stage) { return std::min(kMaxStages, (smem - static_cast<int>(sizeof(Small)) - 1024) / stage); }
 
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+struct ProjectPlan {
+  int cg;
+  ProjectShape s;
+  int blocks;
+  size_t smem;
+};
+
+// Cycles that a tile's slab takes: its products, and its bytes on the way into shared memory.
+// (Calibrated on whole calls; only the order of the choices matters.)
+double slab_cycles(int nt, int cg) {
+  return std::max(2.0 * nt, (kSlabA + nt / cg * 128) / 60.0);
+}
+
+void choose(const ProjectArgs &a, bool e8, bool ad, int sms, int pairs, int smem, ProjectPlan *p) {
+  const int steps = ceil_div(static_cast<int64_t>(a.K) * (e8 ? 1 : 2), 128);
+  const int cap = ad && e8 ? 160 : kMaxTokens;     // three accumulators instead of two
+  double best = 1e300;
+  for (int cg = 1; cg <= 2; ++cg) {
+    const int tiles_o = ceil_div(a.O, kOuts * cg), room = cg == 2 ? pairs : sms;
+    if (room < 1) continue;
+    for (int nt = 16 * cg; nt <= cap; nt += 16 * cg) {
+      const int64_t tiles = static_cast<int64_t>(tiles_o) * ceil_div(a.rows, nt);
+      for (int split = 1; split <= kMaxSplit; ++split) {
+        if (split > 1 && (cg == 2 || tiles * split > room || split > steps || split == 5 || split == 7)) continue;
+        const double rounds = ceil_div(tiles, room);
+        const double busy = static_cast<double>(std::min<int64_t>(tiles * split, room)) * cg;
+        // W comes from memory at 23 bytes a cycle and SM where all take part
+        const double slab = std::max(slab_cycles(nt, cg), kSlabA / 23.0 * busy / sms / std::max(1, ceil_div(a.rows, nt)));
+        const double cost = rounds * ceil_div(steps, split) * slab + 8.0 * nt + (split > 1 ? 1500.0 : 0.0);
+        if (cost < best) {
+          best = cost;
+          p->cg = cg;
+          p->s.nt = nt;
+          p->s.split = split;
+          p->s.tiles_o = tiles_o;
+          p->s.tiles = static_cast<int>(tiles);
+          p->blocks = static_cast<int>(std::min<int64_t>(tiles * split, cg == 2 ? room : static_cast<int64_t>(room))) * cg;
+        }
+      }
+      if (nt >= a.rows) break;
+    }
+  }
+  const int stage = kSlabA + p->s.nt / p->cg * 128;
+  p->s.stages = stages_of(smem, stage);
+  p->s.buffers = 2;
+  p->s.off_small = p->s.stages * stage;
+  p->smem = p->s.off_small + sizeof(Small);
+}
+
+// blocks of the kernel that run at once in pairs: an SM without a partner stays idle
+template <auto Kernel>
+int resident_pairs(int threads, size_t smem, int sms) {
+  static std::atomic<int> known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  int n = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
+  if (n) return n;
+  cudaLaunchAttribute pair = {};
+  pair.id = cudaLaunchAttributeClusterDimension;
+  pair.val.clusterDim.x = 2;
+  pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(sms / 2 * 2);
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.attrs = &pair;
+  config.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, Kernel, &config) != cudaSuccess || n < 1) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_release);
+  return n;
+}
+
+struct ProjectMaps {
+  CUtensorMap w, x, up, down, x16;
+};
+
+template <auto Kernel, typename... Args>
+cudaError_t launch_cluster(int blocks, int threads, size_t smem, int cluster, bool early, cudaStream_t st,
+                           const Args &...args) {
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(blocks);
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = st;
+  config.attrs = attr;
+  config.numAttrs = early ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&config, Kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int DT>
-cudaError_t launch_project(const ProjectArgs &a, bool e8, cudaStream_t st) {
-  if (a.index) {
-    adapter_down_kernel<DT><<<a.rows, 256, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
+cudaError_t launch_down(const ProjectArgs &a, const dt_adapters &ad, const void *x16, int64_t ldx16, int sms,
+                        int smem, cudaStream_t st) {
+  const cudaError_t e = allow_smem<adapter_down_kernel<DT>>();
+  if (e != cudaSuccess) return e;
+  ProjectShape s = {};
+  const int tiles_t = ceil_div(a.rows, kMaxTokens), steps = ceil_div(2 * a.K, 128);
+  s.nt = ceil_div(ceil_div(a.rows, tiles_t), 16) * 16;
+  const int requests = std::min(s.nt, (s.nt + a.n - 2) / a.n + 1);        // of a tile, at most
+  s.tiles_o = ceil_div(std::min(requests, a.count), kOuts / a.rank);
+  s.tiles = s.tiles_o * ceil_div(a.rows, s.nt);
+  s.split = 1;
+  while (s.split < kMaxSplit && s.tiles * s.split * 2 <= sms && s.split * 2 <= steps) s.split *= 2;
+  const int stage = kSlabA + s.nt * 128;
+  s.stages = std::min(stages_of(smem, stage), std::max(ceil_div(steps, s.split), ceil_div(s.nt * 512, stage)));
+  s.off_small = s.stages * stage;
+  CUtensorMap down, x;
+  if (!matrix_map(ad.down, 2, a.K, static_cast<int64_t>(a.count) * a.rank, 2 * a.K, 64, a.rank, &down) ||
+      !matrix_map(x16, 2, a.K, a.rows, ldx16, 64, s.nt, &x))
+    return cudaErrorUnknown;
+  return launch_cluster<adapter_down_kernel<DT>>(s.tiles * s.split, 192, s.off_small + sizeof(Small), s.split, false,
+                                                 st, a, s, down, x);
+}
+
+template <int DT, bool E8, bool AD, int CG>
+cudaError_t launch_main(const ProjectArgs &a, const ProjectPlan &p, const CUtensorMap &w, const CUtensorMap &x,
+                        const CUtensorMap &up, cudaStream_t st) {
+  constexpr auto kernel = project_kernel<DT, E8, AD, CG>;
+  const cudaError_t e = allow_smem<kernel>();
+  if (e != cudaSuccess) return e;
+  return launch_cluster<kernel>(p.blocks, AD ? 320 : 192, p.smem, CG == 2 ? 2 : p.s.split, AD, st, a, p.s, w, x, up);
+}
+
+template <int DT, bool E8, bool AD>
+cudaError_t launch_project(const ProjectArgs &a, const dt_matrix &m, const void *x, int64_t ldx,
+                           const dt_adapters *ad, const void *x16, int64_t ldx16, int sms, int smem,
+                           cudaStream_t st) {
+  const cudaError_t e = allow_smem<project_kernel<DT, E8, AD, 2>>();
+  if (e != cudaSuccess) return e;
+  ProjectPlan p = {};
+  choose(a, E8, AD, sms, resident_pairs<project_kernel<DT, E8, AD, 2>>(AD ? 320 : 192, 200 * 1024, sms), smem, &p);
+  if (AD) {
+    const cudaError_t e = launch_down<DT>(a, *ad, x16, ldx16, sms, smem, st);
     if (e != cudaSuccess) return e;
   }
-  const dim3 grid((a.O + 63) / 64, (a.rows + 63) / 64);
-  if (grid.y > 65535) return cudaErrorInvalidConfiguration;
-  if (e8) project_kernel<DT, true><<<grid, 256, 0, st>>>(a);
-  else project_kernel<DT, false><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  CUtensorMap w, xm, up = {};
+  const int size = E8 ? 1 : 2;
+  if (!matrix_map(m.data, size, a.K, a.O, m.ld * size, 128 / size, kOuts, &w) ||
+      !matrix_map(x, size, a.K, a.rows, ldx, 128 / size, p.s.nt / p.cg, &xm) ||
+      (AD && !matrix_map(ad->up, 2, a.rank, static_cast<int64_t>(a.count) * a.O, 2 * a.rank, 16, kOuts, &up)))
+    return cudaErrorUnknown;
+  return p.cg == 2 ? launch_main<DT, E8, AD, 2>(a, p, w, xm, up, st) : launch_main<DT, E8, AD, 1>(a, p, w, xm, up, st);
 }
 
 }  // namespace
@@ -140,14 +894,10 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
     return DT_ERR_INVALID_ARG;
   if (!adapters != !index || (!adapters || !e8) != !x16) return DT_ERR_INVALID_ARG;
   dt::ProjectArgs a = {};
-  a.w = static_cast<const char *>(w->data);
-  a.x = static_cast<const char *>(x);
   a.y = static_cast<char *>(y);
   a.w_exps = w->exps;
   a.x_exps = x_exps;
   a.status = status;
-  a.ldw = w->ld * size;
-  a.ldx = ldx * size;
   a.ldy = 2 * ldy;
   a.rows = static_cast<int>(rows);
   a.n = n;
@@ -160,13 +910,14 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
         (reinterpret_cast<uintptr_t>(index) & 3u) || !workspace ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
         workspace_bytes < dt_project_workspace_bytes(batch, n, adapters->rank) ||
-        static_cast<int64_t>(adapters->count) * w->O > 0x7fffffff)
+        static_cast<int64_t>(adapters->count) * w->O > 0x7fffff00 ||
+        static_cast<int64_t>(adapters->count) * adapters->rank > 0x7fffff00)
       return DT_ERR_INVALID_ARG;
     if (e8 && (!dt::al16(x16) || ldx16 < w->K || ldx16 % 8 || ldx16 > most)) return DT_ERR_INVALID_ARG;
-    a.x16 = e8 ? static_cast<const char *>(x16) : a.x;
-    a.ldx16 = e8 ? 2 * ldx16 : a.ldx;
-    a.down = static_cast<const char *>(adapters->down);
-    a.up = static_cast<const char *>(adapters->up);
+    if (!e8) {
+      x16 = x;
+      ldx16 = ldx;
+    }
     a.scale = adapters->scale;
     a.index = index;
     a.count = adapters->count;
@@ -177,8 +928,16 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
   const int rc = dt::device_sm_count(&sms, &smem);
   if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == DT_BF16 ? dt::launch_project<DT_BF16>(a, e8, st)
-                                         : dt::launch_project<DT_F16>(a, e8, st);
+  auto go = [&](auto type, auto eight, auto with) {
+    return dt::launch_project<decltype(type)::value, decltype(eight)::value, decltype(with)::value>(
+        a, *w, x, ldx * size, adapters, x16, 2 * ldx16, sms, smem, st);
+  };
+  auto typed = [&](auto type) {
+    if (e8) return adapters ? go(type, std::true_type{}, std::true_type{}) : go(type, std::true_type{}, std::false_type{});
+    return adapters ? go(type, std::false_type{}, std::true_type{}) : go(type, std::false_type{}, std::false_type{});
+  };
+  const cudaError_t e = dtype == DT_BF16 ? typed(std::integral_constant<int, DT_BF16>{})
+                                         : typed(std::integral_constant<int, DT_F16>{});
   return e == cudaSuccess ? DT_OK : DT_ERR_CUDA;
 }
 

@@ -233,4 +233,40 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *mbar, uint32_t parity, uint6
   }
 }
 
+constexpr long long kWaitCycles = 4000000000ll;   // about 2 s
+
+// Bounded wait for a phase. The limit is in SM cycles: a read of the clock register
+// costs a few cycles, of the global timer about a microsecond, which every wait that
+// is not over at once would pay.
+__device__ __forceinline__ bool mbar_wait_cycles(uint64_t *bar, uint32_t parity) {
+  const uint32_t at = smem_u32(bar);
+  long long t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (done) return true;
+    const long long t = clock64();
+    if (it == 0) t0 = t;
+    else if (t - t0 > kWaitCycles) return false;
+  }
+}
+
+// 128-byte swizzled operand descriptor; its address field counts 16-byte units, so an
+// operand further on is a plain addition
+__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return umma_desc(addr, lbo, sbo) | (2ull << 61);
+}
+
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
 }  // namespace dt

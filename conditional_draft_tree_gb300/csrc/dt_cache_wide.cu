@@ -964,7 +964,9 @@ bool matrix_map(const void *base, int size, int64_t cols, int64_t rows, int64_t 
   const cuuint32_t one[2] = {1, 1};
   return enc(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base),
              dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_cols * size == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_128B,
+             box_cols * size == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+             : box_cols * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -71,7 +71,7 @@ int validate_dims(const dt_dims *dims);
 int device_sm_count(int *sms, int *smem_optin);
 
 // [rows][cols] of 1- or 2-byte values, row_bytes apart (a multiple of 16), in boxes of box_rows rows of
-// 32 or 128 bytes, swizzled by as much; what lies outside reads as zero. False where it cannot be made.
+// 32, 64 or 128 bytes, swizzled by as much; what lies outside reads as zero. False where it cannot be made.
 bool matrix_map(const void *base, int size, int64_t cols, int64_t rows, int64_t row_bytes, int box_cols,
                 int box_rows, CUtensorMap *map);
 

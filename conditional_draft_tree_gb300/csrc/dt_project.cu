@@ -26,10 +26,11 @@ namespace {
 
 constexpr int kOuts = 128;             // rows of W of a block's tile: lanes of TMEM
 constexpr int kSlabA = kOuts * 128;    // bytes of a slab of them
-constexpr int kPiece = kOuts * 32;     // bytes of 16 values of B_a for as many rows
 constexpr int kMaxTokens = 256;        // rows of x of a tile
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplit = 8;           // blocks that share a tile's K: a cluster
+constexpr int kGroups = 2;             // warpgroups that empty an accumulator, 16 columns in turn
+constexpr int kDrain = 128 * kGroups;  // their threads; behind them the warps of TMA and products
 
 struct ProjectArgs {
   const uint8_t *w_exps, *x_exps;
@@ -45,6 +46,7 @@ struct ProjectArgs {
 struct ProjectShape {
   int nt, stages, buffers;        // rows of x of a tile; places of the ring; accumulators
   int tiles_o, tiles, split;      // tiles along the outputs, all; blocks that share a tile
+  int outs, piece;                // rows of W of a block's tile; values of B_a's rows of one copy
   int off_small;
 };
 
@@ -65,6 +67,8 @@ struct Small {                    // behind the ring
   uint64_t acc_full[2], acc_empty[2], list_full[2], list_empty[2], idle;
   AdapterList list[2];
   ListScratch scratch;
+  int16_t token_slot[kMaxTokens];
+  alignas(16) int xexp[4 * kGroups][kMaxTokens];   // exponents of the tile's rows of x, as bits of fp32; one copy a warp
   uint32_t tmem;
   int fail;
 };
@@ -84,11 +88,6 @@ __device__ __forceinline__ uint32_t peer_address(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
-}
-__device__ __forceinline__ float load_peer(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
 }
 __device__ __forceinline__ void arrive_peer(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
@@ -167,27 +166,11 @@ __device__ __forceinline__ uint32_t descriptor(int M, int N) {
   return (1u << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
-// operands in rows of 128 or 32 bytes, swizzled by as much
+// operands in rows of 128 bytes, or fewer, swizzled by as much
 __device__ __forceinline__ uint64_t rows128(uint32_t addr) { return umma_desc(addr, 16, 1024) | (2ull << 61); }
-__device__ __forceinline__ uint64_t rows32(uint32_t addr) { return umma_desc(addr, 16, 256) | (6ull << 61); }
-
-// Bounded wait for a phase whose arrivals may come from another block of the cluster.
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity) {
-  const uint32_t at = smem_u32(bar);
-  long long t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(at), "r"(parity)
-        : "memory");
-    if (done) return true;
-    const long long t = clock64();
-    if (it == 0) t0 = t;
-    else if (t - t0 > kWaitCycles) return false;
-  }
+// rows of `values` 16-bit values: 64, 32 or 16
+__device__ __forceinline__ uint64_t rows_of(uint32_t addr, int values) {
+  return umma_desc(addr, 16, 16 * values) | ((values == 64 ? 2ull : values == 32 ? 4ull : 6ull) << 61);
 }
 
 // 16 fp32 columns of this thread's TMEM lane
@@ -203,6 +186,34 @@ __device__ __forceinline__ void load16(uint32_t taddr, float (&v)[16]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Waits of a converged warp. The lanes agree by votes, so that the compiler knows a warp's loops to be
+// uniform and keeps addresses and descriptors where TMA and MMA instructions take them from (with
+// one lane in a loop of its own a slab took 310 ns, whatever its size).
+__device__ __forceinline__ bool passed(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(kFull, done);
+}
+// Bounded. False when the wait ran out, here or (where this one is not over) in another warp.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *fail, int32_t *status) {
+  if (passed(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (passed(bar, parity)) return true;
+    if (__any_sync(kFull, *fail != 0)) return false;
+    if (__any_sync(kFull, clock64() - t0 > kWaitCycles)) {
+      *fail = 1;
+      *status = DT_ERR_TIMEOUT;
+      return false;
+    }
+  }
 }
 
 // a place in a ring of `size` stages, and the parity of its barriers' phase
@@ -244,6 +255,7 @@ __device__ void list_adapters(const ProjectArgs &a, int t0, int t1, AdapterList 
     const int i = tid + 128 * k, at = ad[i];
     int j = i;                                  // the first request with this adapter
     if (at >= 0)
+#pragma unroll 4
       for (int q = i / 4; q >= 0; --q) {
         const int4 v = z.ad[q];
         if (v.w == at && 4 * q + 3 <= i) j = 4 * q + 3;
@@ -284,29 +296,46 @@ __device__ void list_adapters(const ProjectArgs &a, int t0, int t1, AdapterList 
   meet();
 }
 
-// Sums of the cluster's partial accumulators: each block has its own, [columns][128], at `own` in
-// shared memory; this block's share of the columns goes to put(column, sum), a thread a lane,
-// the blocks' terms in their order.
-template <typename Put>
-__device__ __forceinline__ void sum_columns(const float *own, int columns, int split, int rank, int lane, Put put) {
-  const int c0 = columns * rank / split, c1 = columns * (rank + 1) / split;
-  uint32_t at[kMaxSplit];
-#pragma unroll
-  for (int q = 0; q < kMaxSplit; ++q)
-    at[q] = q < split ? peer_address(smem_u32(own), q) + 4 * lane : 0u;
-  for (int c = c0; c < c1; c += 4) {
-    float v[4] = {};
-#pragma unroll
-    for (int q = 0; q < kMaxSplit; ++q)
-      if (q < split)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c + e < c1) v[e] += load_peer(at[q] + (c + e) * 512);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c + e < c1) put(c + e, v[e]);
+// Sums over the blocks of a cluster that share a tile's K. Each block owns a share of the tile's columns:
+// the others write their terms into its shared memory (where the ring was: all blocks have passed a
+// cluster barrier), [block][column of the share][128 lanes]; behind a second barrier it adds them up
+// in the blocks' order. Writes to another block do not wait for each other, as reads would
+// (for 8 blocks and 240 columns these took 12 us).
+struct Shares {
+  uint32_t base;         // of the memory, in this block
+  int width, split, rank, lane;
+  __device__ Shares(const void *memory, int columns, int split_, int rank_, int lane_)
+      : base(smem_u32(memory)), width(share_width(columns, split_)), split(split_), rank(rank_), lane(lane_) {}
+  // columns of a share: whole sixteens, so that those that are read together have one owner
+  __host__ __device__ static int share_width(int columns, int split) {
+    return ((columns + 16 * split - 1) / (16 * split)) * 16;
   }
-}
+  // the i-th sixteen columns that this block sends: the blocks begin with different owners
+  __device__ __forceinline__ int turn(int i, int columns) const {
+    return split > 1 ? (16 * i + rank * width) % columns : 16 * i;
+  }
+  // the terms of columns c .. c + 15
+  __device__ __forceinline__ void push(int c, const float (&v)[16]) {
+    const int owner = c / width;
+    const uint32_t to = peer_address(base, owner) + ((rank * width + c - owner * width) * 128 + lane) * 4;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 512 * e), "f"(v[e]) : "memory");
+  }
+  // put(column, its eight sums), by one of `groups` warpgroups
+  template <typename Put>
+  __device__ __forceinline__ void sum(const unsigned char *memory, int columns, int group, int groups, Put put) {
+    const int c0 = rank * width, end = min(c0 + width, columns);
+    for (int c = c0 + 8 * group; c < end; c += 8 * groups) {
+      const float *own = reinterpret_cast<const float *>(memory) + (c - c0) * 128 + lane;
+      float v[8] = {};
+      for (int q = 0; q < split; ++q, own += width * 128)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += own[e * 128];
+      put(c, v);
+    }
+  }
+};
 
 template <int DT>
 __device__ __forceinline__ uint16_t round16(float v) {
@@ -314,17 +343,17 @@ __device__ __forceinline__ uint16_t round16(float v) {
 }
 
 // v 2^e for any e in [-254, 256], without overflow or underflow on the way
-__device__ __forceinline__ float times_power(float v, int e) {
+__device__ __noinline__ float times_power(float v, int e) {
   const int h = e >> 1;
   return v * __uint_as_float(static_cast<uint32_t>(h + 127) << 23) *
          __uint_as_float(static_cast<uint32_t>(e - h + 127) << 23);
 }
 
 // u = scale x A^T: 128 stacked rows of A_a (the slots [m spt, m spt + spt) of a token tile's list)
-// times nt rows of x, K shared by the blocks of a cluster. Warps 0-3: the list, and the
-// accumulator's rows to u; 4: TMA; 5: products.
+// times nt rows of x, K shared by the blocks of a cluster. Warps 0-7: the list (0-3),
+// and the accumulator's rows to u; 8: TMA; 9: products.
 template <int DT>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(kDrain + 64, 1)
 adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ ProjectShape w,
                     const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap xmap) {
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -335,106 +364,175 @@ adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant
   const int spt = kOuts / a.rank, m = tile % w.tiles_o;
   const int t0 = tile / w.tiles_o * w.nt, t1 = min(t0 + w.nt, a.rows);
   AdapterList &list = ss.list[0];
-  if (warp < 4) list_adapters(a, t0, t1, list, ss.scratch, tid, 1);
-  if (tid == 0) {
+  const int steps = (2 * a.K + 127) / 128, k0 = steps * rank / split, k1 = steps * (rank + 1) / split;
+  const int stage = kSlabA + w.nt * 128;
+  volatile int *fail = &ss.fail;
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, fail, a.status); };
+  const bool issuer = elect_one();
+  // the rows of x need no list: the ring's first round of them is on its way before there is one
+  auto load_x = [&](int s, uint32_t at) {
+    mbar_expect_tx(&ss.full[at], w.nt * 128);
+    tma_2d<1>(sm + at * stage + kSlabA, &xmap, s * 64, t0, smem_u32(&ss.full[at]));
+  };
+  const int ahead = min(w.stages, k1 - k0);
+  if (warp == kDrain / 32 && lane == 0) {
     for (int i = 0; i < w.stages; ++i) {
-      mbar_init(&ss.full[i], 1);
+      mbar_init(&ss.full[i], 2);
       mbar_init(&ss.empty[i], 1);
     }
     mbar_init(&ss.acc_full[0], 1);
     ss.fail = 0;
+    for (int i = 0; i < ahead; ++i) load_x(k0 + i, i);
   }
-  __syncthreads();
-  const int slots = min(list.count - m * spt, spt);
-  if (slots <= 0) return;                       // all blocks of the cluster alike
-  if (warp == 5) tmem_alloc(&ss.tmem, 256);
+  if (warp == kDrain / 32 + 1) tmem_alloc(&ss.tmem, 256);
+  if (warp < 4) {
+    list_adapters(a, t0, t1, list, ss.scratch, tid, 1);
+    for (int t = t0 + tid; t < t0 + w.nt; t += 128)
+      ss.token_slot[t - t0] = t < t1 ? list.slot[t / a.n - list.first] : static_cast<int16_t>(-1);
+  }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = ss.tmem;
-  const int steps = (2 * a.K + 127) / 128, k0 = steps * rank / split, k1 = steps * (rank + 1) / split;
-  const int stage = kSlabA + w.nt * 128;
-  volatile int *fail = &ss.fail;
-  auto wait = [&](uint64_t *bar, uint32_t parity) {
-    if (*fail) return false;
-    if (mbar_wait_cycles(bar, parity)) return true;
-    *fail = 1;
-    *a.status = DT_ERR_TIMEOUT;
-    return false;
-  };
+  const int slots = min(list.count - m * spt, spt);
+  if (slots <= 0) {                             // all blocks of the cluster alike
+    if (warp == kDrain / 32 && lane == 0)
+      for (int i = 0; i < ahead; ++i) {         // (an arrival without bytes ends the phase with the copies)
+        mbar_arrive(&ss.full[i]);
+        mbar_wait_cycles(&ss.full[i], 0);
+      }
+    if (warp == kDrain / 32 + 1) tmem_dealloc(tmem, 256);
+    return;
+  }
   Place p = {0, 0};
-  if (warp == 4 && lane == 0) {
+  if (warp == kDrain / 32) {
     int s = k0;
     for (; s < k1 && wait(&ss.empty[p.at], p.parity ^ 1u); ++s) {
-      unsigned char *to = sm + p.at * stage;
-      const uint32_t bar = smem_u32(&ss.full[p.at]);
-      mbar_expect_tx(&ss.full[p.at], (slots * a.rank + w.nt) * 128);
-      for (int i = 0; i < slots; ++i)
-        tma_2d<1>(to + i * a.rank * 128, &dmap, s * 64, list.ids[m * spt + i] * a.rank, bar);
-      tma_2d<1>(to + kSlabA, &xmap, s * 64, t0, bar);
+      if (issuer) {
+        if (s >= k0 + ahead) load_x(s, p.at);
+        mbar_expect_tx(&ss.full[p.at], slots * a.rank * 128);
+        for (int i = 0; i < slots; ++i)
+          tma_2d<1>(sm + p.at * stage + i * a.rank * 128, &dmap, s * 64, list.ids[m * spt + i] * a.rank,
+                    smem_u32(&ss.full[p.at]));
+      }
       p.step(w.stages);
     }
-    if (*fail)       // nothing may land in memory that the block has given up
+    if (*fail && lane == 0) {        // nothing may land in memory that the block has given up
+      for (; s < k0 + ahead; ++s) mbar_arrive(&ss.full[s - k0]);
       for (int i = max(s - w.stages, k0); i < s; ++i)
         mbar_wait_cycles(&ss.full[(i - k0) % w.stages], ((i - k0) / w.stages) & 1);
-  } else if (warp == 5 && lane == 0) {
+    }
+  } else if (warp == kDrain / 32 + 1) {
     const uint32_t idesc = descriptor<DT, false>(kOuts, w.nt);
     for (int s = k0; s < k1 && wait(&ss.full[p.at], p.parity); ++s) {
       tmem_fence_after();
-      const uint32_t at = smem_u32(sm + p.at * stage);
+      const uint32_t at = smem_u32(sm) + p.at * stage;
+      const uint64_t da = rows128(at), db = rows128(at + kSlabA);
       const int parts = min(4, (a.K - s * 64 + 15) / 16);
-      for (int i = 0; i < parts; ++i)
-        mma<1, false>(tmem, rows128(at) + 2 * i, rows128(at + kSlabA) + 2 * i, idesc, s > k0 || i > 0);
-      commit<1>(&ss.empty[p.at]);
+      if (issuer) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < parts) mma<1, false>(tmem, da + 2 * i, db + 2 * i, idesc, s > k0 || i > 0);
+        commit<1>(&ss.empty[p.at]);
+      }
       p.step(w.stages);
     }
-    commit<1>(&ss.acc_full[0]);
-    if (*fail) mbar_wait_cycles(&ss.acc_full[0], 0);
+    if (issuer) commit<1>(&ss.acc_full[0]);
+    if (*fail && lane == 0) mbar_wait_cycles(&ss.acc_full[0], 0);
   }
-  if (warp < 4) {
+  if (tid < kDrain) {
     __syncwarp();
+    const int row = tid & 127, group = tid >> 7;
+    const int slot = row / a.rank, j = row - slot * a.rank;
+    const bool live = slot < slots;
+    const int want = live ? m * spt + slot : -2;
+    const float scale = live && a.scale ? a.scale[list.ids[want]] : 1.0f;
     wait(&ss.acc_full[0], 0);
     tmem_fence_after();
-    float *own = reinterpret_cast<float *>(sm);
-    const int slot = tid / a.rank, j = tid - slot * a.rank;
-    const bool live = slot < slots;
-    const int id = live ? list.ids[m * spt + slot] : 0;
-    const float scale = live && a.scale ? a.scale[id] : 1.0f;
-    auto put = [&](int c, float v) {
-      const int t = t0 + c;
-      if (live && t < t1 && list.slot[t / a.n - list.first] == m * spt + slot)
-        a.u[static_cast<int64_t>(t) * a.rank + j] = round16<DT>(v * scale);
-    };
-    for (int c = 0; c < w.nt; c += 16) {
-      float v[16];
-      load16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
-      tmem_wait_ld();
+    auto put = [&](int c, const auto &v) {
+      uint16_t *to = a.u + static_cast<int64_t>(t0 + c) * a.rank + j;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        if (split == 1) put(c + e, v[e]);
-        else own[(c + e) * 128 + tid] = v[e];
-      }
+      for (int e = 0; e < static_cast<int>(sizeof(v) / sizeof(float)); ++e)
+        if (ss.token_slot[c + e] == want) to[e * a.rank] = round16<DT>(v[e] * scale);
+    };
+    if (split > 1) cluster_sync();
+    Shares shares(sm, w.nt, split, rank, row);
+#pragma unroll 1
+    for (int i = group; i < w.nt / 16; i += kGroups) {
+      const int c = shares.turn(i, w.nt);
+      float v[16];
+      load16(tmem + (static_cast<uint32_t>(warp & 3) << 21) + c, v);
+      tmem_wait_ld();
+      if (split == 1) put(c, v);
+      else shares.push(c, v);
     }
     tmem_fence_before();
     if (split > 1) {
       cluster_sync();
-      sum_columns(own, w.nt, split, rank, tid, put);
+      shares.sum(sm, w.nt, group, kGroups, put);
     }
   } else if (split > 1) {
     __syncwarp();
+    cluster_sync();
     cluster_sync();
   }
   __syncthreads();
   if (split > 1) cluster_sync();                // its sums have been read
   tmem_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, 256);
+  if (warp == kDrain / 32 + 1) tmem_dealloc(tmem, 256);
 }
 
-// The projection. Warps 0-3: accumulators to y (a thread an output); 4: TMA; 5: products; 6-9 (AD): the
-// adapters' list, and their u rows into the ring. In a pair (CG = 2) each block holds its 128
+// The same for few rows: a block takes a row and four ranks, its warps share K. No list, no cluster, and
+// nothing that a projection's block would have to wait for; A_a is read once a row, from L2 for all but
+// the first.
+template <int DT>
+__global__ void __launch_bounds__(256) adapter_rows_kernel(const __grid_constant__ ProjectArgs a, const char *x,
+                                                           int64_t ldx, const char *down) {
+  __shared__ float s_sum[8][4];
+  const int fours = a.rank >> 2, row = blockIdx.x / fours, j0 = (blockIdx.x - row * fours) * 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int at = a.index[row / a.n];
+  if (at >= a.count && threadIdx.x == 0) *a.status = DT_ERR_BAD_INDEX;
+  if (at < 0 || at >= a.count) return;
+  const char *d = down + 2 * (static_cast<int64_t>(at) * a.rank + j0) * a.K;
+  x += row * ldx;
+  float v[4] = {};
+#pragma unroll 2
+  for (int k = threadIdx.x * 8; k < a.K; k += 256 * 8) {
+    const uint4 p = *reinterpret_cast<const uint4 *>(x + 2 * k);
+    const uint32_t xs[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4 *>(d + 2 * (static_cast<int64_t>(j) * a.K + k)));
+      const uint32_t ds[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = Half16<DT>::unpack(xs[e]), g = Half16<DT>::unpack(ds[e]);
+        v[j] += f.x * g.x;
+        v[j] += f.y * g.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = warp_sum(v[j]);
+    if (lane == 0) s_sum[warp][j] = v[j];
+  }
+  __syncthreads();
+  if (threadIdx.x < 4) {
+    float all = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) all += s_sum[w][threadIdx.x];
+    a.u[static_cast<int64_t>(row) * a.rank + j0 + threadIdx.x] = round16<DT>(all * (a.scale ? a.scale[at] : 1.0f));
+  }
+}
+
+// The projection. Warps 0-7: accumulators to y (a thread an output, two for each); 8: TMA; 9: products; 10-13
+// (AD): the adapters' list, and their u rows into the ring. In a pair (CG = 2) each block holds its 128
 // rows of W and half of the tile's rows of x, and the first one issues the products of both.
 template <int DT, bool E8, bool AD, int CG>
-__global__ void __launch_bounds__(AD ? 320 : 192, 1)
+__global__ void __launch_bounds__(AD ? kDrain + 192 : kDrain + 64, 1)
 project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ ProjectShape w,
                const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                const __grid_constant__ CUtensorMap umap) {
@@ -461,83 +559,83 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ss.acc_full[i], 1);
-      mbar_init(&ss.acc_empty[i], 128 * CG);
+      mbar_init(&ss.acc_empty[i], kDrain * CG);
       mbar_init(&ss.list_full[i], 128);
-      mbar_init(&ss.list_empty[i], E8 ? 6 : 2);
+      mbar_init(&ss.list_empty[i], E8 ? 2 + kDrain / 32 : 2);
     }
     mbar_init(&ss.idle, 1);
     ss.fail = 0;
   }
-  if (warp == 5) tmem_take<CG>(&ss.tmem);
+  if (warp == kDrain / 32 + 1) tmem_take<CG>(&ss.tmem);
   tmem_fence_before();
   __syncthreads();
   if (size > 1) cluster_sync();
   tmem_fence_after();
   const uint32_t tmem = ss.tmem;
   volatile int *fail = &ss.fail;
-  auto wait = [&](uint64_t *bar, uint32_t parity) {
-    if (*fail) return false;
-    if (CG == 2 ? wait_cluster(bar, parity) : mbar_wait_cycles(bar, parity)) return true;
-    *fail = 1;
-    *a.status = DT_ERR_TIMEOUT;
-    return false;
-  };
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, fail, a.status); };
+  const bool issuer = elect_one();
   // the barrier of the block that issues the products
   auto first_block = [&](uint64_t *bar) { return CG == 2 ? peer_address(smem_u32(bar), 0) : smem_u32(bar); };
   auto arrive_first = [&](uint64_t *bar) {
     if (CG == 2) arrive_peer(first_block(bar));
     else mbar_arrive(bar);
   };
-  // the adapters' part of K in pieces of 16, four a stage; this block's stages of them
-  auto pieces_of = [&](const AdapterList &l) { return l.count * (a.rank >> 4); };
-  auto share = [&](int pieces, int *q0, int *q1) {
-    const int n = (pieces + 3) >> 2;
+  // the adapters' part of K in sixteens, four a stage; this block's stages of them
+  auto sixteens_of = [&](const AdapterList &l) { return l.count * (a.rank >> 4); };
+  auto share = [&](int all, int *q0, int *q1) {
+    const int n = (all + 3) >> 2;
     *q0 = n * rank / split;
     *q1 = n * (rank + 1) / split;
   };
 
-  if (warp == 4 && lane == 0) {
+  if (warp == kDrain / 32) {
     Place p = {0, 0};
     uint32_t issued = 0;
     bool go = true;
     for (int t = first, i = 0; t < w.tiles && go; t += step, ++i) {
-      const int o0 = (t % w.tiles_o * CG + pair) * kOuts, x0 = t / w.tiles_o * w.nt + pair * mine;
+      const int o0 = (t % w.tiles_o * CG + pair) * w.outs, x0 = t / w.tiles_o * w.nt + pair * mine;
       for (int s = k0; s < k1 && go; ++s) {
         if (!(go = wait(&ss.empty[p.at], p.parity ^ 1u))) break;
         unsigned char *to = sm + p.at * stage;
         const uint32_t bar = first_block(&ss.full[p.at]);
-        if (pair == 0) mbar_expect_tx(&ss.full[p.at], CG * stage);
-        tma_2d<CG>(to, &wmap, s * kValues, o0, bar);
-        tma_2d<CG>(to + kSlabA, &xmap, s * kValues, x0, bar);
+        if (issuer) {
+          if (pair == 0) mbar_expect_tx(&ss.full[p.at], CG * (w.outs + mine) * 128);
+          tma_2d<CG>(to, &wmap, s * kValues, o0, bar);
+          tma_2d<CG>(to + kSlabA, &xmap, s * kValues, x0, bar);
+        }
         p.step(w.stages);
         ++issued;
       }
       if (!AD || !go) continue;
       if (!(go = wait(&ss.list_full[i & 1], (i >> 1) & 1))) break;
       const AdapterList &l = ss.list[i & 1];
-      const int pieces = pieces_of(l), per = a.rank >> 4;
+      const int all = sixteens_of(l), per = a.rank >> 4, wide = w.piece >> 4;
       int q0, q1;
-      share(pieces, &q0, &q1);
+      share(all, &q0, &q1);
       for (int q = q0; q < q1; ++q) {
         if (!(go = wait(&ss.empty[p.at], p.parity ^ 1u))) break;
-        mbar_arrive(&ss.u_go[p.at]);
+        if (issuer) mbar_arrive(&ss.u_go[p.at]);
         unsigned char *to = sm + p.at * stage;
         const uint32_t bar = first_block(&ss.full[p.at]);
-        const int here = min(4, pieces - 4 * q);
-        if (pair == 0) mbar_expect_tx(&ss.full[p.at], CG * here * kPiece);
-        for (int k = 0; k < here; ++k) {
-          const int u = (4 * q + k) / per, j = (4 * q + k - u * per) * 16;
-          tma_2d<CG>(to + k * kPiece, &umap, j, l.ids[u] * a.O + o0, bar);
+        const int here = min(4, all - 4 * q);
+        if (issuer) {
+          if (pair == 0) mbar_expect_tx(&ss.full[p.at], CG * here * w.outs * 32);
+          for (int k = 0; k < here; k += wide) {
+            const int u = (4 * q + k) / per, j = (4 * q + k - u * per) * 16;
+            tma_2d<CG>(to + k * kOuts * 32, &umap, j, l.ids[u] * a.O + o0, bar);
+          }
         }
         p.step(w.stages);
         ++issued;
       }
-      mbar_arrive(&ss.list_empty[i & 1]);
+      __syncwarp();
+      if (issuer) mbar_arrive(&ss.list_empty[i & 1]);
     }
-    if (*fail && pair == 0)    // nothing may land in memory that the block has given up
+    if (*fail && pair == 0 && lane == 0)    // nothing may land in memory that the block has given up
       for (uint32_t k = issued > static_cast<uint32_t>(w.stages) ? issued - w.stages : 0; k < issued; ++k)
         mbar_wait_cycles(&ss.full[k % w.stages], (k / w.stages) & 1u);
-  } else if (warp == 5 && lane == 0) {
+  } else if (warp == kDrain / 32 + 1) {
     const uint32_t idesc = descriptor<DT, E8>(kOuts * CG, w.nt), idesc16 = descriptor<DT, false>(kOuts * CG, w.nt);
     Place p = {0, 0};
     uint32_t phases = 0;                       // of u_full, a bit a stage
@@ -551,22 +649,24 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         for (int s = k0; s < k1; ++s) {
           if (!(go = wait(&ss.full[p.at], p.parity))) break;
           tmem_fence_after();
-          const uint32_t at = smem_u32(sm + p.at * stage);
+          const uint32_t at = smem_u32(sm) + p.at * stage;
+          const uint64_t da = rows128(at), db = rows128(at + kSlabA);
           const int parts = min(4, (kbytes - s * 128 + 31) / 32);
+          if (issuer) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < parts)
-              mma<CG, E8>(acc, rows128(at) + 2 * k, rows128(at + kSlabA) + 2 * k, idesc, s > k0 || k > 0);
-          commit<CG>(&ss.empty[p.at]);
+            for (int k = 0; k < 4; ++k)
+              if (k < parts) mma<CG, E8>(acc, da + 2 * k, db + 2 * k, idesc, s > k0 || k > 0);
+            commit<CG>(&ss.empty[p.at]);
+          }
           p.step(w.stages);
         }
         if (!go) break;
       }
       if (AD) {
         if (!(go = wait(&ss.list_full[i & 1], (i >> 1) & 1))) break;
-        const int pieces = pieces_of(ss.list[i & 1]);
+        const int all = sixteens_of(ss.list[i & 1]), wide = w.piece >> 4;
         int q0, q1;
-        share(pieces, &q0, &q1);
+        share(all, &q0, &q1);
         if (pair == 0) {
           // the adapters' own accumulator is the only one: the tile before has to have read it
           if (E8 && w.buffers == 2 && i > 0 && q0 < q1) {
@@ -578,26 +678,30 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
             if (!(go = wait(&ss.full[p.at], p.parity) && wait(&ss.u_full[p.at], (phases >> p.at) & 1u))) break;
             phases ^= 1u << p.at;
             tmem_fence_after();
-            const uint32_t at = smem_u32(sm + p.at * stage);
-            const int here = min(4, pieces - 4 * q);
-            for (int k = 0; k < here; ++k)
-              mma<CG, false>(to, rows32(at + k * kPiece), rows32(at + kSlabA + k * mine * 32), idesc16,
+            const uint32_t at = smem_u32(sm) + p.at * stage;
+            const int here = issuer ? min(4, all - 4 * q) : 0;
+            for (int k = 0; k < here; ++k) {
+              const int first_of = k & ~(wide - 1), in = 2 * (k - first_of);     // of its piece; 32 bytes on
+              mma<CG, false>(to, rows_of(at + first_of * kOuts * 32, w.piece) + in,
+                             rows_of(at + kSlabA + first_of * mine * 32, w.piece) + in, idesc16,
                              !E8 || q > q0 || k > 0);
-            commit<CG>(&ss.empty[p.at]);
+            }
+            if (issuer) commit<CG>(&ss.empty[p.at]);
+            __syncwarp();
             p.step(w.stages);
           }
           if (!go) break;
         }
-        mbar_arrive(&ss.list_empty[i & 1]);
+        if (issuer) mbar_arrive(&ss.list_empty[i & 1]);
       }
-      if (pair == 0) commit<CG>(&ss.acc_full[buf]);
+      if (pair == 0 && issuer) commit<CG>(&ss.acc_full[buf]);
     }
-    if (*fail && pair == 0) {
+    if (*fail && pair == 0 && issuer) {
       commit<CG>(&ss.idle);
       mbar_wait_cycles(&ss.idle, 0);
     }
-  } else if (AD && warp >= 6) {
-    const int id = tid - 192;
+  } else if (AD && tid >= kDrain + 64) {
+    const int id = tid - kDrain - 64;
     uint32_t at = 0, phases = 0;               // stage of the ring; phases of u_go
     // (these warps meet for the lists: they go through all tiles, whatever has failed)
     for (int t = first, i = 0; t < w.tiles; t += step, ++i) {
@@ -607,10 +711,12 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       list_adapters(a, tt, min(tt + w.nt, a.rows), l, ss.scratch, id, 1);
       mbar_arrive(&ss.list_full[i & 1]);
       if (i == 0) cudaGridDependencySynchronize();        // u is there
-      const int pieces = pieces_of(l), per = a.rank >> 4;
+      const int all = sixteens_of(l), per = a.rank >> 4;
+      const int row_bytes = 2 * w.piece, chunks = w.piece >> 3;      // of a piece's row
+      const int shift = w.piece == 64 ? 0 : w.piece == 32 ? 1 : 2;   // rows of one swizzle
       int q0, q1, slot[2];
       const uint16_t *u[2];
-      share(pieces, &q0, &q1);
+      share(all, &q0, &q1);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = id + 128 * k, row = x0 + r;
@@ -618,6 +724,21 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         u[k] = a.u + static_cast<int64_t>(row) * a.rank;
       }
       at = (at + (k1 - k0)) % w.stages;
+      uint4 v[2][4][2];
+      auto fetch = [&](int q) {                // loads of the next stage's rows, before there is room
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int at16 = 4 * q + z, s = at16 / per, j = (at16 - s * per) * 16;
+            v[k][z][0] = v[k][z][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (at16 < all && s == slot[k]) {
+              v[k][z][0] = *reinterpret_cast<const uint4 *>(u[k] + j);
+              v[k][z][1] = *reinterpret_cast<const uint4 *>(u[k] + j + 8);
+            }
+          }
+      };
+      if (q0 < q1) fetch(q0);
       for (int q = q0; q < q1 && go; ++q) {
         if (!(go = wait(&ss.u_go[at], (phases >> at) & 1u))) break;
         phases ^= 1u << at;
@@ -626,85 +747,126 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         for (int k = 0; k < 2; ++k) {
           const int r = id + 128 * k;
           if (r >= mine) break;
-          uint4 v[4][2];
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            const int piece = 4 * q + z, s = piece / per, j = (piece - s * per) * 16;
-            v[z][0] = v[z][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (piece < pieces && s == slot[k]) {
-              v[z][0] = *reinterpret_cast<const uint4 *>(u[k] + j);
-              v[z][1] = *reinterpret_cast<const uint4 *>(u[k] + j + 8);
-            }
-          }
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            unsigned char *row = to + z * mine * 32 + r * 32;
-            const int turn = (r >> 2) & 1;
-            *reinterpret_cast<uint4 *>(row + 16 * turn) = v[z][0];
-            *reinterpret_cast<uint4 *>(row + 16 * (turn ^ 1)) = v[z][1];
+            const int c = 2 * z & (chunks - 1), turn = (r >> shift) & (chunks - 1);
+            unsigned char *row = to + (2 * z - c) * mine * 16 + r * row_bytes;
+            *reinterpret_cast<uint4 *>(row + 16 * (c ^ turn)) = v[k][z][0];
+            *reinterpret_cast<uint4 *>(row + 16 * ((c + 1) ^ turn)) = v[k][z][1];
           }
         }
         fence_async_smem();
         arrive_first(&ss.u_full[at]);
+        __syncwarp();
+        if (q + 1 < q1) fetch(q + 1);
         if (++at == static_cast<uint32_t>(w.stages)) at = 0;
       }
     }
-  } else if (warp < 4) {
+  } else if (tid < kDrain) {
+    const int row = tid & 127, group = tid >> 7;
     bool go = true;
     for (int t = first, i = 0; t < w.tiles && go; t += step, ++i) {
       const int buf = w.buffers == 2 ? i & 1 : 0, turn = w.buffers == 2 ? i >> 1 : i;
-      const int o = (t % w.tiles_o * CG + pair) * kOuts + tid, t0 = t / w.tiles_o * w.nt;
+      const int o = row < w.outs ? (t % w.tiles_o * CG + pair) * w.outs + row : a.O, t0 = t / w.tiles_o * w.nt;
       bool both = false;                       // the adapters have something in their accumulator
       if (AD && E8) {
-        go = __all_sync(kFull, wait(&ss.list_full[i & 1], (i >> 1) & 1));
+        __syncwarp();
+        go = wait(&ss.list_full[i & 1], (i >> 1) & 1);
         int q0 = 0, q1 = 0;
-        if (go) share(pieces_of(ss.list[i & 1]), &q0, &q1);
+        if (go) share(sixteens_of(ss.list[i & 1]), &q0, &q1);
         both = q0 < q1;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ss.list_empty[i & 1]);
       }
-      go = __all_sync(kFull, go && wait(&ss.acc_full[buf], turn & 1));
-      tmem_fence_after();
-      const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-      const int wexp = E8 && o < a.O ? a.w_exps[o] - 127 : 0;
-      float *own = reinterpret_cast<float *>(sm);
-      char *y = a.y + static_cast<int64_t>(t0) * a.ldy + 2 * static_cast<int64_t>(o);
       const int rows = min(w.nt, a.rows - t0);
-      auto put = [&](int c, float v) {
-        if (c < rows && o < a.O) *reinterpret_cast<uint16_t *>(y + c * a.ldy) = round16<DT>(v);
+      // 8-bit rows: 2^wexp of this output times 2^xexp of the rows of x, in one number where that
+      // cannot leave fp32's range on the way
+      const int wexp = E8 && o < a.O ? a.w_exps[o] - 127 : 0;
+      bool far = false;
+      if (E8) {
+        far = abs(wexp) > 60;
+        for (int c = lane; c < w.nt; c += 32) {
+          const int e = c < rows ? a.x_exps[t0 + c] - 127 : 0;
+          far |= abs(e) > 60;
+          ss.xexp[warp][c] = e << 23;
+        }
+        far = __any_sync(kFull, far);          // (also orders the writes before the reads below)
+      }
+      const int wbits = (wexp + 127) << 23;
+      __syncwarp();
+      go = go && wait(&ss.acc_full[buf], turn & 1);
+      tmem_fence_after();
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+      Shares shares(sm, w.nt, split, rank, row);
+      if (split > 1) cluster_sync();
+      char *y = a.y + static_cast<int64_t>(t0) * a.ldy + 2 * static_cast<int64_t>(o);
+      const bool inside = o < a.O;
+      const uint32_t ldy = static_cast<uint32_t>(a.ldy);
+      auto put = [&](int c, const auto &v) {
+        if (!inside) return;
+        char *at = y + c * a.ldy;
+        const int live = rows - c;
+#pragma unroll
+        for (int e = 0; e < static_cast<int>(sizeof(v) / sizeof(float)); e += 2) {
+          const uint32_t two = Half16<DT>::pack(v[e], v[e + 1]);
+          if (e < live) *reinterpret_cast<uint16_t *>(at + static_cast<uint64_t>(e * ldy)) = static_cast<uint16_t>(two);
+          if (e + 1 < live)
+            *reinterpret_cast<uint16_t *>(at + static_cast<uint64_t>((e + 1) * ldy)) = static_cast<uint16_t>(two >> 16);
+        }
       };
-      for (int c = 0; c < w.nt && go; c += 16) {
-        float v[16], z[16];
-        load16(lanes + buf * w.nt + c, v);
-        if (AD && E8 && both) load16(lanes + w.buffers * w.nt + c, z);
-        const int xexp = E8 ? (t0 + c + (lane & 15) < a.rows ? a.x_exps[t0 + c + (lane & 15)] : 127) - 127 : 0;
+      float v[16], z[16], next[16], next_z[16];
+      auto fetch = [&](int c) {
+        load16(lanes + buf * w.nt + c, next);
+        if (AD && E8 && both) load16(lanes + w.buffers * w.nt + c, next_z);
+      };
+      // 16 columns are on their way from TMEM while the 16 before them are written. (One copy of this
+      // code, as short as it comes: a warp issues an instruction every six cycles here, and its
+      // instructions have to fit their cache.)
+      const int sixteens = w.nt / 16;
+      if (go && group < sixteens) fetch(shares.turn(group, w.nt));
+#pragma unroll 1
+      for (int i = group; i < sixteens && go; i += kGroups) {
+        const int c = shares.turn(i, w.nt);
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          if (E8) {
-            v[e] = times_power(v[e], wexp + __shfl_sync(kFull, xexp, e));
-            if (AD && both) v[e] += z[e];
-          }
-          if (split == 1) put(c + e, v[e]);
-          else own[(c + e) * 128 + tid] = v[e];
+          v[e] = next[e];
+          if (AD && E8) z[e] = next_z[e];
         }
+        if (i + kGroups < sixteens) fetch(shares.turn(i + kGroups, w.nt));
+        if (E8) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const int4 x = *reinterpret_cast<const int4 *>(&ss.xexp[warp][c + e]);
+            const int bits[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (far) v[e + k] = times_power(v[e + k], wexp + (bits[k] >> 23));
+              else v[e + k] *= __int_as_float(wbits + bits[k]);
+              if (AD && both) v[e + k] += z[e + k];
+            }
+          }
+        }
+        if (split > 1) shares.push(c, v);
+        else put(c, v);
       }
       tmem_fence_before();
       arrive_first(&ss.acc_empty[buf]);
       if (split > 1) {
         cluster_sync();
-        sum_columns(own, w.nt, split, rank, tid, put);
+        shares.sum(sm, w.nt, group, kGroups, put);
       }
     }
   }
-  if (split > 1 && warp >= 4) {
+  if (split > 1 && tid >= kDrain) {
     __syncwarp();
+    cluster_sync();
     cluster_sync();
   }
   __syncthreads();
   if (size > 1) cluster_sync();          // no block ends while another may still read or signal it
   tmem_fence_after();
-  if (warp == 5) tmem_give<CG>(tmem);
+  if (warp == kDrain / 32 + 1) tmem_give<CG>(tmem);
 }
 
 // ------------------------------------------------------------ plans
@@ -717,78 +879,142 @@ bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 struct ProjectPlan {
   int cg;
   ProjectShape s;
-  int blocks;
+  int blocks, idle;      // blocks; how many of the GPU's places have a tile less to do than others
+  double tile;           // cycles of a tile
   size_t smem;
 };
 
-// Cycles that a tile's slab takes: its products, and its bytes on the way into shared memory.
-// (Calibrated on whole calls; only the order of the choices matters.)
-double slab_cycles(int nt, int cg) {
-  return std::max(2.0 * nt, (kSlabA + nt / cg * 128) / 60.0);
+// clusters of each size that run at once, one block an SM (an SM whose cluster is not complete
+// stays idle); [1]: SMs
+struct Rooms {
+  int of[kMaxSplit + 1];
+};
+
+int rooms(int sms, Rooms *r) {
+  static std::atomic<int> known[64][kMaxSplit + 1] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DT_ERR_CUDA;
+  constexpr auto kernel = adapter_down_kernel<DT_BF16>;
+  r->of[0] = 0;
+  r->of[1] = sms;
+  for (int size = 2; size <= kMaxSplit; ++size) {
+    int n = dev < 64 ? known[dev][size].load(std::memory_order_relaxed) : 0;
+    if (!n) {
+      if (allow_smem<kernel>() != cudaSuccess) return DT_ERR_CUDA;
+      cudaLaunchAttribute cluster = {};
+      cluster.id = cudaLaunchAttributeClusterDimension;
+      cluster.val.clusterDim.x = size;
+      cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+      cudaLaunchConfig_t config = {};
+      config.gridDim = dim3(sms / size * size);
+      config.blockDim = dim3(kDrain + 64);
+      config.dynamicSmemBytes = 200 * 1024;
+      config.attrs = &cluster;
+      config.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &config) != cudaSuccess) return DT_ERR_CUDA;
+      n = std::max(n, 0);
+      if (dev < 64) known[dev][size].store(n ? n : -1, std::memory_order_relaxed);
+    }
+    r->of[size] = std::max(n, 0);
+  }
+  return DT_OK;
 }
 
-void choose(const ProjectArgs &a, bool e8, bool ad, int sms, int pairs, int smem, ProjectPlan *p) {
-  const int steps = ceil_div(static_cast<int64_t>(a.K) * (e8 ? 1 : 2), 128);
+constexpr double kCopyRate = 55.0;     // bytes a cycle into an SM's shared memory
+constexpr double kRowsRate = 4000.0;   // bytes a cycle that adapter_rows_kernel reads
+constexpr double kMemoryRate = 3500.0; // bytes a cycle from memory
+
+// Cycles that a slab takes in a block: its products, its bytes on the way in, and what waits and
+// issuing take whatever its size.
+double slab_cycles(int outs, int nt, int cg) {
+  return std::max(std::max(2.0 * nt, 390.0), (outs + nt / cg) * 128 / kCopyRate);
+}
+
+// The tile, and the blocks that share one, of the least estimated time: whole rounds of tiles over the
+// clusters that the GPU has room for, or memory's time, and what a tile's end takes. A pair of blocks
+// (cg = 2) loads half of the rows of x each. Where one round does, tiles have as few rows of W as keep
+// all SMs busy. Only the order of the estimates matters.
+void choose(const ProjectArgs &a, bool e8, bool ad, const Rooms &room, int smem, ProjectPlan *p) {
+  const int size = e8 ? 1 : 2, steps = ceil_div(static_cast<int64_t>(a.K) * size, 128);
   const int cap = ad && e8 ? 160 : kMaxTokens;     // three accumulators instead of two
+  const double memory = (static_cast<double>(a.O) + a.rows) * a.K * size / kMemoryRate;
   double best = 1e300;
-  for (int cg = 1; cg <= 2; ++cg) {
-    const int tiles_o = ceil_div(a.O, kOuts * cg), room = cg == 2 ? pairs : sms;
-    if (room < 1) continue;
+  for (int cg = 1; cg <= 2; ++cg)
     for (int nt = 16 * cg; nt <= cap; nt += 16 * cg) {
-      const int64_t tiles = static_cast<int64_t>(tiles_o) * ceil_div(a.rows, nt);
-      for (int split = 1; split <= kMaxSplit; ++split) {
-        if (split > 1 && (cg == 2 || tiles * split > room || split > steps || split == 5 || split == 7)) continue;
-        const double rounds = ceil_div(tiles, room);
-        const double busy = static_cast<double>(std::min<int64_t>(tiles * split, room)) * cg;
-        // W comes from memory at 23 bytes a cycle and SM where all take part
-        const double slab = std::max(slab_cycles(nt, cg), kSlabA / 23.0 * busy / sms / std::max(1, ceil_div(a.rows, nt)));
-        const double cost = rounds * ceil_div(steps, split) * slab + 8.0 * nt + (split > 1 ? 1500.0 : 0.0);
+      const int tiles_t = ceil_div(a.rows, nt);
+      for (int split = 1; split <= (cg == 2 ? 1 : std::min(kMaxSplit, steps)); ++split) {
+        const int places = room.of[cg == 2 ? 2 : split];
+        if (places < 1) continue;
+        int outs = kOuts;
+        if (cg == 1 && places >= tiles_t)
+          outs = std::min(kOuts, (ceil_div(a.O, places / tiles_t) + 7) / 8 * 8);
+        const int tiles_o = ceil_div(a.O, outs * cg);
+        const int64_t tiles = static_cast<int64_t>(tiles_o) * tiles_t;
+        if (split > 1 && tiles > places) continue;
+        const int rounds = ceil_div(tiles, places);
+        const double tile = ceil_div(steps, split) * slab_cycles(outs, nt, cg);
+        const double cost = std::max(rounds * tile, memory) + 16.0 * nt + (split > 1 ? 3000.0 + 16.0 * nt : 0.0);
         if (cost < best) {
           best = cost;
           p->cg = cg;
+          p->tile = tile;
           p->s.nt = nt;
           p->s.split = split;
+          p->s.outs = outs;
           p->s.tiles_o = tiles_o;
           p->s.tiles = static_cast<int>(tiles);
-          p->blocks = static_cast<int>(std::min<int64_t>(tiles * split, cg == 2 ? room : static_cast<int64_t>(room))) * cg;
+          const int clusters = static_cast<int>(std::min<int64_t>(tiles, places)), members = cg == 2 ? 2 : split;
+          p->blocks = clusters * members;
+          p->idle = room.of[1] - p->blocks + static_cast<int>(static_cast<int64_t>(rounds) * clusters - tiles) * members;
         }
       }
       if (nt >= a.rows) break;
     }
-  }
   const int stage = kSlabA + p->s.nt / p->cg * 128;
   p->s.stages = stages_of(smem, stage);
   p->s.buffers = 2;
   p->s.off_small = p->s.stages * stage;
+  p->s.piece = a.rank % 64 == 0 ? 64 : a.rank % 32 == 0 ? 32 : 16;
   p->smem = p->s.off_small + sizeof(Small);
 }
 
-// blocks of the kernel that run at once in pairs: an SM without a partner stays idle
-template <auto Kernel>
-int resident_pairs(int threads, size_t smem, int sms) {
-  static std::atomic<int> known[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  int n = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
-  if (n) return n;
-  cudaLaunchAttribute pair = {};
-  pair.id = cudaLaunchAttributeClusterDimension;
-  pair.val.clusterDim.x = 2;
-  pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
-  cudaLaunchConfig_t config = {};
-  config.gridDim = dim3(sms / 2 * 2);
-  config.blockDim = dim3(threads);
-  config.dynamicSmemBytes = smem;
-  config.attrs = &pair;
-  config.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, Kernel, &config) != cudaSuccess || n < 1) return 0;
-  if (dev < 64) known[dev].store(n, std::memory_order_release);
-  return n;
+// The launch before: a block a row and four ranks while all that they read (from L2) takes less time
+// than the other kernel (s->tiles = 0); else blocks that fit the places which have a tile less to do cost nothing as long as
+// they end within the others' first tile; else the shortest.
+void choose_down(const ProjectArgs &a, const ProjectPlan &p, const Rooms &room, int smem, ProjectShape *s) {
+  const int steps = ceil_div(2 * a.K, 128), spt = kOuts / a.rank;
+  double best = 1e300, shortest = 1e300;
+  for (int nt = 16; nt <= kMaxTokens; nt += 16) {
+    const int requests = std::min(nt, (nt + a.n - 2) / a.n + 1);        // of a tile, at most
+    const int tiles_o = ceil_div(std::min(requests, a.count), spt);
+    const int64_t tiles = static_cast<int64_t>(tiles_o) * ceil_div(a.rows, nt);
+    for (int split = 1; split <= std::min(kMaxSplit, steps); split *= 2) {
+      if (room.of[split] < 1 || (split > 1 && tiles > room.of[split])) continue;
+      const double rounds = ceil_div(tiles, room.of[split]);
+      const double time = rounds * (ceil_div(steps, split) * slab_cycles(kOuts, nt, 1) + 10000.0 +
+                                    (split > 1 ? 3000.0 + 16.0 * nt : 16.0 * nt));
+      shortest = std::min(shortest, time);
+      const double cost = (tiles * split <= p.idle ? std::max(0.0, time - p.tile) : time) + 1e-3 * time;
+      if (cost < best) {
+        best = cost;
+        s->nt = nt;
+        s->tiles_o = tiles_o;
+        s->tiles = static_cast<int>(tiles);
+        s->split = split;
+      }
+    }
+    if (nt >= a.rows) break;
+  }
+  if (4000.0 + 2.0 * a.rows * a.rank * a.K / kRowsRate < shortest) {
+    s->tiles = 0;
+    return;
+  }
+  const int stage = kSlabA + s->nt * 128;
+  s->stages = std::min(stages_of(smem, stage),
+                       std::max(ceil_div(steps, s->split),
+                                ceil_div(s->split * Shares::share_width(s->nt, s->split) * 512, stage)));
+  s->off_small = s->stages * stage;
 }
-
-struct ProjectMaps {
-  CUtensorMap w, x, up, down, x16;
-};
 
 template <auto Kernel, typename... Args>
 cudaError_t launch_cluster(int blocks, int threads, size_t smem, int cluster, bool early, cudaStream_t st,
@@ -811,27 +1037,21 @@ cudaError_t launch_cluster(int blocks, int threads, size_t smem, int cluster, bo
 }
 
 template <int DT>
-cudaError_t launch_down(const ProjectArgs &a, const dt_adapters &ad, const void *x16, int64_t ldx16, int sms,
-                        int smem, cudaStream_t st) {
+cudaError_t launch_down(const ProjectArgs &a, const ProjectShape &s, const dt_adapters &ad, const void *x16,
+                        int64_t ldx16, cudaStream_t st) {
+  if (s.tiles == 0) {
+    adapter_rows_kernel<DT><<<a.rows * (a.rank / 4), 256, 0, st>>>(a, static_cast<const char *>(x16), ldx16,
+                                                                   static_cast<const char *>(ad.down));
+    return cudaGetLastError();
+  }
   const cudaError_t e = allow_smem<adapter_down_kernel<DT>>();
   if (e != cudaSuccess) return e;
-  ProjectShape s = {};
-  const int tiles_t = ceil_div(a.rows, kMaxTokens), steps = ceil_div(2 * a.K, 128);
-  s.nt = ceil_div(ceil_div(a.rows, tiles_t), 16) * 16;
-  const int requests = std::min(s.nt, (s.nt + a.n - 2) / a.n + 1);        // of a tile, at most
-  s.tiles_o = ceil_div(std::min(requests, a.count), kOuts / a.rank);
-  s.tiles = s.tiles_o * ceil_div(a.rows, s.nt);
-  s.split = 1;
-  while (s.split < kMaxSplit && s.tiles * s.split * 2 <= sms && s.split * 2 <= steps) s.split *= 2;
-  const int stage = kSlabA + s.nt * 128;
-  s.stages = std::min(stages_of(smem, stage), std::max(ceil_div(steps, s.split), ceil_div(s.nt * 512, stage)));
-  s.off_small = s.stages * stage;
   CUtensorMap down, x;
   if (!matrix_map(ad.down, 2, a.K, static_cast<int64_t>(a.count) * a.rank, 2 * a.K, 64, a.rank, &down) ||
       !matrix_map(x16, 2, a.K, a.rows, ldx16, 64, s.nt, &x))
     return cudaErrorUnknown;
-  return launch_cluster<adapter_down_kernel<DT>>(s.tiles * s.split, 192, s.off_small + sizeof(Small), s.split, false,
-                                                 st, a, s, down, x);
+  return launch_cluster<adapter_down_kernel<DT>>(s.tiles * s.split, kDrain + 64, s.off_small + sizeof(Small), s.split,
+                                                 false, st, a, s, down, x);
 }
 
 template <int DT, bool E8, bool AD, int CG>
@@ -840,27 +1060,28 @@ cudaError_t launch_main(const ProjectArgs &a, const ProjectPlan &p, const CUtens
   constexpr auto kernel = project_kernel<DT, E8, AD, CG>;
   const cudaError_t e = allow_smem<kernel>();
   if (e != cudaSuccess) return e;
-  return launch_cluster<kernel>(p.blocks, AD ? 320 : 192, p.smem, CG == 2 ? 2 : p.s.split, AD, st, a, p.s, w, x, up);
+  return launch_cluster<kernel>(p.blocks, AD ? kDrain + 192 : kDrain + 64, p.smem, CG == 2 ? 2 : p.s.split, AD, st, a, p.s, w, x, up);
 }
 
 template <int DT, bool E8, bool AD>
 cudaError_t launch_project(const ProjectArgs &a, const dt_matrix &m, const void *x, int64_t ldx,
-                           const dt_adapters *ad, const void *x16, int64_t ldx16, int sms, int smem,
+                           const dt_adapters *ad, const void *x16, int64_t ldx16, const Rooms &room, int smem,
                            cudaStream_t st) {
-  const cudaError_t e = allow_smem<project_kernel<DT, E8, AD, 2>>();
-  if (e != cudaSuccess) return e;
   ProjectPlan p = {};
-  choose(a, E8, AD, sms, resident_pairs<project_kernel<DT, E8, AD, 2>>(AD ? 320 : 192, 200 * 1024, sms), smem, &p);
-  if (AD) {
-    const cudaError_t e = launch_down<DT>(a, *ad, x16, ldx16, sms, smem, st);
-    if (e != cudaSuccess) return e;
-  }
+  choose(a, E8, AD, room, smem, &p);
   CUtensorMap w, xm, up = {};
   const int size = E8 ? 1 : 2;
-  if (!matrix_map(m.data, size, a.K, a.O, m.ld * size, 128 / size, kOuts, &w) ||
-      !matrix_map(x, size, a.K, a.rows, ldx, 128 / size, p.s.nt / p.cg, &xm) ||
-      (AD && !matrix_map(ad->up, 2, a.rank, static_cast<int64_t>(a.count) * a.O, 2 * a.rank, 16, kOuts, &up)))
+  if (!matrix_map(m.data, size, a.K, a.O, m.ld * size, 128 / size, p.s.outs, &w) ||
+      !matrix_map(x, size, a.K, a.rows, ldx, 128 / size, p.s.nt / p.cg, &xm))
     return cudaErrorUnknown;
+  if (AD) {
+    if (!matrix_map(ad->up, 2, a.rank, static_cast<int64_t>(a.count) * a.O, 2 * a.rank, p.s.piece, p.s.outs, &up))
+      return cudaErrorUnknown;
+    ProjectShape down = {};
+    choose_down(a, p, room, smem, &down);
+    const cudaError_t e = launch_down<DT>(a, down, *ad, x16, ldx16, st);
+    if (e != cudaSuccess) return e;
+  }
   return p.cg == 2 ? launch_main<DT, E8, AD, 2>(a, p, w, xm, up, st) : launch_main<DT, E8, AD, 1>(a, p, w, xm, up, st);
 }
 
@@ -890,7 +1111,7 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
   const bool e8 = w->dtype == DT_E4M3;
   const int64_t size = e8 ? 1 : 2, rows = static_cast<int64_t>(batch) * n, most = int64_t{1} << 32;
   if (w->ld < w->K || w->ld * size % 16 || w->ld > most || ldx < w->K || ldx * size % 16 || ldx > most ||
-      ldy < w->O || ldy > most || e8 != (w->exps != nullptr) || e8 != (x_exps != nullptr))
+      ldy < w->O || ldy > (1 << 26) || e8 != (w->exps != nullptr) || e8 != (x_exps != nullptr))
     return DT_ERR_INVALID_ARG;
   if (!adapters != !index || (!adapters || !e8) != !x16) return DT_ERR_INVALID_ARG;
   dt::ProjectArgs a = {};
@@ -927,10 +1148,12 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
   int sms, smem;
   const int rc = dt::device_sm_count(&sms, &smem);
   if (rc) return rc;
+  dt::Rooms room;
+  if (dt::rooms(sms, &room)) return DT_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto go = [&](auto type, auto eight, auto with) {
     return dt::launch_project<decltype(type)::value, decltype(eight)::value, decltype(with)::value>(
-        a, *w, x, ldx * size, adapters, x16, 2 * ldx16, sms, smem, st);
+        a, *w, x, ldx * size, adapters, x16, 2 * ldx16, room, smem, st);
   };
   auto typed = [&](auto type) {
     if (e8) return adapters ? go(type, std::true_type{}, std::true_type{}) : go(type, std::true_type{}, std::false_type{});

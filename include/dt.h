@@ -566,8 +566,8 @@ int dt_quantize_rows(const dt_rows *x, uint8_t *codes, uint8_t *exps, int outer,
  *          [batch n]; 16-byte aligned, row stride ldx, a multiple of 16 bytes
  *   x16    the rows that the adapters see, for 8-bit weights with adapters (dt_rms_norm
  *          gives both); NULL otherwise
- *   y      [batch n][O] of type dtype (DT_BF16 or DT_F16), row stride ldy >= O, any; must
- *          not overlap the inputs
+ *   y      [batch n][O] of type dtype (DT_BF16 or DT_F16), row stride ldy in [O, 2^26];
+ *          must not overlap the inputs
  *   A (down) [count][rank][K], B (up) [count][O][rank], dense, dtype, 16-byte aligned;
  *          scale [count] fp32 (NULL: ones); adapters NULL: none
  *   index  [batch] int32; with adapters only

@@ -10,7 +10,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import functools
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -90,6 +92,9 @@ class DtRows(C.Structure):
     _fields_ = [("data", C.c_void_p), ("stride_outer", C.c_int64), ("stride_inner", C.c_int64)]
 
 
+_pack_rows = struct.Struct("@Pqq").pack     # a dt_rows as bytes: half the time of a DtRows
+
+
 class DtMatrix(C.Structure):
     _fields_ = [("data", C.c_void_p), ("exps", C.c_void_p), ("ld", C.c_int64)] + \
         [(n, C.c_int) for n in ("O", "K", "dtype")]
@@ -166,7 +171,8 @@ def lib():
         L.dt_cache_attention_workspace_bytes.argtypes = [cache, C.c_int, C.c_int]
         L.dt_cache_attention.argtypes = [cache, heads, C.c_int, C.c_int] + [C.c_void_p] * 3 + \
             [C.c_float, heads, C.c_void_p, C.c_size_t, C.c_void_p]
-        rows, v, i, n64 = C.POINTER(DtRows), C.c_void_p, C.c_int, C.c_int64
+        # the dt_rows of a norm are packed bytes or the address of a DtRows
+        rows, v, i, n64 = C.c_char_p, C.c_void_p, C.c_int, C.c_int64
         L.dt_cache_reserve.argtypes = [cache, C.POINTER(DtPagePool), v, v]
         L.dt_cache_slots.argtypes = [cache, i, v, v, v, v, v]
         L.dt_rms_norm.argtypes = [rows] * 4 + [v] * 3 + [C.c_float] * 2 + [i] * 4 + [v]
@@ -913,6 +919,13 @@ class Rows8:
             raise ValueError("exps must be a contiguous uint8 tensor, one a row, on the codes' device")
         self.codes, self.exps, self.shape = codes, exps, codes.shape
 
+    @classmethod
+    def _made(cls, codes, exps):
+        """Of tensors that need no check."""
+        self = cls.__new__(cls)
+        self.codes, self.exps, self.shape = codes, exps, codes.shape
+        return self
+
     def values(self, dtype=torch.float32):
         """The rows' values (plain torch operations, for looking at them)."""
         e = self.exps.to(torch.int32)
@@ -921,28 +934,44 @@ class Rows8:
         return torch.where((e == 255)[..., None], float("nan"), x).to(dtype)
 
 
-def _row_view(t, what: str, dtype=None, dev=None, shape=None):
-    """A [...][d] tensor as a dt_rows of two outer dimensions: its rows lie at one stride within
-    the second-last dimension and at one within those before it. Returns the view and its sizes."""
-    kind = _TYPE16.get(t.dtype)
-    if kind is None or t.get_device() < 0 or (dtype is not None and (kind != dtype or t.get_device() != dev or
-                                                                       t.shape != shape)):
-        raise ValueError(f"{what} must be a bfloat16 or float16 CUDA tensor" +
-                         ("" if dtype is None else " of the rows' shape, type and device"))
-    size, s = t.shape, t.stride()
-    if len(size) < 2 or s[-1] != 1:
-        raise ValueError(f"{what} must be [...][d] with a dense last dimension")
+@functools.lru_cache(maxsize=4096)
+def _row_layout(size, strides):
+    """A [...][d] shape as rows in two outer dimensions: rows lie at one stride within the
+    second-last dimension and at one across those before it. (outer, its stride, inner, its
+    stride), or None."""
+    if len(size) < 2 or strides[-1] != 1:
+        return None
     outer, step = 1, 0
-    for n, st in zip(reversed(size[:-2]), reversed(s[:-2])):
+    for n, s in zip(reversed(size[:-2]), reversed(strides[:-2])):
         if n == 1:
             continue
         if outer == 1:
-            step = st
-        elif st != step * outer:
-            raise ValueError(f"{what}'s rows must lie at two strides: one within the second-last dimension, one "
-                             "across those before it")
+            step = s
+        elif s != step * outer:
+            return None
         outer *= n
-    return DtRows(t.data_ptr(), step, s[-2]), outer, size[-2], size[-1], kind
+    return outer, step, size[-2], strides[-2]
+
+
+def _rows(t, what: str):
+    """A 16-bit tensor of rows: its packed dt_rows, its layout."""
+    layout = _row_layout(t.shape, t.stride())
+    if layout is None:
+        raise ValueError(f"{what} must be [...][d] with a dense last dimension and rows at two strides: one within "
+                         "the second-last dimension, one across those before it")
+    return _pack_rows(t.data_ptr(), layout[1], layout[3]), layout
+
+
+def _same_rows(t, what: str, like, dev):
+    if t.shape != like.shape or t.dtype != like.dtype or t.get_device() != dev:
+        raise ValueError(f"{what} must be of x's shape, type and device")
+    return _rows(t, what)[0]
+
+
+def _new_rows(like, inner, d, stream):
+    """A dense tensor of like's shape and type, and its packed dt_rows."""
+    t = _dense_like(like, stream)
+    return t, _pack_rows(t.data_ptr(), inner * d, d)
 
 
 class Norm:
@@ -954,6 +983,9 @@ class Norm:
                                    not weight.is_contiguous() or weight.get_device() < 0):
             raise ValueError("weight must be a contiguous [d] bfloat16 or float16 CUDA tensor")
         self.weight, self.eps, self.offset = weight, float(eps), float(offset)
+        self._ptr = _ptr(weight)
+        if weight is not None:
+            self._d, self._type, self._dev = weight.shape[0], _TYPE16[weight.dtype], weight.get_device()
 
 
 def _codes_like(x, stream):
@@ -969,42 +1001,55 @@ def rms_norm(norm: Norm, x, residual=None, kind: str = "16", out=None, total=Non
     x or residual."""
     if kind not in ("16", "e4m3", "both"):
         raise ValueError('kind must be "16", "e4m3" or "both"')
-    vx, outer, inner, d, dtype = _row_view(x, "x")
-    dev, shape, w = x.get_device(), x.shape, norm.weight
+    dtype, dev, w = _TYPE16.get(x.dtype), x.get_device(), norm.weight
+    if dtype is None or dev < 0:
+        raise ValueError("x must be a bfloat16 or float16 CUDA tensor")
     handle = _raw_stream(stream, dev)
-    if w is not None and (w.shape[0] != d or _TYPE16[w.dtype] != dtype or w.get_device() != dev):
+    vx, (outer, _, inner, _) = _rows(x, "x")
+    d = x.shape[-1]
+    if w is not None and (norm._d != d or norm._type != dtype or norm._dev != dev):
         raise ValueError("the norm's weight must have one value a column, of the rows' type and device")
     vr = vt = vo = codes = exps = None
     if residual is not None:
-        vr = _row_view(residual, "residual", dtype, dev, shape)[0]
+        vr = _same_rows(residual, "residual", x, dev)
         if total is None:
-            total = _dense_like(x, stream)
-        vt = _row_view(total, "total", dtype, dev, shape)[0]
+            total, vt = _new_rows(x, inner, d, stream)
+        else:
+            vt = _same_rows(total, "total", x, dev)
     elif total is not None:
         raise ValueError("total is the sum of x and residual: residual is needed")
     if kind != "e4m3":
         if out is None:
-            out = _dense_like(x, stream)
-        vo = _row_view(out, "out", dtype, dev, shape)[0]
+            out, vo = _new_rows(x, inner, d, stream)
+        else:
+            vo = _same_rows(out, "out", x, dev)
     elif out is not None:
         raise ValueError('out is for kind "16" or "both"')
     if kind != "16":
         codes, exps = _codes_like(x, stream)
-    _check(lib().dt_rms_norm(vx, vr, vt, vo, _ptr(codes), _ptr(exps), _ptr(w), norm.offset, norm.eps,
+    _check(lib().dt_rms_norm(vx, vr, vt, vo, _ptr(codes), _ptr(exps), norm._ptr, norm.offset, norm.eps,
                              outer, inner, d, dtype, handle), "dt_rms_norm")
-    y = out if kind == "16" else Rows8(codes, exps) if kind == "e4m3" else (out, Rows8(codes, exps))
+    if kind == "16":
+        y = out
+    else:
+        y = Rows8._made(codes, exps)
+        if kind == "both":
+            y = out, y
     return y if residual is None else (y, total)
 
 
 def quantize_rows(x, stream=None):
     """dt_quantize_rows: the rows x [...][d] as a Rows8 (a weight matrix, or a projection's input
     that comes from no norm)."""
-    vx, outer, inner, d, dtype = _row_view(x, "x")
-    handle = _raw_stream(stream, x.get_device())
+    dtype, dev = _TYPE16.get(x.dtype), x.get_device()
+    if dtype is None or dev < 0:
+        raise ValueError("x must be a bfloat16 or float16 CUDA tensor")
+    handle = _raw_stream(stream, dev)
+    vx, (outer, _, inner, _) = _rows(x, "x")
     codes, exps = _codes_like(x, stream)
-    _check(lib().dt_quantize_rows(vx, codes.data_ptr(), exps.data_ptr(), outer, inner, d, dtype, handle),
+    _check(lib().dt_quantize_rows(vx, codes.data_ptr(), exps.data_ptr(), outer, inner, x.shape[-1], dtype, handle),
            "dt_quantize_rows")
-    return Rows8(codes, exps)
+    return Rows8._made(codes, exps)
 
 
 class Projection:

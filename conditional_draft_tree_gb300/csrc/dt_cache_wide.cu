@@ -126,25 +126,6 @@ __device__ __forceinline__ void group_sync(int X) {
   asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + X) : "memory");
 }
 
-// packed pairs of fp32
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float *lo, float *hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // largest magnitudes of two pairs of 16-bit values (signs are not kept), NaN above all
 template <int DT>
 __device__ __forceinline__ uint32_t top_abs(uint32_t a, uint32_t b) {

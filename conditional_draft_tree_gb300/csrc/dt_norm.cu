@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "dt_cache.cuh"
 #include "dt_internal.h"
@@ -18,184 +19,383 @@ namespace dt {
 
 namespace {
 
+constexpr int kBlock = 0;      // a row's group of threads: the whole block
+
 struct NormArgs {
   const char *x, *res, *weight;
   char *total, *out;
   uint8_t *codes, *exps;
   int64_t xo, xi, ro, ri, to, ti, oo, oi;   // strides in bytes
+  const char *x_lo, *x_hi, *res_lo, *res_hi;   // where the views begin and end
   float offset, eps, inv_d;
   int rows, inner, d, norm;
 };
 
-// sums and largest magnitude bits over the group's threads; whole blocks go through shared
+// the larger magnitude (with some sign), NaN above all
+__device__ __forceinline__ float top_abs(float a, float b) {
+  float r;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// the sum and, TOP, the largest magnitude over the group's threads; whole blocks go through shared
 // memory, one slot a warp, twice so that a row's are not overwritten before all have read
 // the row before it
 template <int GROUP>
-__device__ __forceinline__ void reduce(float &sum, uint32_t &top, float (*s_sum)[32],
-                                       uint32_t (*s_top)[32], int &turn) {
-  constexpr int kIn = GROUP < 32 ? GROUP : 32;
+__device__ __forceinline__ void reduce(float &sum, float &top, bool with_top, float (*s_sum)[32],
+                                       float (*s_top)[32], int &turn) {
+  constexpr int kIn = GROUP == kBlock ? 32 : GROUP;
   const int lane = threadIdx.x & 31;
   const unsigned mask = kIn == 32 ? kFull : ((1u << kIn) - 1u) << (lane & ~(kIn - 1));
+  auto across = [&](int from, unsigned among) {
 #pragma unroll
-  for (int m = kIn / 2; m; m >>= 1) {
-    sum += __shfl_xor_sync(mask, sum, m);
-    top = max(top, __shfl_xor_sync(mask, top, m));
-  }
-  if (GROUP > 32) {
-    constexpr int kWarps = GROUP / 32;
-    const int warp = threadIdx.x >> 5;
+    for (int m = from; m; m >>= 1) sum += __shfl_xor_sync(among, sum, m);
+    if (with_top)
+#pragma unroll
+      for (int m = from; m; m >>= 1) top = top_abs(top, __shfl_xor_sync(among, top, m));
+  };
+  across(kIn / 2, mask);
+  if (GROUP == kBlock) {
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     if (lane == 0) {
       s_sum[turn][warp] = sum;
       s_top[turn][warp] = top;
     }
     __syncthreads();
-    sum = lane < kWarps ? s_sum[turn][lane] : 0.0f;
-    top = lane < kWarps ? s_top[turn][lane] : 0u;
+    sum = lane < warps ? s_sum[turn][lane] : 0.0f;
+    top = lane < warps ? s_top[turn][lane] : 0.0f;
     turn ^= 1;
-#pragma unroll
-    for (int m = (kWarps > 1 ? 16 : 0); m; m >>= 1) {
-      sum += __shfl_xor_sync(kFull, sum, m);
-      top = max(top, __shfl_xor_sync(kFull, top, m));
-    }
+    across(16, kFull);
   }
 }
 
-// GROUP threads a row, each with ITEMS chunks of 8 values: 16 bytes at a time (WIDE), or
-// value by value, neighbours in neighbouring threads.
-template <int DT, bool WIDE, int GROUP, int ITEMS>
-__global__ void __launch_bounds__(GROUP < 256 ? 256 : GROUP)
-rms_norm_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int kRows = GROUP < 256 ? 256 / GROUP : 1;        // rows of a block at a time
-  __shared__ float s_sum[2][32];
-  __shared__ uint32_t s_top[2][32];
-  const int lane = threadIdx.x % GROUP;
+// Sixteen bytes at g (on a 16-byte boundary), those outside [lo, hi) as zeros or left as they are: where
+// a tensor, or a row that is written, does not begin or end on such a boundary.
+__device__ __noinline__ uint4 load_end(const char *g, const char *lo, const char *hi) {
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (g + 2 * e >= lo && g + 2 * e < hi)
+      w[e / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(g + 2 * e)) << (16 * (e & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Granules that lie partly outside [lo, hi), those of the lanes that say so: one after the other, a
+// lane an element (a loop of one lane over its eight is as long as the rest of a row's work).
+__device__ __forceinline__ void store_ends(bool mine, char *g, const char *lo, const char *hi, const uint32_t (&w)[4]) {
+  const int lane = threadIdx.x & 31;
+  for (unsigned left = __ballot_sync(kFull, mine); left; left &= left - 1) {
+    const int from = __ffs(left) - 1;
+    uint32_t v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __shfl_sync(kFull, w[e], from);
+    char *to = reinterpret_cast<char *>(shfl64(reinterpret_cast<uint64_t>(g), from)) + 2 * lane;
+    const uint32_t word = lane & 4 ? (lane & 2 ? v[3] : v[2]) : (lane & 2 ? v[1] : v[0]);
+    if (lane < 8 && to >= lo && to < hi)
+      *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(word >> (16 * (lane & 1)));
+  }
+}
+__device__ __forceinline__ void store_codes_ends(bool mine, uint8_t *g, const uint8_t *lo, const uint8_t *hi, uint64_t w) {
+  const int lane = threadIdx.x & 31;
+  for (unsigned left = __ballot_sync(kFull, mine); left; left &= left - 1) {
+    const int from = __ffs(left) - 1;
+    const uint64_t v = shfl64(w, from);
+    uint8_t *to = reinterpret_cast<uint8_t *>(shfl64(reinterpret_cast<uint64_t>(g), from)) + lane;
+    if (lane < 8 && to >= lo && to < hi) *to = static_cast<uint8_t>(v >> (8 * (lane & 7)));
+  }
+}
+
+// the 16 bytes that begin `off` bytes (even, below 16; the same for a row's threads) into the 32 of a and
+// b. (Branches that the compiler keeps: as selections this takes three times the instructions.)
+__device__ __forceinline__ void shifted(const uint32_t *a, const uint32_t *b, int off, uint32_t (&r)[4]) {
+  const uint32_t w[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  const int half = off & 2 ? 16 : 0;
+  auto from = [&](auto k) {
+    asm volatile("");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __funnelshift_r(w[k.value + i], w[k.value + i + 1], half);
+  };
+  switch (off >> 2) {
+    case 0: from(std::integral_constant<int, 0>{}); break;
+    case 1: from(std::integral_constant<int, 1>{}); break;
+    case 2: from(std::integral_constant<int, 2>{}); break;
+    default: from(std::integral_constant<int, 3>{}); break;
+  }
+}
+
+__device__ __forceinline__ uint32_t up_one(uint32_t v) { return __shfl_up_sync(kFull, v, 1); }
+
+template <int DT>
+__device__ __forceinline__ uint64_t unpack2(uint32_t u) {
+  const float2 f = Half16<DT>::unpack(u);
+  return pair(f.x, f.y);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  float lo, hi;
+  unpair(v, &lo, &hi);
+  return Half16<DT>::pack(lo, hi);
+}
+
+constexpr int kSmall = 256;    // threads of a block whose rows have fewer than 32
+
+// GROUP threads a row (or the block's), each with ITEMS chunks of 8 values. WIDE: all rows lie on 16-byte boundaries,
+// chunks are loads and stores. Else each tensor's rows begin anywhere: a chunk is cut from the two
+// 16-byte granules that it lies in, and a granule of a result put together from a thread's chunk and
+// its left neighbour's; a warp's first lane has the chunk of the warp before it once more for that
+// (31 new chunks a warp). AHEAD: the next row is on its way while this one is worked on. Values
+// go in pairs through the two-wide fp32 instructions: with 8-bit codes there are some ten
+// instructions a value, and they, not memory, bounded the kernel.
+template <int DT, bool WIDE, int GROUP, int ITEMS, bool AHEAD, int REGS>
+__global__ void __maxnreg__(REGS) rms_norm_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int kRows = GROUP == kBlock ? 1 : kSmall / (GROUP == kBlock ? 1 : GROUP);   // of a block at a time
+  constexpr int kWords = WIDE ? 4 : 8;                        // of a chunk's loads
+  constexpr bool kPacked = ITEMS > 2;                         // the weights stay in 16 bits
+  __shared__ float s_sum[2][32], s_top[2][32];
+  const int group = GROUP == kBlock ? blockDim.x : GROUP;
+  const int lane = GROUP == kBlock ? threadIdx.x : threadIdx.x % (GROUP == kBlock ? 1 : GROUP);
+  const int mine = GROUP == kBlock ? 0 : threadIdx.x / (GROUP == kBlock ? 1 : GROUP);   // row of the block's
   int turn = 0;
-  auto at = [&](int it, int e) { return WIDE ? (it * GROUP + lane) * 8 + e : (it * 8 + e) * GROUP + lane; };
-  auto load = [&](const char *p, uint32_t (&w)[ITEMS][4]) {
+  // chunk number of an item; -1: none (the first lane of a row's first warp)
+  auto chunk = [&](int it) {
+    return WIDE ? it * group + lane : (it * (group >> 5) + (lane >> 5)) * 31 + (lane & 31) - 1;
+  };
+  const bool again = !WIDE && (lane & 31) == 0;               // its chunk counts for the warp before
+  const int chunks = (a.d + 7) >> 3;
+  // (bytes beside the row, but within the tensor's memory [lo, hi), may be read: words() drops them)
+  auto load = [&](const char *p, const char *lo, const char *hi, bool there, uint32_t (&w)[ITEMS][kWords]) {
+    const int off = WIDE ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+    const bool inside = p - 16 >= lo && p + 2 * a.d + 32 <= hi;      // (all rows but the first and the last)
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
-      if (WIDE) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (p && at(it, 0) < a.d) v = *reinterpret_cast<const uint4 *>(p + 2 * at(it, 0));
-        w[it][0] = v.x; w[it][1] = v.y; w[it][2] = v.z; w[it][3] = v.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t lo = 0, hi = 0;
-          if (p && at(it, 2 * e) < a.d) lo = *reinterpret_cast<const uint16_t *>(p + 2 * at(it, 2 * e));
-          if (p && at(it, 2 * e + 1) < a.d) hi = *reinterpret_cast<const uint16_t *>(p + 2 * at(it, 2 * e + 1));
-          w[it][e] = lo | (hi << 16);
+      const int c = chunk(it);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u), z = v;
+      if (there && c >= 0 && c < chunks) {
+        const char *g = p + 16 * c - off;
+        if (WIDE) {
+          v = *reinterpret_cast<const uint4 *>(g);
+        } else if (inside) {
+          v = *reinterpret_cast<const uint4 *>(g);
+          z = *reinterpret_cast<const uint4 *>(g + 16);
+        } else {
+          v = load_end(g, lo, hi);
+          z = load_end(g + 16, lo, hi);
         }
+      }
+      w[it][0] = v.x; w[it][1] = v.y; w[it][2] = v.z; w[it][3] = v.w;
+      if (!WIDE) {
+        w[it][kWords - 4] = z.x; w[it][kWords - 3] = z.y; w[it][kWords - 2] = z.z; w[it][kWords - 1] = z.w;
       }
     }
   };
-  auto store = [&](char *p, const float (&f)[ITEMS][8]) {
+  // a chunk's four words, zeros behind the row's end
+  auto words = [&](int it, const uint32_t (&w)[kWords], const char *p, uint32_t (&r)[4]) {
+    if (WIDE) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = w[e];
+    } else {
+      shifted(w, w + kWords - 4, static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u), r);
+      const int left = a.d - 8 * chunk(it);
+      if (left < 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = left > 2 * e + 1 ? r[e] : left > 2 * e ? r[e] & 0xffffu : 0u;
+      }
+    }
+  };
+  auto store = [&](char *p, int it, const uint32_t (&r)[4]) {
+    const int c = chunk(it);
+    if (WIDE) {
+      if (c < chunks) *reinterpret_cast<uint4 *>(p + 16 * c) = make_uint4(r[0], r[1], r[2], r[3]);
+    } else {
+      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+      const uint32_t left[4] = {up_one(r[0]), up_one(r[1]), up_one(r[2]), up_one(r[3])};
+      uint32_t g[4];
+      shifted(left, r, (16 - off) & 15, g);
+      const bool none = again || c > chunks || (c == chunks && !off), whole = c > 0 && c + 1 < chunks;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[e] = off ? g[e] : r[e];
+      char *to = p + 16 * c - off;
+      if (!none && whole) *reinterpret_cast<uint4 *>(to) = make_uint4(g[0], g[1], g[2], g[3]);
+      store_ends(!none && !whole, to, p, p + 2 * a.d, g);
+    }
+  };
+  // eight codes: bytes begin anywhere, a granule has eight
+  auto store8 = [&](uint8_t *p, int it, uint32_t lo, uint32_t hi) {
+    const int c = chunk(it);
+    if (WIDE) {
+      if (c < chunks) *reinterpret_cast<uint2 *>(p + 8 * c) = make_uint2(lo, hi);
+    } else {
+      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 7u);
+      const uint64_t left = up_one(lo) | (static_cast<uint64_t>(up_one(hi)) << 32);
+      const uint64_t mine = lo | (static_cast<uint64_t>(hi) << 32);
+      const bool none = again || c > chunks || (c == chunks && !off), whole = c > 0 && c + 1 < chunks;
+      const uint64_t g = off ? (left >> (64 - 8 * off)) | (mine << (8 * off)) : mine;
+      uint8_t *to = p + 8 * c - off;
+      if (!none && whole) *reinterpret_cast<uint64_t *>(to) = g;
+      store_codes_ends(!none && !whole, to, p, p + a.d, g);
+    }
+  };
+  // the group's row, and where it lies; rows follow at a fixed distance, without a division for each
+  struct Row {
+    int at, o, i;
+  };
+  const int stride = gridDim.x * kRows, outer_step = stride / a.inner, inner_step = stride - outer_step * a.inner;
+  auto next_of = [&](Row r) {
+    r.at += stride;
+    r.o += outer_step;
+    r.i += inner_step;
+    if (r.i >= a.inner) {
+      r.i -= a.inner;
+      ++r.o;
+    }
+    return r;
+  };
+  Row row;
+  row.at = blockIdx.x * kRows + mine;
+  row.o = row.at / a.inner;
+  row.i = row.at - row.o * a.inner;
+  uint32_t wx[ITEMS][kWords], wr[ITEMS][kWords], wg[ITEMS][4];
+  uint64_t gains[ITEMS][4];
+  auto place = [&](const char *p, int64_t outer, int64_t inner, const Row &r) { return p + r.o * outer + r.i * inner; };
+  auto fetch = [&](const Row &r) {
+    const bool there = r.at < a.rows;
+    load(place(a.x, a.xo, a.xi, r), a.x_lo, a.x_hi, there, wx);
+    if (a.res) load(place(a.res, a.ro, a.ri, r), a.res_lo, a.res_hi, there, wr);
+  };
+  if (AHEAD) fetch(row);
+  const uint64_t offset = pair(a.offset, a.offset);
+  auto gain = [&](int it, int e) { return kPacked && a.weight ? add2(unpack2<DT>(wg[it][e]), offset) : gains[kPacked ? 0 : it][kPacked ? 0 : e]; };
+  {
+    uint32_t w[ITEMS][kWords];
+    if (a.weight) load(a.weight, a.weight, a.weight + 2 * a.d, true, w);
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      if (a.weight) words(it, w[it], a.weight, wg[it]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        gains[it][e] = a.weight ? add2(unpack2<DT>(wg[it][e]), offset)
+                       : a.norm ? add2(pair(1.0f, 1.0f), offset) : pair(1.0f, 1.0f);
+    }
+  }
+  // the threads of a block go through as many rows each: the last ones may be none
+  for (; row.at - mine < a.rows; row = next_of(row)) {
+    if (!AHEAD) fetch(row);
+    uint64_t t[ITEMS][4];
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
       uint32_t w[4];
+      words(it, wx[it], place(a.x, a.xo, a.xi, row), w);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = Half16<DT>::pack(f[it][2 * e], f[it][2 * e + 1]);
-      if (WIDE) {
-        if (at(it, 0) < a.d) *reinterpret_cast<uint4 *>(p + 2 * at(it, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (at(it, e) < a.d)
-            *reinterpret_cast<uint16_t *>(p + 2 * at(it, e)) = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
-      }
+      for (int e = 0; e < 4; ++e) t[it][e] = unpack2<DT>(w[e]);
     }
-  };
-  const int stride = gridDim.x * kRows;
-  int row = blockIdx.x * kRows + threadIdx.x / GROUP;
-  uint32_t wx[ITEMS][4], wr[ITEMS][4], wg[ITEMS][4];
-  auto fetch = [&](int r) {
-    const int o = r / a.inner, i = r - o * a.inner;
-    load(r < a.rows ? a.x + o * a.xo + i * a.xi : nullptr, wx);
-    load(a.res && r < a.rows ? a.res + o * a.ro + i * a.ri : nullptr, wr);
-  };
-  fetch(row);
-  load(a.weight, wg);
-  // the threads of a block go through as many rows each: the last ones may be none
-  for (; row - static_cast<int>(threadIdx.x / GROUP) < a.rows; row += stride) {
-    float t[ITEMS][8], p[ITEMS][8];
-    float sum = 0.0f;
-    uint32_t top = 0;
-    // power: the rows of values whose squares leave fp32 are taken times 2^-80
-    auto products = [&](float power) {
-      sum = 0.0f;
-      top = 0;
+    if (a.res) {                       // (without one -0 stays -0)
+      char *total = const_cast<char *>(place(a.total, a.to, a.ti, row));
+      uint32_t w[ITEMS][4];
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it) {
+        words(it, wr[it], place(a.res, a.ro, a.ri, row), w[it]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[it][e] = add2(t[it][e], unpack2<DT>(w[it][e]));
+      }
+      if (AHEAD) fetch(next_of(row));
+      // the sum may take the place of x or the residual: for wide rows each thread writes what it alone
+      // has read, others' granules are written behind the reduction
+      if (WIDE && row.at < a.rows) {
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[it][e] = pack2<DT>(t[it][e]);
+          store(total, it, w[it]);
+        }
+      }
+    } else if (AHEAD) {
+      fetch(next_of(row));
+    }
+    const bool live = row.at < a.rows;
+    float sum, top;
+    auto reduce_row = [&]() {
+      uint64_t s = 0;
+      top = 0.0f;
 #pragma unroll
       for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float v = t[it][e] * power;
-          float g = 1.0f;
-          if (a.weight) {
-            const float2 f = Half16<DT>::unpack(wg[it][e / 2]);
-            g = a.offset + (e & 1 ? f.y : f.x);
-          } else {
-            g = a.norm ? a.offset + 1.0f : 1.0f;
+        for (int e = 0; e < 4; ++e) s = fma2(t[it][e], t[it][e], s);
+      if (a.codes) {
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            unpair(mul2(t[it][e], gain(it, e)), &lo, &hi);
+            top = top_abs(top_abs(top, lo), hi);
           }
-          p[it][e] = v * g;
-          sum += v * v;
-          top = max(top, __float_as_uint(p[it][e]) & 0x7fffffffu);
-        }
-    };
-#pragma unroll
-    for (int it = 0; it < ITEMS; ++it)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 x = Half16<DT>::unpack(wx[it][e]), r = Half16<DT>::unpack(wr[it][e]);
-        t[it][2 * e] = a.res ? x.x + r.x : x.x;      // (-0 stays -0)
-        t[it][2 * e + 1] = a.res ? x.y + r.y : x.y;
       }
-    const int here = row;
-    fetch(row + stride);
-    products(1.0f);
-    reduce<GROUP>(sum, top, s_sum, s_top, turn);
+      float lo, hi;
+      unpair(s, &lo, &hi);
+      sum = again ? 0.0f : lo + hi;
+      reduce<GROUP>(sum, top, a.codes != nullptr, s_sum, s_top, turn);
+    };
+    reduce_row();
+    if (a.res && !WIDE && live) {
+      char *total = const_cast<char *>(place(a.total, a.to, a.ti, row));
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack2<DT>(t[it][e]);
+        store(total, it, w);
+      }
+    }
     float scale = 1.0f;
     if (a.norm) {
-      if (!(sum <= 0x1p100f)) {
-        products(0x1p-80f);
-        reduce<GROUP>(sum, top, s_sum, s_top, turn);
-        scale = rsqrtf(sum * a.inv_d);     // eps 2^-160 is nothing beside a mean above 2^-75
+      if (!(sum <= 0x1p100f)) {          // squares that leave fp32: the row times 2^-80
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[it][e] = mul2(t[it][e], pair(0x1p-80f, 0x1p-80f));
+        reduce_row();
+        scale = rsqrtf(sum * a.inv_d);   // eps 2^-160 is nothing beside a mean above 2^-75
       } else {
         scale = rsqrtf(sum * a.inv_d + a.eps);
       }
     }
-    if (here >= a.rows) continue;
-    const int o = here / a.inner, i = here - o * a.inner;
-    if (a.total) store(a.total + o * a.to + i * a.ti, t);
+    if (!live) continue;                 // a whole group: no other lane of it is left behind
+    const uint64_t scales = pair(scale, scale);
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p[it][e] *= scale;
-    if (a.out) store(a.out + o * a.oo + i * a.oi, p);
-    if (!a.codes) continue;
-    const uint32_t most = __float_as_uint(__uint_as_float(top) * scale) & 0x7fffffffu;
-    const bool whole = most < 0x7f800000u;
-    const int ex = row_exponent(__uint_as_float(most));
-    const float down = exp2i(-ex);
-    if (lane == 0) a.exps[here] = static_cast<uint8_t>(whole ? ex + 127 : 255);
-    uint8_t *codes = a.codes + static_cast<int64_t>(here) * a.d;
-    const float bound = ex == 120 ? 240.0f * 0x1p120f : __int_as_float(0x7f800000);
+      for (int e = 0; e < 4; ++e) t[it][e] = mul2(mul2(t[it][e], gain(it, e)), scales);
+    if (a.out) {
+      char *out = const_cast<char *>(place(a.out, a.oo, a.oi, row));
 #pragma unroll
-    for (int it = 0; it < ITEMS; ++it) {
-      uint32_t w[2];
+      for (int it = 0; it < ITEMS; ++it) {
+        uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        float f[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) f[z] = fminf(fmaxf(p[it][e + z], -bound), bound) * down;
-        const uint32_t y = e4m3_pack2(f[0], f[1]) | (e4m3_pack2(f[2], f[3]) << 16);
-        w[e / 4] = whole ? y : 0x7f7f7f7fu;
+        for (int e = 0; e < 4; ++e) w[e] = pack2<DT>(t[it][e]);
+        store(out, it, w);
       }
-      if (WIDE) {
-        if (at(it, 0) < a.d) *reinterpret_cast<uint2 *>(codes + at(it, 0)) = make_uint2(w[0], w[1]);
-      } else {
+    }
+    if (a.codes) {
+      const uint32_t most = __float_as_uint(fabsf(top) * scale) & 0x7fffffffu;
+      const bool whole = most < 0x7f800000u;
+      const int ex = row_exponent(__uint_as_float(most));
+      const float down = exp2i(-ex);
+      if (lane == 0) a.exps[row.at] = static_cast<uint8_t>(whole ? ex + 127 : 255);
+      uint8_t *codes = a.codes + static_cast<int64_t>(row.at) * a.d;
+      const bool clamp = ex == 120;      // 256 2^120 is no finite bf16 number
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (at(it, e) < a.d) codes[at(it, e)] = static_cast<uint8_t>(w[e / 4] >> (8 * (e & 3)));
+      for (int it = 0; it < ITEMS; ++it) {
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float lo, hi;
+          unpair(mul2(t[it][e], pair(down, down)), &lo, &hi);
+          if (clamp) {
+            lo = fminf(fmaxf(lo, -240.0f), 240.0f);
+            hi = fminf(fmaxf(hi, -240.0f), 240.0f);
+          }
+          y[e] = e4m3_pack2(lo, hi);
+        }
+        store8(codes, it, whole ? y[0] | (y[1] << 16) : 0x7f7f7f7fu, whole ? y[2] | (y[3] << 16) : 0x7f7f7f7fu);
       }
     }
   }
@@ -203,25 +403,42 @@ rms_norm_kernel(const __grid_constant__ NormArgs a) {
 
 template <int DT, bool WIDE>
 cudaError_t launch_norm(const NormArgs &a, int sms, cudaStream_t st) {
-  auto go = [&](auto kernel, int group) {
-    const int threads = group < 256 ? 256 : group, rows = threads / group;
+  // as many blocks as run at once (65536 registers an SM), or fewer
+  auto go = [&](auto kernel, int threads, int rows, int regs) {
     const int64_t blocks = (static_cast<int64_t>(a.rows) + rows - 1) / rows;
-    const int64_t most = static_cast<int64_t>(sms) * (1024 / threads);
+    const int64_t most = static_cast<int64_t>(sms) * std::max(1, std::min(16, 65536 / (threads * regs)));
     kernel<<<static_cast<unsigned>(std::min(blocks, most)), threads, 0, st>>>(a);
     return cudaGetLastError();
   };
-  if (a.d <= 64) return go(rms_norm_kernel<DT, WIDE, 8, 1>, 8);
-  if (a.d <= 128) return go(rms_norm_kernel<DT, WIDE, 16, 1>, 16);
-  if (a.d <= 256) return go(rms_norm_kernel<DT, WIDE, 32, 1>, 32);
-  if (a.d <= 512) return go(rms_norm_kernel<DT, WIDE, 32, 2>, 32);
-  if (a.d <= 2048) return go(rms_norm_kernel<DT, WIDE, 256, 1>, 256);
-  if (a.d <= 4096) return go(rms_norm_kernel<DT, WIDE, 256, 2>, 256);
-  if (a.d <= 8192) return go(rms_norm_kernel<DT, WIDE, 512, 2>, 512);
-  if (a.d <= 16384) return go(rms_norm_kernel<DT, WIDE, 1024, 2>, 1024);
-  return go(rms_norm_kernel<DT, WIDE, 1024, 4>, 1024);
+  const int chunks = (a.d + 7) / 8;
+  if constexpr (WIDE) {
+    if (chunks <= 8) return go(rms_norm_kernel<DT, true, 8, 1, true, 48>, kSmall, kSmall / 8, 48);
+    if (chunks <= 16) return go(rms_norm_kernel<DT, true, 16, 1, true, 48>, kSmall, kSmall / 16, 48);
+    if (chunks <= 32) return go(rms_norm_kernel<DT, true, 32, 1, true, 48>, kSmall, kSmall / 32, 48);
+    if (chunks <= 64) return go(rms_norm_kernel<DT, true, 32, 2, true, 80>, kSmall, kSmall / 32, 80);
+    if (chunks <= 1024) return go(rms_norm_kernel<DT, true, kBlock, 2, true, 80>, (chunks + 63) / 64 * 32, 1, 80);
+    if (chunks <= 2048) return go(rms_norm_kernel<DT, true, kBlock, 4, true, 128>, (chunks + 127) / 128 * 32, 1, 128);
+    return go(rms_norm_kernel<DT, true, kBlock, 4, false, 64>, (chunks + 127) / 128 * 32, 1, 64);
+  } else {
+    // 31 chunks a warp and item, and one for a row's last granule
+    const int need = chunks + 1;
+    if (need <= 31) return go(rms_norm_kernel<DT, false, 32, 1, true, 64>, kSmall, kSmall / 32, 64);
+    if (need <= 62) return go(rms_norm_kernel<DT, false, 32, 2, true, 112>, kSmall, kSmall / 32, 112);
+    if (need <= 992) return go(rms_norm_kernel<DT, false, kBlock, 2, false, 80>, (need + 61) / 62 * 32, 1, 80);
+    if (need <= 1984) return go(rms_norm_kernel<DT, false, kBlock, 4, false, 128>, (need + 123) / 124 * 32, 1, 128);
+    return go(rms_norm_kernel<DT, false, kBlock, 5, false, 64>, (need + 154) / 155 * 32, 1, 64);
+  }
 }
 
 bool al2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+// the bytes that a view of rows of d values spans
+void view_span(const dt_rows *v, int outer, int inner, int d, const char **lo, const char **hi) {
+  const int64_t o = 2 * v->stride_outer * (outer - 1), i = 2 * v->stride_inner * (inner - 1), zero = 0;
+  const char *p = static_cast<const char *>(v->data);
+  *lo = p + std::min(o, zero) + std::min(i, zero);
+  *hi = p + std::max(o, zero) + std::max(i, zero) + 2 * static_cast<int64_t>(d);
+}
 
 // strides into bytes; whether the view's rows lie on 16-byte boundaries
 bool view_wide(const dt_rows *v, int64_t *outer, int64_t *inner) {
@@ -246,7 +463,9 @@ int norm_rows(const dt_rows *x, const dt_rows *residual, const dt_rows *total, c
   a.x = static_cast<const char *>(x->data);
   bool wide = view_wide(x, &a.xo, &a.xi) && d % 8 == 0 &&
               (reinterpret_cast<uintptr_t>(weight) & 15u) == 0 && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0;
+  view_span(x, outer, inner, d, &a.x_lo, &a.x_hi);
   if (residual) {
+    view_span(residual, outer, inner, d, &a.res_lo, &a.res_hi);
     a.res = static_cast<const char *>(residual->data);
     a.total = static_cast<char *>(total->data);
     wide = view_wide(residual, &a.ro, &a.ri) && wide;

@@ -82,6 +82,15 @@ template <> struct Half16<DT_F16> {
   }
 };
 
+// largest magnitudes of two pairs of 16-bit values (signs are not kept), NaN above all
+template <int DT>
+__device__ __forceinline__ uint32_t top_abs(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (DT == DT_BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // ------------------------------------------------------------- 8-bit rows
 
 // 2^e as fp32, e in [-126, 127]

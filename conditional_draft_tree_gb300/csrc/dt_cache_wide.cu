@@ -126,14 +126,6 @@ __device__ __forceinline__ void group_sync(int X) {
   asm volatile("barrier.cta.sync %0, 128;" ::"r"(2 + X) : "memory");
 }
 
-// largest magnitudes of two pairs of 16-bit values (signs are not kept), NaN above all
-template <int DT>
-__device__ __forceinline__ uint32_t top_abs(uint32_t a, uint32_t b) {
-  uint32_t r;
-  if (DT == DT_BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 // instruction descriptor of kind::f16, M = 128, fp32 accumulation; mn: B is MN-major
 template <int DT>
 __device__ __forceinline__ uint32_t idesc16(int N, bool mn) {

@@ -63,9 +63,11 @@ struct ListScratch {
 };
 
 struct Small {                    // behind the ring
-  uint64_t full[kMaxStages], empty[kMaxStages], u_go[kMaxStages], u_full[kMaxStages];
+  uint64_t full[kMaxStages], empty[kMaxStages], u_go[kMaxStages], up_full[kMaxStages], u_full[kMaxStages];
   uint64_t acc_full[2], acc_empty[2], list_full[2], list_empty[2], idle;
   AdapterList list[2];
+  uint32_t odd[2][kOuts][kMaxTokens / 32];   // of each row of W's tile: adapters whose B row is not all finite
+  int any_odd[2];
   ListScratch scratch;
   int16_t token_slot[kMaxTokens];
   alignas(16) int xexp[4 * kGroups][kMaxTokens];   // exponents of the tile's rows of x, as bits of fp32; one copy a warp
@@ -337,6 +339,23 @@ struct Shares {
   }
 };
 
+// whether one of two pairs' halves has all exponent bits set (of magnitudes; `m` of top_abs)
+template <int DT>
+__device__ __forceinline__ bool not_finite(uint32_t m) {
+  constexpr uint32_t kExp = DT == DT_BF16 ? 0x7f807f80u : 0x7c007c00u, kOne = DT == DT_BF16 ? 0x00800080u : 0x04000400u;
+  return (((m & kExp) + kOne) & 0x80008000u) != 0u;       // a full exponent carries into the sign's place
+}
+// such values set to zero
+template <int DT>
+__device__ __noinline__ void make_finite(uint4 *p) {
+  constexpr uint32_t kExp = DT == DT_BF16 ? 0x7f80u : 0x7c00u;
+  uint32_t *w = reinterpret_cast<uint32_t *>(p);
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & kExp) == kExp) w[i] &= 0xffff0000u;
+    if (((w[i] >> 16) & kExp) == kExp) w[i] &= 0xffffu;
+  }
+}
+
 template <int DT>
 __device__ __forceinline__ uint16_t round16(float v) {
   return static_cast<uint16_t>(Half16<DT>::pack(v, 0.0f));
@@ -555,17 +574,21 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       mbar_init(&ss.full[i], 1);
       mbar_init(&ss.empty[i], 1);
       mbar_init(&ss.u_go[i], 1);
+      mbar_init(&ss.up_full[i], 1);
       mbar_init(&ss.u_full[i], 128 * CG);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ss.acc_full[i], 1);
       mbar_init(&ss.acc_empty[i], kDrain * CG);
       mbar_init(&ss.list_full[i], 128);
-      mbar_init(&ss.list_empty[i], E8 ? 2 + kDrain / 32 : 2);
+      mbar_init(&ss.list_empty[i], 2 + kDrain / 32);
+      ss.any_odd[i] = 0;
     }
     mbar_init(&ss.idle, 1);
     ss.fail = 0;
   }
+  if (AD)
+    for (int i = tid; i < 2 * kOuts * (kMaxTokens / 32); i += blockDim.x) (&ss.odd[0][0][0])[i] = 0u;
   if (warp == kDrain / 32 + 1) tmem_take<CG>(&ss.tmem);
   tmem_fence_before();
   __syncthreads();
@@ -591,7 +614,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
 
   if (warp == kDrain / 32) {
     Place p = {0, 0};
-    uint32_t issued = 0;
+    uint32_t issued = 0, ups = 0, flying = 0;   // up_full's phases; stages that it counts last
     bool go = true;
     for (int t = first, i = 0; t < w.tiles && go; t += step, ++i) {
       const int o0 = (t % w.tiles_o * CG + pair) * w.outs, x0 = t / w.tiles_o * w.nt + pair * mine;
@@ -604,6 +627,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
           tma_2d<CG>(to, &wmap, s * kValues, o0, bar);
           tma_2d<CG>(to + kSlabA, &xmap, s * kValues, x0, bar);
         }
+        flying &= ~(1u << p.at);
         p.step(w.stages);
         ++issued;
       }
@@ -613,28 +637,36 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       const int all = sixteens_of(l), per = a.rank >> 4, wide = w.piece >> 4;
       int q0, q1;
       share(all, &q0, &q1);
+      int u = 4 * q0 / per, j = 4 * q0 - u * per;        // adapter, and the sixteen of its rank
       for (int q = q0; q < q1; ++q) {
         if (!(go = wait(&ss.empty[p.at], p.parity ^ 1u))) break;
         if (issuer) mbar_arrive(&ss.u_go[p.at]);
         unsigned char *to = sm + p.at * stage;
-        const uint32_t bar = first_block(&ss.full[p.at]);
+        const uint32_t bar = smem_u32(&ss.up_full[p.at]);
         const int here = min(4, all - 4 * q);
         if (issuer) {
-          if (pair == 0) mbar_expect_tx(&ss.full[p.at], CG * here * w.outs * 32);
-          for (int k = 0; k < here; k += wide) {
-            const int u = (4 * q + k) / per, j = (4 * q + k - u * per) * 16;
-            tma_2d<CG>(to + k * kOuts * 32, &umap, j, l.ids[u] * a.O + o0, bar);
-          }
+          if (pair == 0) mbar_arrive(&ss.full[p.at]);     // (it counts the ring's turns)
+          mbar_expect_tx(&ss.up_full[p.at], here * w.outs * 32);
         }
+        for (int k = 0; k < here; k += wide) {
+          if (issuer) tma_2d<CG>(to + k * kOuts * 32, &umap, 16 * j, l.ids[u] * a.O + o0, bar);
+          if ((j += wide) == per) j = 0, ++u;
+        }
+        ups ^= 1u << p.at;
+        flying |= 1u << p.at;
         p.step(w.stages);
         ++issued;
       }
       __syncwarp();
       if (issuer) mbar_arrive(&ss.list_empty[i & 1]);
     }
-    if (*fail && pair == 0 && lane == 0)    // nothing may land in memory that the block has given up
-      for (uint32_t k = issued > static_cast<uint32_t>(w.stages) ? issued - w.stages : 0; k < issued; ++k)
-        mbar_wait_cycles(&ss.full[k % w.stages], (k / w.stages) & 1u);
+    if (*fail && lane == 0) {               // nothing may land in memory that the block has given up
+      if (pair == 0)
+        for (uint32_t k = issued > static_cast<uint32_t>(w.stages) ? issued - w.stages : 0; k < issued; ++k)
+          mbar_wait_cycles(&ss.full[k % w.stages], (k / w.stages) & 1u);
+      for (int k = 0; k < w.stages; ++k)
+        if ((flying >> k) & 1u) mbar_wait_cycles(&ss.up_full[k], ((ups >> k) & 1u) ^ 1u);
+    }
   } else if (warp == kDrain / 32 + 1) {
     const uint32_t idesc = descriptor<DT, E8>(kOuts * CG, w.nt), idesc16 = descriptor<DT, false>(kOuts * CG, w.nt);
     Place p = {0, 0};
@@ -679,15 +711,18 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
             phases ^= 1u << p.at;
             tmem_fence_after();
             const uint32_t at = smem_u32(sm) + p.at * stage;
-            const int here = issuer ? min(4, all - 4 * q) : 0;
-            for (int k = 0; k < here; ++k) {
-              const int first_of = k & ~(wide - 1), in = 2 * (k - first_of);     // of its piece; 32 bytes on
-              mma<CG, false>(to, rows_of(at + first_of * kOuts * 32, w.piece) + in,
-                             rows_of(at + kSlabA + first_of * mine * 32, w.piece) + in, idesc16,
-                             !E8 || q > q0 || k > 0);
+            const int here = min(4, all - 4 * q);
+            const uint64_t da = rows_of(at, w.piece), db = rows_of(at + kSlabA, w.piece);
+            if (issuer) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int first_of = k & ~(wide - 1), in = 2 * (k - first_of);     // of its piece; 32 bytes on
+                if (k < here)
+                  mma<CG, false>(to, da + first_of * kOuts * 2 + in, db + first_of * mine * 2 + in, idesc16,
+                                 !E8 || q > q0 || k > 0);
+              }
+              commit<CG>(&ss.empty[p.at]);
             }
-            if (issuer) commit<CG>(&ss.empty[p.at]);
-            __syncwarp();
             p.step(w.stages);
           }
           if (!go) break;
@@ -703,11 +738,17 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
   } else if (AD && tid >= kDrain + 64) {
     const int id = tid - kDrain - 64;
     uint32_t at = 0, phases = 0;               // stage of the ring; phases of u_go
+    bool marked[2] = {false, false};           // this thread's row of ss.odd has something
     // (these warps meet for the lists: they go through all tiles, whatever has failed)
     for (int t = first, i = 0; t < w.tiles; t += step, ++i) {
       AdapterList &l = ss.list[i & 1];
       const int tt = t / w.tiles_o * w.nt, x0 = tt + pair * mine;
       bool go = wait(&ss.list_empty[i & 1], ((i >> 1) & 1) ^ 1);
+      if (marked[i & 1]) {
+        for (int k = 0; k < kMaxTokens / 32; ++k) ss.odd[i & 1][id][k] = 0u;
+        ss.any_odd[i & 1] = 0;
+        marked[i & 1] = false;
+      }
       list_adapters(a, tt, min(tt + w.nt, a.rows), l, ss.scratch, id, 1);
       mbar_arrive(&ss.list_full[i & 1]);
       if (i == 0) cudaGridDependencySynchronize();        // u is there
@@ -725,22 +766,26 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       }
       at = (at + (k1 - k0)) % w.stages;
       uint4 v[2][4][2];
+      int of = 4 * q0 / per, j = 4 * q0 - of * per, whose[4];   // adapter and sixteen of its rank to be fetched
       auto fetch = [&](int q) {                // loads of the next stage's rows, before there is room
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int z = 0; z < 4; ++z) {
+          whose[z] = 4 * q + z < all ? of : -2;
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int at16 = 4 * q + z, s = at16 / per, j = (at16 - s * per) * 16;
+          for (int k = 0; k < 2; ++k) {
             v[k][z][0] = v[k][z][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (at16 < all && s == slot[k]) {
-              v[k][z][0] = *reinterpret_cast<const uint4 *>(u[k] + j);
-              v[k][z][1] = *reinterpret_cast<const uint4 *>(u[k] + j + 8);
+            if (whose[z] == slot[k]) {
+              v[k][z][0] = *reinterpret_cast<const uint4 *>(u[k] + 16 * j);
+              v[k][z][1] = *reinterpret_cast<const uint4 *>(u[k] + 16 * j + 8);
             }
           }
+          if (++j == per) j = 0, ++of;
+        }
       };
       if (q0 < q1) fetch(q0);
       for (int q = q0; q < q1 && go; ++q) {
-        if (!(go = wait(&ss.u_go[at], (phases >> at) & 1u))) break;
+        const uint32_t parity = (phases >> at) & 1u;
+        if (!(go = wait(&ss.u_go[at], parity))) break;
         phases ^= 1u << at;
         unsigned char *to = sm + at * stage + kSlabA;
 #pragma unroll
@@ -755,10 +800,46 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
             *reinterpret_cast<uint4 *>(row + 16 * ((c + 1) ^ turn)) = v[k][z][1];
           }
         }
+        int looked[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) looked[z] = whose[z];
+        __syncwarp();
+        if (q + 1 < q1) fetch(q + 1);          // (on its way while this stage's B_a is looked through)
+        // B_a's rows stand beside zeros of other requests' rows: what is not finite there would reach them.
+        // A thread looks through a row, takes such values out, and notes whose they are; the
+        // output is NaN for the rows with that adapter.
+        go = wait(&ss.up_full[at], parity);
+        if (go && id < w.outs) {
+          unsigned char *row = sm + at * stage + id * row_bytes;
+          const int turn = (id >> shift) & (chunks - 1);
+          uint4 *half[4][2];
+          uint32_t most[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int c = 2 * z & (chunks - 1);
+            unsigned char *piece = row + (2 * z - c) * kOuts * 16;
+            half[z][0] = reinterpret_cast<uint4 *>(piece + 16 * (c ^ turn));
+            half[z][1] = reinterpret_cast<uint4 *>(piece + 16 * ((c + 1) ^ turn));
+            const uint4 lo = *half[z][0], hi = *half[z][1];
+            most[z] = top_abs<DT>(top_abs<DT>(top_abs<DT>(lo.x, lo.y), top_abs<DT>(lo.z, lo.w)),
+                                  top_abs<DT>(top_abs<DT>(hi.x, hi.y), top_abs<DT>(hi.z, hi.w)));
+          }
+          if (not_finite<DT>(top_abs<DT>(top_abs<DT>(most[0], most[1]), top_abs<DT>(most[2], most[3])))) {
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              if (looked[z] >= 0 && not_finite<DT>(most[z])) {
+                make_finite<DT>(half[z][0]);
+                make_finite<DT>(half[z][1]);
+                ss.odd[i & 1][id][looked[z] >> 5] |= 1u << (looked[z] & 31);
+                ss.any_odd[i & 1] = 1;
+                marked[i & 1] = true;
+              }
+          }
+        }
+        __syncwarp();
         fence_async_smem();
         arrive_first(&ss.u_full[at]);
         __syncwarp();
-        if (q + 1 < q1) fetch(q + 1);
         if (++at == static_cast<uint32_t>(w.stages)) at = 0;
       }
     }
@@ -775,8 +856,6 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         int q0 = 0, q1 = 0;
         if (go) share(sixteens_of(ss.list[i & 1]), &q0, &q1);
         both = q0 < q1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ss.list_empty[i & 1]);
       }
       const int rows = min(w.nt, a.rows - t0);
       // 8-bit rows: 2^wexp of this output times 2^xexp of the rows of x, in one number where that
@@ -825,15 +904,15 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       const int sixteens = w.nt / 16;
       if (go && group < sixteens) fetch(shares.turn(group, w.nt));
 #pragma unroll 1
-      for (int i = group; i < sixteens && go; i += kGroups) {
-        const int c = shares.turn(i, w.nt);
+      for (int part = group; part < sixteens && go; part += kGroups) {
+        const int c = shares.turn(part, w.nt);
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           v[e] = next[e];
           if (AD && E8) z[e] = next_z[e];
         }
-        if (i + kGroups < sixteens) fetch(shares.turn(i + kGroups, w.nt));
+        if (part + kGroups < sixteens) fetch(shares.turn(part + kGroups, w.nt));
         if (E8) {
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
@@ -841,10 +920,18 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
             const int bits[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              if (far) v[e + k] = times_power(v[e + k], wexp + (bits[k] >> 23));
+              if (__builtin_expect(far, 0)) v[e + k] = times_power(v[e + k], wexp + (bits[k] >> 23));
               else v[e + k] *= __int_as_float(wbits + bits[k]);
               if (AD && both) v[e + k] += z[e + k];
             }
+          }
+        }
+        if (AD && __builtin_expect(ss.any_odd[i & 1], 0)) {
+          const AdapterList &l = ss.list[i & 1];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int of = c + e < rows ? l.slot[(t0 + c + e) / a.n - l.first] : -1;
+            if (of >= 0 && ((ss.odd[i & 1][row][of >> 5] >> (of & 31)) & 1u)) v[e] = __int_as_float(0x7fffffff);
           }
         }
         if (split > 1) shares.push(c, v);
@@ -852,6 +939,10 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       }
       tmem_fence_before();
       arrive_first(&ss.acc_empty[buf]);
+      if (AD) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ss.list_empty[i & 1]);
+      }
       if (split > 1) {
         cluster_sync();
         shares.sum(sm, w.nt, group, kGroups, put);
@@ -1106,7 +1197,8 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
       (reinterpret_cast<uintptr_t>(y) & 1u) || (reinterpret_cast<uintptr_t>(status) & 3u) ||
       batch < 1 || batch > 65535 || n < 1 || static_cast<int64_t>(batch) * n > (1 << 24) ||
       !(dtype == DT_BF16 || dtype == DT_F16) || !(w->dtype == dtype || w->dtype == DT_E4M3) ||
-      w->K < 16 || w->K > 65536 || w->K % 16 || w->O < 1 || w->O > (1 << 24))
+      w->K < 16 || w->K > 65536 || w->K % 16 || w->O < 1 || w->O > (1 << 24) ||
+      static_cast<int64_t>(batch) * n * w->O > (int64_t{1} << 38))
     return DT_ERR_INVALID_ARG;
   const bool e8 = w->dtype == DT_E4M3;
   const int64_t size = e8 ? 1 : 2, rows = static_cast<int64_t>(batch) * n, most = int64_t{1} << 32;

@@ -559,7 +559,8 @@ int dt_quantize_rows(const dt_rows *x, uint8_t *codes, uint8_t *exps, int outer,
  * the second term only where 0 <= a < adapters->count (a negative index: no adapter; one at or
  * above count: none, and DT_ERR_BAD_INDEX in *status). Products are accumulated in fp32; x A^T, times
  * the scale, is rounded to dtype (and so overflows where dtype does) before the
- * product with B, y once.
+ * product with B, y once. A row of B with a value that is not finite makes that output NaN for
+ * the rows with that adapter; what is not finite elsewhere reaches the rows that use it alone.
  *   w      W [O][K], dtype 16-bit or DT_E4M3 with exps [O] (8-bit rows); data 16-byte
  *          aligned, row stride ld elements, a multiple of 16 bytes
  *   x      [batch n][K] rows, of w's type: dtype itself, or 8-bit rows with x_exps
@@ -573,7 +574,7 @@ int dt_quantize_rows(const dt_rows *x, uint8_t *codes, uint8_t *exps, int outer,
  *   index  [batch] int32; with adapters only
  *   status one int32 of the caller's, zeroed once: DT_ERR_BAD_INDEX, DT_ERR_TIMEOUT
  * K: a multiple of 16 in [16, 65536]; O in [1, 2^24]; rank: a multiple of 16 in [16, 128];
- * batch in [1, 65535], batch n <= 2^24. workspace: dt_project_workspace_bytes bytes,
+ * batch in [1, 65535], batch n <= 2^24, batch n O <= 2^38. workspace: dt_project_workspace_bytes bytes,
  * 256-byte aligned, for x A^T (may be 0: NULL without adapters); the size for a batch, n and
  * rank serves smaller ones. Sums run in an order fixed by the sizes: results repeat. */
 typedef struct {

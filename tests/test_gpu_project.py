@@ -228,3 +228,35 @@ def test_after_the_norm(e8):
     low = (c.index, y.cpu().view(-1, K), c.down, c.up, c.scale)
     ref = R.project(vx, vw, n, *low)
     near(got.reshape(-1, O), ref, R.project_slack(vx, vw, n, ref, dtype, *low))
+
+
+@pytest.mark.parametrize("dtype,e8", KINDS)
+@pytest.mark.parametrize("batch,n,K,O,rank,count", [
+    (6, 1, 128, 150, 16, 3), (40, 1, 1040, 300, 32, 9), (130, 1, 96, 140, 48, 130), (5, 45, 256, 513, 64, 3),
+    (2, 128, 144, 513, 128, 2), (33, 65, 320, 4100, 16, 5), (256, 1, 64, 90, 16, 256)])
+def test_an_adapter_that_is_not_finite_stays_with_its_requests(batch, n, K, O, rank, count, dtype, e8):
+    """B rows with infinities and NaN: those outputs are NaN for the rows with that adapter, and all others
+    what they were. The same for A, whose adapter's rows are not finite as a whole."""
+    c = Case(batch, n, K, O, rank, count, dtype, e8, seed=7)
+    p, x, ad, index, x16 = c.cuda()
+    want = dt.project(p, x, ad, index, x16, dtype=dtype)
+    used = sorted(set(int(a) for a in c.index.tolist() if a >= 0))
+    one, two = used[0], used[-1]
+    g = torch.Generator().manual_seed(8)
+    bad = torch.zeros(batch, n, O, dtype=torch.bool)
+    for a, value in ((one, float("nan")), (two, float("inf")), (two, -float("inf"))):
+        rows = torch.randperm(O, generator=g)[:max(1, O // 9)]
+        for o in rows.tolist():
+            ad.up[a, o, int(torch.randint(0, rank, (1,), generator=g))] = value
+        bad[(c.index == a).nonzero()[:, 0][:, None], :, rows[None]] = True
+    bad = bad.cuda()
+    for _ in range(2):
+        got = dt.project(p, x, ad, index, x16, dtype=dtype)
+        assert bool(got[bad].isnan().all()) and torch.equal(got[~bad], want[~bad])
+    ad.up.copy_(c.up)
+    assert torch.equal(dt.project(p, x, ad, index, x16, dtype=dtype), want)      # nothing is left of it
+    ad.down[one, rank // 2, K // 3] = float("nan")
+    whole = (index == one)[:, None, None].expand(batch, n, O)
+    got = dt.project(p, x, ad, index, x16, dtype=dtype)
+    assert bool(got[whole].isnan().all()) and torch.equal(got[~whole], want[~whole])
+    p.check()

@@ -1138,7 +1138,7 @@ def project(projection: Projection, x, adapters: Adapters | None = None, index=N
     kind = _TYPE16.get(dtype)
     if kind is None:
         raise ValueError("dtype must be bfloat16 or float16")
-    ldx16, set_struct = 0, None
+    ldx16, set_struct, indexes = 0, None, _ints(index, "index", (batch,), dev)
     if adapters is not None:
         if adapters._dev != dev or adapters._type != kind or adapters.K != K or adapters.O != p.O:
             raise ValueError("the adapters must match the weight's sizes and device and the result's type")
@@ -1162,8 +1162,7 @@ def project(projection: Projection, x, adapters: Adapters | None = None, index=N
         raise ValueError("out must be [batch][n][O] of the result's type, on the weight's device")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().dt_project(p._struct, t.data_ptr(), _flat_rows(t, "x", batch, n), _ptr(exps), batch, n, kind,
-                            set_struct, _ints(index, "index", (batch,), dev),
-                            x16.data_ptr() if ldx16 else None, ldx16, out.data_ptr(),
+                            set_struct, indexes, x16.data_ptr() if ldx16 else None, ldx16, out.data_ptr(),
                             _flat_rows(out, "out", batch, n), p.status.data_ptr(), _ptr(workspace), ws_bytes,
                             handle), "dt_project")
     return out

@@ -28,6 +28,14 @@
         committed behind the prefix. T = bf16 (default), fp16 or e4m3; 32 query
         heads, 8 key/value heads, dh 128, pages of 64 rows, prefixes of 512 to
         1024 rows, synthetic Q/K/V.
+    python -m conditional_draft_tree_gb300.profile_cases layer [--reps R] [--cfg C] [--cache T]
+        The same round with what a served layer has around it: pages for the trees' rows
+        (page tables from the lengths, the rows' places and positions), the norm with the
+        residual's addition, the projection to queries, keys and values with the requests'
+        low-rank adapters beside it, write, attention and commit as above, the output
+        projection, the norm behind it, and pages that hold no accepted row given back.
+        T = e4m3: the projections are 8-bit too. Hidden size 4096, eight adapters of rank 16,
+        a quarter of the requests without one.
     python -m conditional_draft_tree_gb300.profile_cases chain [--reps R] [--cfg C] [--greedy]
         R Domino chain-decoding rounds (dt_decode_chains) of the workload,
         sampled at its temperatures with seeded uniform draws, or greedy: one
@@ -197,9 +205,91 @@ def case_serve(cfg, reps, dev, cache_type="bf16", H=32, Hkv=8, dh=128, page=64, 
     return out, cache, prefix + lengths
 
 
+def case_layer(cfg, reps, dev, cache_type="bf16", d=4096, H=32, Hkv=8, dh=128, page=64, most=1024, least=512,
+               rank=16, adapters=8):
+    wl = W.make_workload(cfg)
+    tb = dt.TreeBuilder.from_numpy(wl, device=dev)
+    trees = tb.run(**tb.inputs_to_device(wl))
+    n, batch = wl.N + 1, wl.batch
+    eight = cache_type == "e4m3"
+    kind = torch.float16 if cache_type == "fp16" else torch.bfloat16
+    gen = torch.Generator(device=dev).manual_seed(cfg)
+    normal = lambda *shape: torch.randn(shape, device=dev, generator=gen).to(kind)
+    weight = lambda out, inner: dt.Projection(dt.quantize_rows(normal(out, inner) * inner ** -0.5) if eight else
+                                              normal(out, inner) * inner ** -0.5)
+    heads = H + 2 * Hkv
+    qkv, output = weight(heads * dh, d), weight(d, H * dh)
+    own = lambda out, inner: dt.Adapters(normal(adapters, rank, inner) * inner ** -0.5,
+                                         normal(adapters, out, rank) * (0.3 * rank ** -0.5),
+                                         torch.rand(adapters, device=dev, generator=gen))
+    own_qkv, own_output = own(heads * dh, d), own(d, H * dh)
+    index = torch.randint(0, adapters, (batch,), device=dev, generator=gen, dtype=torch.int32)
+    index[::4] = -1
+    norms = [dt.Norm((1 + 0.1 * torch.randn(d, device=dev, generator=gen)).to(kind)) for _ in range(2)]
+    rot = dt.Rotary(dh, base=1e6, device=dev)
+    # a pool with room for every request's longest tree, and the prompts in it
+    prefix = torch.randint(least, most + 1, (batch,), device=dev, generator=gen, dtype=torch.int32)
+    width = -(-(most + n) // page)
+    table = torch.empty((batch, width), dtype=torch.int32, device=dev)
+    cache = dt.PagedCache.empty(batch * width, Hkv, page, dh, table, torch.float8_e4m3fn if eight else kind)
+    pool = dt.PagePool.all_free(cache)
+    start = torch.zeros(batch, dtype=torch.int32, device=dev)
+    dt.cache_reserve(pool, prefix)
+    positions = dt.cache_slots(cache, most, start, prefix)[1]
+    rows = lambda: normal(batch, most, Hkv, dh).transpose(1, 2)
+    dt.cache_write(cache, rows(), rows(), start, prefix, rotary=rot, positions=positions)
+    # the round
+    x, residual = normal(batch, n, d), normal(batch, n, d)
+    wanted = prefix + n
+    path, lengths = (t.to(dev) for t in deepest_paths(trees["parents"], trees["depths"], wl.D + 1))
+    kept = prefix + lengths
+    positions = dt.tree_positions(trees["depths"], prefix)
+    attention_ws = dt.cache_attention_workspace(cache, H, n)
+    project_ws = [dt.project_workspace(p, batch, n, own_qkv) for p in (qkv, output)]
+    out = {}
+
+    def project(projection, y, eights, adapters, workspace):
+        return dt.project(projection, eights if eight else y, adapters, index, x16=y if eight else None,
+                          workspace=workspace)
+
+    def normed(norm, x, residual):
+        y, total = dt.rms_norm(norm, x, residual, kind="both" if eight else "16")
+        return (y if eight else (y, None)) + (total,)
+
+    def layer():
+        dt.cache_reserve(pool, wanted)
+        out["slots"], out["rows"] = dt.cache_slots(cache, n, prefix)
+        out["held"] = pool.held.clone()
+        y, y8, total = normed(norms[0], x, residual)
+        p = project(qkv, y, y8, own_qkv, project_ws[0]).view(batch, n, heads, dh).transpose(1, 2)
+        q = dt.cache_write(cache, p[:, H:H + Hkv], p[:, H + Hkv:], prefix, rotary=rot, positions=positions, q=p[:, :H])
+        seen = torch.empty((batch, n, H, dh), dtype=kind, device=dev)
+        dt.cache_attention(cache, q, prefix, mask=trees["mask"], out=seen.transpose(1, 2), workspace=attention_ws)
+        seen = seen.view(batch, n, H * dh)
+        z = project(output, seen, dt.quantize_rows(seen) if eight else None, own_output, project_ws[1])
+        w, w8, total2 = normed(norms[1], z, total)
+        dt.cache_commit(cache, prefix, path, lengths, n)
+        dt.cache_reserve(pool, kept)
+        out.update(y=y, y8=y8, total=total, p=p, q=q, seen=seen, z=z, w=w, w8=w8, total2=total2)
+
+    def again():          # the round's pages as they were before it
+        dt.cache_reserve(pool, prefix)
+
+    ms = _timed(lambda: (again(), layer()), reps, dev)
+    for status in (cache, qkv, output):
+        status.check()
+    if not bool(torch.isfinite(out["w"]).all()):
+        raise dt.DtError("the layer gave values that are not finite")
+    print(f"layer {wl.name}: batch={batch} n={n} cache={cache_type} committed={int(lengths.sum())} rows "
+          f"layer_us={1000 * ms:.1f}")
+    out.update(x=x, residual=residual, qkv=qkv, output=output, own_qkv=own_qkv, own_output=own_output, index=index,
+               norms=norms, prefix=prefix, kept=kept, cache=cache, pool=pool, trees=trees, positions=positions)
+    return out
+
+
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("case", choices=["topm", "round", "chain", "marginal", "verify", "serve"])
+    ap.add_argument("case", choices=["topm", "round", "chain", "marginal", "verify", "serve", "layer"])
     ap.add_argument("--greedy", action="store_true")
     ap.add_argument("--reps", type=int, default=3)
     ap.add_argument("--cfg", type=int, default=3)
@@ -219,6 +309,8 @@ def main():
         case_verify(args.cfg, args.reps, dev)
     elif args.case == "serve":
         case_serve(args.cfg, args.reps, dev, args.cache)
+    elif args.case == "layer":
+        case_layer(args.cfg, args.reps, dev, args.cache)
     else:
         case_topm(args.cfg, args.reps, dev)
 

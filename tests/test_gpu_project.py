@@ -260,3 +260,44 @@ def test_an_adapter_that_is_not_finite_stays_with_its_requests(batch, n, K, O, r
     got = dt.project(p, x, ad, index, x16, dtype=dtype)
     assert bool(got[whole].isnan().all()) and torch.equal(got[~whole], want[~whole])
     p.check()
+
+
+@pytest.mark.parametrize("batch,n,O", [(3, 5, 40), (4, 300, 700)])
+def test_8bit_rows_far_apart_in_size(batch, n, O):
+    """Rows of x and of W whose powers of two are far from each other's: products in fp32's range come out
+    right whatever the two are."""
+    K, g = 144, torch.Generator().manual_seed(9)
+    x = torch.randn(batch * n, K, generator=g) * torch.exp2(torch.randint(-110, 111, (batch * n, 1), generator=g).float())
+    w = torch.randn(O, K, generator=g) * torch.exp2(torch.randint(-110, 111, (O, 1), generator=g).float())
+    x, w = x.to(BF), w.to(BF)
+    x8, w8 = dt.quantize_rows(x.cuda()), dt.quantize_rows(w.cuda())
+    vx, vw = R.from_rows8(x8.codes.cpu(), x8.exps.cpu()), R.from_rows8(w8.codes.cpu(), w8.exps.cpu())
+    rows = dt.Rows8(x8.codes.view(batch, n, K), x8.exps.view(batch, n))
+    got = dt.project(dt.Projection(w8), rows).reshape(-1, O).double().cpu()
+    ref = R.project(vx, vw, n)
+    # sums of codes within 2^9 K: past fp32's largest number they are infinite, below its least lost
+    inside = (ref.abs() < 2.0 ** 127) & (ref.abs() > 2.0 ** -100)
+    slack = R.project_slack(vx, vw, n, ref, BF)
+    assert bool(((got - ref).abs()[inside] <= slack[inside]).all())
+    assert bool((got[ref.abs() > 2.0 ** 129].isinf()).all()) and bool((got.abs()[ref.abs() < 2.0 ** -140] < 2.0 ** -130).all())
+    assert int(inside.sum()) > 0.5 * ref.numel()      # (of two uniform exponents' sum)
+
+
+@pytest.mark.parametrize("rows,K,O,e8", [(60000, 16, 40000, False), (600000, 4096, 9, False), (1200000, 4096, 24, True)])
+def test_offsets_past_32_bits(rows, K, O, e8):
+    """Results, or rows of x, of more than 4 GB; a sample of the rows."""
+    g = torch.Generator(device="cuda").manual_seed(10)
+    x = torch.empty(rows, K, dtype=BF, device="cuda").normal_(generator=g)
+    w = torch.randn(O, K, generator=g, device="cuda").to(BF)
+    at = torch.cat([torch.arange(5), torch.randint(0, rows, (40,)), torch.arange(rows - 5, rows)])
+    if e8:
+        x8, w8 = dt.quantize_rows(x), dt.quantize_rows(w)
+        del x
+        vx = R.from_rows8(x8.codes.view(torch.uint8)[at.cuda()].cpu().view(torch.float8_e4m3fn), x8.exps.cpu()[at])
+        vw = R.from_rows8(w8.codes.cpu(), w8.exps.cpu())
+        got = dt.project(dt.Projection(w8), dt.Rows8(x8.codes.view(1, rows, K), x8.exps.view(1, rows)))
+    else:
+        vx, vw = x[at.cuda()].cpu().double(), w.cpu().double()
+        got = dt.project(dt.Projection(w), x.view(1, rows, K))
+    ref = R.project(vx, vw, len(at))
+    near(got[0, at.cuda()], ref, R.project_slack(vx, vw, len(at), ref, BF))

@@ -298,6 +298,11 @@ __device__ void list_adapters(const ProjectArgs &a, int t0, int t1, AdapterList 
   meet();
 }
 
+// Slabs of a stage. Two halve what its waits and issuing take, for tiles whose products take less (a
+// single block's: 8 tokens 17.4 to 15.9 us); a pair's tiles of 256 rows have a shallower ring
+// then (two prompts 178 to 187 us).
+__host__ __device__ constexpr int deep_of(int cg) { return cg == 1 ? 2 : 1; }
+
 // Sums over the blocks of a cluster that share a tile's K. Each block owns a share of the tile's columns:
 // the others write their terms into its shared memory (where the ring was: all blocks have passed a
 // cluster barrier), [block][column of the share][128 lanes]; behind a second barrier it adds them up
@@ -563,7 +568,8 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
   const int split = CG == 2 ? 1 : w.split, rank = CG == 2 ? 0 : crank;
   const int pair = CG == 2 ? crank : 0;
   const int mine = w.nt / CG;                             // rows of x in this block's memory
-  const int stage = kSlabA + mine * 128;
+  constexpr int deep = deep_of(CG);
+  const int slab_x = deep * kSlabA, stage = deep * (kSlabA + mine * 128);   // x behind W in a stage
   const int first = blockIdx.x / size, step = gridDim.x / size;
   const int kbytes = E8 ? a.K : 2 * a.K, steps = (kbytes + 127) / 128;
   const int k0 = steps * rank / split, k1 = steps * (rank + 1) / split;
@@ -618,14 +624,19 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
     bool go = true;
     for (int t = first, i = 0; t < w.tiles && go; t += step, ++i) {
       const int o0 = (t % w.tiles_o * CG + pair) * w.outs, x0 = t / w.tiles_o * w.nt + pair * mine;
-      for (int s = k0; s < k1 && go; ++s) {
+      for (int s = k0; s < k1 && go; s += deep) {
         if (!(go = wait(&ss.empty[p.at], p.parity ^ 1u))) break;
         unsigned char *to = sm + p.at * stage;
         const uint32_t bar = first_block(&ss.full[p.at]);
+        const int here = min(deep, k1 - s);
         if (issuer) {
-          if (pair == 0) mbar_expect_tx(&ss.full[p.at], CG * (w.outs + mine) * 128);
+          if (pair == 0) mbar_expect_tx(&ss.full[p.at], CG * here * (w.outs + mine) * 128);
           tma_2d<CG>(to, &wmap, s * kValues, o0, bar);
-          tma_2d<CG>(to + kSlabA, &xmap, s * kValues, x0, bar);
+          tma_2d<CG>(to + slab_x, &xmap, s * kValues, x0, bar);
+          if (deep > 1 && here > 1) {
+            tma_2d<CG>(to + kSlabA, &wmap, (s + 1) * kValues, o0, bar);
+            tma_2d<CG>(to + slab_x + mine * 128, &xmap, (s + 1) * kValues, x0, bar);
+          }
         }
         flying &= ~(1u << p.at);
         p.step(w.stages);
@@ -678,16 +689,22 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       if (pair == 0) {
         if (!(go = wait(&ss.acc_empty[buf], (turn & 1) ^ 1))) break;
         tmem_fence_after();
-        for (int s = k0; s < k1; ++s) {
+        for (int s = k0; s < k1; s += deep) {
           if (!(go = wait(&ss.full[p.at], p.parity))) break;
           tmem_fence_after();
           const uint32_t at = smem_u32(sm) + p.at * stage;
-          const uint64_t da = rows128(at), db = rows128(at + kSlabA);
+          const uint64_t da = rows128(at), db = rows128(at + slab_x);
           const int parts = min(4, (kbytes - s * 128 + 31) / 32);
+          const int more = deep > 1 && k1 - s > 1 ? min(4, (kbytes - s * 128 - 97) / 32) : 0;   // of the next slab
           if (issuer) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               if (k < parts) mma<CG, E8>(acc, da + 2 * k, db + 2 * k, idesc, s > k0 || k > 0);
+            if (deep > 1)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k < more)
+                  mma<CG, E8>(acc, da + kSlabA / 16 + 2 * k, db + mine * 8 + 2 * k, idesc, true);
             commit<CG>(&ss.empty[p.at]);
           }
           p.step(w.stages);
@@ -712,7 +729,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
             tmem_fence_after();
             const uint32_t at = smem_u32(sm) + p.at * stage;
             const int here = min(4, all - 4 * q);
-            const uint64_t da = rows_of(at, w.piece), db = rows_of(at + kSlabA, w.piece);
+            const uint64_t da = rows_of(at, w.piece), db = rows_of(at + slab_x, w.piece);
             if (issuer) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -764,7 +781,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         slot[k] = r < mine && row < a.rows ? l.slot[row / a.n - l.first] : -1;
         u[k] = a.u + static_cast<int64_t>(row) * a.rank;
       }
-      at = (at + (k1 - k0)) % w.stages;
+      at = (at + (k1 - k0 + deep - 1) / deep) % w.stages;
       uint4 v[2][4][2];
       int of = 4 * q0 / per, j = 4 * q0 - of * per, whose[4];   // adapter and sixteen of its rank to be fetched
       auto fetch = [&](int q) {                // loads of the next stage's rows, before there is room
@@ -787,7 +804,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         const uint32_t parity = (phases >> at) & 1u;
         if (!(go = wait(&ss.u_go[at], parity))) break;
         phases ^= 1u << at;
-        unsigned char *to = sm + at * stage + kSlabA;
+        unsigned char *to = sm + at * stage + slab_x;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int r = id + 128 * k;
@@ -1018,7 +1035,7 @@ constexpr double kMemoryRate = 3500.0; // bytes a cycle from memory
 // Cycles that a slab takes in a block: its products, its bytes on the way in, and what waits and
 // issuing take whatever its size.
 double slab_cycles(int outs, int nt, int cg) {
-  return std::max(std::max(2.0 * nt, 390.0), (outs + nt / cg) * 128 / kCopyRate);
+  return std::max(std::max(2.0 * nt, 330.0), (outs + nt / cg) * 128 / kCopyRate);
 }
 
 // The tile, and the blocks that share one, of the least estimated time: whole rounds of tiles over the
@@ -1027,11 +1044,12 @@ double slab_cycles(int outs, int nt, int cg) {
 // all SMs busy. Only the order of the estimates matters.
 void choose(const ProjectArgs &a, bool e8, bool ad, const Rooms &room, int smem, ProjectPlan *p) {
   const int size = e8 ? 1 : 2, steps = ceil_div(static_cast<int64_t>(a.K) * size, 128);
-  const int cap = ad && e8 ? 160 : kMaxTokens;     // three accumulators instead of two
+  // of a pair; with adapters three accumulators instead of two. Of a single block: three stages
+  const int most[3] = {0, 144, ad && e8 ? 160 : kMaxTokens};
   const double memory = (static_cast<double>(a.O) + a.rows) * a.K * size / kMemoryRate;
   double best = 1e300;
   for (int cg = 1; cg <= 2; ++cg)
-    for (int nt = 16 * cg; nt <= cap; nt += 16 * cg) {
+    for (int nt = 16 * cg; nt <= most[cg]; nt += 16 * cg) {
       const int tiles_t = ceil_div(a.rows, nt);
       for (int split = 1; split <= (cg == 2 ? 1 : std::min(kMaxSplit, steps)); ++split) {
         const int places = room.of[cg == 2 ? 2 : split];
@@ -1061,7 +1079,7 @@ void choose(const ProjectArgs &a, bool e8, bool ad, const Rooms &room, int smem,
       }
       if (nt >= a.rows) break;
     }
-  const int stage = kSlabA + p->s.nt / p->cg * 128;
+  const int stage = deep_of(p->cg) * (kSlabA + p->s.nt / p->cg * 128);
   p->s.stages = stages_of(smem, stage);
   p->s.buffers = 2;
   p->s.off_small = p->s.stages * stage;

@@ -11,6 +11,15 @@
 // rows: in an accumulator of their own, as the shared one is scaled at the end.) u comes from a
 // launch before, which stacks the A_a of a tile's adapters on the M side; the projection begins
 // beside it and waits for it only where it reads u.
+//
+// Measured on the GPU, inputs in rotation (K 4096): 32 trees of 65 rows to 6144 outputs, eight adapters
+// of rank 16, bf16, 68 us, 1.54 PFLOP/s (62 us without adapters; the tensor pipe 71 % active with cold
+// caches); two prompts of 4099 rows to 4001, rank 64, fp16, 178 to 185 us, 1.5 PFLOP/s; 8224 rows of
+// 8-bit codes to 6144 117 to 119 us, 3.5 PFLOP/s; one token of 8 requests to 6144 16 us, of which W's
+// 50 MB from memory are 8; of 128 requests with 64 adapters of rank 32, 8-bit, to 4096 23.5 us. Large
+// cases are bound by the tensor cores at the clock that power leaves them, and by tiles that
+// do not fill a last round; small ones by what stands before the first product (launch, barriers,
+// first copy: 3 us) and behind the last (a cluster's sum: 3 us).
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -44,7 +53,7 @@ struct ProjectArgs {
 };
 
 struct ProjectShape {
-  int nt, stages, buffers;        // rows of x of a tile; places of the ring; accumulators
+  int nt, stages;                 // rows of x of a tile; places of the ring
   int tiles_o, tiles, split;      // tiles along the outputs, all; blocks that share a tile
   int outs, piece;                // rows of W of a block's tile; values of B_a's rows of one copy
   int off_small;
@@ -306,8 +315,7 @@ __host__ __device__ constexpr int deep_of(int cg) { return cg == 1 ? 2 : 1; }
 // Sums over the blocks of a cluster that share a tile's K. Each block owns a share of the tile's columns:
 // the others write their terms into its shared memory (where the ring was: all blocks have passed a
 // cluster barrier), [block][column of the share][128 lanes]; behind a second barrier it adds them up
-// in the blocks' order. Writes to another block do not wait for each other, as reads would
-// (for 8 blocks and 240 columns these took 12 us).
+// in the blocks' order. (Writes to another block do not wait for each other, as reads would.)
 struct Shares {
   uint32_t base;         // of the memory, in this block
   int width, split, rank, lane;
@@ -554,7 +562,9 @@ __global__ void __launch_bounds__(256) adapter_rows_kernel(const __grid_constant
 
 // The projection. Warps 0-7: accumulators to y (a thread an output, two for each); 8: TMA; 9: products; 10-13
 // (AD): the adapters' list, and their u rows into the ring. In a pair (CG = 2) each block holds its 128
-// rows of W and half of the tile's rows of x, and the first one issues the products of both.
+// rows of W and half of the tile's rows of x, and the first one issues the products of both. Two
+// accumulators: one is emptied while the next tile's products run; of 8-bit rows a third, for
+// adapters.
 template <int DT, bool E8, bool AD, int CG>
 __global__ void __launch_bounds__(AD ? kDrain + 192 : kDrain + 64, 1)
 project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ ProjectShape w,
@@ -684,7 +694,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
     uint32_t phases = 0;                       // of u_full, a bit a stage
     bool go = true;
     for (int t = first, i = 0; t < w.tiles && go; t += step, ++i) {
-      const int buf = w.buffers == 2 ? i & 1 : 0, turn = w.buffers == 2 ? i >> 1 : i;
+      const int buf = i & 1, turn = i >> 1;
       const uint32_t acc = tmem + buf * w.nt;
       if (pair == 0) {
         if (!(go = wait(&ss.acc_empty[buf], (turn & 1) ^ 1))) break;
@@ -718,11 +728,11 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         share(all, &q0, &q1);
         if (pair == 0) {
           // the adapters' own accumulator is the only one: the tile before has to have read it
-          if (E8 && w.buffers == 2 && i > 0 && q0 < q1) {
+          if (E8 && i > 0 && q0 < q1) {
             if (!(go = wait(&ss.acc_empty[(i - 1) & 1], ((i - 1) >> 1) & 1))) break;
             tmem_fence_after();
           }
-          const uint32_t to = E8 ? tmem + w.buffers * w.nt : acc;
+          const uint32_t to = E8 ? tmem + 2 * w.nt : acc;
           for (int q = q0; q < q1; ++q) {
             if (!(go = wait(&ss.full[p.at], p.parity) && wait(&ss.u_full[p.at], (phases >> p.at) & 1u))) break;
             phases ^= 1u << p.at;
@@ -864,11 +874,11 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
     const int row = tid & 127, group = tid >> 7;
     bool go = true;
     for (int t = first, i = 0; t < w.tiles && go; t += step, ++i) {
-      const int buf = w.buffers == 2 ? i & 1 : 0, turn = w.buffers == 2 ? i >> 1 : i;
+      const int buf = i & 1, turn = i >> 1;
       const int o = row < w.outs ? (t % w.tiles_o * CG + pair) * w.outs + row : a.O, t0 = t / w.tiles_o * w.nt;
       bool both = false;                       // the adapters have something in their accumulator
+      __syncwarp();                            // (all lanes have read the last tile's exponents)
       if (AD && E8) {
-        __syncwarp();
         go = wait(&ss.list_full[i & 1], (i >> 1) & 1);
         int q0 = 0, q1 = 0;
         if (go) share(sixteens_of(ss.list[i & 1]), &q0, &q1);
@@ -913,7 +923,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       float v[16], z[16], next[16], next_z[16];
       auto fetch = [&](int c) {
         load16(lanes + buf * w.nt + c, next);
-        if (AD && E8 && both) load16(lanes + w.buffers * w.nt + c, next_z);
+        if (AD && E8 && both) load16(lanes + 2 * w.nt + c, next_z);
       };
       // 16 columns are on their way from TMEM while the 16 before them are written. (One copy of this
       // code, as short as it comes: a warp issues an instruction every six cycles here, and its
@@ -1041,7 +1051,10 @@ double slab_cycles(int outs, int nt, int cg) {
 // The tile, and the blocks that share one, of the least estimated time: whole rounds of tiles over the
 // clusters that the GPU has room for, or memory's time, and what a tile's end takes. A pair of blocks
 // (cg = 2) loads half of the rows of x each. Where one round does, tiles have as few rows of W as keep
-// all SMs busy. Only the order of the estimates matters.
+// all SMs busy. Only the order of the estimates matters. Both sides measured: pairs of 256 rows against
+// single blocks of 144, trees 68 and 82 us, 8-bit stress rows 119 and 149, prompts 185 and 218; one
+// token of 8 requests by two blocks a tile and by one, 16.3 and 17.0 us; of 128 requests in tiles of 128 rows
+// by four blocks, of 64 by two and of 32 by one, 23.5, 23.0 and 23.8 us.
 void choose(const ProjectArgs &a, bool e8, bool ad, const Rooms &room, int smem, ProjectPlan *p) {
   const int size = e8 ? 1 : 2, steps = ceil_div(static_cast<int64_t>(a.K) * size, 128);
   // of a pair; with adapters three accumulators instead of two. Of a single block: three stages
@@ -1081,18 +1094,19 @@ void choose(const ProjectArgs &a, bool e8, bool ad, const Rooms &room, int smem,
     }
   const int stage = deep_of(p->cg) * (kSlabA + p->s.nt / p->cg * 128);
   p->s.stages = stages_of(smem, stage);
-  p->s.buffers = 2;
   p->s.off_small = p->s.stages * stage;
   p->s.piece = a.rank % 64 == 0 ? 64 : a.rank % 32 == 0 ? 32 : 16;
   p->smem = p->s.off_small + sizeof(Small);
 }
 
 // The launch before: a block a row and four ranks while all that they read (from L2) takes less time
-// than the other kernel (s->tiles = 0); else blocks that fit the places which have a tile less to do cost nothing as long as
-// they end within the others' first tile; else the shortest.
+// than the other kernel adds (s->tiles = 0: 128 tokens of rank 32 24 us instead of 29, but the trees
+// 89 instead of 68); else blocks that fit the places which have a tile less to do cost nothing as long as
+// they end within the others' first tile (the trees: 24 blocks of 152 places, 2 us of 68 for the adapters); else the
+// shortest.
 void choose_down(const ProjectArgs &a, const ProjectPlan &p, const Rooms &room, int smem, ProjectShape *s) {
   const int steps = ceil_div(2 * a.K, 128), spt = kOuts / a.rank;
-  double best = 1e300, shortest = 1e300;
+  double best = 1e300;
   for (int nt = 16; nt <= kMaxTokens; nt += 16) {
     const int requests = std::min(nt, (nt + a.n - 2) / a.n + 1);        // of a tile, at most
     const int tiles_o = ceil_div(std::min(requests, a.count), spt);
@@ -1102,7 +1116,6 @@ void choose_down(const ProjectArgs &a, const ProjectPlan &p, const Rooms &room, 
       const double rounds = ceil_div(tiles, room.of[split]);
       const double time = rounds * (ceil_div(steps, split) * slab_cycles(kOuts, nt, 1) + 10000.0 +
                                     (split > 1 ? 3000.0 + 16.0 * nt : 16.0 * nt));
-      shortest = std::min(shortest, time);
       const double cost = (tiles * split <= p.idle ? std::max(0.0, time - p.tile) : time) + 1e-3 * time;
       if (cost < best) {
         best = cost;
@@ -1114,7 +1127,7 @@ void choose_down(const ProjectArgs &a, const ProjectPlan &p, const Rooms &room, 
     }
     if (nt >= a.rows) break;
   }
-  if (4000.0 + 2.0 * a.rows * a.rank * a.K / kRowsRate < shortest) {
+  if (4000.0 + 2.0 * a.rows * a.rank * a.K / kRowsRate < best) {
     s->tiles = 0;
     return;
   }

@@ -414,6 +414,7 @@ adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant
     }
     mbar_init(&ss.acc_full[0], 1);
     ss.fail = 0;
+    fence_async_smem();
     for (int i = 0; i < ahead; ++i) load_x(k0 + i, i);
   }
   if (warp == kDrain / 32 + 1) tmem_alloc(&ss.tmem, 256);

@@ -352,6 +352,18 @@ struct Shares {
   }
 };
 
+// 16 bytes, or zeros, without a branch
+__device__ __forceinline__ uint4 load_if(const void *p, bool there) {
+  uint4 v;
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %5, 0;\nmov.u32 %0, 0;\nmov.u32 %1, 0;\nmov.u32 %2, 0;\nmov.u32 %3, 0;\n"
+      "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(static_cast<int>(there))
+      : "memory");
+  return v;
+}
+
 // whether one of two pairs' halves has all exponent bits set (of magnitudes; `m` of top_abs)
 template <int DT>
 __device__ __forceinline__ bool not_finite(uint32_t m) {
@@ -767,6 +779,18 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
     const int id = tid - kDrain - 64;
     uint32_t at = 0, phases = 0;               // stage of the ring; phases of u_go
     bool marked[2] = {false, false};           // this thread's row of ss.odd has something
+    // Where a thread's sixteens lie in a stage, as offsets of their first halves (the second ones 16 bytes
+    // away, before or behind): of row `id` of the rows u, and of B_a's. Row id + 128 of u lies as
+    // row id does.
+    const int row_bytes = 2 * w.piece, chunks = w.piece >> 3;      // of a piece's row
+    const int shift = w.piece == 64 ? 0 : w.piece == 32 ? 1 : 2;   // rows of one swizzle
+    int u_at[4], b_at[4];
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      const int c = 2 * z & (chunks - 1), in = id * row_bytes + 16 * (c ^ ((id >> shift) & (chunks - 1)));
+      u_at[z] = slab_x + (2 * z - c) * mine * 16 + in;
+      b_at[z] = (2 * z - c) * kOuts * 16 + in;
+    }
     // (these warps meet for the lists: they go through all tiles, whatever has failed)
     for (int t = first, i = 0; t < w.tiles; t += step, ++i) {
       AdapterList &l = ss.list[i & 1];
@@ -781,8 +805,6 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       mbar_arrive(&ss.list_full[i & 1]);
       if (i == 0) cudaGridDependencySynchronize();        // u is there
       const int all = sixteens_of(l), per = a.rank >> 4;
-      const int row_bytes = 2 * w.piece, chunks = w.piece >> 3;      // of a piece's row
-      const int shift = w.piece == 64 ? 0 : w.piece == 32 ? 1 : 2;   // rows of one swizzle
       int q0, q1, slot[2];
       const uint16_t *u[2];
       share(all, &q0, &q1);
@@ -801,11 +823,9 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
           whose[z] = 4 * q + z < all ? of : -2;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            v[k][z][0] = v[k][z][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (whose[z] == slot[k]) {
-              v[k][z][0] = *reinterpret_cast<const uint4 *>(u[k] + 16 * j);
-              v[k][z][1] = *reinterpret_cast<const uint4 *>(u[k] + 16 * j + 8);
-            }
+            if (k == 1 && mine <= 128) break;
+            v[k][z][0] = load_if(u[k] + 16 * j, whose[z] == slot[k]);
+            v[k][z][1] = load_if(u[k] + 16 * j + 8, whose[z] == slot[k]);
           }
           if (++j == per) j = 0, ++of;
         }
@@ -815,17 +835,15 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         const uint32_t parity = (phases >> at) & 1u;
         if (!(go = wait(&ss.u_go[at], parity))) break;
         phases ^= 1u << at;
-        unsigned char *to = sm + at * stage + slab_x;
+        unsigned char *const place = sm + at * stage;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int r = id + 128 * k;
-          if (r >= mine) break;
+          if (id + 128 * k >= mine) break;
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            const int c = 2 * z & (chunks - 1), turn = (r >> shift) & (chunks - 1);
-            unsigned char *row = to + (2 * z - c) * mine * 16 + r * row_bytes;
-            *reinterpret_cast<uint4 *>(row + 16 * (c ^ turn)) = v[k][z][0];
-            *reinterpret_cast<uint4 *>(row + 16 * ((c + 1) ^ turn)) = v[k][z][1];
+            const int to = u_at[z] + 128 * k * row_bytes;
+            *reinterpret_cast<uint4 *>(place + to) = v[k][z][0];
+            *reinterpret_cast<uint4 *>(place + (to ^ 16)) = v[k][z][1];
           }
         }
         int looked[4];
@@ -838,17 +856,11 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         // output is NaN for the rows with that adapter.
         go = wait(&ss.up_full[at], parity);
         if (go && id < w.outs) {
-          unsigned char *row = sm + at * stage + id * row_bytes;
-          const int turn = (id >> shift) & (chunks - 1);
-          uint4 *half[4][2];
           uint32_t most[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            const int c = 2 * z & (chunks - 1);
-            unsigned char *piece = row + (2 * z - c) * kOuts * 16;
-            half[z][0] = reinterpret_cast<uint4 *>(piece + 16 * (c ^ turn));
-            half[z][1] = reinterpret_cast<uint4 *>(piece + 16 * ((c + 1) ^ turn));
-            const uint4 lo = *half[z][0], hi = *half[z][1];
+            const uint4 lo = *reinterpret_cast<const uint4 *>(place + b_at[z]);
+            const uint4 hi = *reinterpret_cast<const uint4 *>(place + (b_at[z] ^ 16));
             most[z] = top_abs<DT>(top_abs<DT>(top_abs<DT>(lo.x, lo.y), top_abs<DT>(lo.z, lo.w)),
                                   top_abs<DT>(top_abs<DT>(hi.x, hi.y), top_abs<DT>(hi.z, hi.w)));
           }
@@ -856,8 +868,8 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
 #pragma unroll
             for (int z = 0; z < 4; ++z)
               if (looked[z] >= 0 && not_finite<DT>(most[z])) {
-                make_finite<DT>(half[z][0]);
-                make_finite<DT>(half[z][1]);
+                make_finite<DT>(reinterpret_cast<uint4 *>(place + b_at[z]));
+                make_finite<DT>(reinterpret_cast<uint4 *>(place + (b_at[z] ^ 16)));
                 ss.odd[i & 1][id][looked[z] >> 5] |= 1u << (looked[z] & 31);
                 ss.any_odd[i & 1] = 1;
                 marked[i & 1] = true;

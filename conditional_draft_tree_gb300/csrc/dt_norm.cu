@@ -145,11 +145,12 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v) {
 
 constexpr int kSmall = 256;    // threads of a block whose rows have fewer than 32
 
-// GROUP threads a row (kBlock: those that the block has), each with ITEMS chunks of 8 values. WIDE: all rows lie on 16-byte boundaries,
-// chunks are loads and stores. Else each tensor's rows begin anywhere: a chunk is cut from the two
-// 16-byte granules that it lies in, and a granule of a result put together from a thread's chunk and
-// its left neighbour's; a warp's first lane has the chunk of the warp before it once more for that
-// (31 new chunks a warp). AHEAD: the next row is on its way while this one is worked on. Values
+// GROUP threads a row (kBlock: those that the block has), each with ITEMS chunks of 8 values. WIDE: all
+// rows lie on 16-byte boundaries, chunks are loads and stores. Else each tensor's rows begin anywhere:
+// a chunk is cut from the two 16-byte granules that it lies in, and a granule of a result put together
+// from a thread's chunk and its left neighbour's; a warp's first lane has the chunk of the warp before
+// it once more for that (31 new chunks a warp). (Chunks that follow x's own boundaries, one granule
+// each, were no faster: 57 us for 56.) AHEAD: the next row is on its way while this one is worked on. Values
 // go in pairs through the two-wide fp32 instructions: one by one, some 25 instructions a value
 // bounded the kernel (heads 43 us, 5000 wide 53 us; now 25.5 and 28).
 template <int DT, bool WIDE, int GROUP, int ITEMS, bool AHEAD, int REGS>

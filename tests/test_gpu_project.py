@@ -301,3 +301,35 @@ def test_offsets_past_32_bits(rows, K, O, e8):
         got = dt.project(dt.Projection(w), x.view(1, rows, K))
     ref = R.project(vx, vw, len(at))
     near(got[0, at.cuda()], ref, R.project_slack(vx, vw, len(at), ref, BF))
+
+
+def test_two_streams_at_once():
+    """Calls of different forms (pairs, clusters, few rows, 8-bit) side by side on two streams, each with a
+    workspace of its own, among norms: the results of one call after the other."""
+    cases = [Case(32, 65, 640, 1100, 16, 5, BF, False, seed=11), Case(9, 1, 2048, 700, 32, 9, BF, True, seed=12),
+             Case(3, 400, 512, 900, 64, 3, FP, False, seed=13), Case(130, 1, 1024, 300, 16, 60, FP, True, seed=14)]
+    made = [c.cuda() for c in cases]
+    norm = dt.Norm(None)
+    run = lambda c, m, **kw: dt.project(*m, dtype=c.dtype, **kw)
+    wants = [run(c, m) for c, m in zip(cases, made)]
+    x = torch.randn(3000, 1032, generator=torch.Generator().manual_seed(15)).to(BF).cuda()
+    want = dt.rms_norm(norm, x, kind="both")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [[dt.project_workspace(m[0], c.batch, c.n, m[2]) for c, m in zip(cases, made)] for _ in streams]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for k in range(25):
+        for i, s in enumerate(streams):
+            order = list(range(4)) if i == 0 else [3, 1, 2, 0]
+            for j in order:
+                got[i].append((j, run(cases[j], made[j], workspace=spaces[i][j], stream=s)))
+            got[i].append((-1, dt.rms_norm(norm, x, kind="both", stream=s)))
+    torch.cuda.synchronize()
+    for j, y in got[0] + got[1]:
+        if j >= 0:
+            assert torch.equal(y, wants[j]), j
+        else:
+            assert torch.equal(y[0], want[0]) and torch.equal(y[1].exps, want[1].exps)
+            assert torch.equal(y[1].codes.view(torch.uint8), want[1].codes.view(torch.uint8))
+    for m in made:
+        m[0].check()

@@ -17,10 +17,13 @@
 // caches); two prompts of 4099 rows to 4001, rank 64, fp16, 178 to 185 us, 1.5 PFLOP/s; 8224 rows of
 // 8-bit codes to 6144 117 to 119 us, 3.5 PFLOP/s; one token of 8 requests to 6144 16 us, of which W's
 // 50 MB from memory are 8; of 128 requests with 64 adapters of rank 32, 8-bit, to 4096 23.5 us. Large
-// cases are bound by the tensor cores, at the clock that power leaves them (a slab's four products of nt
-// columns take 2 nt + 130 cycles: 8-bit rows in tiles of 128 to 256 rows 201 to 335 ns a slab), and by
-// tiles that do not fill a last round. Two pairs that share their rows of x by multicast were no faster
-// (8-bit rows 117 us for 119, the trees 76 for 67: 144 of 152 SMs). Small ones by what stands before the first product (launch, barriers,
+// cases are bound by the tensor cores, at the clock that power leaves them, and by tiles that
+// do not fill a last round. A pair's slab (128 bytes of K), with one tile a pair and from the
+// times of K = 2048, 4096 and 8192: 256 rows 282 to 295 ns with 8-bit codes and 275 to 305 with
+// 16 bits, where 2.25 and 4.5 PFLOP/s would be 283; 128 rows 183 to 186 and 181 to 210, where
+// they would be 142, so that short tiles pay for more than their products. Two pairs that share
+// their rows of x by multicast were built: 8-bit rows 117 us for 119, the trees 76 for 67. Small
+// cases are bound by what stands before the first product (launch, barriers,
 // first copy: 3 us) and behind the last (a cluster's sum: 3 us).
 #include <algorithm>
 #include <atomic>

@@ -62,8 +62,8 @@ __device__ __forceinline__ Wants wants(const ReserveArgs &a, int b) {
 
 // Every block adds up the requests' wants for itself (the running sums of pages taken and
 // given back in shared memory) and places its share of the pages; the last block to finish writes
-// what the others read. Bound by latency: three dependent reads and two scans, 3 us for 32 requests,
-// 7 us for 512 that take or give back 60 thousand pages of 16 rows.
+// what the others read. Bound by latency: three dependent reads and two scans, a call
+// 2.9 us for 32 requests and 5.6 for 512 with pages of 16 rows (means of three calls).
 __global__ void __launch_bounds__(kThreads) cache_reserve_kernel(const __grid_constant__ ReserveArgs a) {
   extern __shared__ int32_t s_sums[];                 // [batch + 1] taken, [batch + 1] given back
   __shared__ int64_t s_warp[2][kThreads / 32];

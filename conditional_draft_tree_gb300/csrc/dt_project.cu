@@ -1120,8 +1120,8 @@ void choose(const ProjectArgs &a, bool e8, bool ad, const Rooms &room, int smem,
 // The launch before: a block a row and four ranks while all that they read (from L2) takes less time
 // than the other kernel adds (s->tiles = 0: 128 tokens of rank 32 24 us instead of 29, but the trees
 // 89 instead of 68); else blocks that fit the places which have a tile less to do cost nothing as long as
-// they end within the others' first tile (the trees: 24 blocks of 152 places, 2 us of 68 for the adapters); else the
-// shortest.
+// they end within the others' first tile (the trees: 24 blocks of 152 places;
+// 68 us, 64 where no request has an adapter, 62 without any); else the shortest.
 void choose_down(const ProjectArgs &a, const ProjectPlan &p, const Rooms &room, int smem, ProjectShape *s) {
   const int steps = ceil_div(2 * a.K, 128), spt = kOuts / a.rank;
   double best = 1e300;

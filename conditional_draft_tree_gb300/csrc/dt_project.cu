@@ -772,6 +772,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
           }
           if (!go) break;
         }
+        __syncwarp();              // every lane has read the list's count
         if (issuer) mbar_arrive(&ss.list_empty[i & 1]);
       }
       if (pair == 0 && issuer) commit<CG>(&ss.acc_full[buf]);

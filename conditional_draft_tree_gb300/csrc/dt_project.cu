@@ -408,7 +408,6 @@ adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant
   extern __shared__ __align__(1024) unsigned char sm[];
   Small &ss = *reinterpret_cast<Small *>(sm + w.off_small);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  cudaTriggerProgrammaticLaunchCompletion();
   const int split = w.split, rank = static_cast<int>(blockIdx.x) % split, tile = blockIdx.x / split;
   const int spt = kOuts / a.rank, m = tile % w.tiles_o;
   const int t0 = tile / w.tiles_o * w.nt, t1 = min(t0 + w.nt, a.rows);
@@ -443,6 +442,9 @@ adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
+  // The projection may begin now and not before: one of its blocks on this SM takes all columns of TMEM
+  // and keeps them until every block of this launch has ended, so each of these has to own its columns first.
+  cudaTriggerProgrammaticLaunchCompletion();
   const uint32_t tmem = ss.tmem;
   const int slots = min(list.count - m * spt, spt);
   if (slots <= 0) {                             // all blocks of the cluster alike

@@ -1,0 +1,37 @@
+"""Paths of the projection that sizes alone choose, and calls beside one another (needs a GB300): each
+against the plain 64-bit form, as tests/test_gpu_project.py has it."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import _layer_ref as R
+from test_gpu_project import BF, FP, Case, _built, dt, near  # noqa: F401  (_built is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def test_a_launch_before_with_room_beside_it():
+    """Tiles of 80 rows in single blocks, and x A^T in blocks of one stage: their shared memory together is less
+    than an SM has, so that nothing but registers keeps a block of each from the same SM. The second one
+    takes all of TMEM and waits for the first launch, whose blocks must have their columns by then."""
+    c = Case(1, 3996, 64, 1072, 64, 2, index=[1], seed=21)
+    p, x, ad, index, _ = c.cuda()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [dt.project_workspace(p, 1, 3996, ad) for _ in streams]
+    torch.cuda.synchronize()
+    got = [dt.project(p, x, ad, index, workspace=spaces[k % 2], stream=streams[k % 2]) for k in range(20)]
+    torch.cuda.synchronize()
+    near(got[0].reshape(-1, 1072), c.y, c.slack)
+    assert all(torch.equal(g, got[0]) for g in got)
+    p.check()
+
+
+@pytest.mark.parametrize("e8", [False, True])
+def test_tiles_without_an_adapter_between_tiles_with_one(e8):
+    """Many tiles a block, most of whose lists are empty: a list is given back where no product has
+    read more than its length."""
+    batch, n = 90, 200
+    index = [b % 3 if b % 7 == 5 else -1 for b in range(batch)]
+    Case(batch, n, 64, 1100, 16, 3, BF, e8, index=index, seed=22).check()
+    Case(9000, 2, 64, 300, 16, 3, BF, e8, index=[2 if b % 1000 == 0 else -1 for b in range(9000)], seed=23).check()

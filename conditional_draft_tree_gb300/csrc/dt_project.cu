@@ -1159,9 +1159,16 @@ void choose_down(const ProjectArgs &a, const ProjectPlan &p, const Rooms &room, 
   s->off_small = s->stages * stage;
 }
 
+// Blocks of a cluster wait for one another, each with its columns of TMEM. Were two such launches (of two streams)
+// to share SMs, a block of each could wait for columns that the other one's peer holds, without end. So a
+// cluster's blocks ask for all shared memory (`most`) but these bytes, less than any block here has.
+constexpr int kLeave = 32 * 1024;
+static_assert(sizeof(Small) + kSlabA + 16 * 128 > kLeave);
+
 template <auto Kernel, typename... Args>
-cudaError_t launch_cluster(int blocks, int threads, size_t smem, int cluster, bool early, cudaStream_t st,
+cudaError_t launch_cluster(int blocks, int threads, size_t smem, int most, int cluster, bool early, cudaStream_t st,
                            const Args &...args) {
+  if (cluster > 1) smem = std::max(smem, static_cast<size_t>(most - kLeave));
   cudaLaunchAttribute attr[2] = {};
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster;
@@ -1181,7 +1188,7 @@ cudaError_t launch_cluster(int blocks, int threads, size_t smem, int cluster, bo
 
 template <int DT>
 cudaError_t launch_down(const ProjectArgs &a, const ProjectShape &s, const dt_adapters &ad, const void *x16,
-                        int64_t ldx16, cudaStream_t st) {
+                        int64_t ldx16, int smem, cudaStream_t st) {
   if (s.tiles == 0) {
     adapter_rows_kernel<DT><<<a.rows * (a.rank / 4), 256, 0, st>>>(a, static_cast<const char *>(x16), ldx16,
                                                                    static_cast<const char *>(ad.down));
@@ -1193,17 +1200,18 @@ cudaError_t launch_down(const ProjectArgs &a, const ProjectShape &s, const dt_ad
   if (!matrix_map(ad.down, 2, a.K, static_cast<int64_t>(a.count) * a.rank, 2 * a.K, 64, a.rank, &down) ||
       !matrix_map(x16, 2, a.K, a.rows, ldx16, 64, s.nt, &x))
     return cudaErrorUnknown;
-  return launch_cluster<adapter_down_kernel<DT>>(s.tiles * s.split, kDrain + 64, s.off_small + sizeof(Small), s.split,
+  return launch_cluster<adapter_down_kernel<DT>>(s.tiles * s.split, kDrain + 64, s.off_small + sizeof(Small), smem, s.split,
                                                  false, st, a, s, down, x);
 }
 
 template <int DT, bool E8, bool AD, int CG>
 cudaError_t launch_main(const ProjectArgs &a, const ProjectPlan &p, const CUtensorMap &w, const CUtensorMap &x,
-                        const CUtensorMap &up, cudaStream_t st) {
+                        const CUtensorMap &up, int smem, cudaStream_t st) {
   constexpr auto kernel = project_kernel<DT, E8, AD, CG>;
   const cudaError_t e = allow_smem<kernel>();
   if (e != cudaSuccess) return e;
-  return launch_cluster<kernel>(p.blocks, AD ? kDrain + 192 : kDrain + 64, p.smem, CG == 2 ? 2 : p.s.split, AD, st, a, p.s, w, x, up);
+  return launch_cluster<kernel>(p.blocks, AD ? kDrain + 192 : kDrain + 64, p.smem, smem, CG == 2 ? 2 : p.s.split, AD, st,
+                                a, p.s, w, x, up);
 }
 
 template <int DT, bool E8, bool AD>
@@ -1222,10 +1230,11 @@ cudaError_t launch_project(const ProjectArgs &a, const dt_matrix &m, const void 
       return cudaErrorUnknown;
     ProjectShape down = {};
     choose_down(a, p, room, smem, &down);
-    const cudaError_t e = launch_down<DT>(a, down, *ad, x16, ldx16, st);
+    const cudaError_t e = launch_down<DT>(a, down, *ad, x16, ldx16, smem, st);
     if (e != cudaSuccess) return e;
   }
-  return p.cg == 2 ? launch_main<DT, E8, AD, 2>(a, p, w, xm, up, st) : launch_main<DT, E8, AD, 1>(a, p, w, xm, up, st);
+  return p.cg == 2 ? launch_main<DT, E8, AD, 2>(a, p, w, xm, up, smem, st)
+                   : launch_main<DT, E8, AD, 1>(a, p, w, xm, up, smem, st);
 }
 
 }  // namespace

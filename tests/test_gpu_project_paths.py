@@ -35,3 +35,26 @@ def test_tiles_without_an_adapter_between_tiles_with_one(e8):
     index = [b % 3 if b % 7 == 5 else -1 for b in range(batch)]
     Case(batch, n, 64, 1100, 16, 3, BF, e8, index=index, seed=22).check()
     Case(9000, 2, 64, 300, 16, 3, BF, e8, index=[2 if b % 1000 == 0 else -1 for b in range(9000)], seed=23).check()
+
+
+def test_clusters_of_three_streams():
+    """Launches in clusters of 2 to 8 blocks, x A^T's among them, and pairs, on three streams: a cluster has its
+    SMs for itself, so that no block waits for columns that another launch's waiting block holds."""
+    cases = [Case(80, 1, 2048, 300, seed=24), Case(400, 1, 1024, 700, 128, 2, seed=25), Case(77, 1, 4096, 1200, seed=26),
+             Case(20, 65, 320, 2100, 16, 5, seed=27)]
+    made = [c.cuda() for c in cases]
+    wants = [dt.project(*m, dtype=BF) for m in made]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    spaces = [[dt.project_workspace(m[0], c.batch, c.n, m[2]) for c, m in zip(cases, made)] for _ in streams]
+    torch.cuda.synchronize()
+    got = []
+    for k in range(40):
+        for i, s in enumerate(streams):
+            j = (k + i) % 4
+            got.append((j, dt.project(*made[j], dtype=BF, workspace=spaces[i][j], stream=s)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, wants[j]) for j, y in got)
+    for c, w in zip(cases, wants):
+        near(w.reshape(-1, c.O), c.y, c.slack)
+    for m in made:
+        m[0].check()

@@ -97,7 +97,7 @@ _pack_rows = struct.Struct("@Pqq").pack     # a dt_rows as bytes: half the time 
 
 class DtMatrix(C.Structure):
     _fields_ = [("data", C.c_void_p), ("exps", C.c_void_p), ("ld", C.c_int64)] + \
-        [(n, C.c_int) for n in ("O", "K", "dtype")]
+        [(n, C.c_int) for n in ("O", "K", "dtype", "wait_cycles")]
 
 
 class DtAdapters(C.Structure):

@@ -54,6 +54,7 @@ struct ProjectArgs {
   uint16_t *u;           // [rows][rank]: scale x A^T, rounded
   int32_t *status;
   int64_t ldy;           // in bytes
+  uint32_t limit;        // SM cycles after which a wait is given up
   int rows, n, O, K, count, rank;
 };
 
@@ -86,7 +87,11 @@ struct Small {                    // behind the ring
   int16_t token_slot[kMaxTokens];
   alignas(16) int xexp[4 * kGroups][kMaxTokens];   // exponents of the tile's rows of x, as bits of fp32; one copy a warp
   uint32_t tmem;
-  int fail;
+  int fail, peer_fail;            // a wait ran out in this block; in the other one of its pair
+  // how far the copies have come, for what follows on a wait that ran out: the ring's turns; stages whose
+  // last turn is one of W and x; stages with a copy of B_a that up_full counts, and its phases
+  uint32_t turns, mains, flying, ups;
+  uint32_t peer_turns, peer_mains;
 };
 
 // ------------------------------------------------------------ clusters
@@ -104,6 +109,9 @@ __device__ __forceinline__ uint32_t peer_address(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
+}
+__device__ __forceinline__ void store_peer(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void arrive_peer(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
@@ -175,6 +183,11 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
     umma_commit(bar);
 }
 
+// counts bytes as arrived on a barrier
+__device__ __forceinline__ void mbar_complete_tx(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // instruction descriptor: fp32 accumulation, both operands K-major
 template <int DT, bool E8>
 __device__ __forceinline__ uint32_t descriptor(int M, int N) {
@@ -207,24 +220,32 @@ __device__ __forceinline__ void load16(uint32_t taddr, float (&v)[16]) {
 // Waits of a converged warp. The lanes agree by votes, so that the compiler knows a warp's loops to be
 // uniform and keeps addresses and descriptors where TMA and MMA instructions take them from (with
 // one lane in a loop of its own a slab took 310 ns, whatever its size).
+template <bool SLEEP>
 __device__ __forceinline__ bool passed(uint64_t *bar, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      "selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+#define DT_PASSED(op)                                                                    \
+  asm volatile("{\n.reg .pred p;\nmbarrier." op ".parity.shared::cta.b64 p, [%1], %2;\n" \
+               "selp.u32 %0, 1, 0, p;\n}\n"                                              \
+               : "=r"(done)                                                              \
+               : "r"(smem_u32(bar)), "r"(parity)                                         \
+               : "memory")
+  if (SLEEP) DT_PASSED("try_wait");
+  else DT_PASSED("test_wait");
+#undef DT_PASSED
   return __all_sync(kFull, done);
 }
-// Bounded. False when the wait ran out, here or (where this one is not over) in another warp.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *fail, int32_t *status) {
-  if (passed(bar, parity)) return true;
-  const long long t0 = clock64();
+// Bounded. False when the wait ran out, here or (where this one is not over) in another warp. With a limit of a
+// test's the warp does not sleep, which may take longer than that. (Norm and 8-bit trees 67.7 us a call
+// for 66.2 without that branch, one token and 16-bit trees the same.)
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *fail, int32_t *status,
+                                          uint32_t limit) {
+  if (passed<false>(bar, parity)) return true;
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+  const bool sleep = limit >= static_cast<uint32_t>(kWaitCycles);
   for (;;) {
-    if (passed(bar, parity)) return true;
+    if (sleep ? passed<true>(bar, parity) : passed<false>(bar, parity)) return true;
     if (__any_sync(kFull, *fail != 0)) return false;
-    if (__any_sync(kFull, clock64() - t0 > kWaitCycles)) {
+    if (__any_sync(kFull, static_cast<uint32_t>(clock()) - t0 > limit)) {
       *fail = 1;
       *status = DT_ERR_TIMEOUT;
       return false;
@@ -415,7 +436,7 @@ adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant
   const int steps = (2 * a.K + 127) / 128, k0 = steps * rank / split, k1 = steps * (rank + 1) / split;
   const int stage = kSlabA + w.nt * 128;
   volatile int *fail = &ss.fail;
-  auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, fail, a.status); };
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, fail, a.status, a.limit); };
   const bool issuer = elect_one();
   // the rows of x need no list: the ring's first round of them is on its way before there is one
   auto load_x = [&](int s, uint32_t at) {
@@ -469,11 +490,7 @@ adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant
       }
       p.step(w.stages);
     }
-    if (*fail && lane == 0) {        // nothing may land in memory that the block has given up
-      for (; s < k0 + ahead; ++s) mbar_arrive(&ss.full[s - k0]);
-      for (int i = max(s - w.stages, k0); i < s; ++i)
-        mbar_wait_cycles(&ss.full[(i - k0) % w.stages], ((i - k0) / w.stages) & 1);
-    }
+    if (lane == 0) ss.turns = s - k0;
   } else if (warp == kDrain / 32 + 1) {
     const uint32_t idesc = descriptor<DT, false>(kOuts, w.nt);
     for (int s = k0; s < k1 && wait(&ss.full[p.at], p.parity); ++s) {
@@ -490,7 +507,6 @@ adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant
       p.step(w.stages);
     }
     if (issuer) commit<1>(&ss.acc_full[0]);
-    if (*fail && lane == 0) mbar_wait_cycles(&ss.acc_full[0], 0);
   }
   if (tid < kDrain) {
     __syncwarp();
@@ -499,7 +515,7 @@ adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant
     const bool live = slot < slots;
     const int want = live ? m * spt + slot : -2;
     const float scale = live && a.scale ? a.scale[list.ids[want]] : 1.0f;
-    wait(&ss.acc_full[0], 0);
+    const bool go = wait(&ss.acc_full[0], 0);
     tmem_fence_after();
     auto put = [&](int c, const auto &v) {
       uint16_t *to = a.u + static_cast<int64_t>(t0 + c) * a.rank + j;
@@ -510,7 +526,7 @@ adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant
     if (split > 1) cluster_sync();
     Shares shares(sm, w.nt, split, rank, row);
 #pragma unroll 1
-    for (int i = group; i < w.nt / 16; i += kGroups) {
+    for (int i = group; i < w.nt / 16 && go; i += kGroups) {
       const int c = shares.turn(i, w.nt);
       float v[16];
       load16(tmem + (static_cast<uint32_t>(warp & 3) << 21) + c, v);
@@ -529,6 +545,15 @@ adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant
     cluster_sync();
   }
   __syncthreads();
+  if (ss.fail) {       // a wait ran out: no copy may land, and no product read, where the block has ended
+    if (warp == kDrain / 32 && lane == 0) {
+      int i = static_cast<int>(ss.turns);
+      for (; i < ahead; ++i) mbar_arrive(&ss.full[i]);      // (ends a phase that has its rows of x alone)
+      for (int k = max(i - w.stages, 0); k < i; ++k) mbar_wait_cycles(&ss.full[k % w.stages], (k / w.stages) & 1);
+    }
+    if (warp == kDrain / 32 + 1 && lane == 0) mbar_wait_cycles(&ss.acc_full[0], 0);
+    __syncthreads();
+  }
   if (split > 1) cluster_sync();                // its sums have been read
   tmem_fence_after();
   if (warp == kDrain / 32 + 1) tmem_dealloc(tmem, 256);
@@ -621,7 +646,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       ss.any_odd[i] = 0;
     }
     mbar_init(&ss.idle, 1);
-    ss.fail = 0;
+    ss.fail = ss.peer_fail = 0;
   }
   if (AD)
     for (int i = tid; i < 2 * kOuts * (kMaxTokens / 32); i += blockDim.x) (&ss.odd[0][0][0])[i] = 0u;
@@ -632,7 +657,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
   tmem_fence_after();
   const uint32_t tmem = ss.tmem;
   volatile int *fail = &ss.fail;
-  auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, fail, a.status); };
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_warp(bar, parity, fail, a.status, a.limit); };
   const bool issuer = elect_one();
   // the barrier of the block that issues the products
   auto first_block = [&](uint64_t *bar) { return CG == 2 ? peer_address(smem_u32(bar), 0) : smem_u32(bar); };
@@ -650,7 +675,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
 
   if (warp == kDrain / 32) {
     Place p = {0, 0};
-    uint32_t issued = 0, ups = 0, flying = 0;   // up_full's phases; stages that it counts last
+    uint32_t issued = 0, mains = 0, ups = 0, flying = 0;
     bool go = true;
     for (int t = first, i = 0; t < w.tiles && go; t += step, ++i) {
       const int o0 = (t % w.tiles_o * CG + pair) * w.outs, x0 = t / w.tiles_o * w.nt + pair * mine;
@@ -669,6 +694,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
           }
         }
         flying &= ~(1u << p.at);
+        mains |= 1u << p.at;
         p.step(w.stages);
         ++issued;
       }
@@ -695,18 +721,18 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         }
         ups ^= 1u << p.at;
         flying |= 1u << p.at;
+        mains &= ~(1u << p.at);
         p.step(w.stages);
         ++issued;
       }
       __syncwarp();
       if (issuer) mbar_arrive(&ss.list_empty[i & 1]);
     }
-    if (*fail && lane == 0) {               // nothing may land in memory that the block has given up
-      if (pair == 0)
-        for (uint32_t k = issued > static_cast<uint32_t>(w.stages) ? issued - w.stages : 0; k < issued; ++k)
-          mbar_wait_cycles(&ss.full[k % w.stages], (k / w.stages) & 1u);
-      for (int k = 0; k < w.stages; ++k)
-        if ((flying >> k) & 1u) mbar_wait_cycles(&ss.up_full[k], ((ups >> k) & 1u) ^ 1u);
+    if (lane == 0) {
+      ss.turns = issued;
+      ss.mains = mains;
+      ss.flying = flying;
+      ss.ups = ups;
     }
   } else if (warp == kDrain / 32 + 1) {
     const uint32_t idesc = descriptor<DT, E8>(kOuts * CG, w.nt), idesc16 = descriptor<DT, false>(kOuts * CG, w.nt);
@@ -778,10 +804,6 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         if (issuer) mbar_arrive(&ss.list_empty[i & 1]);
       }
       if (pair == 0 && issuer) commit<CG>(&ss.acc_full[buf]);
-    }
-    if (*fail && pair == 0 && issuer) {
-      commit<CG>(&ss.idle);
-      mbar_wait_cycles(&ss.idle, 0);
     }
   } else if (AD && tid >= kDrain + 64) {
     const int id = tid - kDrain - 64;
@@ -1003,7 +1025,41 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
     cluster_sync();
   }
   __syncthreads();
+  if (CG == 2 && ss.fail && tid == 0) store_peer(peer_address(smem_u32(&ss.peer_fail), pair ^ 1), 1u);
   if (size > 1) cluster_sync();          // no block ends while another may still read or signal it
+  if (__builtin_expect(ss.fail | ss.peer_fail, 0)) {
+    // A wait ran out (for a pair: in either block). No copy may land, and no product read or write, where a block
+    // has ended.
+    if (warp == kDrain / 32 + 1) {
+      if (pair == 0 && issuer) commit<CG>(&ss.idle);
+      if (lane == 0) mbar_wait_cycles(&ss.idle, 0);
+    }
+    if (warp == kDrain / 32 && lane == 0) {
+      if (pair == 1) {
+        store_peer(peer_address(smem_u32(&ss.peer_turns), 0), ss.turns);
+        store_peer(peer_address(smem_u32(&ss.peer_mains), 0), ss.mains);
+      }
+      for (int k = 0; k < w.stages; ++k)
+        if ((ss.flying >> k) & 1u) mbar_wait_cycles(&ss.up_full[k], ((ss.ups >> k) & 1u) ^ 1u);
+    }
+    if (CG == 2) cluster_sync();
+    if (warp == kDrain / 32 && lane == 0 && pair == 0) {
+      // full counts the copies of both blocks of a pair, which may have come differently far
+      const uint32_t stages = w.stages, bytes = (w.outs + mine) * 128;
+      const uint32_t own = ss.turns, peer = CG == 2 ? ss.peer_turns : own, all = max(own, peer);
+      for (uint32_t k = all > stages ? all - stages : 0; k < all; ++k) {
+        const uint32_t at = k % stages;
+        if (k >= peer && ((ss.mains >> at) & 1u)) mbar_complete_tx(&ss.full[at], bytes);     // that never come
+        if (k >= own) {
+          if (!((ss.peer_mains >> at) & 1u)) continue;
+          mbar_expect_tx(&ss.full[at], bytes);
+        }
+        mbar_wait_cycles(&ss.full[at], (k / stages) & 1u);
+      }
+    }
+    __syncthreads();
+    if (CG == 2) cluster_sync();
+  }
   tmem_fence_after();
   if (warp == kDrain / 32 + 1) tmem_give<CG>(tmem);
 }
@@ -1259,7 +1315,7 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
       batch < 1 || batch > 65535 || n < 1 || static_cast<int64_t>(batch) * n > (1 << 24) ||
       !(dtype == DT_BF16 || dtype == DT_F16) || !(w->dtype == dtype || w->dtype == DT_E4M3) ||
       w->K < 16 || w->K > 65536 || w->K % 16 || w->O < 1 || w->O > (1 << 24) ||
-      static_cast<int64_t>(batch) * n * w->O > (int64_t{1} << 38))
+      w->wait_cycles < 0 || static_cast<int64_t>(batch) * n * w->O > (int64_t{1} << 38))
     return DT_ERR_INVALID_ARG;
   const bool e8 = w->dtype == DT_E4M3;
   const int64_t size = e8 ? 1 : 2, rows = static_cast<int64_t>(batch) * n, most = int64_t{1} << 32;
@@ -1273,6 +1329,7 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
   a.x_exps = x_exps;
   a.status = status;
   a.ldy = 2 * ldy;
+  a.limit = w->wait_cycles ? w->wait_cycles : static_cast<uint32_t>(dt::kWaitCycles);
   a.rows = static_cast<int>(rows);
   a.n = n;
   a.O = w->O;

@@ -582,6 +582,7 @@ typedef struct {
   const uint8_t *exps;
   int64_t ld;
   int O, K, dtype;
+  int wait_cycles;        /* 0; else (a test hook) waits give up after so many SM cycles, not about 2 s */
 } dt_matrix;
 typedef struct {
   const void *down, *up;

@@ -58,3 +58,34 @@ def test_clusters_of_three_streams():
         near(w.reshape(-1, c.O), c.y, c.slack)
     for m in made:
         m[0].check()
+
+
+# single blocks, one tile and several; clusters that share K; pairs, one tile and several; x A^T a row a
+# block, in single blocks and in clusters; 16 and 8 bits
+WAITS = {"single": (40, 1, 128, 700), "cluster": (8, 1, 2048, 1040), "pairs": (20, 65, 640, 2100),
+         "pairs e4m3": (20, 65, 640, 2100, 0, 0, BF, True), "pairs, many tiles": (3, 300, 64, 9000),
+         "cluster, rows": (8, 1, 2048, 1040, 16, 5), "single, rows": (40, 1, 256, 5000, 32, 9, BF, True),
+         "single, many tiles": (1, 3996, 64, 1072, 64, 2), "single, x A^T in clusters": (400, 1, 1024, 700, 128, 2),
+         "pairs, adapters": (20, 65, 640, 2100, 16, 5), "pairs e4m3, adapters": (20, 65, 640, 2100, 16, 5, FP, True),
+         "pairs, many tiles, adapters": (6, 300, 640, 9000, 64, 4, FP),
+         "pairs e4m3, many tiles, adapters": (6, 300, 640, 9000, 48, 4, BF, True)}
+
+
+@pytest.mark.parametrize("what", WAITS)
+def test_waits_that_run_out(what):
+    """Limits from one SM cycle on: a call ends by itself with DT_ERR_TIMEOUT (or, where no wait took as long, with its
+    result), and the next one is right."""
+    c = Case(*WAITS[what], seed=28)
+    p, x, ad, index, x16 = c.cuda()
+    run = lambda: dt.project(p, x, ad, index, x16, dtype=c.dtype)
+    want = run()
+    near(want.reshape(-1, c.O), c.y, c.slack)
+    for limit in (1, 200, 500, 1000, 1500, 2000, 3000, 5000, 8000, 15000, 40000):
+        p._struct.wait_cycles = limit
+        got = run()
+        said = int(p.status)
+        assert said == dt.ERR_TIMEOUT or (limit > 1 and said == dt.OK and torch.equal(got, want)), limit
+        p._struct.wait_cycles = 0
+        p.status.zero_()
+        assert torch.equal(run(), want), limit
+        p.check()

@@ -102,7 +102,7 @@ class DtMatrix(C.Structure):
 
 class DtAdapters(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("down", "up", "scale")] + \
-        [(n, C.c_int) for n in ("count", "rank")]
+        [(n, C.c_int) for n in ("count", "rank", "terms")]
 
 
 class DtError(RuntimeError):
@@ -1077,9 +1077,10 @@ class Projection:
 class Adapters:
     """Low-rank adapters of one projection: down [count][rank][K], up [count][O][rank] (bfloat16 or
     float16, dense) and scale [count] fp32 (ones when None). Adapters of lower ranks are padded
-    with zeros."""
+    with zeros. ``terms``: how many 16-bit terms hold scale x A^T before its product with B (dt_project);
+    1 takes half the workspace and rounds it as a 16-bit tensor would be."""
 
-    def __init__(self, down, up, scale=None):
+    def __init__(self, down, up, scale=None, terms: int = 2):
         dev = down.get_device()
         if down.dim() != 3 or up.dim() != 3 or down.dtype not in _TYPE16 or up.dtype != down.dtype or dev < 0 or \
                 up.get_device() != dev or not (down.is_contiguous() and up.is_contiguous()) or \
@@ -1089,10 +1090,12 @@ class Adapters:
         if scale is not None and (scale.shape != down.shape[:1] or scale.dtype != torch.float32 or
                                   not scale.is_contiguous() or scale.get_device() != dev):
             raise ValueError("scale must be a contiguous [count] float32 tensor on the adapters' device")
-        self.down, self.up, self.scale = down, up, scale
+        if terms not in (1, 2):
+            raise ValueError("terms must be 1 or 2")
+        self.down, self.up, self.scale, self.terms = down, up, scale, terms
         self.count, self.rank, self.K, self.O = down.shape[0], down.shape[1], down.shape[2], up.shape[1]
         self._dev, self._type = dev, _TYPE16[down.dtype]
-        self._struct = DtAdapters(down.data_ptr(), up.data_ptr(), _ptr(scale), self.count, self.rank)
+        self._struct = DtAdapters(down.data_ptr(), up.data_ptr(), _ptr(scale), self.count, self.rank, terms)
 
 
 def project_workspace(projection: Projection, batch: int, n: int, adapters: Adapters | None, stream=None):
@@ -1101,7 +1104,7 @@ def project_workspace(projection: Projection, batch: int, n: int, adapters: Adap
     _raw_stream(stream, projection._dev)
     if adapters is None:
         return None
-    nbytes = lib().dt_project_workspace_bytes(int(batch), int(n), adapters.rank)
+    nbytes = adapters.terms * lib().dt_project_workspace_bytes(int(batch), int(n), adapters.rank)
     if nbytes == 0:
         raise DtError("dt_project_workspace_bytes failed (invalid sizes)")
     with _made_on(stream):

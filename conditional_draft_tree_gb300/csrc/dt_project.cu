@@ -10,7 +10,11 @@
 // products meet in one accumulator and B_a is read once a tile, however its requests lie. (8-bit
 // rows: in an accumulator of their own, as the shared one is scaled at the end.) u comes from a
 // launch before, which stacks the A_a of a tile's adapters on the M side; the projection begins
-// beside it and waits for it only where it reads u.
+// beside it and waits for it only where it reads u. u is a sum in 32 bits, and the tensor cores take 16: it goes
+// as two terms, the rounded value and what the rounding left, two products with the same B_a. Results are then as
+// far from sums in fp32 in another order as without adapters (trees 1.5e-4 of y's norm, most of it y's own
+// rounding falling to the other side), with one term eight times as far (1.2e-3). Two terms add 2 to 3 us:
+// one-term figures 68.9 us for the trees below, 22.2 for the 8-bit tokens, 193.8 for the prompts.
 //
 // Measured on the GPU, inputs in rotation (K 4096): 32 trees of 65 rows to 6144 outputs, eight adapters
 // of rank 16, bf16, 68 us, 1.54 PFLOP/s (62 us without adapters; the tensor pipe 71 % active with cold
@@ -51,11 +55,11 @@ struct ProjectArgs {
   const float *scale;
   const int32_t *index;
   char *y;
-  uint16_t *u;           // [rows][rank]: scale x A^T, rounded
+  uint16_t *u;           // [terms][rows][rank]: scale x A^T, rounded, and what the rounding left, rounded
   int32_t *status;
   int64_t ldy;           // in bytes
   uint32_t limit;        // SM cycles after which a wait is given up
-  int rows, n, O, K, count, rank;
+  int rows, n, O, K, count, rank, terms;
 };
 
 struct ProjectShape {
@@ -337,6 +341,8 @@ __device__ void list_adapters(const ProjectArgs &a, int t0, int t1, AdapterList 
 // single block's: 8 tokens 17.4 to 15.9 us); a pair's tiles of 256 rows have a shallower ring
 // then (two prompts 178 to 187 us).
 __host__ __device__ constexpr int deep_of(int cg) { return cg == 1 ? 2 : 1; }
+// Sixteens of B_a's ranks in a stage, whose place of x takes each row's values of u in `terms` terms.
+__host__ __device__ constexpr int fill_of(int cg, int terms) { return cg == 2 && terms == 2 ? 2 : 4; }
 
 // Sums over the blocks of a cluster that share a tile's K. Each block owns a share of the tile's columns:
 // the others write their terms into its shared memory (where the ring was: all blocks have passed a
@@ -410,6 +416,17 @@ __device__ __noinline__ void make_finite(uint4 *p) {
 template <int DT>
 __device__ __forceinline__ uint16_t round16(float v) {
   return static_cast<uint16_t>(Half16<DT>::pack(v, 0.0f));
+}
+
+// scale x A^T of a row and a rank: one 16-bit term, or two
+template <int DT>
+__device__ __forceinline__ void store_u(const ProjectArgs &a, uint16_t *to, float v) {
+  const uint16_t first = round16<DT>(v);
+  *to = first;
+  if (a.terms == 2) {
+    const float at = Half16<DT>::unpack(first).x;
+    to[static_cast<int64_t>(a.rows) * a.rank] = round16<DT>(isfinite(at) ? v - at : 0.0f);
+  }
 }
 
 // v 2^e for any e in [-254, 256], without overflow or underflow on the way
@@ -521,7 +538,7 @@ adapter_down_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant
       uint16_t *to = a.u + static_cast<int64_t>(t0 + c) * a.rank + j;
 #pragma unroll
       for (int e = 0; e < static_cast<int>(sizeof(v) / sizeof(float)); ++e)
-        if (ss.token_slot[c + e] == want) to[e * a.rank] = round16<DT>(v[e] * scale);
+        if (ss.token_slot[c + e] == want) store_u<DT>(a, to + e * a.rank, v[e] * scale);
     };
     if (split > 1) cluster_sync();
     Shares shares(sm, w.nt, split, rank, row);
@@ -601,7 +618,7 @@ __global__ void __launch_bounds__(256) adapter_rows_kernel(const __grid_constant
     float all = 0.0f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) all += s_sum[w][threadIdx.x];
-    a.u[static_cast<int64_t>(row) * a.rank + j0 + threadIdx.x] = round16<DT>(all * (a.scale ? a.scale[at] : 1.0f));
+    store_u<DT>(a, a.u + static_cast<int64_t>(row) * a.rank + j0 + threadIdx.x, all * (a.scale ? a.scale[at] : 1.0f));
   }
 }
 
@@ -610,7 +627,7 @@ __global__ void __launch_bounds__(256) adapter_rows_kernel(const __grid_constant
 // rows of W and half of the tile's rows of x, and the first one issues the products of both. Two
 // accumulators: one is emptied while the next tile's products run; of 8-bit rows a third, for
 // adapters.
-template <int DT, bool E8, bool AD, int CG>
+template <int DT, bool E8, int AD, int CG>
 __global__ void __launch_bounds__(AD ? kDrain + 192 : kDrain + 64, 1)
 project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ ProjectShape w,
                const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
@@ -665,10 +682,13 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
     if (CG == 2) arrive_peer(first_block(bar));
     else mbar_arrive(bar);
   };
-  // the adapters' part of K in sixteens, four a stage; this block's stages of them
+  // The adapters' part of K in sixteens, `fill` a stage; this block's stages of them. The second terms of u lie behind
+  // the first ones, in the place of a second slab of x (single blocks) or of its second half.
+  constexpr int fill = fill_of(CG, AD);
+  const int second = fill * mine * 32;
   auto sixteens_of = [&](const AdapterList &l) { return l.count * (a.rank >> 4); };
   auto share = [&](int all, int *q0, int *q1) {
-    const int n = (all + 3) >> 2;
+    const int n = (all + fill - 1) / fill;
     *q0 = n * rank / split;
     *q1 = n * (rank + 1) / split;
   };
@@ -704,13 +724,13 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       const int all = sixteens_of(l), per = a.rank >> 4, wide = w.piece >> 4;
       int q0, q1;
       share(all, &q0, &q1);
-      int u = 4 * q0 / per, j = 4 * q0 - u * per;        // adapter, and the sixteen of its rank
+      int u = fill * q0 / per, j = fill * q0 - u * per;  // adapter, and the sixteen of its rank
       for (int q = q0; q < q1; ++q) {
         if (!(go = wait(&ss.empty[p.at], p.parity ^ 1u))) break;
         if (issuer) mbar_arrive(&ss.u_go[p.at]);
         unsigned char *to = sm + p.at * stage;
         const uint32_t bar = smem_u32(&ss.up_full[p.at]);
-        const int here = min(4, all - 4 * q);
+        const int here = min(fill, all - fill * q);
         if (issuer) {
           if (pair == 0) mbar_arrive(&ss.full[p.at]);     // (it counts the ring's turns)
           mbar_expect_tx(&ss.up_full[p.at], here * w.outs * 32);
@@ -784,15 +804,15 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
             phases ^= 1u << p.at;
             tmem_fence_after();
             const uint32_t at = smem_u32(sm) + p.at * stage;
-            const int here = min(4, all - 4 * q);
+            const int here = min(fill, all - fill * q);
             const uint64_t da = rows_of(at, w.piece), db = rows_of(at + slab_x, w.piece);
             if (issuer) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
+              for (int k = 0; k < fill; ++k) {
                 const int first_of = k & ~(wide - 1), in = 2 * (k - first_of);     // of its piece; 32 bytes on
-                if (k < here)
-                  mma<CG, false>(to, da + first_of * kOuts * 2 + in, db + first_of * mine * 2 + in, idesc16,
-                                 !E8 || q > q0 || k > 0);
+                const uint64_t dw = da + first_of * kOuts * 2 + in, du = db + first_of * mine * 2 + in;
+                if (k < here) mma<CG, false>(to, dw, du, idesc16, !E8 || q > q0 || k > 0);
+                if (AD == 2 && k < here) mma<CG, false>(to, dw, du + second / 16, idesc16, true);
               }
               commit<CG>(&ss.empty[p.at]);
             }
@@ -810,13 +830,12 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
     uint32_t at = 0, phases = 0;               // stage of the ring; phases of u_go
     bool marked[2] = {false, false};           // this thread's row of ss.odd has something
     // Where a thread's sixteens lie in a stage, as offsets of their first halves (the second ones 16 bytes
-    // away, before or behind): of row `id` of the rows u, and of B_a's. Row id + 128 of u lies as
-    // row id does.
+    // away, before or behind): of row `id` of the rows u (there are 128 at most), and of B_a's.
     const int row_bytes = 2 * w.piece, chunks = w.piece >> 3;      // of a piece's row
     const int shift = w.piece == 64 ? 0 : w.piece == 32 ? 1 : 2;   // rows of one swizzle
-    int u_at[4], b_at[4];
+    int u_at[fill], b_at[fill];
 #pragma unroll
-    for (int z = 0; z < 4; ++z) {
+    for (int z = 0; z < fill; ++z) {
       const int c = 2 * z & (chunks - 1), in = id * row_bytes + 16 * (c ^ ((id >> shift) & (chunks - 1)));
       u_at[z] = slab_x + (2 * z - c) * mine * 16 + in;
       b_at[z] = (2 * z - c) * kOuts * 16 + in;
@@ -835,27 +854,23 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
       mbar_arrive(&ss.list_full[i & 1]);
       if (i == 0) cudaGridDependencySynchronize();        // u is there
       const int all = sixteens_of(l), per = a.rank >> 4;
-      int q0, q1, slot[2];
-      const uint16_t *u[2];
+      int q0, q1;
       share(all, &q0, &q1);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = id + 128 * k, row = x0 + r;
-        slot[k] = r < mine && row < a.rows ? l.slot[row / a.n - l.first] : -1;
-        u[k] = a.u + static_cast<int64_t>(row) * a.rank;
-      }
+      const int row = x0 + id, slot = id < mine && row < a.rows ? l.slot[row / a.n - l.first] : -1;
+      const uint16_t *u[2];                    // the terms
+      u[0] = a.u + static_cast<int64_t>(row) * a.rank;
+      u[1] = u[0] + static_cast<int64_t>(a.rows) * a.rank;
       at = (at + (k1 - k0 + deep - 1) / deep) % w.stages;
-      uint4 v[2][4][2];
-      int of = 4 * q0 / per, j = 4 * q0 - of * per, whose[4];   // adapter and sixteen of its rank to be fetched
+      uint4 v[2][fill][2];
+      int of = fill * q0 / per, j = fill * q0 - of * per, whose[fill];   // adapter and sixteen of its rank to be fetched
       auto fetch = [&](int q) {                // loads of the next stage's rows, before there is room
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          whose[z] = 4 * q + z < all ? of : -2;
+        for (int z = 0; z < fill; ++z) {
+          whose[z] = fill * q + z < all ? of : -2;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (k == 1 && mine <= 128) break;
-            v[k][z][0] = load_if(u[k] + 16 * j, whose[z] == slot[k]);
-            v[k][z][1] = load_if(u[k] + 16 * j + 8, whose[z] == slot[k]);
+          for (int k = 0; k < AD; ++k) {
+            v[k][z][0] = load_if(u[k] + 16 * j, whose[z] == slot);
+            v[k][z][1] = load_if(u[k] + 16 * j + 8, whose[z] == slot);
           }
           if (++j == per) j = 0, ++of;
         }
@@ -867,18 +882,18 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         phases ^= 1u << at;
         unsigned char *const place = sm + at * stage;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (id + 128 * k >= mine) break;
+        for (int k = 0; k < AD; ++k) {
+          if (id >= mine) break;
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int to = u_at[z] + 128 * k * row_bytes;
+          for (int z = 0; z < fill; ++z) {
+            const int to = u_at[z] + k * second;
             *reinterpret_cast<uint4 *>(place + to) = v[k][z][0];
             *reinterpret_cast<uint4 *>(place + (to ^ 16)) = v[k][z][1];
           }
         }
-        int looked[4];
+        int looked[fill];
 #pragma unroll
-        for (int z = 0; z < 4; ++z) looked[z] = whose[z];
+        for (int z = 0; z < fill; ++z) looked[z] = whose[z];
         __syncwarp();
         if (q + 1 < q1) fetch(q + 1);          // (on its way while this stage's B_a is looked through)
         // B_a's rows stand beside zeros of other requests' rows: what is not finite there would reach them.
@@ -886,9 +901,9 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
         // output is NaN for the rows with that adapter.
         go = wait(&ss.up_full[at], parity);
         if (go && id < w.outs) {
-          uint32_t most[4];
+          uint32_t most[4] = {};
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
+          for (int z = 0; z < fill; ++z) {
             const uint4 lo = *reinterpret_cast<const uint4 *>(place + b_at[z]);
             const uint4 hi = *reinterpret_cast<const uint4 *>(place + (b_at[z] ^ 16));
             most[z] = top_abs<DT>(top_abs<DT>(top_abs<DT>(lo.x, lo.y), top_abs<DT>(lo.z, lo.w)),
@@ -896,7 +911,7 @@ project_kernel(const __grid_constant__ ProjectArgs a, const __grid_constant__ Pr
           }
           if (not_finite<DT>(top_abs<DT>(top_abs<DT>(most[0], most[1]), top_abs<DT>(most[2], most[3])))) {
 #pragma unroll
-            for (int z = 0; z < 4; ++z)
+            for (int z = 0; z < fill; ++z)
               if (looked[z] >= 0 && not_finite<DT>(most[z])) {
                 make_finite<DT>(reinterpret_cast<uint4 *>(place + b_at[z]));
                 make_finite<DT>(reinterpret_cast<uint4 *>(place + (b_at[z] ^ 16)));
@@ -1134,8 +1149,9 @@ double slab_cycles(int outs, int nt, int cg) {
 // by four blocks, of 64 by two and of 32 by one, 23.5, 23.0 and 23.8 us.
 void choose(const ProjectArgs &a, bool e8, bool ad, const Rooms &room, int smem, ProjectPlan *p) {
   const int size = e8 ? 1 : 2, steps = ceil_div(static_cast<int64_t>(a.K) * size, 128);
-  // of a pair; with adapters three accumulators instead of two. Of a single block: three stages
-  const int most[3] = {0, 144, ad && e8 ? 160 : kMaxTokens};
+  // of a pair; with adapters three accumulators instead of two. Of a single block: three stages; with adapters a thread
+  // a row of u
+  const int most[3] = {0, ad ? 128 : 144, ad && e8 ? 160 : kMaxTokens};
   const double memory = (static_cast<double>(a.O) + a.rows) * a.K * size / kMemoryRate;
   double best = 1e300;
   for (int cg = 1; cg <= 2; ++cg)
@@ -1173,6 +1189,7 @@ void choose(const ProjectArgs &a, bool e8, bool ad, const Rooms &room, int smem,
   p->s.stages = stages_of(smem, stage);
   p->s.off_small = p->s.stages * stage;
   p->s.piece = a.rank % 64 == 0 ? 64 : a.rank % 32 == 0 ? 32 : 16;
+  p->s.piece = std::min(p->s.piece, 16 * fill_of(p->cg, a.terms));
   p->smem = p->s.off_small + sizeof(Small);
 }
 
@@ -1260,7 +1277,7 @@ cudaError_t launch_down(const ProjectArgs &a, const ProjectShape &s, const dt_ad
                                                  false, st, a, s, down, x);
 }
 
-template <int DT, bool E8, bool AD, int CG>
+template <int DT, bool E8, int AD, int CG>
 cudaError_t launch_main(const ProjectArgs &a, const ProjectPlan &p, const CUtensorMap &w, const CUtensorMap &x,
                         const CUtensorMap &up, int smem, cudaStream_t st) {
   constexpr auto kernel = project_kernel<DT, E8, AD, CG>;
@@ -1270,7 +1287,7 @@ cudaError_t launch_main(const ProjectArgs &a, const ProjectPlan &p, const CUtens
                                 a, p.s, w, x, up);
 }
 
-template <int DT, bool E8, bool AD>
+template <int DT, bool E8, int AD>
 cudaError_t launch_project(const ProjectArgs &a, const dt_matrix &m, const void *x, int64_t ldx,
                            const dt_adapters *ad, const void *x16, int64_t ldx16, const Rooms &room, int smem,
                            cudaStream_t st) {
@@ -1337,10 +1354,10 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
   if (adapters) {
     if (!adapters->down || !adapters->up || !dt::al16(adapters->down) || !dt::al16(adapters->up) ||
         (reinterpret_cast<uintptr_t>(adapters->scale) & 3u) || adapters->count < 1 ||
-        adapters->count > (1 << 20) || adapters->rank < 16 || adapters->rank > 128 || adapters->rank % 16 ||
+        adapters->count > (1 << 20) || adapters->terms < 0 || adapters->terms > 2 || adapters->rank < 16 || adapters->rank > 128 || adapters->rank % 16 ||
         (reinterpret_cast<uintptr_t>(index) & 3u) || !workspace ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-        workspace_bytes < dt_project_workspace_bytes(batch, n, adapters->rank) ||
+        workspace_bytes < std::max(adapters->terms, 1) * dt_project_workspace_bytes(batch, n, adapters->rank) ||
         static_cast<int64_t>(adapters->count) * w->O > 0x7fffff00 ||
         static_cast<int64_t>(adapters->count) * adapters->rank > 0x7fffff00)
       return DT_ERR_INVALID_ARG;
@@ -1353,6 +1370,7 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
     a.index = index;
     a.count = adapters->count;
     a.rank = adapters->rank;
+    a.terms = std::max(adapters->terms, 1);
     a.u = static_cast<uint16_t *>(workspace);
   }
   int sms, smem;
@@ -1366,8 +1384,10 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
         a, *w, x, ldx * size, adapters, x16, 2 * ldx16, room, smem, st);
   };
   auto typed = [&](auto type) {
-    if (e8) return adapters ? go(type, std::true_type{}, std::true_type{}) : go(type, std::true_type{}, std::false_type{});
-    return adapters ? go(type, std::false_type{}, std::true_type{}) : go(type, std::false_type{}, std::false_type{});
+    auto with = [&](auto terms) { return e8 ? go(type, std::true_type{}, terms) : go(type, std::false_type{}, terms); };
+    return a.terms == 2   ? with(std::integral_constant<int, 2>{})
+           : a.terms == 1 ? with(std::integral_constant<int, 1>{})
+                          : with(std::integral_constant<int, 0>{});
   };
   const cudaError_t e = dtype == DT_BF16 ? typed(std::integral_constant<int, DT_BF16>{})
                                          : typed(std::integral_constant<int, DT_F16>{});

@@ -557,9 +557,11 @@ int dt_quantize_rows(const dt_rows *x, uint8_t *codes, uint8_t *exps, int outer,
  * it: for row i of request b, with a = index[b],
  *   y = x W^T + scale[a] (x A_a^T) B_a^T,
  * the second term only where 0 <= a < adapters->count (a negative index: no adapter; one at or
- * above count: none, and DT_ERR_BAD_INDEX in *status). Products are accumulated in fp32; x A^T, times
- * the scale, is rounded to dtype (and so overflows where dtype does) before the
- * product with B, y once. A row of B with a value that is not finite makes that output NaN for
+ * above count: none, and DT_ERR_BAD_INDEX in *status). Products are accumulated in fp32; y is rounded once.
+ * Before the product with B x A^T, times the scale, is held in 16-bit terms of type dtype: two (terms = 2), the
+ * second one what rounding the first left, so that 2^-16 of a value is lost in bf16 and 2^-22 in fp16 (or
+ * 2^-25, its least step's half, where that is more); or one (terms 0 or 1), half the workspace and a stage's copies,
+ * 2^-8 and 2^-11. Either overflows where dtype does. A row of B with a value that is not finite makes that output NaN for
  * the rows with that adapter; what is not finite elsewhere reaches the rows that use it alone.
  *   w      W [O][K], dtype 16-bit or DT_E4M3 with exps [O] (8-bit rows); data 16-byte
  *          aligned, row stride ld elements, a multiple of 16 bytes
@@ -574,9 +576,9 @@ int dt_quantize_rows(const dt_rows *x, uint8_t *codes, uint8_t *exps, int outer,
  *   index  [batch] int32; with adapters only
  *   status one int32 of the caller's, zeroed once: DT_ERR_BAD_INDEX, DT_ERR_TIMEOUT
  * K: a multiple of 16 in [16, 65536]; O in [1, 2^24]; rank: a multiple of 16 in [16, 128];
- * batch in [1, 65535], batch n <= 2^24, batch n O <= 2^38. workspace: dt_project_workspace_bytes bytes,
- * 256-byte aligned, for x A^T (may be 0: NULL without adapters); the size for a batch, n and
- * rank serves smaller ones. Sums run in an order fixed by the sizes: results repeat. */
+ * batch in [1, 65535], batch n <= 2^24, batch n O <= 2^38. workspace: `terms` times
+ * dt_project_workspace_bytes bytes, 256-byte aligned, for x A^T (may be 0: NULL without adapters); the size
+ * for a batch, n and rank serves smaller ones. Sums run in an order fixed by the sizes: results repeat. */
 typedef struct {
   const void *data;
   const uint8_t *exps;
@@ -588,6 +590,7 @@ typedef struct {
   const void *down, *up;
   const float *scale;
   int count, rank;
+  int terms;              /* 16-bit terms of x A^T: 0 or 1, or 2 */
 } dt_adapters;
 size_t dt_project_workspace_bytes(int batch, int n, int rank);
 int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_exps, int batch,

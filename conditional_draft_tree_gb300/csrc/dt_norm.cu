@@ -170,10 +170,12 @@ __global__ void __maxnreg__(REGS) rms_norm_kernel(const __grid_constant__ NormAr
   };
   const bool again = !WIDE && (lane & 31) == 0;               // its chunk counts for the warp before
   const int chunks = (a.d + 7) >> 3;
-  // (bytes beside the row, but within the tensor's memory [lo, hi), may be read: words() drops them)
+  // Granules that hold some of the row's values are read, and no others: memory between the rows need not be there.
+  // (What else lies in them is dropped by words(); the tensor's first and last ones are read by value.)
   auto load = [&](const char *p, const char *lo, const char *hi, bool there, uint32_t (&w)[ITEMS][kWords]) {
     const int off = WIDE ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
     const bool inside = p - 16 >= lo && p + 2 * a.d + 32 <= hi;      // (all rows but the first and the last)
+    const bool after = 16 * chunks - off < 2 * a.d;       // the last chunk ends behind its first granule
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
       const int c = chunk(it);
@@ -184,7 +186,7 @@ __global__ void __maxnreg__(REGS) rms_norm_kernel(const __grid_constant__ NormAr
           v = *reinterpret_cast<const uint4 *>(g);
         } else if (inside) {
           v = *reinterpret_cast<const uint4 *>(g);
-          z = *reinterpret_cast<const uint4 *>(g + 16);
+          if (c + 1 < chunks || after) z = *reinterpret_cast<const uint4 *>(g + 16);
         } else {
           v = load_end(g, lo, hi);
           z = load_end(g + 16, lo, hi);

@@ -1064,8 +1064,8 @@ class Projection:
         self.weight, self.O, self.K, self.device = weight, t.shape[0], t.shape[1], t.device
         self._dev, self._type = t.get_device(), E4M3 if exps is not None else _TYPE16[t.dtype]
         self.status = torch.zeros(1, dtype=torch.int32, device=t.device)
-        self._struct = DtMatrix(t.data_ptr(), _ptr(exps), max(t.stride(0), self.K) if self.O == 1 else t.stride(0),
-                                self.O, self.K, self._type)
+        self._struct = DtMatrix(t.data_ptr(), _ptr(exps), self.K if self.O == 1 else t.stride(0), self.O, self.K,
+                                self._type)
 
     def check(self):
         """Wait for the device and raise if a call met a bad adapter index or timed out."""
@@ -1116,7 +1116,7 @@ def _flat_rows(t, what: str, batch: int, n: int):
     s = t.stride()
     if s[2] != 1 or (batch > 1 and n > 1 and s[0] != n * s[1]):
         raise ValueError(f"{what}'s rows must be dense and lie at one stride")
-    return s[1] if n > 1 else s[0] if batch > 1 else max(s[0], s[1], t.shape[2])
+    return s[1] if n > 1 else s[0] if batch > 1 else t.shape[2]      # (of a single row: none that counts)
 
 
 def project(projection: Projection, x, adapters: Adapters | None = None, index=None, x16=None, dtype=None,

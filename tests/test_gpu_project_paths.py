@@ -89,3 +89,22 @@ def test_waits_that_run_out(what):
         p.status.zero_()
         assert torch.equal(run(), want), limit
         p.check()
+
+
+@pytest.mark.parametrize("e8", [False, True])
+def test_the_last_row_of_a_long_sequence(e8):
+    """A single row whose tensor's strides are those of what it was cut from, and a row of results likewise."""
+    c = Case(1, 1, 80, 37, 16, 2, BF, e8, index=[1], seed=29)
+    p, x, ad, index, x16 = c.cuda()
+    want = dt.project(p, x, ad, index, x16, dtype=BF)
+    near(want.reshape(-1, 37), c.y, c.slack)
+    last = lambda t, rows, more: torch.cat([torch.zeros(1, rows, t.shape[2] + more, dtype=t.dtype, device="cuda")], 1)[:, -1:, :t.shape[2]].copy_(t)
+    if e8:
+        y = dt.Rows8(last(x.codes.view(torch.uint8), 3, 5 * 16 + 48), x.exps)
+        y16 = last(x16, 4, 8)
+    else:
+        y, y16 = last(x, 1, 16), None
+    frame = torch.full((1, 40000, 1700), 7.0, dtype=BF, device="cuda")          # 40000 * 1700 > 2^26
+    got = dt.project(p, y, ad, index, y16, dtype=BF, out=frame[:, -1:, 3:40])
+    assert torch.equal(got, want)
+    assert bool((frame[0, :-1] == 7).all()) and bool((frame[0, -1, :3] == 7).all()) and bool((frame[0, -1, 40:] == 7).all())

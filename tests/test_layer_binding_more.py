@@ -17,3 +17,27 @@ def test_two_terms_take_twice_the_workspace(lib):
     for terms in (0, 3):
         with pytest.raises(ValueError, match="terms"):
             dt.Adapters(Tensor(4, 16, K), Tensor(4, O, 16), terms=terms)
+
+
+class Strided(Tensor):
+    def __init__(self, *shape, strides, **kw):
+        super().__init__(*shape, **kw)
+        self.strides = strides
+
+    def stride(self, *d):
+        return self.strides[d[0]] if d else self.strides
+
+
+@pytest.mark.parametrize("strides", [(K, K, 1), (5 * K, K, 1), (7, 9, 1), (1 << 40, K + 3, 1)])
+def test_the_stride_of_a_single_row_does_not_count(lib, strides):
+    """The last row of a long sequence, or a row of a padded one: its distance to a next row may be past what a call
+    takes, or no multiple of 16 bytes."""
+    x = Strided(1, 1, K, strides=strides)
+    out = Strided(1, 1, O, strides=strides)
+    dt.project(projection(), x, out=out)
+    args = lib.calls[-1][1]
+    assert (args[2], args[12]) == (K, O)
+    assert dt.Projection(Strided(1, K, strides=strides[1:]))._struct.ld == K
+    one = Strided(2, 1, K, strides=(96, 7, 1))          # of several, the first stride does
+    dt.project(projection(), one)
+    assert lib.calls[-1][1][2] == 96

@@ -998,7 +998,7 @@ def rms_norm(norm: Norm, x, residual=None, kind: str = "16", out=None, total=Non
     """dt_rms_norm of the rows x [...][d], of x + residual where that is given. ``kind``: "16" (a
     tensor of x's type), "e4m3" (a Rows8), or "both" ((tensor, Rows8), from the same fp32 values).
     Returns that, and with ``residual`` also the sum: (y, total). ``total`` and ``out`` may be
-    x or residual."""
+    x and residual, in either order, but not the same."""
     if kind not in ("16", "e4m3", "both"):
         raise ValueError('kind must be "16", "e4m3" or "both"')
     dtype, dev, w = _TYPE16.get(x.dtype), x.get_device(), norm.weight

@@ -478,6 +478,7 @@ int norm_rows(const dt_rows *x, const dt_rows *residual, const dt_rows *total, c
     return DT_ERR_INVALID_ARG;
   for (const dt_rows *v : {residual, total, out})
     if (v && (!v->data || !al2(v->data))) return DT_ERR_INVALID_ARG;
+  if (total && out && total->data == out->data) return DT_ERR_INVALID_ARG;      // one of the two would be lost
   NormArgs a = {};
   a.x = static_cast<const char *>(x->data);
   bool wide = view_wide(x, &a.xo, &a.xi) && d % 8 == 0 &&

@@ -537,8 +537,8 @@ int dt_cache_slots(const dt_cache *c, int n, const int32_t *first, const int32_t
  * computed in fp32. total (with residual only) gets t, out gets y, rounded once each;
  * codes and exps get y in 8 bits, taken from fp32. out, or codes and exps, may be NULL,
  * not both. weight [d] has the rows' type (NULL: ones). An output may be one of the inputs
- * (the same view), and must not overlap them otherwise; codes and exps are buffers of
- * their own. d in [1, 32768], dtype DT_BF16 or DT_F16, eps >= 1e-30. Rows of a multiple
+ * (the same view), and must not overlap them otherwise, nor another output (total and out that
+ * begin at the same place are refused); codes and exps are buffers of their own. d in [1, 32768], dtype DT_BF16 or DT_F16, eps >= 1e-30. Rows of a multiple
  * of 8 values on 16-byte boundaries are moved 16 bytes at a time. Others are too, in the aligned 16-byte granules
  * that they lie in: what else a granule between a view's first and last value holds is read with it and
  * plays no part, and only the row's values are written.

@@ -736,6 +736,7 @@ class PagedCache:
 
     def check(self):
         """Wait for the device and raise if a call met a bad page or timed out."""
+        torch.cuda.synchronize(self.device)     # calls may have run on any stream
         bad = [(b, c) for b, c in enumerate(self.status.tolist()) if c != OK]
         if bad:
             raise DtError("paged cache: " + ", ".join(f"request {b}: {status_string(c)}"
@@ -1069,6 +1070,7 @@ class Projection:
 
     def check(self):
         """Wait for the device and raise if a call met a bad adapter index or timed out."""
+        torch.cuda.synchronize(self.device)     # calls may have run on any stream
         code = int(self.status)
         if code != OK:
             raise DtError(f"projection: {status_string(code)}")

@@ -108,3 +108,24 @@ def test_the_last_row_of_a_long_sequence(e8):
     got = dt.project(p, y, ad, index, y16, dtype=BF, out=frame[:, -1:, 3:40])
     assert torch.equal(got, want)
     assert bool((frame[0, :-1] == 7).all()) and bool((frame[0, -1, :3] == 7).all()) and bool((frame[0, -1, 40:] == 7).all())
+
+
+def test_check_waits_for_calls_on_every_stream():
+    """What a call on a stream of its own has to report is there when check() returns."""
+    c = Case(2, 3, 64, 40, 16, 2, index=[0, 5], seed=30)
+    p, x, ad, index, _ = c.cuda()
+    table = torch.tensor([[9, 0]], dtype=torch.int32, device="cuda")
+    cache = dt.PagedCache.empty(4, 1, 16, 16, table)
+    first = torch.zeros(1, dtype=torch.int32, device="cuda")
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(200_000_000)          # some 0.1 s
+        dt.project(p, x, ad, index)
+    with pytest.raises(dt.DtError, match="adapter index"):
+        p.check()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(200_000_000)
+        dt.cache_slots(cache, 3, first)
+    with pytest.raises(dt.DtError, match="request 0"):
+        cache.check()

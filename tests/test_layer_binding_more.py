@@ -41,3 +41,28 @@ def test_the_stride_of_a_single_row_does_not_count(lib, strides):
     one = Strided(2, 1, K, strides=(96, 7, 1))          # of several, the first stride does
     dt.project(projection(), one)
     assert lib.calls[-1][1][2] == 96
+
+
+def test_check_waits_for_the_device(monkeypatch):
+    """Not for the current stream alone: the status is read once all streams are done."""
+    said = []
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda dev=None: said.append(dev))
+
+    class Status(Tensor):
+        def __int__(self):
+            assert said == ["cuda:0"]
+            return dt.ERR_BAD_INDEX
+
+        def tolist(self):
+            assert said == ["cuda:0"]
+            return [0, dt.ERR_NO_PAGES]
+    monkeypatch.setattr(dt, "status_string", str)
+    p = projection()
+    p.status = Status(1, dtype=torch.int32)
+    with pytest.raises(dt.DtError, match="-9"):
+        p.check()
+    said.clear()
+    cache = dt.PagedCache.__new__(dt.PagedCache)
+    cache.device, cache.status = "cuda:0", Status(2, dtype=torch.int32)
+    with pytest.raises(dt.DtError, match="request 1: -8"):
+        cache.check()

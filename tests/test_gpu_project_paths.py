@@ -129,3 +129,94 @@ def test_check_waits_for_calls_on_every_stream():
         dt.cache_slots(cache, 3, first)
     with pytest.raises(dt.DtError, match="request 0"):
         cache.check()
+
+
+@pytest.mark.parametrize("batch,n,K,O,rank,count,dtype,e8", [(2, 3, 65536, 200, 128, 2, BF, False), (9, 1, 65536, 40, 16, 3, FP, True),
+                                                             (1, 300, 65536, 300, 16, 1, BF, True), (65535, 1, 16, 24, 16, 3, BF, False),
+                                                             (5, 1, 32, 140000, 16, 4, FP, False)])
+def test_the_largest_sizes(batch, n, K, O, rank, count, dtype, e8):
+    Case(batch, n, K, O, rank, count, dtype, e8, seed=33).check()
+
+
+def test_adapters_past_32_bits():
+    """B of more than 4 GB, and values of A past 2^31: the last adapters' places."""
+    count, rank, K, O, batch, n = 3000, 64, 16384, 20000, 5, 9
+    g = torch.Generator().manual_seed(34)
+    rnd = lambda *s: torch.randn(s, generator=g).to(BF)
+    x, w = rnd(batch * n, K), rnd(O, K) * K ** -0.5
+    used = [count - 1, 0, count - 2, -1, 2047]
+    ad = dt.Adapters(torch.zeros(count, rank, K, dtype=BF, device="cuda"), torch.zeros(count, O, rank, dtype=BF, device="cuda"))
+    small = {a: i for i, a in enumerate(sorted(set(used) - {-1}))}
+    down, up = rnd(len(small), rank, K) * K ** -0.5, rnd(len(small), O, rank) * rank ** -0.5
+    for a, i in small.items():
+        ad.down[a], ad.up[a] = down[i].cuda(), up[i].cuda()
+    index = torch.tensor([small.get(a, -1) for a in used], dtype=torch.int32)
+    y = R.project(x.double(), w.double(), n, index, x, down, up)
+    slack = R.project_slack(x.double(), w.double(), n, y, BF, index, x, down, up)
+    p = dt.Projection(w.cuda())
+    got = dt.project(p, x.cuda().view(batch, n, K), ad, torch.tensor(used, dtype=torch.int32, device="cuda"))
+    near(got.reshape(-1, O), y, slack)
+    p.check()
+
+
+FIRST = """
+import torch, conditional_draft_tree_gb300 as dt
+g = torch.Generator().manual_seed(0)
+rnd = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16).cuda()
+x, w, down, up = rnd(20, 65, 640), rnd(2100, 640), rnd(3, 16, 640), rnd(3, 2100, 16)
+index = torch.tensor([b % 4 - 1 for b in range(20)], dtype=torch.int32, device="cuda")
+weight = rnd(640)
+p, ad, norm = dt.Projection(w), dt.Adapters(down, up), dt.Norm(weight)
+table = torch.full((20, 9), -1, dtype=torch.int32, device="cuda")
+cache = dt.PagedCache.empty(180, 1, 16, 16, table)
+pool = dt.PagePool.all_free(cache)
+lengths, first = (torch.full((20,), v, dtype=torch.int32, device="cuda") for v in (100, 35))
+def run():
+    dt.cache_reserve(pool, lengths)
+    places = dt.cache_slots(cache, 65, first)
+    y, total = dt.rms_norm(norm, x, x)
+    return (dt.project(p, y, ad, index), total) + places
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+want = run()
+assert all(torch.equal(a, b) for a, b in zip(got, want)), "first"
+p.check(); cache.check()
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_are_captured():
+    """Kernels, limits and clusters that a process has not met yet, under a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_threads_that_call_at_once():
+    """Calls of four host threads, each on a stream of its own."""
+    import threading
+    cases = [Case(20, 65, 320, 2100, 16, 5, seed=35), Case(8, 1, 2048, 1040, 16, 5, seed=36), Case(40, 7, 128, 260, 112, 40, FP, True, seed=37),
+             Case(3, 400, 512, 900, 64, 3, FP, seed=38)]
+    made = [c.cuda() for c in cases]
+    wants = [dt.project(*m, dtype=c.dtype) for c, m in zip(cases, made)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        got = [dt.project(*made[(i + k) % 4], dtype=cases[(i + k) % 4].dtype, stream=stream) for k in range(40)]
+        stream.synchronize()
+        wrong.extend((i, k) for k, y in enumerate(got) if not torch.equal(y, wants[(i + k) % 4]))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    for m in made:
+        m[0].check()

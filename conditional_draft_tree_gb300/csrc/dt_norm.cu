@@ -10,8 +10,14 @@
 //
 // Bound by memory where rows lie on 16-byte boundaries: 262336 heads of 128 fp16 values 25.5 us, 5.3
 // TB/s; 8192 rows of 4096 with their sum 41.8 us, 6.4 TB/s; 2080 of them, much of them in L2, 9.4 us,
-// to 16 and 8 bits 12.0; eight 2.3. Rows off such boundaries are bound by instructions (shifts, shuffles,
-// the ends): 4099 of 5001 values 56 us, 2.9 TB/s, where loads and stores of single values took 163.
+// to 16 and 8 bits 12.0; eight 2.3. Rows to 8 bits alone: 8192 of 4096 25.8 us, 3.9 TB/s, 2080 8.1. Rows off such
+// boundaries: 4099 of 5001 values 56 us, 2.9 TB/s, where loads and stores of single values took 163. Instructions
+// (shifts, shuffles, the ends) and latency bound them together: 62 a value, which at full rate would be 32 us, issued
+// in 53 % of the cycles by 22 warps an SM (two blocks, by registers, without a row ahead) that wait for
+// results and loads most, for barriers and shared memory next; DRAM is 28 % busy. Forms of more than two chunks a thread
+// in few registers spill: aligned rows above 16384 values 2500 of 16392 108 us, 3.0 TB/s, 1300 of 32768 88, 3.9
+// (16384: 54 us, 6.1 TB/s); off boundaries above 15864, 2500 of 15871 182 us, 1.75 TB/s (15863: 106, 3.0), 1300
+// of 32767 189.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

@@ -13,15 +13,17 @@
 // beside it and waits for it only where it reads u. u is a sum in 32 bits, and the tensor cores take 16: it goes
 // as two terms, the rounded value and what the rounding left, two products with the same B_a. Results are then as
 // far from sums in fp32 in another order as without adapters (trees 1.5e-4 of y's norm, most of it y's own
-// rounding falling to the other side), with one term eight times as far (1.2e-3). Two terms add 2 to 3 us:
-// one-term figures 68.9 us for the trees below, 22.2 for the 8-bit tokens, 193.8 for the prompts.
+// rounding falling to the other side), with one term eight times as far (1.2e-3). The second term costs 2 to 3
+// us: with one the trees below take 69 us for 71, the 8-bit tokens 22 for 25.
 //
 // Measured on the GPU, inputs in rotation (K 4096): 32 trees of 65 rows to 6144 outputs, eight adapters
-// of rank 16, bf16, 68 us, 1.54 PFLOP/s (62 us without adapters; the tensor pipe 71 % active with cold
-// caches); two prompts of 4099 rows to 4001, rank 64, fp16, 178 to 185 us, 1.5 PFLOP/s; 8224 rows of
-// 8-bit codes to 6144 117 to 119 us, 3.5 PFLOP/s; one token of 8 requests to 6144 16 us, of which W's
-// 50 MB from memory are 8; of 128 requests with 64 adapters of rank 32, 8-bit, to 4096 23.5 us. Large
-// cases are bound by the tensor cores, at the clock that power leaves them, and by tiles that
+// of rank 16, bf16, 71 to 72 us, 1.46 PFLOP/s (62 to 63 us without adapters; the tensor pipe 72 % active with
+// cold caches); two prompts of 4099 rows to 4001, rank 64, fp16, 190 to 196 us, 1.4 PFLOP/s; 8224 rows of
+// 8-bit codes to 6144 120 us, 3.45 PFLOP/s; one token of 8 requests to 6144 16 us, of which W's
+// 50 MB from memory are 8; of 128 requests with 64 adapters of rank 32, 8-bit, to 4096 25.4 us. These are
+// bursts of a few ms at 2070 MHz. Calls of 2 s in a row come to the power limit (1250 to 1290 W): trees 79 us
+// at 1770 MHz, prompts 208 at 1650, 8-bit rows 139 at 1477; the small cases keep the clock and their times.
+// Large cases are bound by the tensor cores, at the clock that power leaves them, and by tiles that
 // do not fill a last round. A pair's slab (128 bytes of K), with one tile a pair and from the
 // times of K = 2048, 4096 and 8192: 256 rows 282 to 295 ns with 8-bit codes and 275 to 305 with
 // 16 bits, where 2.25 and 4.5 PFLOP/s would be 283; 128 rows 183 to 186 and 181 to 210, where
@@ -339,7 +341,7 @@ __device__ void list_adapters(const ProjectArgs &a, int t0, int t1, AdapterList 
 
 // Slabs of a stage. Two halve what its waits and issuing take, for tiles whose products take less (a
 // single block's: 8 tokens 17.4 to 15.9 us); a pair's tiles of 256 rows have a shallower ring
-// then (two prompts 178 to 187 us).
+// then (two prompts, u in one term, 178 to 187 us).
 __host__ __device__ constexpr int deep_of(int cg) { return cg == 1 ? 2 : 1; }
 // Sixteens of B_a's ranks in a stage, whose place of x takes each row's values of u in `terms` terms.
 __host__ __device__ constexpr int fill_of(int cg, int terms) { return cg == 2 && terms == 2 ? 2 : 4; }
@@ -1144,9 +1146,11 @@ double slab_cycles(int outs, int nt, int cg) {
 // clusters that the GPU has room for, or memory's time, and what a tile's end takes. A pair of blocks
 // (cg = 2) loads half of the rows of x each. Where one round does, tiles have as few rows of W as keep
 // all SMs busy. Only the order of the estimates matters. Both sides measured: pairs of 256 rows against
-// single blocks of 144, trees 68 and 82 us, 8-bit stress rows 119 and 149, prompts 185 and 218; one
-// token of 8 requests by two blocks a tile and by one, 16.3 and 17.0 us; of 128 requests in tiles of 128 rows
-// by four blocks, of 64 by two and of 32 by one, 23.5, 23.0 and 23.8 us.
+// single blocks of 144 (with adapters 128), trees 72 and 93 us, 8-bit stress rows 120 and 151, prompts 190 and
+// 236; one token of 8 requests by two blocks a tile and by one, 16.3 and 18.3 us; of 128 requests in tiles of
+// 128 rows by four blocks, of 64 by two and of 32 by one, 25.2, 24.6 and 25.4 us. The adapters' stages are
+// not in the estimates: how many distinct adapters a tile's requests have the host does not know. With a small
+// K and many adapters of a high rank they are most of a tile's time, and the plan is that of their absence.
 void choose(const ProjectArgs &a, bool e8, bool ad, const Rooms &room, int smem, ProjectPlan *p) {
   const int size = e8 ? 1 : 2, steps = ceil_div(static_cast<int64_t>(a.K) * size, 128);
   // of a pair; with adapters three accumulators instead of two. Of a single block: three stages; with adapters a thread
@@ -1194,10 +1198,10 @@ void choose(const ProjectArgs &a, bool e8, bool ad, const Rooms &room, int smem,
 }
 
 // The launch before: a block a row and four ranks while all that they read (from L2) takes less time
-// than the other kernel adds (s->tiles = 0: 128 tokens of rank 32 24 us instead of 29, but the trees
-// 89 instead of 68); else blocks that fit the places which have a tile less to do cost nothing as long as
+// than the other kernel adds (s->tiles = 0: 128 tokens of rank 32 25.4 us instead of 30, but the trees
+// 93 instead of 72); else blocks that fit the places which have a tile less to do cost nothing as long as
 // they end within the others' first tile (the trees: 24 blocks of 152 places;
-// 68 us, 64 where no request has an adapter, 62 without any); else the shortest.
+// 72 us, 66 where no request has an adapter, 63 without any); else the shortest.
 void choose_down(const ProjectArgs &a, const ProjectPlan &p, const Rooms &room, int smem, ProjectShape *s) {
   const int steps = ceil_div(2 * a.K, 128), spt = kOuts / a.rank;
   double best = 1e300;

@@ -1358,7 +1358,8 @@ int dt_project(const dt_matrix *w, const void *x, int64_t ldx, const uint8_t *x_
   if (adapters) {
     if (!adapters->down || !adapters->up || !dt::al16(adapters->down) || !dt::al16(adapters->up) ||
         (reinterpret_cast<uintptr_t>(adapters->scale) & 3u) || adapters->count < 1 ||
-        adapters->count > (1 << 20) || adapters->terms < 0 || adapters->terms > 2 || adapters->rank < 16 || adapters->rank > 128 || adapters->rank % 16 ||
+        adapters->count > (1 << 20) || adapters->terms < 0 || adapters->terms > 2 ||
+        adapters->rank < 16 || adapters->rank > 128 || adapters->rank % 16 ||
         (reinterpret_cast<uintptr_t>(index) & 3u) || !workspace ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
         workspace_bytes < std::max(adapters->terms, 1) * dt_project_workspace_bytes(batch, n, adapters->rank) ||

@@ -537,11 +537,12 @@ int dt_cache_slots(const dt_cache *c, int n, const int32_t *first, const int32_t
  * computed in fp32. total (with residual only) gets t, out gets y, rounded once each;
  * codes and exps get y in 8 bits, taken from fp32. out, or codes and exps, may be NULL,
  * not both. weight [d] has the rows' type (NULL: ones). An output may be one of the inputs
- * (the same view), and must not overlap them otherwise, nor another output (total and out that
- * begin at the same place are refused); codes and exps are buffers of their own. d in [1, 32768], dtype DT_BF16 or DT_F16, eps >= 1e-30. Rows of a multiple
- * of 8 values on 16-byte boundaries are moved 16 bytes at a time. Others are too, in the aligned 16-byte granules
- * that they lie in: what else a granule between a view's first and last value holds is read with it and
- * plays no part, and only the row's values are written.
+ * (the same view), and must not overlap them otherwise, nor another output (total and out
+ * that begin at the same place are refused); codes and exps are buffers of their own.
+ * d in [1, 32768], dtype DT_BF16 or DT_F16, eps >= 1e-30. Rows of a multiple of 8 values on
+ * 16-byte boundaries are moved 16 bytes at a time. Others are too, in the aligned 16-byte
+ * granules that they lie in: what else a granule between a view's first and last value holds
+ * is read with it and plays no part, and only the rows' values are written.
  *
  * dt_quantize_rows: x itself in 8 bits. */
 typedef struct {
@@ -559,11 +560,12 @@ int dt_quantize_rows(const dt_rows *x, uint8_t *codes, uint8_t *exps, int outer,
  * it: for row i of request b, with a = index[b],
  *   y = x W^T + scale[a] (x A_a^T) B_a^T,
  * the second term only where 0 <= a < adapters->count (a negative index: no adapter; one at or
- * above count: none, and DT_ERR_BAD_INDEX in *status). Products are accumulated in fp32; y is rounded once.
- * Before the product with B x A^T, times the scale, is held in 16-bit terms of type dtype: two (terms = 2), the
- * second one what rounding the first left, so that 2^-16 of a value is lost in bf16 and 2^-22 in fp16 (or
- * 2^-25, its least step's half, where that is more); or one (terms 0 or 1), half the workspace and a stage's copies,
- * 2^-8 and 2^-11. Either overflows where dtype does. A row of B with a value that is not finite makes that output NaN for
+ * above count: none, and DT_ERR_BAD_INDEX in *status). Products are accumulated in fp32, y is
+ * rounded once. For its product with B, x A^T times the scale is held in 16-bit terms of type
+ * dtype. Two (terms = 2), the second one what rounding the first left, lose 2^-16 of a value at
+ * most in bf16 and 2^-22 in fp16 (or 2^-25, half its least step, where that is more). One (terms
+ * 0 or 1) loses 2^-8 and 2^-11, and takes half the workspace. Both overflow where dtype does.
+ * A row of B with a value that is not finite makes that output NaN for
  * the rows with that adapter; what is not finite elsewhere reaches the rows that use it alone.
  *   w      W [O][K], dtype 16-bit or DT_E4M3 with exps [O] (8-bit rows); data 16-byte
  *          aligned, row stride ld elements, a multiple of 16 bytes
@@ -578,9 +580,9 @@ int dt_quantize_rows(const dt_rows *x, uint8_t *codes, uint8_t *exps, int outer,
  *   index  [batch] int32; with adapters only
  *   status one int32 of the caller's, zeroed once: DT_ERR_BAD_INDEX, DT_ERR_TIMEOUT
  * K: a multiple of 16 in [16, 65536]; O in [1, 2^24]; rank: a multiple of 16 in [16, 128];
- * batch in [1, 65535], batch n <= 2^24, batch n O <= 2^38. workspace: `terms` times
- * dt_project_workspace_bytes bytes, 256-byte aligned, for x A^T (may be 0: NULL without adapters); the size
- * for a batch, n and rank serves smaller ones. Sums run in an order fixed by the sizes: results repeat. */
+ * batch in [1, 65535], batch n <= 2^24, batch n O <= 2^38. workspace: for each term of x A^T
+ * dt_project_workspace_bytes bytes, 256-byte aligned (may be 0: NULL without adapters); the
+ * size for a batch, n and rank serves smaller ones. Sums run in an order fixed by the sizes: results repeat. */
 typedef struct {
   const void *data;
   const uint8_t *exps;
